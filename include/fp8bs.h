@@ -384,6 +384,126 @@ int fp8bs_quantize_1x128(const void* x, int x_dtype, void* q, float* sfa, int gr
 int fp8bs_quantize_128x128(const void* x, int x_dtype, void* q, float* sfb, int groups, int n,
                            int k, hipStream_t stream);
 
+/*
+ * MXFP4: operands of 4-bit values with a shared power-of-two scale, and the feed-forward
+ * operators on them.
+ *
+ * 32 consecutive values along K share the scale 2^(e-127), e an 8-bit exponent (E8M0);
+ * each value is a 4-bit e2m1 number v (bit 3 the sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6) and
+ * stands for v * 2^(e-127).  e = 255 is not a number: the 32 values are NaN.
+ *   codes      uint8 [rows][k/2]: the value of K position 2i in the low, 2i+1 in the high
+ *              nibble of byte i.
+ *   exponents  int32 [k/128][fp8bs_get_sfa_ld(rows)], K-group-major: byte j (least
+ *              significant first) of word [c][r] is the exponent of row r's values
+ *              128c + 32j .. 128c + 32j + 31.
+ * Operands with groups (masked slots, experts' weights) repeat both per group.  K is a
+ * positive multiple of 128.  Pointers are 16-byte aligned (grouped_layout and masked_m
+ * 4-byte); sizes, valid rows, streams and errors are as for the FP8 calls above.
+ *
+ * fp8bs_quantize_mxfp4 -- x f32 or bf16 [groups][rows][k] -> codes and exponents:
+ *     e - 127 = floor(log2(max |x|)) - 2 over the block (at least -127; a block of zeros
+ *     gets -127), code = e2m1(x * 2^(127-e)), the nearest value, ties to the even code,
+ *     magnitudes above 6 saturating.  A block holding an infinity or a NaN gets e = 255 and
+ *     zero codes.  The alignment padding of the exponents is not written.
+ * fp8bs_dequantize_mxfp4 -- the values they stand for, in f32 or bf16 (both hold every
+ *     value the quantiser produces exactly).
+ */
+int fp8bs_quantize_mxfp4(const void* x, int x_dtype, void* q, int32_t* sf, int groups, int rows,
+                         int k, hipStream_t stream);
+int fp8bs_dequantize_mxfp4(const void* q, const int32_t* sf, void* x, int x_dtype, int groups,
+                           int rows, int k, hipStream_t stream);
+
+/*
+ * MXFP4 products D = bf16(A B^T), one per layout (D, grouped_layout, masked_m, expected_m
+ * and the valid rows as for fp8bs_dense_nt, fp8bs_grouped_contiguous_nt and
+ * fp8bs_grouped_masked_nt):
+ *   a  codes [m][k/2] (masked [num_groups][max_m][k/2]), sfa its exponents
+ *   b  codes [n][k/2] per group,                         sfb its exponents, ld(n) per row
+ * The matrix core applies the scales and accumulates in FP32; D is rounded once.
+ */
+int fp8bs_dense_nt_mxfp4(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                         void* d, int m, int n, int k, hipStream_t stream);
+int fp8bs_grouped_contiguous_nt_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                                      const int32_t* sfb, void* d, const int32_t* grouped_layout,
+                                      int m_total, int n, int k, int num_groups,
+                                      hipStream_t stream);
+int fp8bs_grouped_masked_nt_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                                  const int32_t* sfb, void* d, const int32_t* masked_m,
+                                  int num_groups, int max_m, int expected_m, int n, int k,
+                                  hipStream_t stream);
+
+/* Activation of a gated block. */
+typedef enum {
+    FP8BS_ACT_SILU = 0,        /* x / (1 + exp(-x))                                    */
+    FP8BS_ACT_GELU_TANH = 1    /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2      */
+} fp8bs_activation;
+
+/*
+ * Gated feed-forward block: both projections, the activation and the product in one
+ * kernel,
+ *     h = act(A Wg^T) * (A Wu^T)
+ *   b  codes of [2f][k] per group: rows 0 .. f-1 the gate projection Wg, rows f .. 2f-1
+ *      the up projection Wu; sfb its exponents, ld(2f) words per row
+ *   h  bf16 [m][f] (masked [num_groups][max_m][f]); f a positive multiple of 32
+ * The _q calls quantise h to MXFP4 (from its FP32 values, as fp8bs_quantize_mxfp4 would)
+ * for the product that follows: hq codes [m][f/2], sfh exponents [f/128][ld(m)] (masked:
+ * per slot); f a multiple of 128.  Rows that are not valid are written in neither.
+ */
+int fp8bs_gated_dense_mxfp4(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                            void* h, int m, int f, int k, int activation, hipStream_t stream);
+int fp8bs_gated_contiguous_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                                 const int32_t* sfb, void* h, const int32_t* grouped_layout,
+                                 int m_total, int f, int k, int num_groups, int activation,
+                                 hipStream_t stream);
+int fp8bs_gated_masked_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                             const int32_t* sfb, void* h, const int32_t* masked_m,
+                             int num_groups, int max_m, int expected_m, int f, int k,
+                             int activation, hipStream_t stream);
+int fp8bs_gated_dense_mxfp4_q(const void* a, const int32_t* sfa, const void* b,
+                              const int32_t* sfb, void* hq, int32_t* sfh, int m, int f, int k,
+                              int activation, hipStream_t stream);
+int fp8bs_gated_contiguous_mxfp4_q(const void* a, const int32_t* sfa, const void* b,
+                                   const int32_t* sfb, void* hq, int32_t* sfh,
+                                   const int32_t* grouped_layout, int m_total, int f, int k,
+                                   int num_groups, int activation, hipStream_t stream);
+int fp8bs_gated_masked_mxfp4_q(const void* a, const int32_t* sfa, const void* b,
+                               const int32_t* sfb, void* hq, int32_t* sfh,
+                               const int32_t* masked_m, int num_groups, int max_m,
+                               int expected_m, int f, int k, int activation,
+                               hipStream_t stream);
+
+/*
+ * Backward pass of the gated block, with respect to the values that the codes and
+ * exponents of A and W stand for.  Gate and up projections are computed again (they are
+ * not stored by the forward call);
+ *     dg = dh * up * act'(gate),  du = dh * act(gate)      (rounded to bf16)
+ *     da = dg Wg + du Wu,         db = [dg^T A; du^T A]
+ * with 4-bit values widened to bf16, which holds them exactly, and FP32 accumulation.
+ *   dh  bf16 [m][f]
+ *   da  bf16 [m][k], or NULL (not wanted); written at valid rows
+ *   db  bf16 or f32 (db_dtype) [2f][k] per group, or NULL; every element written (zeros
+ *       for an expert without rows).  accumulate != 0 (f32 only): added to what db holds.
+ *   workspace  device memory of at least fp8bs_gated_backward_workspace_size() bytes,
+ *       16-byte aligned, contents ignored; not needed after the stream work ends.  Less is
+ *       refused with FP8BS_ERR_UNSUPPORTED.
+ * f is a positive multiple of 32.  Rows of the contiguous layout that are not valid (and
+ * whatever they hold) take no part.  The size call takes the dense or contiguous layout
+ * code and whether da / db are wanted; it returns -FP8BS_ERR_SHAPE for an invalid request.
+ */
+int64_t fp8bs_gated_backward_workspace_size(int layout, int64_t m, int f, int k, int num_groups,
+                                            int want_da, int want_db);
+int fp8bs_gated_dense_mxfp4_backward(const void* a, const int32_t* sfa, const void* b,
+                                     const int32_t* sfb, const void* dh, void* da, void* db,
+                                     int db_dtype, int accumulate, int m, int f, int k,
+                                     int activation, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream);
+int fp8bs_gated_contiguous_mxfp4_backward(const void* a, const int32_t* sfa, const void* b,
+                                          const int32_t* sfb, const void* dh, void* da, void* db,
+                                          int db_dtype, int accumulate,
+                                          const int32_t* grouped_layout, int m_total, int f,
+                                          int k, int num_groups, int activation, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+
 /* Row alignment of expert segments in the contiguous layout (128).  Analogue
  * of get_mk_alignment_for_contiguous_layout (hada page, section "Tiện ích và
  * biến môi trường"). */

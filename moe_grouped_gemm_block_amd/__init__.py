@@ -814,3 +814,11 @@ def _k_grouped(a, sfa, b, sfb, d, ks, c, workspace, stream, e8):
         st = getattr(_load(), name)(*args, cp, dp, ks_host, g, m, n, k_total, wp, wb,
                                     _stream_handle(s, a.device))
     _check(st, name)
+
+
+# ---- MXFP4 operators (mxfp4.py) ------------------------------------------------
+
+from . import mxfp4 as _mxfp4  # noqa: E402  (needs the helpers above)
+from .mxfp4 import *  # noqa: E402,F401,F403
+
+__all__ += _mxfp4.__all__

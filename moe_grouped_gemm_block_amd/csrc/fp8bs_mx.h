@@ -1,0 +1,155 @@
+// fp8bs_mx.h -- device helpers and host types shared by the MXFP4 translation units
+// (fp8bs_mx_quant.hip, fp8bs_mx_gemm.hip, fp8bs_mx_stream.hip, fp8bs_mx_api.hip).
+// Not part of the public interface.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8bs.h"
+
+namespace fp8bs {
+namespace mx {
+
+// Row layouts, as the FP8 entry points have them.  kBlocks: the contraction runs over the
+// token blocks of one expert (the weight gradient of the contiguous layout).
+enum Layout : int { kDense = 0, kContiguous = 1, kMasked = 2, kBlocks = 3 };
+
+// Operand types of the matrix kernel: 32 4-bit values with a shared power-of-two scale, or
+// bfloat16.
+enum Operand : int { kFp4 = 0, kBf16 = 1 };
+
+// What is done with the accumulators.
+//   kStore      D = bf16(acc)
+//   kStoreF32   D = acc, or D + acc when MxParams::accumulate is set
+//   kGated      h = act(gate) * up, rounded to bf16
+//   kGatedQuant the same h quantised to MXFP4
+//   kGatedGrad  dg = dh * up * act'(gate), du = dh * act(gate), rounded to bf16 and stored
+//               row-major and transposed
+enum Epilogue : int { kStore = 0, kStoreF32 = 1, kGated = 2, kGatedQuant = 3, kGatedGrad = 4 };
+constexpr bool gated(int epi) { return epi == kGated || epi == kGatedQuant || epi == kGatedGrad; }
+
+// Tiles along M that one launch lists in LDS (contiguous, masked); the host cuts longer
+// problems into several launches.
+constexpr int kMaxListed = 2048;
+
+struct MxParams {
+    const uint8_t* a;           // [rows] of a_row bytes
+    const uint8_t* b;           // [groups][B rows] of b_row bytes
+    const int32_t* sfa;         // kFp4: [kwords][sfa_ld] (masked: per slot)
+    const int32_t* sfb;         // kFp4: [groups][kwords][sfb_ld]
+    void* d;                    // output; kGatedQuant: codes; kGatedGrad: [rows][2f]
+    void* d2;                   // kGatedQuant: exponents; kGatedGrad: transposed [2f][d2_ld]
+    const uint16_t* dh;         // kGatedGrad: bf16 [rows][f]
+    const int32_t* group_data;  // contiguous: grouped_layout; masked: masked_m
+    const int32_t* blocks;      // kBlocks: [groups + 1] offsets, then block numbers
+    int64_t a_row, b_row;       // row strides in bytes
+    int64_t d_ld, d2_ld;        // elements (kGatedQuant: d_ld bytes of codes, d2_ld words)
+    int m;                      // dense: M; contiguous: m_total; masked: rows of a slot
+    int n;                      // output columns (gated: f)
+    int kwords;                 // k / 128 (kFp4)
+    int chunks;                 // 128-byte steps of a row
+    int sfa_ld, sfb_ld;
+    int num_groups;
+    int m_tiles, n_tiles;       // m_tiles: dense, and per slot for masked
+    int first, last;            // contiguous: blocks, masked: tiles, that this launch covers
+    int raster;
+    int act;
+    int accumulate;
+};
+
+#ifdef __HIPCC__
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+__device__ __forceinline__ float from_bf16(uint32_t h) {
+    return __builtin_bit_cast(float, h << 16);
+}
+
+// E8M0 exponent of a 32-value block from the largest magnitude's FP32 bits: its exponent
+// less 2 (6 = 1.5 * 2^2 is the largest e2m1 value), at least 0; 255 (not a number) when the
+// block holds an infinity or a NaN.  Magnitudes below 2^-124, zero among them, give 0.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t amax_bits) {
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? 255u : e > 2u ? e - 2u : 0u;
+}
+// 2^(127 - e), normal for every finite block's e (at most 252); multiplying by it is exact
+__device__ __forceinline__ float inverse_scale(uint32_t e) {
+    return __builtin_bit_cast(float, (254u - e) << 23);
+}
+
+// Value of code c (0..15) at exponent e, exact in FP32 and in bf16: the smallest magnitude
+// is 0.5 * 2^-127 (a subnormal of both), the largest 6 * 2^127 only reachable by hand-made
+// exponents (infinity then); e = 255 is not a number.
+__device__ __forceinline__ float code_value(uint32_t c, float scale_hi, float scale_lo) {
+    // magnitude as a float: exponent field 126 + (c >> 1 & 3), mantissa bit c & 1; codes 0
+    // and 1 are 0 and 0.5
+    const uint32_t mag = c & 7u;
+    const uint32_t bits = mag < 2u ? (mag ? 0x3F000000u : 0u)
+                                   : ((126u + (mag >> 1)) << 23) | ((mag & 1u) << 22);
+    return __builtin_bit_cast(float, bits | ((c & 8u) << 28)) * scale_hi * scale_lo;
+}
+// 2^(e - 127) as a product of two normal factors, the second a power of two that is exact
+// to multiply by last (one rounding at most, none for values that FP32 holds)
+__device__ __forceinline__ void scale_factors(uint32_t e, float& hi, float& lo) {
+    if (e == 255u) {
+        hi = __builtin_nanf("");
+        lo = 1.0f;
+    } else if (e < 64u) {
+        hi = __builtin_bit_cast(float, (e + 63u) << 23);        // 2^(e - 64)
+        lo = 0x1p-63f;
+    } else {
+        hi = __builtin_bit_cast(float, e << 23);
+        lo = 1.0f;
+    }
+}
+
+// Activation of the gate and its derivative.  One exponential and one reciprocal each
+// (v_exp_f32, v_rcp_f32: about one unit in the last place, far below the bf16 rounding of
+// what they end in).
+template <bool GRAD>
+__device__ __forceinline__ float activate(int act, float v, float& slope) {
+    if (act == FP8BS_ACT_SILU) {
+        const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+        if (GRAD) slope = sig * (1.0f + v * (1.0f - sig));
+        return v * sig;
+    }
+    // 0.5 v (1 + tanh(y)) = v / (1 + exp(-2y)),  y = sqrt(2/pi) (v + 0.044715 v^3)
+    constexpr float c = 0.7978845608028654f;
+    const float y = c * (v + 0.044715f * v * v * v);
+    const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-2.0f * y));
+    if (GRAD) slope = sig + 2.0f * v * sig * (1.0f - sig) * c * (1.0f + 0.134145f * v * v);
+    return v * sig;
+}
+
+#endif  // __HIPCC__
+
+// Launchers (fp8bs_mx_gemm.hip, fp8bs_mx_quant.hip); return a hipError_t value.
+//
+// Values of codes [groups][rows][k/2] in bf16, transposed: xt [groups][k][ld], columns rows
+// .. ld-1 (ld a multiple of 64, rows <= ld < rows + 64) and, where grouped_layout is given,
+// rows that hold no token as zeros.
+int launch_transpose(const uint8_t* q, const int32_t* sf, uint16_t* xt, int groups, int rows,
+                     int k, int64_t ld, const int32_t* grouped_layout, int num_experts,
+                     hipStream_t stream);
+// Contiguous layout: out = [num_groups + 1] offsets, then each expert's 128-row blocks in
+// order (a block belongs to the expert of its first row).
+int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups, int32_t* out,
+                       hipStream_t stream);
+int launch_gemm(int operand, int layout, int epilogue, const MxParams& p, int groups,
+                int expected_rows, int num_cus, hipStream_t stream);
+
+}  // namespace mx
+}  // namespace fp8bs

@@ -1,0 +1,347 @@
+// fp8bs_mx_api.cpp -- C entry points of the MXFP4 products and of the gated feed-forward
+// block (declared in include/fp8bs.h): checks of sizes and pointers, the kernels' parameters
+// and the launches.  No allocation, no synchronisation, no host read of device data.
+#include <hip/hip_runtime.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "fp8bs_mx.h"
+
+namespace {
+
+using namespace fp8bs::mx;
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_cus[kMaxDevices];           // 0: not asked yet
+
+// Compute units of the current device under the process's cap; 0 on error.
+int device_cus() {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    int cus = dev >= 0 && dev < kMaxDevices ? g_cus[dev].load(std::memory_order_relaxed) : 0;
+    if (cus == 0) {
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            return 0;
+        if (dev >= 0 && dev < kMaxDevices) g_cus[dev].store(cus, std::memory_order_relaxed);
+    }
+    const int cap = fp8bs_get_num_cus();
+    return cap > 0 && cap < cus ? cap : cus;
+}
+
+bool aligned(const void* p, uintptr_t to) { return p && ((uintptr_t)p & (to - 1)) == 0; }
+
+// Sizes of one call: rows (dense M, contiguous m_total, masked max_m), columns of the
+// weight (product n, gated 2f), k, groups.
+int check_sizes(int layout, int64_t m, int64_t cols, int k, int groups) {
+    if (k < 128 || k % 128 != 0 || m < 0 || cols < 1 || groups < 1) return FP8BS_ERR_SHAPE;
+    if (layout == kContiguous && m % 128 != 0) return FP8BS_ERR_SHAPE;
+    // copy offsets within a 256-row tile and exponent words are 32-bit
+    if (k > (1 << 24)) return FP8BS_ERR_SHAPE;
+    const double words = k / 128.0;
+    if ((m + 3) * words * 4 >= 4294967296.0 || (cols + 3) * words * 4 >= 4294967296.0)
+        return FP8BS_ERR_SHAPE;
+    if (m > 0x7ffffe00 || cols > 0x7ffffe00) return FP8BS_ERR_SHAPE;
+    return FP8BS_OK;
+}
+
+// The parameters that every call shares.
+MxParams base_params(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                     const int32_t* group_data, int m, int64_t cols, int k, int groups) {
+    MxParams p;
+    memset(&p, 0, sizeof p);
+    p.a = (const uint8_t*)a;
+    p.b = (const uint8_t*)b;
+    p.sfa = sfa;
+    p.sfb = sfb;
+    p.group_data = group_data;
+    p.a_row = p.b_row = k / 2;
+    p.m = m;
+    p.kwords = k / 128;
+    p.chunks = (k + 255) / 256;
+    p.sfa_ld = (int)fp8bs_get_sfa_ld(m);
+    p.sfb_ld = (int)fp8bs_get_sfa_ld(cols);
+    p.num_groups = groups;
+    return p;
+}
+
+bool pointers_ok(const void* a, const void* sfa, const void* b, const void* sfb, int layout,
+                 const int32_t* group_data) {
+    return aligned(a, 16) && aligned(sfa, 16) && aligned(b, 16) && aligned(sfb, 16) &&
+           (layout == kDense || aligned(group_data, 4));
+}
+
+int status(int hip) {
+    return hip == (int)hipSuccess ? FP8BS_OK
+           : hip == (int)hipErrorInvalidValue ? FP8BS_ERR_UNSUPPORTED : FP8BS_ERR_HIP;
+}
+
+int product(int layout, const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+            void* d, const int32_t* group_data, int m, int expected_m, int n, int k, int groups,
+            hipStream_t stream) {
+    const int st = check_sizes(layout, m, n, k, groups);
+    if (st != FP8BS_OK || m == 0) return st;
+    if (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(d, 16))
+        return FP8BS_ERR_POINTER;
+    const int cus = device_cus();
+    if (cus <= 0) return FP8BS_ERR_HIP;
+    MxParams p = base_params(a, sfa, b, sfb, group_data, m, n, k, groups);
+    p.d = d;
+    p.d_ld = n;
+    p.n = n;
+    const int rows = layout == kMasked && expected_m > 0 && expected_m < m ? expected_m : m;
+    return status(launch_gemm(kFp4, layout, kStore, p, groups, rows, cus, stream));
+}
+
+int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
+                  const int32_t* sfb, void* h, int32_t* sfh, bool quantise,
+                  const int32_t* group_data, int m, int expected_m, int f, int k, int groups,
+                  int activation, hipStream_t stream) {
+    if (f < 1 || f % (quantise ? 128 : 32) != 0) return FP8BS_ERR_SHAPE;
+    const int st = check_sizes(layout, m, 2 * (int64_t)f, k, groups);
+    if (st != FP8BS_OK) return st;
+    if (activation != FP8BS_ACT_SILU && activation != FP8BS_ACT_GELU_TANH)
+        return FP8BS_ERR_UNSUPPORTED;
+    if (m == 0) return FP8BS_OK;
+    if (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(h, 16) ||
+        (quantise && !aligned(sfh, 16)))
+        return FP8BS_ERR_POINTER;
+    const int cus = device_cus();
+    if (cus <= 0) return FP8BS_ERR_HIP;
+    MxParams p = base_params(a, sfa, b, sfb, group_data, m, 2 * (int64_t)f, k, groups);
+    p.d = h;
+    p.d2 = sfh;
+    p.d_ld = quantise ? f / 2 : f;
+    p.d2_ld = quantise ? p.sfa_ld : 0;
+    p.n = f;
+    p.act = activation;
+    const int rows = layout == kMasked && expected_m > 0 && expected_m < m ? expected_m : m;
+    return status(launch_gemm(kFp4, layout, quantise ? kGatedQuant : kGated, p, groups, rows, cus,
+                              stream));
+}
+
+// Workspace of the backward pass: dg | du row-major, the weights widened and transposed (for
+// da); dg | du and A transposed, the blocks by expert (for db).  Every part starts at a
+// multiple of 256 bytes.
+struct Parts {
+    int64_t grad, weights, grad_t, a_t, order, total;
+    int64_t m_ld;                    // leading dimension of the transposed tokens
+};
+Parts parts(int layout, int64_t m, int f, int k, int groups, bool want_da, bool want_db) {
+    Parts w;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    w.m_ld = (m + 63) / 64 * 64;
+    w.grad = take(want_da ? m * 2 * f * 2 : 0);
+    w.weights = take(want_da ? (int64_t)groups * k * 2 * f * 2 : 0);
+    w.grad_t = take(want_db ? 2 * (int64_t)f * w.m_ld * 2 : 0);
+    w.a_t = take(want_db ? (int64_t)k * w.m_ld * 2 : 0);
+    // (four entries to spare: the copies look up to two steps past the last block)
+    w.order = take(want_db && layout == kContiguous ? (groups + 1 + m / 128 + 4) * 4 : 0);
+    w.total = at;
+    return w;
+}
+
+int check_backward(int layout, int64_t m, int f, int k, int groups) {
+    if (layout != kDense && layout != kContiguous) return FP8BS_ERR_SHAPE;
+    if (f < 1 || f % 32 != 0) return FP8BS_ERR_SHAPE;
+    const int st = check_sizes(layout, m, 2 * (int64_t)f, k, groups);
+    if (st != FP8BS_OK) return st;
+    // 256 rows of a transposed operand within 32-bit copy offsets, step offsets below 4 GiB
+    if (m > (1 << 23) || f > (1 << 22)) return FP8BS_ERR_SHAPE;
+    return FP8BS_OK;
+}
+
+int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
+                   const int32_t* sfb, const void* dh, void* da, void* db, int db_dtype,
+                   int accumulate, const int32_t* group_data, int m, int f, int k, int groups,
+                   int activation, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_backward(layout, m, f, k, groups);
+    if (st != FP8BS_OK) return st;
+    if (activation != FP8BS_ACT_SILU && activation != FP8BS_ACT_GELU_TANH)
+        return FP8BS_ERR_UNSUPPORTED;
+    const bool f32 = db_dtype == FP8BS_DTYPE_F32;
+    if (!f32 && db_dtype != FP8BS_DTYPE_BF16) return FP8BS_ERR_UNSUPPORTED;
+    if (accumulate && !f32) return FP8BS_ERR_UNSUPPORTED;
+    if (!da && !db) return FP8BS_OK;
+    if ((da && !aligned(da, 16)) || (db && !aligned(db, 16))) return FP8BS_ERR_POINTER;
+    if (m > 0 && (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(dh, 16)))
+        return FP8BS_ERR_POINTER;
+    if (m == 0 && (!db || accumulate)) return FP8BS_OK;
+    const Parts w = parts(layout, m, f, k, groups, da != nullptr, db != nullptr);
+    if (w.total > 0 && workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
+    if (w.total > 0 && !aligned(workspace, 16)) return FP8BS_ERR_POINTER;
+    const int cus = device_cus();
+    if (cus <= 0) return FP8BS_ERR_HIP;
+    uint8_t* ws = (uint8_t*)workspace;
+    uint16_t* grad = (uint16_t*)(ws + w.grad);
+    uint16_t* weights = (uint16_t*)(ws + w.weights);
+    uint16_t* grad_t = (uint16_t*)(ws + w.grad_t);
+    uint16_t* a_t = (uint16_t*)(ws + w.a_t);
+    int32_t* order = (int32_t*)(ws + w.order);
+
+    if (m > 0) {
+        MxParams p = base_params(a, sfa, b, sfb, group_data, m, 2 * (int64_t)f, k, groups);
+        p.n = f;
+        p.act = activation;
+        p.dh = (const uint16_t*)dh;
+        p.d = da ? grad : nullptr;
+        p.d_ld = 2 * (int64_t)f;
+        p.d2 = db ? grad_t : nullptr;
+        p.d2_ld = w.m_ld;
+        st = status(launch_gemm(kFp4, layout, kGatedGrad, p, groups, m, cus, stream));
+        if (st != FP8BS_OK) return st;
+    }
+    if (da && m > 0) {
+        st = status(launch_transpose((const uint8_t*)b, sfb, weights, groups, 2 * f, k,
+                                     2 * (int64_t)f, nullptr, 0, stream));
+        if (st != FP8BS_OK) return st;
+        MxParams p;
+        memset(&p, 0, sizeof p);
+        p.a = (const uint8_t*)grad;
+        p.b = (const uint8_t*)weights;
+        p.a_row = p.b_row = 4 * (int64_t)f;
+        p.group_data = group_data;
+        p.m = m;
+        p.n = k;
+        p.chunks = f / 32;
+        p.num_groups = groups;
+        p.d = da;
+        p.d_ld = k;
+        st = status(launch_gemm(kBf16, layout, kStore, p, groups, m, cus, stream));
+        if (st != FP8BS_OK) return st;
+    }
+    if (db) {
+        if (m > 0) {
+            st = status(launch_transpose((const uint8_t*)a, sfa, a_t, 1, m, k, w.m_ld,
+                                         layout == kContiguous ? group_data : nullptr, groups,
+                                         stream));
+            if (st != FP8BS_OK) return st;
+        }
+        if (layout == kContiguous) {
+            st = status(launch_block_order(group_data, m / 128, groups, order, stream));
+            if (st != FP8BS_OK) return st;
+        }
+        MxParams p;
+        memset(&p, 0, sizeof p);
+        p.a = (const uint8_t*)grad_t;
+        p.b = (const uint8_t*)a_t;
+        p.a_row = p.b_row = 2 * w.m_ld;
+        p.blocks = order;
+        p.m = 2 * f;
+        p.n = k;
+        p.chunks = (int)(w.m_ld / 64);
+        p.num_groups = groups;
+        p.d = db;
+        p.d_ld = k;
+        p.accumulate = accumulate;
+        st = status(launch_gemm(kBf16, layout == kContiguous ? kBlocks : kDense,
+                                f32 ? kStoreF32 : kStore, p, groups, 2 * f, cus, stream));
+    }
+    return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8bs_dense_nt_mxfp4(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                         void* d, int m, int n, int k, hipStream_t stream) {
+    return product(kDense, a, sfa, b, sfb, d, nullptr, m, 0, n, k, 1, stream);
+}
+
+int fp8bs_grouped_contiguous_nt_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                                      const int32_t* sfb, void* d, const int32_t* grouped_layout,
+                                      int m_total, int n, int k, int num_groups,
+                                      hipStream_t stream) {
+    return product(kContiguous, a, sfa, b, sfb, d, grouped_layout, m_total, 0, n, k, num_groups,
+                   stream);
+}
+
+int fp8bs_grouped_masked_nt_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                                  const int32_t* sfb, void* d, const int32_t* masked_m,
+                                  int num_groups, int max_m, int expected_m, int n, int k,
+                                  hipStream_t stream) {
+    return product(kMasked, a, sfa, b, sfb, d, masked_m, max_m, expected_m, n, k, num_groups,
+                   stream);
+}
+
+int fp8bs_gated_dense_mxfp4(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                            void* h, int m, int f, int k, int activation, hipStream_t stream) {
+    return gated_forward(kDense, a, sfa, b, sfb, h, nullptr, false, nullptr, m, 0, f, k, 1,
+                         activation, stream);
+}
+
+int fp8bs_gated_contiguous_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                                 const int32_t* sfb, void* h, const int32_t* grouped_layout,
+                                 int m_total, int f, int k, int num_groups, int activation,
+                                 hipStream_t stream) {
+    return gated_forward(kContiguous, a, sfa, b, sfb, h, nullptr, false, grouped_layout, m_total,
+                         0, f, k, num_groups, activation, stream);
+}
+
+int fp8bs_gated_masked_mxfp4(const void* a, const int32_t* sfa, const void* b,
+                             const int32_t* sfb, void* h, const int32_t* masked_m,
+                             int num_groups, int max_m, int expected_m, int f, int k,
+                             int activation, hipStream_t stream) {
+    return gated_forward(kMasked, a, sfa, b, sfb, h, nullptr, false, masked_m, max_m, expected_m,
+                         f, k, num_groups, activation, stream);
+}
+
+int fp8bs_gated_dense_mxfp4_q(const void* a, const int32_t* sfa, const void* b,
+                              const int32_t* sfb, void* hq, int32_t* sfh, int m, int f, int k,
+                              int activation, hipStream_t stream) {
+    return gated_forward(kDense, a, sfa, b, sfb, hq, sfh, true, nullptr, m, 0, f, k, 1,
+                         activation, stream);
+}
+
+int fp8bs_gated_contiguous_mxfp4_q(const void* a, const int32_t* sfa, const void* b,
+                                   const int32_t* sfb, void* hq, int32_t* sfh,
+                                   const int32_t* grouped_layout, int m_total, int f, int k,
+                                   int num_groups, int activation, hipStream_t stream) {
+    return gated_forward(kContiguous, a, sfa, b, sfb, hq, sfh, true, grouped_layout, m_total, 0,
+                         f, k, num_groups, activation, stream);
+}
+
+int fp8bs_gated_masked_mxfp4_q(const void* a, const int32_t* sfa, const void* b,
+                               const int32_t* sfb, void* hq, int32_t* sfh,
+                               const int32_t* masked_m, int num_groups, int max_m,
+                               int expected_m, int f, int k, int activation,
+                               hipStream_t stream) {
+    return gated_forward(kMasked, a, sfa, b, sfb, hq, sfh, true, masked_m, max_m, expected_m, f,
+                         k, num_groups, activation, stream);
+}
+
+int64_t fp8bs_gated_backward_workspace_size(int layout, int64_t m, int f, int k, int num_groups,
+                                            int want_da, int want_db) {
+    const int st = check_backward(layout, m, f, k, layout == kDense ? 1 : num_groups);
+    if (st != FP8BS_OK) return -(int64_t)st;
+    return parts(layout, m, f, k, layout == kDense ? 1 : num_groups, want_da != 0, want_db != 0)
+        .total;
+}
+
+int fp8bs_gated_dense_mxfp4_backward(const void* a, const int32_t* sfa, const void* b,
+                                     const int32_t* sfb, const void* dh, void* da, void* db,
+                                     int db_dtype, int accumulate, int m, int f, int k,
+                                     int activation, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
+    return gated_backward(kDense, a, sfa, b, sfb, dh, da, db, db_dtype, accumulate, nullptr, m, f,
+                          k, 1, activation, workspace, workspace_bytes, stream);
+}
+
+int fp8bs_gated_contiguous_mxfp4_backward(const void* a, const int32_t* sfa, const void* b,
+                                          const int32_t* sfb, const void* dh, void* da, void* db,
+                                          int db_dtype, int accumulate,
+                                          const int32_t* grouped_layout, int m_total, int f,
+                                          int k, int num_groups, int activation, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream) {
+    return gated_backward(kContiguous, a, sfa, b, sfb, dh, da, db, db_dtype, accumulate,
+                          grouped_layout, m_total, f, k, num_groups, activation, workspace,
+                          workspace_bytes, stream);
+}
+
+}  // extern "C"

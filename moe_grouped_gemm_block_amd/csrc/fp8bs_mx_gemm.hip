@@ -1,0 +1,514 @@
+// fp8bs_mx_gemm.hip -- the matrix kernel of the MXFP4 operators on gfx950: D = A B^T with
+// 4-bit operands (32-value blocks along K, power-of-two scales applied by the matrix core)
+// or bf16 ones, and what the operators do with the accumulators (fp8bs_mx.h, Epilogue).
+//
+// Both operand types move in steps of 128 bytes per row -- 256 4-bit or 64 bf16 values --
+// and each step feeds two rounds of v_mfma (16x16x128 f8f6f4 with block scales, 16x16x32
+// bf16): both take 16 cycles for 64 bytes of a row, lane (j, q) = (l % 16, l / 16) holding
+// 16 bytes at byte 16 q of row j, so one kernel serves both types.
+//
+// Tile: BM x BN by WM x WN wavefronts, each 16 TM x 64.  B rows are the instruction's first
+// operand and A rows its second, so a lane's results belong to one A row.  Rows are dealt to
+// the 16-row blocks with strides (A row TM * j + i is row j of block i; B row 4 r + jn is row
+// r of block jn): a lane then owns TM neighbouring rows and 16 neighbouring columns, stores
+// whole 16-byte pieces and reads its scale words as vectors.  The copies into LDS do the
+// dealing: a direct-to-LDS copy writes 1024 consecutive bytes but reads from any address per
+// lane.  A gated tile takes half its B rows from the gate and half from the up projection,
+// blocks 0-1 and 2-3 of every wavefront, so a lane holds both of each output element.
+//
+// Pipeline: two stages in LDS.  A step is 2 TM groups of 4 products, one A fragment each;
+// fragments are read three groups ahead, into the next step's stage at the end.  Between
+// the last read of a stage and the first of the next stands the only barrier of the step:
+// past it the stage read out is refilled with the step after next, so a copy has a whole
+// step's products (2048 cycles of 256x256) to land.  Copies are inline assembly: the
+// compiler knows of no LDS write in flight and adds no waits of its own to the fragment
+// reads; the waits for copies are the ones written here.  They write LDS only, no register.
+//
+// The grid is persistent: workgroup w takes units w, w + grid, ... in an order in which the
+// workgroups of an XCD (dealt round-robin) run neighbouring tiles, and copies the next
+// unit's first steps while it finishes and stores the present one.
+#include "fp8bs_mx.h"
+
+namespace fp8bs {
+namespace mx {
+namespace {
+
+#define LDS_AS __attribute__((address_space(3)))
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(LDS_AS const void*)p;
+}
+
+// Buffer descriptor of `bytes` bytes at base: reads past the end give zeros (the matrix
+// rows they feed are never stored) and touch no memory.
+__device__ __forceinline__ i32x4 descriptor(const void* base, int64_t bytes) {
+    const uint64_t at = (uint64_t)base;
+    const int64_t n = bytes < 0 ? 0 : bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes;
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+                 __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu)),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)n), 0x00020000};
+}
+
+// 16 bytes per lane from buffer offset voff + soff to LDS bytes lds + 16 * lane.  The five
+// wait states cover a scalar register written by the vector unit just before, and M0 (a
+// reserved register that nothing else here uses: LDS instructions do not need it).
+__device__ __forceinline__ void copy16(const i32x4& buffer, uint32_t voff, uint32_t soff,
+                                       uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                    "s"(__builtin_amdgcn_readfirstlane(lds)));
+}
+// every copy, load and store of this wavefront done, then the workgroup meets
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ i32x8 widen(const i32x4& v) {
+    return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+}
+
+// Workgroup b runs on XCD b % 8: XCD x takes the contiguous range [x, x + 1) * grid / 8.
+__device__ __forceinline__ int logical_block() {
+    const int n = gridDim.x, b = blockIdx.x;
+    return (n & 7) ? b : (b & 7) * (n >> 3) + (b >> 3);
+}
+
+struct Tile {
+    int g;              // expert (weight group)
+    int slot;           // masked: slot of A and D; else 0
+    int m0, n0;         // first row (of the slot) and first output column
+    int rows;           // rows of the slot that may be read, from m0
+    int c0, c1;         // steps along the contraction
+};
+
+__device__ __forceinline__ int expert_of(const MxParams& p, int block) {
+    const int e = p.group_data[block * 128];
+    return e >= 0 && e < p.num_groups ? e : -1;
+}
+
+// The tiles along M that hold a valid row, listed in LDS by one wavefront; returns how many.
+// Contiguous: block number * 2 + whether the next 128-row block, of the same expert, belongs
+// to the tile (256-row tiles pair the blocks of a run of one expert).  Masked: slot *
+// m_tiles + tile.
+template <int BM, int LAYOUT>
+__device__ int list_tiles(const MxParams& p, uint32_t* list) {
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    if constexpr (LAYOUT == kContiguous) {
+        int run = p.first, before = -2;               // start and expert of the run so far
+        for (int w = p.first; w < p.last; w += 64) {
+            const int b = w + lane;
+            const int e = b < p.last ? expert_of(p, b) : -1;
+            const int after = b + 1 < p.last ? expert_of(p, b + 1) : -1;
+            const int prev = __shfl_up(e, 1, 64);
+            const uint64_t starts = __ballot(e != (lane ? prev : before));
+            const uint64_t upto = starts & (lane == 63 ? ~0ull : (2ull << lane) - 1ull);
+            const int first = upto ? w + 63 - __clzll(upto) : run;
+            const bool head = e >= 0 && (BM < 256 || ((b - first) & 1) == 0);
+            const uint64_t heads = __ballot(head);
+            if (head)
+                list[count + __popcll(heads & ((1ull << lane) - 1ull))] =
+                    (uint32_t)(2 * b + (BM >= 256 && after == e ? 1 : 0));
+            count += __popcll(heads);
+            run = starts ? w + 63 - __clzll(starts) : run;
+            before = __shfl(e, 63, 64);
+        }
+    } else {
+        for (int w = p.first; w < p.last; w += 64) {
+            const int i = w + lane;
+            const int g = min(i, p.last - 1) / p.m_tiles;
+            const bool in = i < p.last && (i - g * p.m_tiles) * BM < min(p.group_data[g], p.m);
+            const uint64_t heads = __ballot(in);
+            if (in) list[count + __popcll(heads & ((1ull << lane) - 1ull))] = (uint32_t)i;
+            count += __popcll(heads);
+        }
+    }
+    return count;
+}
+
+template <int BM, int BN, int LAYOUT, int EPI>
+__device__ __forceinline__ void tile_at(const MxParams& p, const uint32_t* list, int m_tiles,
+                                        int u, Tile& t) {
+    constexpr int COLS = gated(EPI) ? BN / 2 : BN;
+    int g = 0;
+    if constexpr (LAYOUT == kBlocks) {
+        g = u / (m_tiles * p.n_tiles);
+        u -= g * (m_tiles * p.n_tiles);
+    }
+    // groups of `raster` tiles along M sweep the columns
+    const int band = u / (p.raster * p.n_tiles);
+    const int in_band = u - band * p.raster * p.n_tiles;
+    const int first = band * p.raster;
+    const int tall = min(p.raster, m_tiles - first);
+    const int mt = first + in_band % tall;
+    t.n0 = in_band / tall * COLS;
+    t.g = g;
+    t.slot = 0;
+    t.c0 = 0;
+    t.c1 = p.chunks;
+    if constexpr (LAYOUT == kContiguous) {
+        const uint32_t e = __builtin_amdgcn_readfirstlane(list[mt]);
+        t.m0 = (int)(e >> 1) * 128;
+        t.rows = BM < 256 ? min(BM, 128) : (e & 1) ? 256 : 128;
+        t.g = __builtin_amdgcn_readfirstlane(p.group_data[t.m0]);
+    } else if constexpr (LAYOUT == kMasked) {
+        const int e = (int)__builtin_amdgcn_readfirstlane(list[mt]);
+        t.g = t.slot = e / p.m_tiles;
+        t.m0 = (e - t.g * p.m_tiles) * BM;
+        t.rows = __builtin_amdgcn_readfirstlane(min(p.group_data[t.g], p.m)) - t.m0;
+    } else {
+        t.m0 = mt * BM;
+        t.rows = p.m - t.m0;
+        if constexpr (LAYOUT == kBlocks) {
+            t.c0 = 2 * __builtin_amdgcn_readfirstlane(p.blocks[g]);
+            t.c1 = 2 * __builtin_amdgcn_readfirstlane(p.blocks[g + 1]);
+        }
+    }
+}
+
+template <int T, int BM, int BN, int WM, int WN, int LAYOUT, int EPI>
+__global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams p) {
+    constexpr int NW = WM * WN, TM = BM / WM / 16, TN = 4;
+    static_assert(BN / WN == 64, "a wavefront has four column blocks");
+    constexpr bool FP4 = T == kFp4, GATED = gated(EPI);
+    constexpr int COLS = GATED ? BN / 2 : BN;              // output columns of a tile
+    constexpr int A_COPIES = BM / 8 / NW, B_COPIES = BN / 8 / NW;
+    static_assert(A_COPIES * NW * 8 == BM && B_COPIES * NW * 8 == BN, "whole copies");
+    // scale words of a step: two (128 values each) per row, [2][rows], at least one copy
+    constexpr int SA_COPIES = FP4 ? (BM * 8 + 1023) / 1024 : 0;
+    constexpr int SB_COPIES = FP4 ? (BN * 8 + 1023) / 1024 : 0;
+    static_assert(SA_COPIES + SB_COPIES <= NW, "one scale copy per wavefront");
+    constexpr int B_OFF = BM * 128, SA_OFF = B_OFF + BN * 128, SB_OFF = SA_OFF + SA_COPIES * 1024;
+    // (the other wavefronts copy nothing into a spare kilobyte, which keeps a step branch-free)
+    constexpr int SPARE_OFF = SB_OFF + SB_COPIES * 1024;
+    constexpr int STAGE = SPARE_OFF + (FP4 ? 1024 : 0);
+    constexpr bool LISTED = LAYOUT == kContiguous || LAYOUT == kMasked;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+    __shared__ uint32_t list[LISTED ? kMaxListed + 1 : 1];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int j = lane & 15, q = lane >> 4;
+
+    int m_tiles = p.m_tiles;
+    if constexpr (LISTED) {
+        if (wave == 0) {
+            const int n = list_tiles<BM, LAYOUT>(p, list);
+            if (lane == 0) list[kMaxListed] = (uint32_t)n;
+        }
+        __syncthreads();
+        m_tiles = __builtin_amdgcn_readfirstlane(list[kMaxListed]);
+    }
+    const int units = m_tiles * p.n_tiles * (LAYOUT == kBlocks ? p.num_groups : 1);
+    int u = logical_block();
+    if (u >= units) return;
+
+    // ---- copies ----
+    // Copy `ins` of an operand fills LDS rows 8 ins .. 8 ins + 7 of its tile; lane L fills
+    // 16-byte slot L % 8 of row 8 ins + L / 8 with unit slot ^ key(row), key(row) = row % 8 ^
+    // (row / 8) % 2: the 16 lanes that read one unit of 16 consecutive rows then meet every
+    // LDS bank once.
+    uint32_t a_at[A_COPIES], b_at[B_COPIES];
+    static_assert(!GATED || B_COPIES == 4, "a wavefront's B copies: two blocks, gate or up");
+    const bool b_up = GATED && (wave & 1);
+#pragma unroll
+    for (int k = 0; k < A_COPIES; ++k) {
+        const int ins = wave * A_COPIES + k;
+        const int unit = (lane & 7) ^ (lane >> 3) ^ (ins & 1);
+        const int at = ins * 8 + (lane >> 3);              // LDS row
+        const int strip = at / (16 * TM), i = at / 16 % TM, r = at % 16;
+        a_at[k] = (uint32_t)(strip * 16 * TM + TM * r + i) * (uint32_t)p.a_row + 16u * unit;
+    }
+#pragma unroll
+    for (int k = 0; k < B_COPIES; ++k) {
+        const int ins = wave * B_COPIES + k;
+        const int unit = (lane & 7) ^ (lane >> 3) ^ (ins & 1);
+        const int at = ins * 8 + (lane >> 3);
+        const int strip = at / 64, jn = at / 16 % 4, r = at % 16;
+        const int row = GATED ? strip * 32 + 2 * r + (jn & 1) : strip * 64 + 4 * r + jn;
+        b_at[k] = (uint32_t)row * (uint32_t)p.b_row + 16u * unit;
+    }
+    // scale copies, one per wavefront: waves 0 .. SA_COPIES-1 bring A's, the next B's
+    const bool sa_mine = wave < SA_COPIES;
+    const bool sb_mine = !sa_mine && wave < SA_COPIES + SB_COPIES;
+    uint32_t s_at = 0, s_lds = 0;
+    if constexpr (FP4) {
+        const int rows = sa_mine ? BM : BN;
+        const int ins = sa_mine ? wave : wave - SA_COPIES;
+        const int word = ins * 256 + lane * 4;             // of the [2][rows] words
+        const int h = word / rows, r = word % rows;
+        const uint32_t ld = (uint32_t)(sa_mine ? p.sfa_ld : p.sfb_ld);
+        s_at = ((uint32_t)h * ld + (uint32_t)r) * 4u;
+        if (GATED && !sa_mine && r >= COLS) s_at += 4u * (uint32_t)(p.n - COLS);
+        if (h > 1) s_at = 0;                               // past the words: a harmless read
+        s_lds = (uint32_t)(sa_mine ? SA_OFF + ins * 1024 : sb_mine ? SB_OFF + ins * 1024 : SPARE_OFF);
+    }
+
+    const uint32_t lds0 = lds_offset(smem);
+    struct Source {
+        i32x4 a, b, s;
+        uint32_t s_step;                                   // bytes of scale words per step
+    };
+    auto open = [&](const Tile& t, Source& s) {
+        const int64_t group = LAYOUT == kBlocks ? 0 : (int64_t)t.g * (GATED ? 2 * p.n : p.n);
+        s.a = descriptor(p.a + ((int64_t)t.slot * p.m + t.m0) * p.a_row, t.rows * p.a_row);
+        s.b = descriptor(p.b + (group + t.n0 + (b_up ? p.n : 0)) * p.b_row,
+                         (int64_t)(p.n - t.n0) * p.b_row);
+        if constexpr (FP4) {
+            const int64_t words = p.kwords;
+            const int ld = sa_mine ? p.sfa_ld : p.sfb_ld, at = sa_mine ? t.m0 : t.n0;
+            const int32_t* base = sa_mine ? p.sfa + (int64_t)t.slot * words * ld
+                                          : p.sfb + (int64_t)t.g * words * ld;
+            s.s = descriptor(base + at, sa_mine || sb_mine ? (words * ld - at) * 4 : 0);
+            s.s_step = 8u * (uint32_t)ld;
+        }
+    };
+    // copies step c of the tile that s is open on; nothing (a zero-length buffer) past the
+    // stream's end
+    // (kBlocks: step c of an expert is half c % 2 of its block c / 2, 128 tokens of 2 bytes)
+    auto copy_step = [&](const Source& s, int c, int block, int stage) {
+        const uint32_t to = lds0 + (uint32_t)(stage * STAGE);
+        const uint32_t at = LAYOUT == kBlocks ? (uint32_t)(block * 256 + (c & 1) * 128)
+                                              : (uint32_t)c * 128u;
+#pragma unroll
+        for (int k = 0; k < A_COPIES; ++k)
+            copy16(s.a, a_at[k], at, to + (uint32_t)(wave * A_COPIES + k) * 1024u);
+#pragma unroll
+        for (int k = 0; k < B_COPIES; ++k)
+            copy16(s.b, b_at[k], at, to + (uint32_t)B_OFF + (uint32_t)(wave * B_COPIES + k) * 1024u);
+        if constexpr (FP4) copy16(s.s, s_at, (uint32_t)c * s.s_step, to + s_lds);
+    };
+
+    // ---- fragment and scale reads ----
+    const int key = (j & 7) ^ (j >> 3);
+    int a_rd[2], b_rd[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        a_rd[h] = (wm * 16 * TM + j) * 128 + (((4 * h + q) ^ key) << 4);
+        b_rd[h] = B_OFF + (wn * 64 + j) * 128 + (((4 * h + q) ^ key) << 4);
+    }
+    const int sa_rd = SA_OFF + (wm * 16 * TM + TM * j) * 4;
+    const int sb_rd = SB_OFF + (GATED ? wn * 32 + 2 * j : wn * 64 + 4 * j) * 4;
+    auto read_a = [&](int base, int h, int i) {
+        return *(const i32x4*)(smem + base + a_rd[h] + 2048 * i);
+    };
+    auto read_b = [&](int base, int h, int n) {
+        return *(const i32x4*)(smem + base + b_rd[h] + 2048 * n);
+    };
+    // Words of the 128 values of round h; the lane's block is their byte q, shifted down when
+    // the word is used (the matrix instruction takes a scale register's low byte).  The second
+    // round of a row's last step does not exist when K / 128 is odd: its exponents become
+    // 2^-127, whose products with any 4-bit values vanish.
+    const int shift = 8 * q;
+    auto read_sa = [&](int base, int h, int i) {
+        return FP4 ? *(const int*)(smem + base + sa_rd + h * BM * 4 + 4 * i) : 0;
+    };
+    auto read_sb = [&](int base, int h, int (&s)[TN]) {
+        if constexpr (FP4) {
+#pragma unroll
+            for (int n = 0; n < TN; ++n) {
+                const int word = GATED ? (n & 1) + (n >> 1) * COLS : n;
+                s[n] = *(const int*)(smem + base + sb_rd + h * BN * 4 + 4 * word);
+            }
+        }
+    };
+
+    f32x4 acc[TM][TN];
+    auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int n = 0; n < TN; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+
+    // ---- the stream of (unit, step): what is multiplied, and what is copied next ----
+    Tile cur, nxt;
+    Source src = {};
+    int nu = u, nc;                            // the next step to copy: step nc of unit nu
+    int block = 0;                             // kBlocks: the token block it lies in
+    // moves to the next unit with at least one step (one without, an expert without tokens,
+    // is left to the storing loop); past the last one the copies get empty buffers
+    auto seek = [&](int from) {
+        for (nu = from; nu < units; nu += gridDim.x) {
+            tile_at<BM, BN, LAYOUT, EPI>(p, list, m_tiles, nu, nxt);
+            if (nxt.c0 < nxt.c1) {
+                open(nxt, src);
+                nc = nxt.c0;
+                return;
+            }
+        }
+        src.a[2] = src.b[2] = src.s[2] = 0;
+        nc = 0;                                // (at most two more steps are asked for)
+        nxt.c1 = 0x7fffffff;
+    };
+    auto find_block = [&] {
+        if constexpr (LAYOUT == kBlocks) block = p.blocks[p.num_groups + 1 + (nc >> 1)];
+    };
+    auto advance = [&] {
+        if (++nc >= nxt.c1) seek(nu + gridDim.x);
+        find_block();
+    };
+
+#include "fp8bs_mx_store.inc"
+
+    clear();
+    seek(u);
+    find_block();
+    copy_step(src, nc, block, 0);
+    advance();
+    wait_and_meet();
+    copy_step(src, nc, block, 1);
+    constexpr int GROUPS = 2 * TM, AHEAD = 3;
+    i32x4 fa[4], fb[2][TN];
+    int sa[4], sb[2][TN];                      // scale words as read
+    int eb[TN];                                // this round's B exponents
+    int base = 0;
+#pragma unroll
+    for (int n = 0; n < TN; ++n) fb[0][n] = read_b(0, 0, n);
+    read_sb(0, 0, sb[0]);
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+        fa[g] = read_a(0, 0, g);
+        sa[g] = read_sa(0, 0, g);
+    }
+
+    for (; u < units; u += gridDim.x) {
+        tile_at<BM, BN, LAYOUT, EPI>(p, list, m_tiles, u, cur);
+        for (int c = cur.c0; c < cur.c1; ++c) {
+            const int other = base ? 0 : STAGE;
+            const int keep = 2 * c + 1 < p.kwords ? 255 : 0;
+            advance();
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                constexpr int LAST = GROUPS - AHEAD;
+                const int h = g / TM, i = g % TM;
+                if (g == LAST) {
+                    wait_and_meet();
+                    copy_step(src, nc, block, base ? 1 : 0);
+                }
+                const int ahead = g + AHEAD;
+                if (ahead < GROUPS) {
+                    fa[ahead % 4] = read_a(base, ahead / TM, ahead % TM);
+                    sa[ahead % 4] = read_sa(base, ahead / TM, ahead % TM);
+                } else {
+                    fa[ahead % 4] = read_a(other, 0, ahead - GROUPS);
+                    sa[ahead % 4] = read_sa(other, 0, ahead - GROUPS);
+                }
+                if (g < TN) fb[1][g] = read_b(base, 1, g);
+                if (g == 0) read_sb(base, 1, sb[1]);
+                if (g == LAST) {
+                    read_sb(other, 0, sb[0]);
+#pragma unroll
+                    for (int n = 0; n < TN; ++n) fb[0][n] = read_b(other, 0, n);
+                }
+                int ea = 0;
+                if constexpr (FP4) {
+                    const int mask = h ? keep : 255;
+                    ea = (sa[g % 4] >> shift) & mask;
+                    if (i == 0) {
+#pragma unroll
+                        for (int n = 0; n < TN; ++n) eb[n] = (sb[h][n] >> shift) & mask;
+                    }
+                }
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    if constexpr (FP4)
+                        acc[i][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            widen(fb[h][n]), widen(fa[g % 4]), acc[i][n], 4, 4, 0, eb[n], 0, ea);
+                    else
+                        acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, fb[h][n]),
+                            __builtin_bit_cast(bf16x8, fa[g % 4]), acc[i][n], 0, 0, 0);
+                }
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            base = other;
+        }
+        store(cur);
+        clear();
+    }
+}
+
+typedef void (*KernelFn)(MxParams);
+
+struct Shape {
+    int bm, bn;
+};
+
+template <int T, int LAYOUT, int EPI>
+void pick(bool large, KernelFn* fn, Shape* shape, int* threads, int* per_cu) {
+    if (large) {
+        *fn = mx_gemm_kernel<T, 256, 256, 2, 4, LAYOUT, EPI>;
+        *shape = {256, 256};
+        *threads = 512;
+        *per_cu = 1;
+    } else {
+        *fn = mx_gemm_kernel<T, 128, 128, 2, 2, LAYOUT, EPI>;
+        *shape = {128, 128};
+        *threads = 256;
+        *per_cu = 2;
+    }
+}
+
+}  // namespace
+
+int launch_gemm(int operand, int layout, int epilogue, const MxParams& params, int groups,
+                int expected_rows, int num_cus, hipStream_t stream) {
+    MxParams p = params;
+    KernelFn fn = nullptr;
+    Shape s{0, 0};
+    int threads = 0, per_cu = 1;
+    const int64_t cols = gated(epilogue) ? 2 * (int64_t)p.n : p.n;
+    const int64_t slots = layout == kMasked || layout == kBlocks ? groups : 1;
+    auto tiles = [&](int bm, int bn) {
+        return slots * ((expected_rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
+    };
+    const bool large = tiles(256, 256) >= num_cus;
+#define MX_CASE(T, L, E)                                                     \
+    if (operand == T && layout == L && epilogue == E)                        \
+        pick<T, L, E>(large, &fn, &s, &threads, &per_cu);
+    MX_CASE(kFp4, kDense, kStore)
+    MX_CASE(kFp4, kContiguous, kStore)
+    MX_CASE(kFp4, kMasked, kStore)
+    MX_CASE(kFp4, kDense, kGated)
+    MX_CASE(kFp4, kContiguous, kGated)
+    MX_CASE(kFp4, kMasked, kGated)
+    MX_CASE(kFp4, kDense, kGatedQuant)
+    MX_CASE(kFp4, kContiguous, kGatedQuant)
+    MX_CASE(kFp4, kMasked, kGatedQuant)
+    MX_CASE(kFp4, kDense, kGatedGrad)
+    MX_CASE(kFp4, kContiguous, kGatedGrad)
+    MX_CASE(kBf16, kDense, kStore)
+    MX_CASE(kBf16, kDense, kStoreF32)
+    MX_CASE(kBf16, kContiguous, kStore)
+    MX_CASE(kBf16, kBlocks, kStore)
+    MX_CASE(kBf16, kBlocks, kStoreF32)
+#undef MX_CASE
+    if (!fn) return (int)hipErrorInvalidValue;
+    const int bn_cols = gated(epilogue) ? s.bn / 2 : s.bn;
+    p.m_tiles = (p.m + s.bm - 1) / s.bm;
+    p.n_tiles = (p.n + bn_cols - 1) / bn_cols;
+    p.raster = 8;
+    const bool listed = layout == kContiguous || layout == kMasked;
+    const int64_t all = layout == kContiguous ? p.m / 128 : slots * p.m_tiles;
+    if (all * p.n_tiles > 0x7fffffff) return (int)hipErrorInvalidValue;
+    // a launch lists at most kMaxListed tiles along M
+    for (int64_t first = 0; first < all; first += kMaxListed) {
+        p.first = (int)first;
+        p.last = (int)(listed && first + kMaxListed < all ? first + kMaxListed : all);
+        int64_t grid = (int64_t)num_cus * per_cu;
+        const int64_t most = (p.last - p.first) * (int64_t)p.n_tiles;
+        if (grid > most) grid = most;
+        void* argv[] = {&p};
+        const hipError_t err = hipLaunchKernel((const void*)fn, dim3((unsigned)grid),
+                                               dim3(threads), argv, 0, stream);
+        if (err != hipSuccess || !listed) return (int)err;
+    }
+    return (int)hipSuccess;
+}
+
+}  // namespace mx
+}  // namespace fp8bs

@@ -1,0 +1,289 @@
+// fp8bs_mx_quant.hip -- MXFP4 quantiser and its inverse on gfx950.
+//
+// 32 consecutive values of a row share the scale 2^(e - 127), e - 127 =
+// floor(log2(max |x|)) - 2; each becomes e2m1(x * 2^(127 - e)), nearest with ties to the
+// even code, magnitudes above 6 saturating.  Scaling by a power of two is exact, so a value
+// is rounded once and the result does not depend on how the work is laid out.
+//
+// Both kernels read every input byte once and write every output byte once; HBM bounds
+// them.  A workgroup takes 32 rows x 256 columns: a row's codes are one 128-byte line, the
+// 32 exponent words of a 128-column group (exponents lie K-group-major, rows consecutive)
+// another, so no line is written in two pieces by different workgroups.
+#include "fp8bs_mx.h"
+
+namespace fp8bs {
+namespace mx {
+namespace {
+
+constexpr int kRows = 32, kCols = 256;
+
+// 8 consecutive inputs widened to FP32
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
+    if constexpr (BF16) {
+        const u32x4 w = *(const u32x4*)((const uint16_t*)x + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = from_bf16(w[i] & 0xFFFFu);
+            v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+        }
+    } else {
+        const f32x4 lo = *(const f32x4*)((const float*)x + at);
+        const f32x4 hi = *(const f32x4*)((const float*)x + at + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = lo[i];
+            v[4 + i] = hi[i];
+        }
+    }
+}
+
+// Thread t of a workgroup: columns 8 * (t % 32) .. + 7 of rows t / 32 + 8 i.  Four
+// neighbouring lanes hold a 32-value block.
+template <bool BF16>
+__global__ void __launch_bounds__(256) mx_quant_kernel(const void* __restrict__ x,
+                                                       uint8_t* __restrict__ q,
+                                                       uint32_t* __restrict__ sf, int rows, int k,
+                                                       int ld, int row_tiles, int col_tiles) {
+    __shared__ uint32_t words[2][kRows];
+    const int ct = blockIdx.x % col_tiles;
+    const int rt = blockIdx.x / col_tiles % row_tiles;
+    const int slot = blockIdx.x / col_tiles / row_tiles;
+    const int t = threadIdx.x, seg = t & 31;
+    const int col = ct * kCols + 8 * seg;
+    const int64_t row0 = (int64_t)slot * rows;
+    float v[4][8];
+    bool in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = rt * kRows + (t >> 5) + 8 * i;
+        in[i] = r < rows && col < k;
+        if (in[i]) load8<BF16>(x, (row0 + r) * k + col, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int rr = (t >> 5) + 8 * i;
+        uint32_t top = 0;
+        if (in[i]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t b = __builtin_bit_cast(uint32_t, v[i][e]) & 0x7FFFFFFFu;
+                top = b > top ? b : top;
+            }
+        }
+#pragma unroll
+        for (int w = 1; w <= 2; w <<= 1) {
+            const uint32_t o = __shfl_xor(top, w, 64);
+            top = o > top ? o : top;
+        }
+        const uint32_t e = block_exponent(top);
+        if (in[i]) {
+            // A block that holds an infinity or a NaN is not a number as a whole (e2m1 has
+            // neither); its codes are zeros.
+            uint32_t codes = 0;
+            if (e != 255u) {
+                const float inv = inverse_scale(e);
+                float s[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) s[c] = v[i][c] * inv;
+                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[0], s[1], 1.0f, 0);
+                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[2], s[3], 1.0f, 1);
+                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[4], s[5], 1.0f, 2);
+                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[6], s[7], 1.0f, 3);
+            }
+            *(uint32_t*)(q + ((row0 + rt * kRows + rr) * k + col) / 2) = codes;
+        }
+        // the four exponents of a 128-column group, one byte each
+        uint32_t word = e << (8 * ((seg >> 2) & 3));
+        word |= __shfl_xor(word, 4, 64);
+        word |= __shfl_xor(word, 8, 64);
+        if ((seg & 15) == 0) words[seg >> 4][rr] = word;
+    }
+    __syncthreads();
+    if (t < 2 * kRows) {
+        const int c = ct * 2 + (t >> 5), r = rt * kRows + (t & 31);
+        if (r < rows && c < k / 128)
+            sf[((int64_t)slot * (k / 128) + c) * ld + r] = words[t >> 5][t & 31];
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restrict__ q,
+                                                         const uint32_t* __restrict__ sf,
+                                                         void* __restrict__ x, int rows, int k,
+                                                         int ld, int row_tiles, int col_tiles) {
+    __shared__ uint32_t words[2][kRows];
+    const int ct = blockIdx.x % col_tiles;
+    const int rt = blockIdx.x / col_tiles % row_tiles;
+    const int slot = blockIdx.x / col_tiles / row_tiles;
+    const int t = threadIdx.x, seg = t & 31;
+    const int col = ct * kCols + 8 * seg;
+    const int64_t row0 = (int64_t)slot * rows;
+    if (t < 2 * kRows) {
+        const int c = ct * 2 + (t >> 5), r = rt * kRows + (t & 31);
+        words[t >> 5][t & 31] =
+            (r < rows && c < k / 128) ? sf[((int64_t)slot * (k / 128) + c) * ld + r] : 0u;
+    }
+    uint32_t codes[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = rt * kRows + (t >> 5) + 8 * i;
+        codes[i] = (r < rows && col < k) ? *(const uint32_t*)(q + ((row0 + r) * k + col) / 2) : 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int rr = (t >> 5) + 8 * i, r = rt * kRows + rr;
+        if (r >= rows || col >= k) continue;
+        const uint32_t e = (words[seg >> 4][rr] >> (8 * ((seg >> 2) & 3))) & 255u;
+        float hi, lo, v[8];
+        scale_factors(e, hi, lo);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = code_value((codes[i] >> (4 * c)) & 15u, hi, lo);
+        const int64_t at = (row0 + r) * k + col;
+        if constexpr (BF16) {
+            *(u32x4*)((uint16_t*)x + at) = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        } else {
+            *(f32x4*)((float*)x + at) = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4*)((float*)x + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        }
+    }
+}
+
+// Transposed widening.  Workgroup = 64 rows x 128 columns.  Thread t decodes 16 columns
+// (16 * (t % 8) ..) of the rows 2 (t / 8) and 2 (t / 8) + 1 and leaves them in LDS as pairs,
+// [column][row pair] with one word of padding; a column then goes out as one 128-byte line.
+__global__ void __launch_bounds__(256) mx_transpose_kernel(
+    const uint8_t* __restrict__ q, const uint32_t* __restrict__ sf, uint16_t* __restrict__ xt,
+    int rows, int k, int sf_ld, int64_t ld, int row_tiles, const int32_t* __restrict__ layout,
+    int experts) {
+    __shared__ uint32_t tile[128][33];
+    const int c = blockIdx.x % (k / 128);
+    const int rt = blockIdx.x / (k / 128) % row_tiles;
+    const int64_t slot = blockIdx.x / (k / 128) / row_tiles;
+    const int t = threadIdx.x, seg = t & 7, pair = t >> 3;
+    uint16_t v[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = rt * 64 + 2 * pair + h;
+        bool ok = r < rows;
+        if (ok && layout) ok = layout[r] >= 0 && layout[r] < experts;
+        uint32_t lo = 0, hi = 0, word = 0;
+        if (ok) {
+            const uint2 w = *(const uint2*)(q + ((slot * rows + r) * (int64_t)k + 128 * c + 16 * seg) / 2);
+            lo = w.x;
+            hi = w.y;
+            word = sf[(slot * (k / 128) + c) * sf_ld + r];
+        }
+        float s0, s1;
+        scale_factors((word >> (8 * (seg >> 1))) & 255u, s0, s1);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[h][e] = to_bf16(code_value(((e < 8 ? lo : hi) >> (4 * (e & 7))) & 15u, s0, s1));
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) tile[16 * seg + e][pair] = v[0][e] | (uint32_t)v[1][e] << 16;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int col = (t >> 3) + 32 * i;
+        const uint32_t* w = &tile[col][4 * seg];
+        *(u32x4*)(xt + (slot * k + 128 * c + col) * ld + rt * 64 + 8 * seg) =
+            u32x4{w[0], w[1], w[2], w[3]};
+    }
+}
+
+// One workgroup; thread e (and e + 256, ...) counts expert e's blocks, then writes them in
+// order behind the blocks of the experts before it.
+__global__ void __launch_bounds__(256) mx_block_order_kernel(const int32_t* __restrict__ layout,
+                                                             int blocks, int groups,
+                                                             int32_t* __restrict__ out) {
+    for (int e = threadIdx.x; e < groups; e += 256) {
+        int n = 0;
+        for (int b = 0; b < blocks; ++b) n += layout[b * 128] == e;
+        out[e + 1] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int at = 0;
+        out[0] = 0;
+        for (int e = 0; e < groups; ++e) out[e + 1] = at += out[e + 1];
+    }
+    __syncthreads();
+    int32_t* order = out + groups + 1;
+    for (int e = threadIdx.x; e < groups; e += 256) {
+        int at = out[e];
+        for (int b = 0; b < blocks; ++b)
+            if (layout[b * 128] == e) order[at++] = b;
+    }
+}
+
+bool aligned(const void* p, uintptr_t to) { return p && ((uintptr_t)p & (to - 1)) == 0; }
+
+// Checks shared by both directions; *grid = workgroups.
+int check(const void* x, int dtype, const void* q, const void* sf, int groups, int rows, int k,
+          int64_t* grid) {
+    if (k < 128 || k % 128 != 0 || rows < 0 || groups < 1) return FP8BS_ERR_SHAPE;
+    if (dtype != FP8BS_DTYPE_F32 && dtype != FP8BS_DTYPE_BF16) return FP8BS_ERR_UNSUPPORTED;
+    if ((double)groups * rows * k >= 9.0e15) return FP8BS_ERR_SHAPE;
+    *grid = (int64_t)groups * ((rows + kRows - 1) / kRows) * ((k + kCols - 1) / kCols);
+    if (*grid > 0x7fffffff) return FP8BS_ERR_SHAPE;
+    if (rows == 0) return FP8BS_OK;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return FP8BS_ERR_POINTER;
+    return FP8BS_OK;
+}
+
+}  // namespace
+
+int launch_transpose(const uint8_t* q, const int32_t* sf, uint16_t* xt, int groups, int rows,
+                     int k, int64_t ld, const int32_t* grouped_layout, int num_experts,
+                     hipStream_t stream) {
+    int sf_ld = (int)fp8bs_get_sfa_ld(rows), rt = (int)(ld / 64);
+    const int64_t grid = (int64_t)groups * rt * (k / 128);
+    if (grid > 0x7fffffff) return (int)hipErrorInvalidValue;
+    if (grid == 0) return (int)hipSuccess;
+    void* args[] = {&q, &sf, &xt, &rows, &k, &sf_ld, &ld, &rt, &grouped_layout, &num_experts};
+    return (int)hipLaunchKernel((const void*)mx_transpose_kernel, dim3((unsigned)grid), dim3(256),
+                                args, 0, stream);
+}
+
+int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups, int32_t* out,
+                       hipStream_t stream) {
+    void* args[] = {&grouped_layout, &blocks, &num_groups, &out};
+    return (int)hipLaunchKernel((const void*)mx_block_order_kernel, dim3(1), dim3(256), args, 0,
+                                stream);
+}
+
+}  // namespace mx
+}  // namespace fp8bs
+
+extern "C" int fp8bs_quantize_mxfp4(const void* x, int x_dtype, void* q, int32_t* sf, int groups,
+                                    int rows, int k, hipStream_t stream) {
+    using namespace fp8bs::mx;
+    int64_t grid = 0;
+    const int st = check(x, x_dtype, q, sf, groups, rows, k, &grid);
+    if (st != FP8BS_OK || rows == 0) return st;
+    int ld = (int)fp8bs_get_sfa_ld(rows), rt = (rows + kRows - 1) / kRows,
+        ct = (k + kCols - 1) / kCols;
+    void* args[] = {(void*)&x, (void*)&q, (void*)&sf, &rows, &k, &ld, &rt, &ct};
+    const void* fn = x_dtype == FP8BS_DTYPE_BF16 ? (const void*)mx_quant_kernel<true>
+                                                 : (const void*)mx_quant_kernel<false>;
+    return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), args, 0, stream) == hipSuccess
+               ? FP8BS_OK : FP8BS_ERR_HIP;
+}
+
+extern "C" int fp8bs_dequantize_mxfp4(const void* q, const int32_t* sf, void* x, int x_dtype,
+                                      int groups, int rows, int k, hipStream_t stream) {
+    using namespace fp8bs::mx;
+    int64_t grid = 0;
+    const int st = check(x, x_dtype, q, sf, groups, rows, k, &grid);
+    if (st != FP8BS_OK || rows == 0) return st;
+    int ld = (int)fp8bs_get_sfa_ld(rows), rt = (rows + kRows - 1) / kRows,
+        ct = (k + kCols - 1) / kCols;
+    void* args[] = {(void*)&q, (void*)&sf, (void*)&x, &rows, &k, &ld, &rt, &ct};
+    const void* fn = x_dtype == FP8BS_DTYPE_BF16 ? (const void*)mx_dequant_kernel<true>
+                                                 : (const void*)mx_dequant_kernel<false>;
+    return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), args, 0, stream) == hipSuccess
+               ? FP8BS_OK : FP8BS_ERR_HIP;
+}
