@@ -134,6 +134,49 @@ __device__ __forceinline__ float activate(int act, float v, float& slope) {
     return v * sig;
 }
 
+// Quantises a row's 32 values, eight in each of the lanes l, l + 16, l + 32, l + 48: this
+// lane's eight codes, and the block's exponent.
+__device__ __forceinline__ uint32_t quantise_row_block(const float (&h)[8], uint32_t& exponent) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, h[e]) & 0x7FFFFFFFu;
+        top = b > top ? b : top;
+    }
+#pragma unroll
+    for (int w = 16; w <= 32; w <<= 1) {
+        const uint32_t o = __shfl_xor(top, w, 64);
+        top = o > top ? o : top;
+    }
+    exponent = block_exponent(top);
+    if (exponent == 255u) return 0u;
+    const float inv = inverse_scale(exponent);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[0] * inv, h[1] * inv, 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[2] * inv, h[3] * inv, 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[4] * inv, h[5] * inv, 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[6] * inv, h[7] * inv, 1.0f, 3);
+    return c;
+}
+
+// Buffer descriptor of `bytes` bytes at base.  A read whose lane offset lies past the end
+// gives zeros and touches no memory.  Only the lane offset is relied on for that (whether the
+// scalar offset counts in the check differs between descriptions of it): callers keep lane
+// offset + scalar offset inside the buffer for every lane offset inside it.
+__device__ __forceinline__ i32x4 descriptor(const void* base, int64_t bytes) {
+    const uint64_t at = (uint64_t)base;
+    const int64_t n = bytes < 0 ? 0 : bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes;
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+                 __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu)),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)n), 0x00020000};
+}
+
+// Workgroup b runs on XCD b % 8: XCD x takes the contiguous range [x, x + 1) * grid / 8.
+__device__ __forceinline__ int logical_block() {
+    const int n = gridDim.x, b = blockIdx.x;
+    return (n & 7) ? b : (b & 7) * (n >> 3) + (b >> 3);
+}
+
 #endif  // __HIPCC__
 
 // Launchers (fp8bs_mx_gemm.hip, fp8bs_mx_quant.hip); return a hipError_t value.
@@ -150,6 +193,9 @@ int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups
                        hipStream_t stream);
 int launch_gemm(int operand, int layout, int epilogue, const MxParams& p, int groups,
                 int expected_rows, int num_cus, hipStream_t stream);
+// Few rows, dense and masked layouts: tiles of 16 tm x 16 tn (fp8bs_mx_stream.hip).
+int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& p, int groups,
+                  int expected_rows, hipStream_t stream);
 
 }  // namespace mx
 }  // namespace fp8bs

@@ -27,6 +27,8 @@
 // The grid is persistent: workgroup w takes units w, w + grid, ... in an order in which the
 // workgroups of an XCD (dealt round-robin) run neighbouring tiles, and copies the next
 // unit's first steps while it finishes and stores the present one.
+#include <math.h>
+
 #include "fp8bs_mx.h"
 
 namespace fp8bs {
@@ -39,24 +41,20 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(LDS_AS const void*)p;
 }
 
-// Buffer descriptor of `bytes` bytes at base: reads past the end give zeros (the matrix
-// rows they feed are never stored) and touch no memory.
-__device__ __forceinline__ i32x4 descriptor(const void* base, int64_t bytes) {
-    const uint64_t at = (uint64_t)base;
-    const int64_t n = bytes < 0 ? 0 : bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes;
-    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
-                 __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu)),
-                 __builtin_amdgcn_readfirstlane((int)(uint32_t)n), 0x00020000};
-}
-
 // 16 bytes per lane from buffer offset voff + soff to LDS bytes lds + 16 * lane.  The five
 // wait states cover a scalar register written by the vector unit just before, and M0 (a
 // reserved register that nothing else here uses: LDS instructions do not need it).
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(const i32x4& buffer, uint32_t voff, uint32_t soff,
                                        uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff)),
-                    "s"(__builtin_amdgcn_readfirstlane(lds)));
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                     :: "v"(voff), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                        "s"(__builtin_amdgcn_readfirstlane(lds)));
+    else
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                     :: "v"(voff), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                        "s"(__builtin_amdgcn_readfirstlane(lds)));
 }
 // every copy, load and store of this wavefront done, then the workgroup meets
 __device__ __forceinline__ void wait_and_meet() {
@@ -65,12 +63,6 @@ __device__ __forceinline__ void wait_and_meet() {
 
 __device__ __forceinline__ i32x8 widen(const i32x4& v) {
     return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-}
-
-// Workgroup b runs on XCD b % 8: XCD x takes the contiguous range [x, x + 1) * grid / 8.
-__device__ __forceinline__ int logical_block() {
-    const int n = gridDim.x, b = blockIdx.x;
-    return (n & 7) ? b : (b & 7) * (n >> 3) + (b >> 3);
 }
 
 struct Tile {
@@ -206,16 +198,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
 
     // ---- copies ----
     // Copy `ins` of an operand fills LDS rows 8 ins .. 8 ins + 7 of its tile; lane L fills
-    // 16-byte slot L % 8 of row 8 ins + L / 8 with unit slot ^ key(row), key(row) = row % 8 ^
-    // (row / 8) % 2: the 16 lanes that read one unit of 16 consecutive rows then meet every
-    // LDS bank once.
+    // 16-byte slot L % 8 of row 8 ins + L / 8 with unit slot ^ (row % 8), which spreads the
+    // fragment reads over the LDS banks: a 16-byte read takes the lanes in four groups of 16
+    // that are not consecutive, and within each no bank comes twice (keys that also use bit
+    // 3 of the row, conflict-free for consecutive lanes, measured 58% of the LDS's busy
+    // cycles in conflicts).
+    // (Where K / 128 is odd the upper half of a row's last step does not exist: lanes that
+    // would read it read the lower half again, tail_a, tail_s bytes before.)
     uint32_t a_at[A_COPIES], b_at[B_COPIES];
+    const uint32_t tail_a = ((lane & 7) ^ (lane >> 3)) >= 4 ? 64u : 0u;
     static_assert(!GATED || B_COPIES == 4, "a wavefront's B copies: two blocks, gate or up");
     const bool b_up = GATED && (wave & 1);
 #pragma unroll
     for (int k = 0; k < A_COPIES; ++k) {
         const int ins = wave * A_COPIES + k;
-        const int unit = (lane & 7) ^ (lane >> 3) ^ (ins & 1);
+        const int unit = (lane & 7) ^ (lane >> 3);
         const int at = ins * 8 + (lane >> 3);              // LDS row
         const int strip = at / (16 * TM), i = at / 16 % TM, r = at % 16;
         a_at[k] = (uint32_t)(strip * 16 * TM + TM * r + i) * (uint32_t)p.a_row + 16u * unit;
@@ -223,7 +220,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
 #pragma unroll
     for (int k = 0; k < B_COPIES; ++k) {
         const int ins = wave * B_COPIES + k;
-        const int unit = (lane & 7) ^ (lane >> 3) ^ (ins & 1);
+        const int unit = (lane & 7) ^ (lane >> 3);
         const int at = ins * 8 + (lane >> 3);
         const int strip = at / 64, jn = at / 16 % 4, r = at % 16;
         const int row = GATED ? strip * 32 + 2 * r + (jn & 1) : strip * 64 + 4 * r + jn;
@@ -232,23 +229,23 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     // scale copies, one per wavefront: waves 0 .. SA_COPIES-1 bring A's, the next B's
     const bool sa_mine = wave < SA_COPIES;
     const bool sb_mine = !sa_mine && wave < SA_COPIES + SB_COPIES;
-    uint32_t s_at = 0, s_lds = 0;
+    uint32_t s_row = 0, s_word = 0, s_lds = 0;             // row of the tile, word row (0, 1)
     if constexpr (FP4) {
         const int rows = sa_mine ? BM : BN;
         const int ins = sa_mine ? wave : wave - SA_COPIES;
         const int word = ins * 256 + lane * 4;             // of the [2][rows] words
         const int h = word / rows, r = word % rows;
-        const uint32_t ld = (uint32_t)(sa_mine ? p.sfa_ld : p.sfb_ld);
-        s_at = ((uint32_t)h * ld + (uint32_t)r) * 4u;
-        if (GATED && !sa_mine && r >= COLS) s_at += 4u * (uint32_t)(p.n - COLS);
-        if (h > 1) s_at = 0;                               // past the words: a harmless read
+        s_word = h < 2 ? (uint32_t)h : 0u;
+        s_row = (uint32_t)(GATED && !sa_mine && r >= COLS ? r - COLS + p.n : r);
+        if (h > 1) s_row = 0;                              // past the words: a harmless read
         s_lds = (uint32_t)(sa_mine ? SA_OFF + ins * 1024 : sb_mine ? SB_OFF + ins * 1024 : SPARE_OFF);
     }
 
     const uint32_t lds0 = lds_offset(smem);
     struct Source {
         i32x4 a, b, s;
-        uint32_t s_step;                                   // bytes of scale words per step
+        uint32_t s_at;                                     // this lane's offset in the scale words
+        uint32_t s_ld;                                     // bytes of a word row
     };
     auto open = [&](const Tile& t, Source& s) {
         const int64_t group = LAYOUT == kBlocks ? 0 : (int64_t)t.g * (GATED ? 2 * p.n : p.n);
@@ -260,28 +257,35 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
             const int ld = sa_mine ? p.sfa_ld : p.sfb_ld, at = sa_mine ? t.m0 : t.n0;
             const int32_t* base = sa_mine ? p.sfa + (int64_t)t.slot * words * ld
                                           : p.sfb + (int64_t)t.g * words * ld;
-            s.s = descriptor(base + at, sa_mine || sb_mine ? (words * ld - at) * 4 : 0);
-            s.s_step = 8u * (uint32_t)ld;
+            s.s = descriptor(base + at, (words * ld - at) * 4);
+            s.s_ld = 4u * (uint32_t)ld;
+            // rows past the padded end read its last four words (they belong to no result)
+            s.s_at = 4u * min(s_row, (uint32_t)(ld - at - 4)) + s_word * s.s_ld;
         }
     };
-    // copies step c of the tile that s is open on; nothing (a zero-length buffer) past the
-    // stream's end
-    // (kBlocks: step c of an expert is half c % 2 of its block c / 2, 128 tokens of 2 bytes)
-    auto copy_step = [&](const Source& s, int c, int block, int stage) {
+    // A wavefront's copies of a step, numbered: A's, B's, its part of the scale words.  Past the
+    // stream's end they repeat the last step.
+    constexpr int COPIES = A_COPIES + B_COPIES + (FP4 ? 1 : 0);
+    struct Step {
+        Source s;
+        uint32_t at;                                       // byte offset within a row
+        uint32_t s_at;                                     // ... within the scale words
+        uint32_t tail;                                     // all ones in a half step, else 0
+    };
+    auto copy_part = [&](const Step& x, int stage, int k) {
         const uint32_t to = lds0 + (uint32_t)(stage * STAGE);
-        const uint32_t at = LAYOUT == kBlocks ? (uint32_t)(block * 256 + (c & 1) * 128)
-                                              : (uint32_t)c * 128u;
-#pragma unroll
-        for (int k = 0; k < A_COPIES; ++k)
-            copy16(s.a, a_at[k], at, to + (uint32_t)(wave * A_COPIES + k) * 1024u);
-#pragma unroll
-        for (int k = 0; k < B_COPIES; ++k)
-            copy16(s.b, b_at[k], at, to + (uint32_t)B_OFF + (uint32_t)(wave * B_COPIES + k) * 1024u);
-        if constexpr (FP4) copy16(s.s, s_at, (uint32_t)c * s.s_step, to + s_lds);
+        if (k < A_COPIES)
+            copy16(x.s.a, a_at[k] - (tail_a & x.tail), x.at,
+                   to + (uint32_t)(wave * A_COPIES + k) * 1024u);
+        else if (k < A_COPIES + B_COPIES)
+            copy16<LAYOUT == kMasked>(x.s.b, b_at[k - A_COPIES] - (tail_a & x.tail), x.at,
+                   to + (uint32_t)(B_OFF + (wave * B_COPIES + k - A_COPIES) * 1024));
+        else if (FP4)
+            copy16(x.s.s, x.s.s_at - (s_word * x.s.s_ld & x.tail), x.s_at, to + s_lds);
     };
 
     // ---- fragment and scale reads ----
-    const int key = (j & 7) ^ (j >> 3);
+    const int key = j & 7;
     int a_rd[2], b_rd[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -324,42 +328,55 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
 
     // ---- the stream of (unit, step): what is multiplied, and what is copied next ----
     Tile cur, nxt;
-    Source src = {};
-    int nu = u, nc;                            // the next step to copy: step nc of unit nu
-    int block = 0;                             // kBlocks: the token block it lies in
+    Step next = {};                            // the next step to copy: step nc of unit nu
+    int nu = u, nc;
+    auto locate = [&] {
+        // (kBlocks: step nc of an expert is half nc % 2 of its block nc / 2, 128 tokens of 2
+        // bytes)
+        next.at = LAYOUT == kBlocks
+                      ? (uint32_t)(p.blocks[p.num_groups + 1 + (nc >> 1)] * 256 + (nc & 1) * 128)
+                      : (uint32_t)nc * 128u;
+        if constexpr (FP4) {
+            next.s_at = (uint32_t)nc * 2u * next.s.s_ld;
+            next.tail = 2 * nc + 1 < p.kwords ? 0u : ~0u;
+        }
+    };
     // moves to the next unit with at least one step (one without, an expert without tokens,
-    // is left to the storing loop); past the last one the copies get empty buffers
+    // is left to the storing loop); false past the last one
     auto seek = [&](int from) {
         for (nu = from; nu < units; nu += gridDim.x) {
             tile_at<BM, BN, LAYOUT, EPI>(p, list, m_tiles, nu, nxt);
             if (nxt.c0 < nxt.c1) {
-                open(nxt, src);
+                open(nxt, next.s);
                 nc = nxt.c0;
-                return;
+                return true;
             }
         }
-        src.a[2] = src.b[2] = src.s[2] = 0;
-        nc = 0;                                // (at most two more steps are asked for)
-        nxt.c1 = 0x7fffffff;
-    };
-    auto find_block = [&] {
-        if constexpr (LAYOUT == kBlocks) block = p.blocks[p.num_groups + 1 + (nc >> 1)];
+        return false;
     };
     auto advance = [&] {
-        if (++nc >= nxt.c1) seek(nu + gridDim.x);
-        find_block();
+        if (nu >= units || (++nc >= nxt.c1 && !seek(nu + gridDim.x))) return;
+        locate();
     };
 
 #include "fp8bs_mx_store.inc"
 
+    // Groups of a step; fragments are read AHEAD groups early.  At group LAST the present
+    // stage has been read out: the barrier stands there, and from there on, PER a group, go
+    // the copies that refill it, the rest of them early in the next step.  (All of them at
+    // once kept every wavefront from its products until the eight had pushed 72 kilobyte-wide
+    // copies through one address unit.)
+    constexpr int GROUPS = 2 * TM, AHEAD = 3, LAST = GROUPS - AHEAD;
+    constexpr int PER = (COPIES + GROUPS / 2) / (GROUPS / 2 + 1);
+    static_assert(PER * (GROUPS - 1) >= COPIES, "a step's copies fit between two barriers");
     clear();
-    seek(u);
-    find_block();
-    copy_step(src, nc, block, 0);
+    if (seek(u)) locate();                     // (no step at all: zero-length buffers)
+#pragma unroll
+    for (int k = 0; k < COPIES; ++k) copy_part(next, 0, k);
     advance();
     wait_and_meet();
-    copy_step(src, nc, block, 1);
-    constexpr int GROUPS = 2 * TM, AHEAD = 3;
+#pragma unroll
+    for (int k = 0; k < PER * AHEAD && k < COPIES; ++k) copy_part(next, 1, k);
     i32x4 fa[4], fb[2][TN];
     int sa[4], sb[2][TN];                      // scale words as read
     int eb[TN];                                // this round's B exponents
@@ -378,14 +395,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
         for (int c = cur.c0; c < cur.c1; ++c) {
             const int other = base ? 0 : STAGE;
             const int keep = 2 * c + 1 < p.kwords ? 255 : 0;
+            const Step started = next;                     // its first copies are out
             advance();
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                constexpr int LAST = GROUPS - AHEAD;
                 const int h = g / TM, i = g % TM;
                 if (g == LAST) {
                     wait_and_meet();
-                    copy_step(src, nc, block, base ? 1 : 0);
+                }
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    if (g >= LAST) {
+                        if ((g - LAST) * PER + k < COPIES) copy_part(next, base ? 1 : 0, (g - LAST) * PER + k);
+                    } else if ((g + AHEAD) * PER + k < COPIES) {
+                        copy_part(started, base ? 0 : 1, (g + AHEAD) * PER + k);
+                    }
                 }
                 const int ahead = g + AHEAD;
                 if (ahead < GROUPS) {
@@ -411,7 +435,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
                         for (int n = 0; n < TN; ++n) eb[n] = (sb[h][n] >> shift) & mask;
                     }
                 }
-                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
                     if constexpr (FP4)
@@ -422,7 +445,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
                             __builtin_bit_cast(bf16x8, fb[h][n]),
                             __builtin_bit_cast(bf16x8, fa[g % 4]), acc[i][n], 0, 0, 0);
                 }
-                __builtin_amdgcn_s_setprio(0);
                 __builtin_amdgcn_sched_barrier(0);
             }
             base = other;
@@ -463,10 +485,45 @@ int launch_gemm(int operand, int layout, int epilogue, const MxParams& params, i
     int threads = 0, per_cu = 1;
     const int64_t cols = gated(epilogue) ? 2 * (int64_t)p.n : p.n;
     const int64_t slots = layout == kMasked || layout == kBlocks ? groups : 1;
+    // tiles that hold rows; a masked slot's row count is spread around the expected one
     auto tiles = [&](int bm, int bn) {
-        return slots * ((expected_rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
+        const double tall = layout == kMasked ? expected_rows / (double)bm + 0.5
+                                              : (double)((expected_rows + bm - 1) / bm);
+        return slots * (tall < 1 ? 1 : tall) * (double)((cols + bn - 1) / bn);
     };
-    const bool large = tiles(256, 256) >= num_cus;
+    // Which kernel, by the time each would take (microseconds; MI355X, weights not in cache):
+    // - 256x256 tiles, one workgroup per CU: 1.4 a step of 128 bytes, 5 to fill and store.
+    // - 128x128, two per CU: 1.0 a step and 5 to fill and store; 0.77 and 2 while every
+    //   workgroup has a CU for itself.  28 steps, up to 256 tiles: 26 against 43 with 256x256;
+    //   256 x 7168 x 2048: 11.5 against 19.6; 2048 x 7168 x 2048: 30 against 26; 16 slots of
+    //   up to 256 rows, gated, f = 2048, k = 7168: 95 against 69, of 32 rows: 56 against 70.
+    // - few rows, dense or a few slots: a CU draws 27 GB/s into registers whatever the ring's
+    //   depth, so the bytes of its tiles' rows and columns count.  1 x 4096 x 7168: 6.5
+    //   (16x16) against 26; 64: 12.9 (32x32); 128: 16.6 (64x32); 256: 22 (64x64) against 26;
+    //   256 x 7168 x 2048: 17 against 11.5.
+    const double steps = p.chunks;
+    const double big = tiles(256, 256), small = tiles(128, 128);
+    const double large_us = ceil(big / num_cus) * (1.4 * steps + 5);
+    const double small_us = small <= num_cus ? 0.77 * steps + 2
+                                             : ceil(small / (2 * num_cus)) * (1.0 * steps + 5);
+    const bool large = large_us <= small_us;
+    if (operand == kFp4 && epilogue != kGatedGrad && layout != kContiguous) {
+        double best = large ? large_us : small_us;
+        int best_tm = 0, best_tn = 0;
+        for (int tm = 4; tm >= 1; tm /= 2) {               // (of equals the tallest: reads B least)
+            for (int tn = epilogue == kGatedQuant ? 4 : epilogue == kGated ? 2 : 1; tn <= 4; tn *= 2) {
+                const int rows = expected_rows < 16 * tm ? expected_rows : 16 * tm;
+                const double us = ceil(tiles(16 * tm, 16 * tn) / num_cus) *
+                                  (rows + 16 * tn) * (double)p.a_row / 27e3;
+                if (us < best) {
+                    best = us;
+                    best_tm = tm;
+                    best_tn = tn;
+                }
+            }
+        }
+        if (best_tm) return launch_stream(layout, epilogue, best_tm, best_tn, p, groups, expected_rows, stream);
+    }
 #define MX_CASE(T, L, E)                                                     \
     if (operand == T && layout == L && epilogue == E)                        \
         pick<T, L, E>(large, &fn, &s, &threads, &per_cu);

@@ -194,15 +194,17 @@ __global__ void __launch_bounds__(256) mx_transpose_kernel(
     }
 }
 
-// One workgroup; thread e (and e + 256, ...) counts expert e's blocks, then writes them in
-// order behind the blocks of the experts before it.
-__global__ void __launch_bounds__(256) mx_block_order_kernel(const int32_t* __restrict__ layout,
-                                                             int blocks, int groups,
-                                                             int32_t* __restrict__ out) {
-    for (int e = threadIdx.x; e < groups; e += 256) {
+// One workgroup; wavefront w takes the experts w, w + 16, ...: it counts their blocks 64 at a
+// time, then writes them in order behind the blocks of the experts before.
+__global__ void __launch_bounds__(1024) mx_block_order_kernel(const int32_t* __restrict__ layout,
+                                                              int blocks, int groups,
+                                                              int32_t* __restrict__ out) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    auto owned = [&](int b, int e) { return b < blocks && layout[(int64_t)b * 128] == e; };
+    for (int e = wave; e < groups; e += 16) {
         int n = 0;
-        for (int b = 0; b < blocks; ++b) n += layout[b * 128] == e;
-        out[e + 1] = n;
+        for (int w = 0; w < blocks; w += 64) n += __popcll(__ballot(owned(w + lane, e)));
+        if (lane == 0) out[e + 1] = n;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -212,10 +214,14 @@ __global__ void __launch_bounds__(256) mx_block_order_kernel(const int32_t* __re
     }
     __syncthreads();
     int32_t* order = out + groups + 1;
-    for (int e = threadIdx.x; e < groups; e += 256) {
+    for (int e = wave; e < groups; e += 16) {
         int at = out[e];
-        for (int b = 0; b < blocks; ++b)
-            if (layout[b * 128] == e) order[at++] = b;
+        for (int w = 0; w < blocks; w += 64) {
+            const bool mine = owned(w + lane, e);
+            const uint64_t all = __ballot(mine);
+            if (mine) order[at + __popcll(all & ((1ull << lane) - 1ull))] = w + lane;
+            at += __popcll(all);
+        }
     }
 }
 
@@ -251,7 +257,7 @@ int launch_transpose(const uint8_t* q, const int32_t* sf, uint16_t* xt, int grou
 int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups, int32_t* out,
                        hipStream_t stream) {
     void* args[] = {&grouped_layout, &blocks, &num_groups, &out};
-    return (int)hipLaunchKernel((const void*)mx_block_order_kernel, dim3(1), dim3(256), args, 0,
+    return (int)hipLaunchKernel((const void*)mx_block_order_kernel, dim3(1), dim3(1024), args, 0,
                                 stream);
 }
 
