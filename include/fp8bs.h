@@ -504,6 +504,27 @@ int fp8bs_gated_contiguous_mxfp4_backward(const void* a, const int32_t* sfa, con
                                           int k, int num_groups, int activation, void* workspace,
                                           size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Feed-forward layer on MXFP4 weights: x is quantised, goes through the gated block (its
+ * output quantised in the same kernel) and the down projection,
+ *     d = MXFP4(act(q Wg^T) * (q Wu^T)) W2^T,   q = MXFP4(x)
+ * -- fp8bs_quantize_mxfp4, fp8bs_gated_*_mxfp4_q and fp8bs_*_nt_mxfp4 in one call, with the
+ * same results.
+ *   layout  FP8BS_LAYOUT_DENSE, _CONTIGUOUS (group_data: grouped_layout) or _MASKED
+ *           (group_data: masked_m; m = max_m, expected_m as there)
+ *   x       f32 or bf16 (x_dtype) [m][k] (masked [num_groups][max_m][k])
+ *   b, sfb  codes of [2f][k] per group, b2, sfb2 codes of [n][f] per group; f a multiple of 128
+ *   d       bf16 [m][n] (masked [num_groups][max_m][n]), written at valid rows
+ *   workspace  at least fp8bs_feed_forward_workspace_size() bytes, 16-byte aligned, contents
+ *           ignored; less is refused with FP8BS_ERR_UNSUPPORTED.
+ */
+int64_t fp8bs_feed_forward_workspace_size(int layout, int64_t m, int f, int k, int num_groups);
+int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void* b,
+                             const int32_t* sfb, const void* b2, const int32_t* sfb2, void* d,
+                             const int32_t* group_data, int m, int expected_m, int f, int k,
+                             int n, int num_groups, int activation, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
 /* Row alignment of expert segments in the contiguous layout (128).  Analogue
  * of get_mk_alignment_for_contiguous_layout (hada page, section "Tiện ích và
  * biến môi trường"). */

@@ -245,9 +245,84 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     return st;
 }
 
+// Workspace of the feed-forward layer: x's codes and exponents, h's.
+struct LayerParts {
+    int64_t q, sf, hq, sfh, total;
+};
+LayerParts layer_parts(int64_t slots, int64_t m, int f, int k) {
+    LayerParts w;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const int64_t ld = fp8bs_get_sfa_ld(m);
+    w.q = take(slots * m * (k / 2));
+    w.sf = take(slots * (k / 128) * ld * 4);
+    w.hq = take(slots * m * (f / 2));
+    w.sfh = take(slots * (f / 128) * ld * 4);
+    w.total = at;
+    return w;
+}
+
+int check_layer(int layout, int64_t m, int f, int k, int groups) {
+    if (layout != kDense && layout != kContiguous && layout != kMasked) return FP8BS_ERR_SHAPE;
+    if (f < 128 || f % 128 != 0) return FP8BS_ERR_SHAPE;
+    const int st = check_sizes(layout, m, 2 * (int64_t)f, k, groups);
+    return st != FP8BS_OK ? st : check_sizes(layout, m, 1, f, groups);
+}
+
+int feed_forward(int layout, const void* x, int x_dtype, const void* b, const int32_t* sfb,
+                 const void* b2, const int32_t* sfb2, void* d, const int32_t* group_data, int m,
+                 int expected_m, int f, int k, int n, int groups, int activation, void* workspace,
+                 size_t workspace_bytes, hipStream_t stream) {
+    int st = check_layer(layout, m, f, k, groups);
+    if (st == FP8BS_OK) st = check_sizes(layout, m, n, f, groups);
+    if (st != FP8BS_OK) return st;
+    if (x_dtype != FP8BS_DTYPE_F32 && x_dtype != FP8BS_DTYPE_BF16) return FP8BS_ERR_UNSUPPORTED;
+    if (activation != FP8BS_ACT_SILU && activation != FP8BS_ACT_GELU_TANH)
+        return FP8BS_ERR_UNSUPPORTED;
+    if (m == 0) return FP8BS_OK;
+    if (!pointers_ok(x, b, sfb, b2, layout, group_data) || !aligned(sfb2, 16) || !aligned(d, 16))
+        return FP8BS_ERR_POINTER;
+    const int64_t slots = layout == kMasked ? groups : 1;
+    const LayerParts w = layer_parts(slots, m, f, k);
+    if (workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
+    if (!aligned(workspace, 16)) return FP8BS_ERR_POINTER;
+    uint8_t* ws = (uint8_t*)workspace;
+    int32_t* sf = (int32_t*)(ws + w.sf);
+    int32_t* sfh = (int32_t*)(ws + w.sfh);
+    st = fp8bs_quantize_mxfp4(x, x_dtype, ws + w.q, sf, (int)slots, m, k, stream);
+    if (st == FP8BS_OK)
+        st = gated_forward(layout, ws + w.q, sf, b, sfb, ws + w.hq, sfh, true, group_data, m,
+                           expected_m, f, k, groups, activation, stream);
+    if (st == FP8BS_OK)
+        st = product(layout, ws + w.hq, sfh, b2, sfb2, d, group_data, m, expected_m, n, f, groups,
+                     stream);
+    return st;
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t fp8bs_feed_forward_workspace_size(int layout, int64_t m, int f, int k, int num_groups) {
+    const int groups = layout == kDense ? 1 : num_groups;
+    const int st = check_layer(layout, m, f, k, groups);
+    if (st != FP8BS_OK) return -(int64_t)st;
+    return layer_parts(layout == kMasked ? groups : 1, m, f, k).total;
+}
+
+int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void* b,
+                             const int32_t* sfb, const void* b2, const int32_t* sfb2, void* d,
+                             const int32_t* group_data, int m, int expected_m, int f, int k,
+                             int n, int num_groups, int activation, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+    return feed_forward(layout, x, x_dtype, b, sfb, b2, sfb2, d, group_data, m, expected_m, f, k,
+                        n, layout == kDense ? 1 : num_groups, activation, workspace,
+                        workspace_bytes, stream);
+}
 
 int fp8bs_dense_nt_mxfp4(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
                          void* d, int m, int n, int k, hipStream_t stream) {

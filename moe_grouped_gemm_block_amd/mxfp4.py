@@ -14,9 +14,8 @@ from __future__ import annotations
 import ctypes
 
 import moe_grouped_gemm_block_amd as _pkg
-from moe_grouped_gemm_block_amd import (FP8BSError, LAYOUT_CONTIGUOUS, LAYOUT_DENSE, _bf16_dtypes,
-                                        _check, _dev_ptr, _DTYPES, _on_device,
-                                        _stream_handle, _torch, get_sfa_ld)
+from moe_grouped_gemm_block_amd import (FP8BSError, LAYOUT_CONTIGUOUS, LAYOUT_DENSE, LAYOUT_MASKED,
+                                        _dev_ptr, _torch)
 
 __all__ = [
     "fp8bs_quantize_mxfp4", "fp8bs_dequantize_mxfp4", "quantize_mxfp4", "dequantize_mxfp4",
@@ -24,20 +23,34 @@ __all__ = [
     "fp8bs_gated_dense_mxfp4", "fp8bs_gated_contiguous_mxfp4", "fp8bs_gated_masked_mxfp4",
     "fp8bs_gated_dense_mxfp4_q", "fp8bs_gated_contiguous_mxfp4_q", "fp8bs_gated_masked_mxfp4_q",
     "fp8bs_gated_dense_mxfp4_backward", "fp8bs_gated_contiguous_mxfp4_backward",
-    "gated_backward_workspace_size", "feed_forward_mxfp4", "ACTIVATIONS",
+    "gated_backward_workspace_size", "fp8bs_feed_forward_mxfp4", "feed_forward_workspace_size",
+    "feed_forward_mxfp4", "ACTIVATIONS",
 ]
 
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
-_NULL = ctypes.c_void_p(None)
 _lib = None
 
 
 def _load():
-    global _lib
+    """The library with this module's prototypes, and torch's types and queries (torch is
+    imported at the first call, like the library)."""
+    global _lib, _Tensor, _empty, _device_index, _raw_stream
+    global _FP4, _INT32, _FLOAT, _BF16, _UINT8, _bf16, _f32, _u8, _i32
     if _lib is not None:
         return _lib
     lib = _pkg._load()
+    torch = _torch()
+    _Tensor, _empty = torch.Tensor, torch.empty
+    _device_index = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+        else torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _bf16, _f32, _u8, _i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    packed = getattr(torch, "float4_e2m1fn_x2", None)
+    _FP4 = (_u8,) if packed is None else (_u8, packed)
+    _INT32, _FLOAT, _UINT8 = (_i32,), (_bf16, _f32), (_u8,)
+    _BF16 = _pkg._bf16_dtypes()
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     for name, args in {
         "fp8bs_quantize_mxfp4": [P, I, P, P, I, I, I, P],
@@ -56,6 +69,10 @@ def _load():
     }.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
+    lib.fp8bs_feed_forward_mxfp4.argtypes = [I, P, I] + [P] * 6 + [I] * 7 + [P, S, P]
+    lib.fp8bs_feed_forward_mxfp4.restype = I
+    lib.fp8bs_feed_forward_workspace_size.argtypes = [I, ctypes.c_int64] + [I] * 3
+    lib.fp8bs_feed_forward_workspace_size.restype = ctypes.c_int64
     lib.fp8bs_gated_backward_workspace_size.argtypes = [I, ctypes.c_int64] + [I] * 5
     lib.fp8bs_gated_backward_workspace_size.restype = ctypes.c_int64
     _lib = lib
@@ -63,32 +80,59 @@ def _load():
 
 
 # ---- argument checks ---------------------------------------------------------
+# These run on every call of a decode step, so the common case -- contiguous tensors of the
+# right type -- is a handful of attribute reads; _dev_ptr names what is wrong otherwise.
 
-def _fp4_dtypes():
-    d = _DTYPES.get("fp4")
-    if d is None:
+def _ptr(t, name, dtypes, ndim, index):
+    """Address of a contiguous tensor of ndim dims on device `index`."""
+    if (type(t) is _Tensor and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and t.ndim == ndim):
+        if t.get_device() == index:
+            return t.data_ptr()
+    else:
+        p = _dev_ptr(t, name, dtypes, ndim)
+        if t.get_device() == index:
+            return p.value
+    raise ValueError(f"{name} is on another device than the first operand")
+
+
+def _scales(t, name, count, index):
+    """Address of an exponent tensor of `count` words."""
+    if type(t) is _Tensor and t.is_cuda and t.dtype is _i32 and t.is_contiguous():
+        p = t.data_ptr()
+    else:
+        p = _dev_ptr(t, name, _INT32).value
+    if t.numel() != count:
+        raise ValueError(f"{name}: scale tensor sizes do not match the shapes")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on another device than the first operand")
+    return p
+
+
+def _ld(rows):
+    return (rows + 3) & -4
+
+
+def _first(t, name):
+    """Device index of a call's first operand."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
+
+
+def _call(name, index, stream, *args):
+    """Calls the library on device `index` and the given (or its current) stream."""
+    if index == _device_index():
+        st = getattr(_lib, name)(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
         torch = _torch()
-        d = (torch.uint8,)
-        packed = getattr(torch, "float4_e2m1fn_x2", None)
-        if packed is not None:
-            d += (packed,)
-        _DTYPES["fp4"] = d
-    return d
-
-
-def _float_dtypes():
-    d = _DTYPES.get("float")
-    if d is None:
-        torch = _torch()
-        d = _DTYPES["float"] = (torch.bfloat16, torch.float32)
-    return d
-
-
-def _int32():
-    d = _DTYPES.get("int32")
-    if d is None:
-        d = _DTYPES["int32"] = (_torch().int32,)
-    return d
+        with torch.cuda.device(index):
+            st = getattr(_lib, name)(*args, _raw_stream(index) if stream is None
+                                     else stream.cuda_stream)
+    if st:
+        raise FP8BSError(st, name)
 
 
 def _activation(name):
@@ -98,188 +142,169 @@ def _activation(name):
     return code
 
 
-def _same_device(*tensors):
-    index = tensors[0].get_device()
-    for t in tensors[1:]:
-        if t.get_device() != index:
-            raise ValueError("all tensors must be on one device")
-
-
-def _operands(a, sfa, b, sfb, a_ndim, b_ndim):
-    """Checked pointers of A, its exponents, B and its exponents; (rows of a slot, B rows, k,
-    groups of B)."""
-    ptrs = (_dev_ptr(a, "a", _fp4_dtypes(), a_ndim), _dev_ptr(sfa, "sfa", _int32()),
-            _dev_ptr(b, "b", _fp4_dtypes(), b_ndim), _dev_ptr(sfb, "sfb", _int32()))
-    m, k = a.shape[-2], 2 * a.shape[-1]
-    n, groups = b.shape[-2], b.shape[0] if b_ndim == 3 else 1
-    if 2 * b.shape[-1] != k:
+def _operands(a, sfa, b, sfb, masked, grouped):
+    """Device, checked addresses of A, its exponents, B and its exponents; rows of a slot, B
+    rows, k, groups of B."""
+    if _lib is None:
+        _load()
+    index = _first(a, "a")
+    pa = _ptr(a, "a", _FP4, 3 if masked else 2, index)
+    pb = _ptr(b, "b", _FP4, 3 if grouped else 2, index)
+    sa, sb = a.shape, b.shape
+    m, n, half = sa[-2], sb[-2], sa[-1]
+    if sb[-1] != half:
         raise ValueError("shape mismatch between a and b")
-    if k % 128 == 0:
-        kw = k // 128
-        slots = a.shape[0] if a_ndim == 3 else 1
-        if (sfa.numel() != slots * kw * get_sfa_ld(m)
-                or sfb.numel() != groups * kw * get_sfa_ld(n)):
-            raise ValueError("scale tensor sizes do not match the shapes")
-    return ptrs, m, n, k, groups
+    if half & 63 or not half:
+        raise FP8BSError(1, "k must be a positive multiple of 128")
+    groups = sb[0] if grouped else 1
+    words = half // 64
+    return (index, pa, _scales(sfa, "sfa", (sa[0] if masked else 1) * words * ((m + 3) & -4), index),
+            pb, _scales(sfb, "sfb", groups * words * ((n + 3) & -4), index), m, n, 2 * half, groups)
 
 
-def _layout_data(layout, data, a, b):
-    """Pointer of grouped_layout ("contiguous") or masked_m ("masked"), checked against a, b."""
+def _rows_out(d, name, dtypes, a, cols, index):
+    """Address of an output with a's rows and `cols` columns."""
+    p = _ptr(d, name, dtypes, a.ndim, index)
+    if d.shape[:-1] != a.shape[:-1] or d.shape[-1] != cols:
+        raise ValueError(f"{name} must be {tuple(a.shape[:-1]) + (cols,)}, got {tuple(d.shape)}")
+    return p
+
+
+def _layout_data(layout, data, a, b, index):
+    """Address of grouped_layout ("contiguous") or masked_m ("masked"), checked against a, b."""
     if layout == "contiguous":
-        p = _dev_ptr(data, "grouped_layout", _int32(), 1)
+        p = _ptr(data, "grouped_layout", _INT32, 1, index)
         if data.shape[0] != a.shape[0]:
             raise ValueError("grouped_layout must have one entry per row of a")
     else:
-        p = _dev_ptr(data, "masked_m", _int32(), 1)
+        p = _ptr(data, "masked_m", _INT32, 1, index)
         if b.shape[0] != a.shape[0] or data.shape[0] != a.shape[0]:
             raise ValueError("a, b and masked_m must have the same number of groups")
     return p
 
 
+def _new(shape, dtype, index, stream):
+    """Uninitialised device tensor, allocated for the stream it is used on."""
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=index)
+    with _torch().cuda.stream(stream):
+        return _empty(shape, dtype=dtype, device=index)
+
+
 # ---- quantiser ---------------------------------------------------------------
 
-def _quant_shape(x, q, sf):
-    if x.dim() not in (2, 3):
-        raise ValueError("x must be [rows][k] or [groups][rows][k]")
-    rows, k = x.shape[-2], x.shape[-1]
-    groups = x.shape[0] if x.dim() == 3 else 1
-    if tuple(q.shape) != tuple(x.shape[:-1]) + (k // 2,):
-        raise ValueError("q must be [..., rows, k/2] of x")
-    if k % 128 == 0 and sf.numel() != groups * (k // 128) * get_sfa_ld(rows):
-        raise ValueError("sf must be [..., k/128, get_sfa_ld(rows)]")
-    _same_device(x, q, sf)
-    return groups, rows, k
+def _values(x, name):
+    """(device, groups, rows, k) of a matrix of values or of codes."""
+    if _lib is None:
+        _load()
+    index = _first(x, name)
+    s = x.shape
+    if len(s) == 2:
+        return index, 1, s[0], s[1]
+    if len(s) != 3:
+        raise ValueError(f"{name} must be 2-D, or 3-D with groups")
+    return index, s[0], s[1], s[2]
 
 
 def fp8bs_quantize_mxfp4(x, q, sf, stream=None):
     """x bf16 or f32 [(groups,) rows, k] -> q codes [..., rows, k/2], sf int32 exponents
     [..., k/128, get_sfa_ld(rows)] (alignment padding not written)."""
-    groups, rows, k = _quant_shape(x, q, sf)
-    xp = _dev_ptr(x, "x", _float_dtypes())
-    args = (_dev_ptr(q, "q", _fp4_dtypes()), _dev_ptr(sf, "sf", _int32()))
-    dtype = 1 if x.dtype == _torch().bfloat16 else 0
-    with _on_device(x):
-        st = _load().fp8bs_quantize_mxfp4(xp, dtype, *args, groups, rows, k,
-                                          _stream_handle(stream, x.device))
-    _check(st, "fp8bs_quantize_mxfp4")
+    index, groups, rows, k = _values(x, "x")
+    xp = _ptr(x, "x", _FLOAT, x.ndim, index)
+    qp = _rows_out(q, "q", _FP4, x, k // 2, index)
+    sp = _scales(sf, "sf", groups * (k // 128) * _ld(rows), index)
+    _call("fp8bs_quantize_mxfp4", index, stream, xp, 1 if x.dtype is _bf16 else 0, qp, sp, groups,
+          rows, k)
 
 
 def fp8bs_dequantize_mxfp4(q, sf, x, stream=None):
     """The values that q and sf stand for, into x (bf16 or f32 [(groups,) rows, k])."""
-    groups, rows, k = _quant_shape(x, q, sf)
-    args = (_dev_ptr(q, "q", _fp4_dtypes()), _dev_ptr(sf, "sf", _int32()))
-    xp = _dev_ptr(x, "x", _float_dtypes())
-    dtype = 1 if x.dtype == _torch().bfloat16 else 0
-    with _on_device(x):
-        st = _load().fp8bs_dequantize_mxfp4(*args, xp, dtype, groups, rows, k,
-                                            _stream_handle(stream, x.device))
-    _check(st, "fp8bs_dequantize_mxfp4")
-
-
-def _empty(shape, dtype, like, stream):
-    """Uninitialised tensor on like's device, allocated for the stream it is used on."""
-    torch = _torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+    index, groups, rows, half = _values(q, "q")
+    qp = _ptr(q, "q", _FP4, q.ndim, index)
+    sp = _scales(sf, "sf", groups * (half // 64) * _ld(rows), index)
+    xp = _rows_out(x, "x", _FLOAT, q, 2 * half, index)
+    _call("fp8bs_dequantize_mxfp4", index, stream, qp, sp, xp, 1 if x.dtype is _bf16 else 0,
+          groups, rows, 2 * half)
 
 
 def quantize_mxfp4(x, stream=None):
     """(codes, exponents) of x; see ``fp8bs_quantize_mxfp4``."""
-    torch = _torch()
-    if x.dim() not in (2, 3):
-        raise ValueError("x must be [rows][k] or [groups][rows][k]")
-    lead, (rows, k) = tuple(x.shape[:-2]), x.shape[-2:]
-    q = _empty(lead + (rows, k // 2), torch.uint8, x, stream)
-    sf = _empty(lead + (k // 128, get_sfa_ld(rows)), torch.int32, x, stream)
-    fp8bs_quantize_mxfp4(x, q, sf, stream)
+    index, groups, rows, k = _values(x, "x")
+    xp = _ptr(x, "x", _FLOAT, x.ndim, index)
+    lead = () if x.ndim == 2 else (groups,)
+    q = _new((*lead, rows, k // 2), _u8, index, stream)
+    sf = _new((*lead, k // 128, (rows + 3) & -4), _i32, index, stream)
+    _call("fp8bs_quantize_mxfp4", index, stream, xp, 1 if x.dtype is _bf16 else 0, q.data_ptr(),
+          sf.data_ptr(), groups, rows, k)
     return q, sf
 
 
 def dequantize_mxfp4(q, sf, dtype=None, stream=None):
     """The values that q and sf stand for, bf16 (exact) unless dtype says float32."""
-    torch = _torch()
-    x = _empty(tuple(q.shape[:-1]) + (2 * q.shape[-1],), dtype or torch.bfloat16, q, stream)
-    fp8bs_dequantize_mxfp4(q, sf, x, stream)
+    index, groups, rows, half = _values(q, "q")
+    qp = _ptr(q, "q", _FP4, q.ndim, index)
+    sp = _scales(sf, "sf", groups * (half // 64) * ((rows + 3) & -4), index)
+    if dtype is None:
+        dtype = _bf16
+    elif dtype not in _FLOAT:
+        raise TypeError(f"dtype must be one of {_FLOAT}")
+    x = _new((*q.shape[:-1], 2 * half), dtype, index, stream)
+    _call("fp8bs_dequantize_mxfp4", index, stream, qp, sp, x.data_ptr(),
+          1 if dtype is _bf16 else 0, groups, rows, 2 * half)
     return x
 
 
 # ---- product -----------------------------------------------------------------
 
-def _rows_out(d, name, a, cols):
-    if tuple(d.shape) != tuple(a.shape[:-1]) + (cols,):
-        raise ValueError(f"{name} must be {tuple(a.shape[:-1]) + (cols,)}, got {tuple(d.shape)}")
-
-
 def fp8bs_dense_nt_mxfp4(a, sfa, b, sfb, d, stream=None):
     """D = A B^T: a codes [m][k/2], b codes [n][k/2], d bf16 [m][n] (written)."""
-    ptrs, m, n, k, _ = _operands(a, sfa, b, sfb, 2, 2)
-    dp = _dev_ptr(d, "d", _bf16_dtypes(), 2)
-    _rows_out(d, "d", a, n)
-    _same_device(a, sfa, b, sfb, d)
-    with _on_device(a):
-        st = _load().fp8bs_dense_nt_mxfp4(*ptrs, dp, m, n, k, _stream_handle(stream, a.device))
-    _check(st, "fp8bs_dense_nt_mxfp4")
+    index, pa, psa, pb, psb, m, n, k, _ = _operands(a, sfa, b, sfb, False, False)
+    dp = _rows_out(d, "d", _BF16, a, n, index)
+    _call("fp8bs_dense_nt_mxfp4", index, stream, pa, psa, pb, psb, dp, m, n, k)
 
 
 def fp8bs_grouped_contiguous_nt_mxfp4(a, sfa, b, sfb, d, grouped_layout, stream=None):
     """Contiguous MoE layout: a [m_total][k/2], b [g][n][k/2], grouped_layout int32 [m_total]."""
-    ptrs, m, n, k, g = _operands(a, sfa, b, sfb, 2, 3)
-    lp = _layout_data("contiguous", grouped_layout, a, b)
-    dp = _dev_ptr(d, "d", _bf16_dtypes(), 2)
-    _rows_out(d, "d", a, n)
-    _same_device(a, sfa, b, sfb, d, grouped_layout)
-    with _on_device(a):
-        st = _load().fp8bs_grouped_contiguous_nt_mxfp4(*ptrs, dp, lp, m, n, k, g,
-                                                       _stream_handle(stream, a.device))
-    _check(st, "fp8bs_grouped_contiguous_nt_mxfp4")
+    index, pa, psa, pb, psb, m, n, k, g = _operands(a, sfa, b, sfb, False, True)
+    lp = _layout_data("contiguous", grouped_layout, a, b, index)
+    dp = _rows_out(d, "d", _BF16, a, n, index)
+    _call("fp8bs_grouped_contiguous_nt_mxfp4", index, stream, pa, psa, pb, psb, dp, lp, m, n, k, g)
 
 
 def fp8bs_grouped_masked_nt_mxfp4(a, sfa, b, sfb, d, masked_m, expected_m: int = 0, stream=None):
     """Masked MoE layout: a [g][max_m][k/2], b [g][n][k/2], d bf16 [g][max_m][n]."""
-    ptrs, m, n, k, g = _operands(a, sfa, b, sfb, 3, 3)
-    mp = _layout_data("masked", masked_m, a, b)
-    dp = _dev_ptr(d, "d", _bf16_dtypes(), 3)
-    _rows_out(d, "d", a, n)
-    _same_device(a, sfa, b, sfb, d, masked_m)
-    with _on_device(a):
-        st = _load().fp8bs_grouped_masked_nt_mxfp4(*ptrs, dp, mp, g, m, int(expected_m), n, k,
-                                                   _stream_handle(stream, a.device))
-    _check(st, "fp8bs_grouped_masked_nt_mxfp4")
+    index, pa, psa, pb, psb, m, n, k, g = _operands(a, sfa, b, sfb, True, True)
+    mp = _layout_data("masked", masked_m, a, b, index)
+    dp = _rows_out(d, "d", _BF16, a, n, index)
+    _call("fp8bs_grouped_masked_nt_mxfp4", index, stream, pa, psa, pb, psb, dp, mp, g, m,
+          int(expected_m), n, k)
 
 
 # ---- gated block -------------------------------------------------------------
 
 def _gated(layout, a, sfa, b, sfb, out, data, expected_m, activation, stream):
     """out: (h,) or (hq, sfh)."""
-    quantised = len(out) == 2
-    grouped = layout != "dense"
-    ptrs, m, n, k, g = _operands(a, sfa, b, sfb, 3 if layout == "masked" else 2,
-                                 3 if grouped else 2)
+    grouped, masked = layout != "dense", layout == "masked"
+    index, pa, psa, pb, psb, m, n, k, g = _operands(a, sfa, b, sfb, masked, grouped)
     act = _activation(activation)
     if n % 2:
         raise ValueError("b must hold 2f rows")
     f = n // 2
-    if quantised:
-        hq, sfh = out
-        outs = (_dev_ptr(hq, "hq", _fp4_dtypes()), _dev_ptr(sfh, "sfh", _int32()))
-        _rows_out(hq, "hq", a, f // 2)
-        slots = a.shape[0] if layout == "masked" else 1
-        if f % 128 == 0 and sfh.numel() != slots * (f // 128) * get_sfa_ld(m):
-            raise ValueError("sfh must be [..., f/128, get_sfa_ld(rows)]")
+    if len(out) == 2:
+        name = f"fp8bs_gated_{layout}_mxfp4_q"
+        outs = (_rows_out(out[0], "hq", _FP4, a, f // 2, index),
+                _scales(out[1], "sfh", (a.shape[0] if masked else 1) * (f // 128) * _ld(m), index))
     else:
-        outs = (_dev_ptr(out[0], "h", _bf16_dtypes()),)
-        _rows_out(out[0], "h", a, f)
-    extra = (_layout_data(layout, data, a, b),) if grouped else ()
-    _same_device(a, sfa, b, sfb, *out, *((data,) if grouped else ()))
-    sizes = {"dense": (m, f, k), "contiguous": (m, f, k, g),
-             "masked": (g, m, int(expected_m), f, k)}[layout]
-    name = f"fp8bs_gated_{layout}_mxfp4" + ("_q" if quantised else "")
-    with _on_device(a):
-        st = getattr(_load(), name)(*ptrs, *outs, *extra, *sizes, act,
-                                    _stream_handle(stream, a.device))
-    _check(st, name)
+        name = f"fp8bs_gated_{layout}_mxfp4"
+        outs = (_rows_out(out[0], "h", _BF16, a, f, index),)
+    if not grouped:
+        _call(name, index, stream, pa, psa, pb, psb, *outs, m, f, k, act)
+        return
+    p = _layout_data(layout, data, a, b, index)
+    if masked:
+        _call(name, index, stream, pa, psa, pb, psb, *outs, p, g, m, int(expected_m), f, k, act)
+    else:
+        _call(name, index, stream, pa, psa, pb, psb, *outs, p, m, f, k, g, act)
 
 
 def fp8bs_gated_dense_mxfp4(a, sfa, b, sfb, h, activation: str = "silu", stream=None):
@@ -330,49 +355,39 @@ def gated_backward_workspace_size(layout: int, m: int, f: int, k: int, num_group
     return v
 
 
+def _workspace(workspace, size, index, stream):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one of size() bytes."""
+    if workspace is None:
+        workspace = _new((size(),), _u8, index, stream)
+    return _ptr(workspace, "workspace", _UINT8, 1, index), workspace.shape[0], workspace
+
+
 def _backward(layout, a, sfa, b, sfb, dh, da, db, data, activation, accumulate, workspace, stream):
-    torch = _torch()
     grouped = layout == "contiguous"
-    ptrs, m, n, k, g = _operands(a, sfa, b, sfb, 2, 3 if grouped else 2)
+    index, pa, psa, pb, psb, m, n, k, g = _operands(a, sfa, b, sfb, False, grouped)
     act = _activation(activation)
     if n % 2:
         raise ValueError("b must hold 2f rows")
     f = n // 2
-    dhp = _dev_ptr(dh, "dh", _bf16_dtypes(), 2)
-    _rows_out(dh, "dh", a, f)
-    tensors = [a, sfa, b, sfb, dh]
-    dap = dbp = _NULL
-    f32 = False
-    if da is not None:
-        dap = _dev_ptr(da, "da", _bf16_dtypes(), 2)
-        _rows_out(da, "da", a, k)
-        tensors.append(da)
+    dhp = _rows_out(dh, "dh", _BF16, a, f, index)
+    dap = None if da is None else _rows_out(da, "da", _BF16, a, k, index)
+    dbp, f32 = None, False
     if db is not None:
-        dbp = _dev_ptr(db, "db", _float_dtypes(), b.dim())
-        if tuple(db.shape) != tuple(b.shape[:-1]) + (k,):
-            raise ValueError("db must have b's shape with k columns")
-        f32 = db.dtype == torch.float32
-        tensors.append(db)
+        dbp = _rows_out(db, "db", _FLOAT, b, k, index)
+        f32 = db.dtype is _f32
     if accumulate and not f32:
         raise ValueError("accumulate needs a float32 db")
-    extra = ()
+    wp, wb, _keep = _workspace(
+        workspace, lambda: gated_backward_workspace_size(
+            LAYOUT_CONTIGUOUS if grouped else LAYOUT_DENSE, m, f, k, g, da is not None,
+            db is not None), index, stream)
+    head = (pa, psa, pb, psb, dhp, dap, dbp, 0 if f32 else 1, 1 if accumulate else 0)
     if grouped:
-        extra = (_layout_data(layout, data, a, b),)
-        tensors.append(data)
-    _same_device(*tensors)
-    sizes = (m, f, k, g) if grouped else (m, f, k)
-    name = f"fp8bs_gated_{layout}_mxfp4_backward"
-    with _on_device(a):
-        if workspace is None:
-            size = gated_backward_workspace_size(LAYOUT_CONTIGUOUS if grouped else LAYOUT_DENSE, m,
-                                                 f, k, g, da is not None, db is not None)
-            workspace = _empty((size,), torch.uint8, a, stream)
-        wp = _dev_ptr(workspace, "workspace", (torch.uint8,), 1)
-        _same_device(a, workspace)
-        st = getattr(_load(), name)(*ptrs, dhp, dap, dbp, 0 if f32 else 1, int(bool(accumulate)),
-                                    *extra, *sizes, act, wp, workspace.numel(),
-                                    _stream_handle(stream, a.device))
-    _check(st, name)
+        p = _layout_data(layout, data, a, b, index)
+        _call("fp8bs_gated_contiguous_mxfp4_backward", index, stream, *head, p, m, f, k, g, act, wp,
+              wb)
+    else:
+        _call("fp8bs_gated_dense_mxfp4_backward", index, stream, *head, m, f, k, act, wp, wb)
 
 
 def fp8bs_gated_dense_mxfp4_backward(a, sfa, b, sfb, dh, da, db, activation: str = "silu",
@@ -394,33 +409,60 @@ def fp8bs_gated_contiguous_mxfp4_backward(a, sfa, b, sfb, dh, da, db, grouped_la
 
 # ---- a feed-forward layer ----------------------------------------------------
 
-def feed_forward_mxfp4(x, b, sfb, b2, sfb2, activation: str = "silu", out=None,
-                       grouped_layout=None, masked_m=None, expected_m: int = 0, stream=None):
-    """y = MXFP4(act(x Wg^T) * (x Wu^T)) W2^T with x quantised to MXFP4.
+def feed_forward_workspace_size(layout: int, m: int, f: int, k: int, num_groups: int = 1) -> int:
+    """Workspace bytes of ``fp8bs_feed_forward_mxfp4`` (m: rows, of a slot if masked)."""
+    v = int(_load().fp8bs_feed_forward_workspace_size(int(layout), int(m), int(f), int(k),
+                                                      int(num_groups)))
+    if v < 0:
+        raise FP8BSError(-v, "fp8bs_feed_forward_workspace_size")
+    return v
+
+
+def fp8bs_feed_forward_mxfp4(x, b, sfb, b2, sfb2, out, activation: str = "silu",
+                             grouped_layout=None, masked_m=None, expected_m: int = 0,
+                             workspace=None, stream=None):
+    """out = MXFP4(act(x Wg^T) * (x Wu^T)) W2^T with x quantised to MXFP4.
 
     x bf16 or f32 [m][k] (masked: [g][max_m][k]); b codes [(g,) 2f, k/2] of the gate and up
-    projections, b2 codes [(g,) n, f/2] of the down projection.  grouped_layout or masked_m
-    select the MoE layouts.  Three launches: quantiser, gated block (h quantised in its
-    epilogue), product.  out: bf16, allocated if None (rows that are not valid are not
-    written)."""
-    torch = _torch()
+    projections, b2 codes [(g,) n, f/2] of the down projection; out bf16 [.., n].
+    grouped_layout or masked_m select the MoE layouts.  workspace: uint8 tensor of
+    feed_forward_workspace_size() bytes, or None to allocate one."""
     if grouped_layout is not None and masked_m is not None:
         raise ValueError("grouped_layout and masked_m exclude each other")
-    q, sf = quantize_mxfp4(x, stream)
-    lead, m = tuple(x.shape[:-2]), x.shape[-2]
-    f, n = b.shape[-2] // 2, b2.shape[-2]
-    hq = _empty(lead + (m, f // 2), torch.uint8, x, stream)
-    sfh = _empty(lead + (f // 128, get_sfa_ld(m)), torch.int32, x, stream)
+    index, slots, m, k = _values(x, "x")
+    masked, grouped = masked_m is not None, masked_m is not None or grouped_layout is not None
+    xp = _ptr(x, "x", _FLOAT, 3 if masked else 2, index)
+    pb = _ptr(b, "b", _FP4, 3 if grouped else 2, index)
+    pb2 = _ptr(b2, "b2", _FP4, 3 if grouped else 2, index)
+    groups = b.shape[0] if grouped else 1
+    two_f, n = b.shape[-2], b2.shape[-2]
+    f = two_f // 2
+    if 2 * b.shape[-1] != k or two_f % 2 or 2 * b2.shape[-1] != f or (
+            grouped and b2.shape[0] != groups):
+        raise ValueError("shape mismatch between x, b and b2")
+    psb = _scales(sfb, "sfb", groups * (k // 128) * _ld(two_f), index)
+    psb2 = _scales(sfb2, "sfb2", groups * (f // 128) * _ld(n), index)
+    act = _activation(activation)
+    op = _rows_out(out, "out", _BF16, x, n, index)
+    code, data = LAYOUT_DENSE, None
+    if masked:
+        code, data = LAYOUT_MASKED, _layout_data("masked", masked_m, x, b, index)
+    elif grouped:
+        code, data = LAYOUT_CONTIGUOUS, _layout_data("contiguous", grouped_layout, x, b, index)
+    wp, wb, _keep = _workspace(workspace,
+                               lambda: feed_forward_workspace_size(code, m, f, k, groups), index,
+                               stream)
+    _call("fp8bs_feed_forward_mxfp4", index, stream, code, xp, 1 if x.dtype is _bf16 else 0, pb, psb,
+          pb2, psb2, op, data, m, int(expected_m), f, k, n, groups, act, wp, wb)
+
+
+def feed_forward_mxfp4(x, b, sfb, b2, sfb2, activation: str = "silu", out=None,
+                       grouped_layout=None, masked_m=None, expected_m: int = 0, stream=None):
+    """``fp8bs_feed_forward_mxfp4`` that returns its output, a new tensor unless given (rows
+    that are not valid are not written)."""
     if out is None:
-        out = _empty(lead + (m, n), torch.bfloat16, x, stream)
-    if grouped_layout is not None:
-        fp8bs_gated_contiguous_mxfp4_q(q, sf, b, sfb, hq, sfh, grouped_layout, activation, stream)
-        fp8bs_grouped_contiguous_nt_mxfp4(hq, sfh, b2, sfb2, out, grouped_layout, stream)
-    elif masked_m is not None:
-        fp8bs_gated_masked_mxfp4_q(q, sf, b, sfb, hq, sfh, masked_m, expected_m, activation,
-                                   stream)
-        fp8bs_grouped_masked_nt_mxfp4(hq, sfh, b2, sfb2, out, masked_m, expected_m, stream)
-    else:
-        fp8bs_gated_dense_mxfp4_q(q, sf, b, sfb, hq, sfh, activation, stream)
-        fp8bs_dense_nt_mxfp4(hq, sfh, b2, sfb2, out, stream)
+        index, _, _, _ = _values(x, "x")
+        out = _new((*x.shape[:-1], b2.shape[-2]), _bf16, index, stream)
+    fp8bs_feed_forward_mxfp4(x, b, sfb, b2, sfb2, out, activation, grouped_layout, masked_m,
+                             expected_m, None, stream)
     return out

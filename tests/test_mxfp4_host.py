@@ -108,6 +108,27 @@ def test_backward_refusals(lib, p):
             size(*bad)
 
 
+def test_layer_refusals(lib, p):
+    size = fp8bs.feed_forward_workspace_size
+
+    def layer(layout=0, x=p, dt=1, d=p, data=p, m=4, f=128, k=128, n=8, g=2, act=0, ws=p, nb=1 << 40):
+        return lib.fp8bs_feed_forward_mxfp4(layout, x, dt, p, p, p, p, d, data, m, 0, f, k, n, g, act,
+                                            ws, nb, None)
+
+    assert layer(layout=3) == SHAPE and layer(f=64) == SHAPE and layer(k=64) == SHAPE
+    assert layer(n=0) == SHAPE and layer(m=-1) == SHAPE and layer(layout=2, g=0) == SHAPE
+    assert layer(layout=1, m=100) == SHAPE
+    assert layer(dt=5) == UNSUPPORTED and layer(act=2) == UNSUPPORTED
+    assert layer(x=None) == POINTER and layer(d=p + 2) == POINTER and layer(ws=None) == POINTER
+    assert layer(layout=2, data=None) == POINTER and layer(layout=1, m=128, data=p + 1) == POINTER
+    assert layer(nb=size(0, 4, 128, 128) - 1) == UNSUPPORTED
+    assert layer(m=0, x=None, d=None, ws=None, nb=0) == OK
+    assert size(fp8bs.LAYOUT_MASKED, 16, 256, 384, 5) >= 5 * 16 * (192 + 128)
+    for bad in ((3, 4, 128, 128), (fp8bs.LAYOUT_DENSE, 4, 96, 128), (fp8bs.LAYOUT_MASKED, 4, 128, 128, 0)):
+        with pytest.raises(fp8bs.FP8BSError):
+            size(*bad)
+
+
 def test_binding_refuses_host_tensors_and_unknown_activations():
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
