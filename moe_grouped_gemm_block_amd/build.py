@@ -24,7 +24,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = os.environ.get("FP8BS_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["fp8bs_gemm.hip", "fp8bs_quant.hip", "fp8bs_api.cpp", "fp8bs_planner.cpp",
-           "fp8bs_mx_gemm.hip", "fp8bs_mx_stream.hip", "fp8bs_mx_quant.hip", "fp8bs_mx_api.cpp"]
+           "fp8bs_mx_gemm.hip", "fp8bs_mx_stream.hip", "fp8bs_mx_grad.hip",
+           "fp8bs_mx_quant.hip", "fp8bs_mx_api.cpp"]
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -14,17 +14,12 @@ namespace mx {
 // token blocks of one expert (the weight gradient of the contiguous layout).
 enum Layout : int { kDense = 0, kContiguous = 1, kMasked = 2, kBlocks = 3 };
 
-// Operand types of the matrix kernel: 32 4-bit values with a shared power-of-two scale, or
-// bfloat16.
-enum Operand : int { kFp4 = 0, kBf16 = 1 };
-
 // What is done with the accumulators.
 //   kStore      D = bf16(acc)
 //   kStoreF32   D = acc, or D + acc when MxParams::accumulate is set
 //   kGated      h = act(gate) * up, rounded to bf16
 //   kGatedQuant the same h quantised to MXFP4
-//   kGatedGrad  dg = dh * up * act'(gate), du = dh * act(gate), rounded to bf16 and stored
-//               row-major and transposed
+//   kGatedGrad  dg = dh * up * act'(gate), du = dh * act(gate), rounded to bf16
 enum Epilogue : int { kStore = 0, kStoreF32 = 1, kGated = 2, kGatedQuant = 3, kGatedGrad = 4 };
 constexpr bool gated(int epi) { return epi == kGated || epi == kGatedQuant || epi == kGatedGrad; }
 
@@ -33,12 +28,12 @@ constexpr bool gated(int epi) { return epi == kGated || epi == kGatedQuant || ep
 constexpr int kMaxListed = 2048;
 
 struct MxParams {
-    const uint8_t* a;           // [rows] of a_row bytes
-    const uint8_t* b;           // [groups][B rows] of b_row bytes
-    const int32_t* sfa;         // kFp4: [kwords][sfa_ld] (masked: per slot)
-    const int32_t* sfb;         // kFp4: [groups][kwords][sfb_ld]
-    void* d;                    // output; kGatedQuant: codes; kGatedGrad: [rows][2f]
-    void* d2;                   // kGatedQuant: exponents; kGatedGrad: transposed [2f][d2_ld]
+    const uint8_t* a;           // codes [rows] of a_row bytes; fp8bs_mx_grad.hip: bf16
+    const uint8_t* b;           // codes [groups][B rows] of b_row bytes
+    const int32_t* sfa;         // [kwords][sfa_ld] (masked: per slot)
+    const int32_t* sfb;         // [groups][kwords][sfb_ld]
+    void* d;                    // output; kGatedQuant: codes; kGatedGrad: bf16 [rows][2f]
+    void* d2;                   // kGatedQuant: exponents
     const uint16_t* dh;         // kGatedGrad: bf16 [rows][f]
     const int32_t* group_data;  // contiguous: grouped_layout; masked: masked_m
     const int32_t* blocks;      // kBlocks: [groups + 1] offsets, then block numbers
@@ -46,8 +41,9 @@ struct MxParams {
     int64_t d_ld, d2_ld;        // elements (kGatedQuant: d_ld bytes of codes, d2_ld words)
     int m;                      // dense: M; contiguous: m_total; masked: rows of a slot
     int n;                      // output columns (gated: f)
-    int kwords;                 // k / 128 (kFp4)
-    int chunks;                 // 128-byte steps of a row
+    int depth;                  // fp8bs_mx_grad.hip: rows of the contraction
+    int kwords;                 // words of a row's exponents (its values / 128)
+    int chunks;                 // steps of the contraction
     int sfa_ld, sfb_ld;
     int num_groups;
     int m_tiles, n_tiles;       // m_tiles: dense, and per slot for masked
@@ -179,20 +175,17 @@ __device__ __forceinline__ int logical_block() {
 
 #endif  // __HIPCC__
 
-// Launchers (fp8bs_mx_gemm.hip, fp8bs_mx_quant.hip); return a hipError_t value.
-//
-// Values of codes [groups][rows][k/2] in bf16, transposed: xt [groups][k][ld], columns rows
-// .. ld-1 (ld a multiple of 64, rows <= ld < rows + 64) and, where grouped_layout is given,
-// rows that hold no token as zeros.
-int launch_transpose(const uint8_t* q, const int32_t* sf, uint16_t* xt, int groups, int rows,
-                     int k, int64_t ld, const int32_t* grouped_layout, int num_experts,
-                     hipStream_t stream);
+// Launchers; return a hipError_t value.
 // Contiguous layout: out = [num_groups + 1] offsets, then each expert's 128-row blocks in
 // order (a block belongs to the expert of its first row).
 int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups, int32_t* out,
                        hipStream_t stream);
-int launch_gemm(int operand, int layout, int epilogue, const MxParams& p, int groups,
-                int expected_rows, int num_cus, hipStream_t stream);
+int launch_gemm(int layout, int epilogue, const MxParams& p, int groups, int expected_rows,
+                int num_cus, hipStream_t stream);
+// Products of bf16 rows with widened codes (fp8bs_mx_grad.hip): D = A W, or with a_t
+// D = A^T X, the contraction running over the rows of the second operand.
+int launch_grad(int layout, bool a_t, int epilogue, const MxParams& p, int groups, int num_cus,
+                hipStream_t stream);
 // Few rows, dense and masked layouts: tiles of 16 tm x 16 tn (fp8bs_mx_stream.hip).
 int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& p, int groups,
                   int expected_rows, hipStream_t stream);

@@ -90,7 +90,7 @@ int product(int layout, const void* a, const int32_t* sfa, const void* b, const 
     p.d_ld = n;
     p.n = n;
     const int rows = layout == kMasked && expected_m > 0 && expected_m < m ? expected_m : m;
-    return status(launch_gemm(kFp4, layout, kStore, p, groups, rows, cus, stream));
+    return status(launch_gemm(layout, kStore, p, groups, rows, cus, stream));
 }
 
 int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
@@ -116,33 +116,20 @@ int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
     p.n = f;
     p.act = activation;
     const int rows = layout == kMasked && expected_m > 0 && expected_m < m ? expected_m : m;
-    return status(launch_gemm(kFp4, layout, quantise ? kGatedQuant : kGated, p, groups, rows, cus,
+    return status(launch_gemm(layout, quantise ? kGatedQuant : kGated, p, groups, rows, cus,
                               stream));
 }
 
-// Workspace of the backward pass: dg | du row-major, the weights widened and transposed (for
-// da); dg | du and A transposed, the blocks by expert (for db).  Every part starts at a
-// multiple of 256 bytes.
+// Workspace of the backward pass: dg | du, [rows up to a multiple of 64][2f], and for db of the
+// contiguous layout the blocks by expert.  Both parts start at a multiple of 256 bytes.
 struct Parts {
-    int64_t grad, weights, grad_t, a_t, order, total;
-    int64_t m_ld;                    // leading dimension of the transposed tokens
+    int64_t order, total;
 };
-Parts parts(int layout, int64_t m, int f, int k, int groups, bool want_da, bool want_db) {
+Parts parts(int layout, int64_t m, int f, int groups, bool want_db) {
     Parts w;
-    int64_t at = 0;
-    auto take = [&](int64_t bytes) {
-        const int64_t here = at;
-        at += (bytes + 255) / 256 * 256;
-        return here;
-    };
-    w.m_ld = (m + 63) / 64 * 64;
-    w.grad = take(want_da ? m * 2 * f * 2 : 0);
-    w.weights = take(want_da ? (int64_t)groups * k * 2 * f * 2 : 0);
-    w.grad_t = take(want_db ? 2 * (int64_t)f * w.m_ld * 2 : 0);
-    w.a_t = take(want_db ? (int64_t)k * w.m_ld * 2 : 0);
+    w.order = ((m + 63) / 64 * 64 * 2 * f * 2 + 255) / 256 * 256;
     // (four entries to spare: the copies look up to two steps past the last block)
-    w.order = take(want_db && layout == kContiguous ? (groups + 1 + m / 128 + 4) * 4 : 0);
-    w.total = at;
+    w.total = w.order + (want_db && layout == kContiguous ? (groups + 1 + m / 128 + 4) * 4 : 0);
     return w;
 }
 
@@ -151,8 +138,8 @@ int check_backward(int layout, int64_t m, int f, int k, int groups) {
     if (f < 1 || f % 32 != 0) return FP8BS_ERR_SHAPE;
     const int st = check_sizes(layout, m, 2 * (int64_t)f, k, groups);
     if (st != FP8BS_OK) return st;
-    // 256 rows of a transposed operand within 32-bit copy offsets, step offsets below 4 GiB
-    if (m > (1 << 23) || f > (1 << 22)) return FP8BS_ERR_SHAPE;
+    // 256 rows of dg | du within 32-bit copy offsets
+    if (f > (1 << 21)) return FP8BS_ERR_SHAPE;
     return FP8BS_OK;
 }
 
@@ -172,75 +159,54 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     if (m > 0 && (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(dh, 16)))
         return FP8BS_ERR_POINTER;
     if (m == 0 && (!db || accumulate)) return FP8BS_OK;
-    const Parts w = parts(layout, m, f, k, groups, da != nullptr, db != nullptr);
+    const Parts w = parts(layout, m, f, groups, db != nullptr);
     if (w.total > 0 && workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
     if (w.total > 0 && !aligned(workspace, 16)) return FP8BS_ERR_POINTER;
     const int cus = device_cus();
     if (cus <= 0) return FP8BS_ERR_HIP;
-    uint8_t* ws = (uint8_t*)workspace;
-    uint16_t* grad = (uint16_t*)(ws + w.grad);
-    uint16_t* weights = (uint16_t*)(ws + w.weights);
-    uint16_t* grad_t = (uint16_t*)(ws + w.grad_t);
-    uint16_t* a_t = (uint16_t*)(ws + w.a_t);
-    int32_t* order = (int32_t*)(ws + w.order);
+    uint8_t* grad = (uint8_t*)workspace;
+    int32_t* order = (int32_t*)(grad + w.order);
 
+    MxParams p = base_params(a, sfa, b, sfb, group_data, m, 2 * (int64_t)f, k, groups);
     if (m > 0) {
-        MxParams p = base_params(a, sfa, b, sfb, group_data, m, 2 * (int64_t)f, k, groups);
         p.n = f;
         p.act = activation;
         p.dh = (const uint16_t*)dh;
-        p.d = da ? grad : nullptr;
+        p.d = grad;
         p.d_ld = 2 * (int64_t)f;
-        p.d2 = db ? grad_t : nullptr;
-        p.d2_ld = w.m_ld;
-        st = status(launch_gemm(kFp4, layout, kGatedGrad, p, groups, m, cus, stream));
+        st = status(launch_gemm(layout, kGatedGrad, p, groups, m, cus, stream));
         if (st != FP8BS_OK) return st;
     }
+    // both products: bf16 dg | du, 4-bit second operand with k columns
+    p.a = grad;
+    p.a_row = 4 * (int64_t)f;
+    p.n = k;
+    p.d_ld = k;
     if (da && m > 0) {
-        st = status(launch_transpose((const uint8_t*)b, sfb, weights, groups, 2 * f, k,
-                                     2 * (int64_t)f, nullptr, 0, stream));
-        if (st != FP8BS_OK) return st;
-        MxParams p;
-        memset(&p, 0, sizeof p);
-        p.a = (const uint8_t*)grad;
-        p.b = (const uint8_t*)weights;
-        p.a_row = p.b_row = 4 * (int64_t)f;
-        p.group_data = group_data;
-        p.m = m;
-        p.n = k;
-        p.chunks = f / 32;
-        p.num_groups = groups;
-        p.d = da;
-        p.d_ld = k;
-        st = status(launch_gemm(kBf16, layout, kStore, p, groups, m, cus, stream));
+        MxParams x = p;
+        x.depth = 2 * f;
+        x.chunks = f / 32;
+        x.d = da;
+        st = status(launch_grad(layout, false, kStore, x, groups, cus, stream));
         if (st != FP8BS_OK) return st;
     }
     if (db) {
-        if (m > 0) {
-            st = status(launch_transpose((const uint8_t*)a, sfa, a_t, 1, m, k, w.m_ld,
-                                         layout == kContiguous ? group_data : nullptr, groups,
-                                         stream));
-            if (st != FP8BS_OK) return st;
-        }
         if (layout == kContiguous) {
             st = status(launch_block_order(group_data, m / 128, groups, order, stream));
             if (st != FP8BS_OK) return st;
         }
-        MxParams p;
-        memset(&p, 0, sizeof p);
-        p.a = (const uint8_t*)grad_t;
-        p.b = (const uint8_t*)a_t;
-        p.a_row = p.b_row = 2 * w.m_ld;
-        p.blocks = order;
-        p.m = 2 * f;
-        p.n = k;
-        p.chunks = (int)(w.m_ld / 64);
-        p.num_groups = groups;
-        p.d = db;
-        p.d_ld = k;
-        p.accumulate = accumulate;
-        st = status(launch_gemm(kBf16, layout == kContiguous ? kBlocks : kDense,
-                                f32 ? kStoreF32 : kStore, p, groups, 2 * f, cus, stream));
+        MxParams x = p;
+        x.b = (const uint8_t*)a;
+        x.sfb = sfa;
+        x.sfb_ld = p.sfa_ld;
+        x.blocks = order;
+        x.depth = m;
+        x.chunks = (m + 63) / 64;
+        x.m = 2 * f;
+        x.d = db;
+        x.accumulate = accumulate;
+        st = status(launch_grad(layout == kContiguous ? kBlocks : kDense, true,
+                                f32 ? kStoreF32 : kStore, x, groups, cus, stream));
     }
     return st;
 }
@@ -395,8 +361,8 @@ int64_t fp8bs_gated_backward_workspace_size(int layout, int64_t m, int f, int k,
                                             int want_da, int want_db) {
     const int st = check_backward(layout, m, f, k, layout == kDense ? 1 : num_groups);
     if (st != FP8BS_OK) return -(int64_t)st;
-    return parts(layout, m, f, k, layout == kDense ? 1 : num_groups, want_da != 0, want_db != 0)
-        .total;
+    if (!want_da && !want_db) return 0;
+    return parts(layout, m, f, layout == kDense ? 1 : num_groups, want_db != 0).total;
 }
 
 int fp8bs_gated_dense_mxfp4_backward(const void* a, const int32_t* sfa, const void* b,

@@ -1,11 +1,10 @@
 // fp8bs_mx_gemm.hip -- the matrix kernel of the MXFP4 operators on gfx950: D = A B^T with
 // 4-bit operands (32-value blocks along K, power-of-two scales applied by the matrix core)
-// or bf16 ones, and what the operators do with the accumulators (fp8bs_mx.h, Epilogue).
+// and what the operators do with the accumulators (fp8bs_mx.h, Epilogue).
 //
-// Both operand types move in steps of 128 bytes per row -- 256 4-bit or 64 bf16 values --
-// and each step feeds two rounds of v_mfma (16x16x128 f8f6f4 with block scales, 16x16x32
-// bf16): both take 16 cycles for 64 bytes of a row, lane (j, q) = (l % 16, l / 16) holding
-// 16 bytes at byte 16 q of row j, so one kernel serves both types.
+// Operands move in steps of 128 bytes -- 256 values -- per row; a step feeds two rounds of
+// v_mfma_scale_f32_16x16x128_f8f6f4 (16 cycles each), lane (j, q) = (l % 16, l / 16) holding
+// the 16 bytes, one scale block, at byte 16 q of row j's round.
 //
 // Tile: BM x BN by WM x WN wavefronts, each 16 TM x 64.  B rows are the instruction's first
 // operand and A rows its second, so a lane's results belong to one A row.  Rows are dealt to
@@ -29,151 +28,32 @@
 // unit's first steps while it finishes and stores the present one.
 #include <math.h>
 
-#include "fp8bs_mx.h"
+#include "fp8bs_mx_tile.h"
 
 namespace fp8bs {
 namespace mx {
 namespace {
 
-#define LDS_AS __attribute__((address_space(3)))
-
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-    return (uint32_t)(uintptr_t)(LDS_AS const void*)p;
-}
-
-// 16 bytes per lane from buffer offset voff + soff to LDS bytes lds + 16 * lane.  The five
-// wait states cover a scalar register written by the vector unit just before, and M0 (a
-// reserved register that nothing else here uses: LDS instructions do not need it).
-template <bool ONCE = false>
-__device__ __forceinline__ void copy16(const i32x4& buffer, uint32_t voff, uint32_t soff,
-                                       uint32_t lds) {
-    if constexpr (ONCE)
-        asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-                     :: "v"(voff), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff)),
-                        "s"(__builtin_amdgcn_readfirstlane(lds)));
-    else
-        asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                     :: "v"(voff), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff)),
-                        "s"(__builtin_amdgcn_readfirstlane(lds)));
-}
-// every copy, load and store of this wavefront done, then the workgroup meets
-__device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 __device__ __forceinline__ i32x8 widen(const i32x4& v) {
     return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
 }
 
-struct Tile {
-    int g;              // expert (weight group)
-    int slot;           // masked: slot of A and D; else 0
-    int m0, n0;         // first row (of the slot) and first output column
-    int rows;           // rows of the slot that may be read, from m0
-    int c0, c1;         // steps along the contraction
-};
-
-__device__ __forceinline__ int expert_of(const MxParams& p, int block) {
-    const int e = p.group_data[block * 128];
-    return e >= 0 && e < p.num_groups ? e : -1;
-}
-
-// The tiles along M that hold a valid row, listed in LDS by one wavefront; returns how many.
-// Contiguous: block number * 2 + whether the next 128-row block, of the same expert, belongs
-// to the tile (256-row tiles pair the blocks of a run of one expert).  Masked: slot *
-// m_tiles + tile.
-template <int BM, int LAYOUT>
-__device__ int list_tiles(const MxParams& p, uint32_t* list) {
-    const int lane = threadIdx.x & 63;
-    int count = 0;
-    if constexpr (LAYOUT == kContiguous) {
-        int run = p.first, before = -2;               // start and expert of the run so far
-        for (int w = p.first; w < p.last; w += 64) {
-            const int b = w + lane;
-            const int e = b < p.last ? expert_of(p, b) : -1;
-            const int after = b + 1 < p.last ? expert_of(p, b + 1) : -1;
-            const int prev = __shfl_up(e, 1, 64);
-            const uint64_t starts = __ballot(e != (lane ? prev : before));
-            const uint64_t upto = starts & (lane == 63 ? ~0ull : (2ull << lane) - 1ull);
-            const int first = upto ? w + 63 - __clzll(upto) : run;
-            const bool head = e >= 0 && (BM < 256 || ((b - first) & 1) == 0);
-            const uint64_t heads = __ballot(head);
-            if (head)
-                list[count + __popcll(heads & ((1ull << lane) - 1ull))] =
-                    (uint32_t)(2 * b + (BM >= 256 && after == e ? 1 : 0));
-            count += __popcll(heads);
-            run = starts ? w + 63 - __clzll(starts) : run;
-            before = __shfl(e, 63, 64);
-        }
-    } else {
-        for (int w = p.first; w < p.last; w += 64) {
-            const int i = w + lane;
-            const int g = min(i, p.last - 1) / p.m_tiles;
-            const bool in = i < p.last && (i - g * p.m_tiles) * BM < min(p.group_data[g], p.m);
-            const uint64_t heads = __ballot(in);
-            if (in) list[count + __popcll(heads & ((1ull << lane) - 1ull))] = (uint32_t)i;
-            count += __popcll(heads);
-        }
-    }
-    return count;
-}
-
-template <int BM, int BN, int LAYOUT, int EPI>
-__device__ __forceinline__ void tile_at(const MxParams& p, const uint32_t* list, int m_tiles,
-                                        int u, Tile& t) {
-    constexpr int COLS = gated(EPI) ? BN / 2 : BN;
-    int g = 0;
-    if constexpr (LAYOUT == kBlocks) {
-        g = u / (m_tiles * p.n_tiles);
-        u -= g * (m_tiles * p.n_tiles);
-    }
-    // groups of `raster` tiles along M sweep the columns
-    const int band = u / (p.raster * p.n_tiles);
-    const int in_band = u - band * p.raster * p.n_tiles;
-    const int first = band * p.raster;
-    const int tall = min(p.raster, m_tiles - first);
-    const int mt = first + in_band % tall;
-    t.n0 = in_band / tall * COLS;
-    t.g = g;
-    t.slot = 0;
-    t.c0 = 0;
-    t.c1 = p.chunks;
-    if constexpr (LAYOUT == kContiguous) {
-        const uint32_t e = __builtin_amdgcn_readfirstlane(list[mt]);
-        t.m0 = (int)(e >> 1) * 128;
-        t.rows = BM < 256 ? min(BM, 128) : (e & 1) ? 256 : 128;
-        t.g = __builtin_amdgcn_readfirstlane(p.group_data[t.m0]);
-    } else if constexpr (LAYOUT == kMasked) {
-        const int e = (int)__builtin_amdgcn_readfirstlane(list[mt]);
-        t.g = t.slot = e / p.m_tiles;
-        t.m0 = (e - t.g * p.m_tiles) * BM;
-        t.rows = __builtin_amdgcn_readfirstlane(min(p.group_data[t.g], p.m)) - t.m0;
-    } else {
-        t.m0 = mt * BM;
-        t.rows = p.m - t.m0;
-        if constexpr (LAYOUT == kBlocks) {
-            t.c0 = 2 * __builtin_amdgcn_readfirstlane(p.blocks[g]);
-            t.c1 = 2 * __builtin_amdgcn_readfirstlane(p.blocks[g + 1]);
-        }
-    }
-}
-
-template <int T, int BM, int BN, int WM, int WN, int LAYOUT, int EPI>
+template <int BM, int BN, int WM, int WN, int LAYOUT, int EPI>
 __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams p) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = 4;
     static_assert(BN / WN == 64, "a wavefront has four column blocks");
-    constexpr bool FP4 = T == kFp4, GATED = gated(EPI);
+    constexpr bool GATED = gated(EPI);
     constexpr int COLS = GATED ? BN / 2 : BN;              // output columns of a tile
     constexpr int A_COPIES = BM / 8 / NW, B_COPIES = BN / 8 / NW;
     static_assert(A_COPIES * NW * 8 == BM && B_COPIES * NW * 8 == BN, "whole copies");
     // scale words of a step: two (128 values each) per row, [2][rows], at least one copy
-    constexpr int SA_COPIES = FP4 ? (BM * 8 + 1023) / 1024 : 0;
-    constexpr int SB_COPIES = FP4 ? (BN * 8 + 1023) / 1024 : 0;
+    constexpr int SA_COPIES = (BM * 8 + 1023) / 1024;
+    constexpr int SB_COPIES = (BN * 8 + 1023) / 1024;
     static_assert(SA_COPIES + SB_COPIES <= NW, "one scale copy per wavefront");
     constexpr int B_OFF = BM * 128, SA_OFF = B_OFF + BN * 128, SB_OFF = SA_OFF + SA_COPIES * 1024;
     // (the other wavefronts copy nothing into a spare kilobyte, which keeps a step branch-free)
     constexpr int SPARE_OFF = SB_OFF + SB_COPIES * 1024;
-    constexpr int STAGE = SPARE_OFF + (FP4 ? 1024 : 0);
+    constexpr int STAGE = SPARE_OFF + 1024;
     constexpr bool LISTED = LAYOUT == kContiguous || LAYOUT == kMasked;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
     __shared__ uint32_t list[LISTED ? kMaxListed + 1 : 1];
@@ -192,7 +72,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
         __syncthreads();
         m_tiles = __builtin_amdgcn_readfirstlane(list[kMaxListed]);
     }
-    const int units = m_tiles * p.n_tiles * (LAYOUT == kBlocks ? p.num_groups : 1);
+    const int units = m_tiles * p.n_tiles;
     int u = logical_block();
     if (u >= units) return;
 
@@ -230,7 +110,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     const bool sa_mine = wave < SA_COPIES;
     const bool sb_mine = !sa_mine && wave < SA_COPIES + SB_COPIES;
     uint32_t s_row = 0, s_word = 0, s_lds = 0;             // row of the tile, word row (0, 1)
-    if constexpr (FP4) {
+    {
         const int rows = sa_mine ? BM : BN;
         const int ins = sa_mine ? wave : wave - SA_COPIES;
         const int word = ins * 256 + lane * 4;             // of the [2][rows] words
@@ -248,24 +128,22 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
         uint32_t s_ld;                                     // bytes of a word row
     };
     auto open = [&](const Tile& t, Source& s) {
-        const int64_t group = LAYOUT == kBlocks ? 0 : (int64_t)t.g * (GATED ? 2 * p.n : p.n);
+        const int64_t group = (int64_t)t.g * (GATED ? 2 * p.n : p.n);
         s.a = descriptor(p.a + ((int64_t)t.slot * p.m + t.m0) * p.a_row, t.rows * p.a_row);
         s.b = descriptor(p.b + (group + t.n0 + (b_up ? p.n : 0)) * p.b_row,
                          (int64_t)(p.n - t.n0) * p.b_row);
-        if constexpr (FP4) {
-            const int64_t words = p.kwords;
-            const int ld = sa_mine ? p.sfa_ld : p.sfb_ld, at = sa_mine ? t.m0 : t.n0;
-            const int32_t* base = sa_mine ? p.sfa + (int64_t)t.slot * words * ld
-                                          : p.sfb + (int64_t)t.g * words * ld;
-            s.s = descriptor(base + at, (words * ld - at) * 4);
-            s.s_ld = 4u * (uint32_t)ld;
-            // rows past the padded end read its last four words (they belong to no result)
-            s.s_at = 4u * min(s_row, (uint32_t)(ld - at - 4)) + s_word * s.s_ld;
-        }
+        const int64_t words = p.kwords;
+        const int ld = sa_mine ? p.sfa_ld : p.sfb_ld, at = sa_mine ? t.m0 : t.n0;
+        const int32_t* base = sa_mine ? p.sfa + (int64_t)t.slot * words * ld
+                                      : p.sfb + (int64_t)t.g * words * ld;
+        s.s = descriptor(base + at, (words * ld - at) * 4);
+        s.s_ld = 4u * (uint32_t)ld;
+        // rows past the padded end read its last four words (they belong to no result)
+        s.s_at = 4u * min(s_row, (uint32_t)(ld - at - 4)) + s_word * s.s_ld;
     };
     // A wavefront's copies of a step, numbered: A's, B's, its part of the scale words.  Past the
     // stream's end they repeat the last step.
-    constexpr int COPIES = A_COPIES + B_COPIES + (FP4 ? 1 : 0);
+    constexpr int COPIES = A_COPIES + B_COPIES + 1;
     struct Step {
         Source s;
         uint32_t at;                                       // byte offset within a row
@@ -280,7 +158,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
         else if (k < A_COPIES + B_COPIES)
             copy16<LAYOUT == kMasked>(x.s.b, b_at[k - A_COPIES] - (tail_a & x.tail), x.at,
                    to + (uint32_t)(B_OFF + (wave * B_COPIES + k - A_COPIES) * 1024));
-        else if (FP4)
+        else
             copy16(x.s.s, x.s.s_at - (s_word * x.s.s_ld & x.tail), x.s_at, to + s_lds);
     };
 
@@ -306,15 +184,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     // 2^-127, whose products with any 4-bit values vanish.
     const int shift = 8 * q;
     auto read_sa = [&](int base, int h, int i) {
-        return FP4 ? *(const int*)(smem + base + sa_rd + h * BM * 4 + 4 * i) : 0;
+        return *(const int*)(smem + base + sa_rd + h * BM * 4 + 4 * i);
     };
     auto read_sb = [&](int base, int h, int (&s)[TN]) {
-        if constexpr (FP4) {
 #pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                const int word = GATED ? (n & 1) + (n >> 1) * COLS : n;
-                s[n] = *(const int*)(smem + base + sb_rd + h * BN * 4 + 4 * word);
-            }
+        for (int n = 0; n < TN; ++n) {
+            const int word = GATED ? (n & 1) + (n >> 1) * COLS : n;
+            s[n] = *(const int*)(smem + base + sb_rd + h * BN * 4 + 4 * word);
         }
     };
 
@@ -329,37 +205,141 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     // ---- the stream of (unit, step): what is multiplied, and what is copied next ----
     Tile cur, nxt;
     Step next = {};                            // the next step to copy: step nc of unit nu
-    int nu = u, nc;
+    int nu = u, nc = 0;
     auto locate = [&] {
-        // (kBlocks: step nc of an expert is half nc % 2 of its block nc / 2, 128 tokens of 2
-        // bytes)
-        next.at = LAYOUT == kBlocks
-                      ? (uint32_t)(p.blocks[p.num_groups + 1 + (nc >> 1)] * 256 + (nc & 1) * 128)
-                      : (uint32_t)nc * 128u;
-        if constexpr (FP4) {
-            next.s_at = (uint32_t)nc * 2u * next.s.s_ld;
-            next.tail = 2 * nc + 1 < p.kwords ? 0u : ~0u;
-        }
-    };
-    // moves to the next unit with at least one step (one without, an expert without tokens,
-    // is left to the storing loop); false past the last one
-    auto seek = [&](int from) {
-        for (nu = from; nu < units; nu += gridDim.x) {
-            tile_at<BM, BN, LAYOUT, EPI>(p, list, m_tiles, nu, nxt);
-            if (nxt.c0 < nxt.c1) {
-                open(nxt, next.s);
-                nc = nxt.c0;
-                return true;
-            }
-        }
-        return false;
+        next.at = (uint32_t)nc * 128u;
+        next.s_at = (uint32_t)nc * 2u * next.s.s_ld;
+        next.tail = 2 * nc + 1 < p.kwords ? 0u : ~0u;
     };
     auto advance = [&] {
-        if (nu >= units || (++nc >= nxt.c1 && !seek(nu + gridDim.x))) return;
+        if (nu >= units) return;               // past the last unit
+        if (++nc >= p.chunks) {
+            nu += gridDim.x;
+            if (nu >= units) return;
+            tile_at<BM, COLS, LAYOUT>(p, list, m_tiles, nu, nxt);
+            open(nxt, next.s);
+            nc = 0;
+        }
         locate();
     };
-
-#include "fp8bs_mx_store.inc"
+    // Lane (j, q) holds rows m0 + 16 TM wm + TM j + i, i < TM, and columns n0 + 64 wn + 16 q +
+    // 4 v + n (element v of block n); gated: n0 + 32 wn + 8 q + 2 v + n of the gate (blocks 0,
+    // 1) and of the up projection (blocks 2, 3).
+    auto store = [&](const Tile& t) {
+        const int r0 = t.m0 + wm * 16 * TM + TM * j;       // this lane's first row
+        bool ok[TM];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = r0 + i;
+            ok[i] = r - t.m0 < t.rows;
+            if constexpr (LAYOUT == kContiguous) ok[i] = ok[i] && p.group_data[r] == t.g;
+        }
+        if constexpr (EPI == kStore) {
+            const int col = t.n0 + wn * 64 + 16 * q;
+            const int64_t first = LAYOUT == kMasked ? (int64_t)t.slot * p.m : (int64_t)0;
+            const bool whole = col + 16 <= p.n && (p.d_ld & 7) == 0;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if (!ok[i]) continue;
+                uint16_t* d = (uint16_t*)p.d + (first + r0 + i) * p.d_ld + col;
+                if (whole) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        w[2 * v] = pack_bf16(acc[i][0][v], acc[i][1][v]);
+                        w[2 * v + 1] = pack_bf16(acc[i][2][v], acc[i][3][v]);
+                    }
+                    *(u32x4*)d = u32x4{w[0], w[1], w[2], w[3]};
+                    *(u32x4*)(d + 8) = u32x4{w[4], w[5], w[6], w[7]};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (col + e < p.n) d[e] = to_bf16(acc[i][e & 3][e >> 2]);
+                }
+            }
+        } else {
+            // f is a multiple of 32 (of 128 for kGatedQuant): a wavefront's 32 columns exist
+            // or do not exist together
+            const int col = t.n0 + wn * 32 + 8 * q;
+            if (t.n0 + wn * 32 >= p.n) return;
+            const int64_t first = LAYOUT == kMasked ? (int64_t)t.slot * p.m : (int64_t)0;
+            if constexpr (EPI == kGatedGrad) {
+                // dense: rows past the last one, up to a multiple of 64, are written as zeros
+                // (the weight's gradient runs over them), and so are rows that hold no token,
+                // which may read as anything.  Half of the rows' dh at a time: all at once do
+                // not fit the registers beside the accumulators and the next tile's fragments.
+                const int last = LAYOUT == kContiguous ? t.m0 + t.rows : (p.m + 63) & -64;
+                constexpr int PART = TM / 2;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    u32x4 dh[PART];
+#pragma unroll
+                    for (int i = 0; i < PART; ++i) {
+                        dh[i] = u32x4{0u, 0u, 0u, 0u};
+                        if (ok[part * PART + i])
+                            dh[i] = *(const u32x4*)(p.dh + (int64_t)(r0 + part * PART + i) * p.n + col);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < PART; ++i) {
+                        const int a = part * PART + i, r = r0 + a;
+                        u32x4 dg, du;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            float g[2], u[2];
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                const uint32_t w = dh[i][v];
+                                const float x = __builtin_bit_cast(float, n ? w & 0xFFFF0000u : w << 16);
+                                float slope;
+                                const float value = activate<true>(p.act, acc[a][n][v], slope);
+                                g[n] = x * acc[a][2 + n][v] * slope;
+                                u[n] = x * value;
+                            }
+                            dg[v] = ok[a] ? pack_bf16(g[0], g[1]) : 0u;
+                            du[v] = ok[a] ? pack_bf16(u[0], u[1]) : 0u;
+                        }
+                        if (r < last) {
+                            uint16_t* at = (uint16_t*)p.d + (int64_t)r * p.d_ld + col;
+                            *(u32x4*)at = dg;
+                            *(u32x4*)(at + (int64_t)p.n) = du;
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    float h[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float slope;
+                        h[e] = activate<false>(p.act, acc[i][e & 1][e >> 1], slope) *
+                               acc[i][2 + (e & 1)][e >> 1];
+                    }
+                    const int64_t row = first + r0 + i;
+                    if constexpr (EPI == kGated) {
+                        if (ok[i])
+                            *(u32x4*)((uint16_t*)p.d + row * p.d_ld + col) =
+                                u32x4{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]),
+                                      pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7])};
+                    } else {
+                        uint32_t ex;
+                        const uint32_t codes = quantise_row_block(h, ex);
+                        if (ok[i]) {
+                            *(uint32_t*)((uint8_t*)p.d + row * p.d_ld + col / 2) = codes;
+                            if (q == 0) {
+                                const int block = col / 32;
+                                uint8_t* sf = (uint8_t*)p.d2 +
+                                    (((int64_t)t.slot * (p.n / 128) + block / 4) * p.d2_ld + r0 + i) * 4;
+                                sf[block & 3] = (uint8_t)ex;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    };
 
     // Groups of a step; fragments are read AHEAD groups early.  At group LAST the present
     // stage has been read out: the barrier stands there, and from there on, PER a group, go
@@ -370,7 +350,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     constexpr int PER = (COPIES + GROUPS / 2) / (GROUPS / 2 + 1);
     static_assert(PER * (GROUPS - 1) >= COPIES, "a step's copies fit between two barriers");
     clear();
-    if (seek(u)) locate();                     // (no step at all: zero-length buffers)
+    tile_at<BM, COLS, LAYOUT>(p, list, m_tiles, u, nxt);
+    open(nxt, next.s);
+    locate();
 #pragma unroll
     for (int k = 0; k < COPIES; ++k) copy_part(next, 0, k);
     advance();
@@ -391,8 +373,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     }
 
     for (; u < units; u += gridDim.x) {
-        tile_at<BM, BN, LAYOUT, EPI>(p, list, m_tiles, u, cur);
-        for (int c = cur.c0; c < cur.c1; ++c) {
+        tile_at<BM, COLS, LAYOUT>(p, list, m_tiles, u, cur);
+        for (int c = 0; c < p.chunks; ++c) {
             const int other = base ? 0 : STAGE;
             const int keep = 2 * c + 1 < p.kwords ? 255 : 0;
             const Step started = next;                     // its first copies are out
@@ -426,25 +408,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
 #pragma unroll
                     for (int n = 0; n < TN; ++n) fb[0][n] = read_b(other, 0, n);
                 }
-                int ea = 0;
-                if constexpr (FP4) {
-                    const int mask = h ? keep : 255;
-                    ea = (sa[g % 4] >> shift) & mask;
-                    if (i == 0) {
+                const int mask = h ? keep : 255;
+                const int ea = (sa[g % 4] >> shift) & mask;
+                if (i == 0) {
 #pragma unroll
-                        for (int n = 0; n < TN; ++n) eb[n] = (sb[h][n] >> shift) & mask;
-                    }
+                    for (int n = 0; n < TN; ++n) eb[n] = (sb[h][n] >> shift) & mask;
                 }
 #pragma unroll
-                for (int n = 0; n < TN; ++n) {
-                    if constexpr (FP4)
-                        acc[i][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            widen(fb[h][n]), widen(fa[g % 4]), acc[i][n], 4, 4, 0, eb[n], 0, ea);
-                    else
-                        acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, fb[h][n]),
-                            __builtin_bit_cast(bf16x8, fa[g % 4]), acc[i][n], 0, 0, 0);
-                }
+                for (int n = 0; n < TN; ++n)
+                    acc[i][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        widen(fb[h][n]), widen(fa[g % 4]), acc[i][n], 4, 4, 0, eb[n], 0, ea);
                 __builtin_amdgcn_sched_barrier(0);
             }
             base = other;
@@ -460,15 +433,15 @@ struct Shape {
     int bm, bn;
 };
 
-template <int T, int LAYOUT, int EPI>
+template <int LAYOUT, int EPI>
 void pick(bool large, KernelFn* fn, Shape* shape, int* threads, int* per_cu) {
     if (large) {
-        *fn = mx_gemm_kernel<T, 256, 256, 2, 4, LAYOUT, EPI>;
+        *fn = mx_gemm_kernel<256, 256, 2, 4, LAYOUT, EPI>;
         *shape = {256, 256};
         *threads = 512;
         *per_cu = 1;
     } else {
-        *fn = mx_gemm_kernel<T, 128, 128, 2, 2, LAYOUT, EPI>;
+        *fn = mx_gemm_kernel<128, 128, 2, 2, LAYOUT, EPI>;
         *shape = {128, 128};
         *threads = 256;
         *per_cu = 2;
@@ -477,14 +450,14 @@ void pick(bool large, KernelFn* fn, Shape* shape, int* threads, int* per_cu) {
 
 }  // namespace
 
-int launch_gemm(int operand, int layout, int epilogue, const MxParams& params, int groups,
+int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
                 int expected_rows, int num_cus, hipStream_t stream) {
     MxParams p = params;
     KernelFn fn = nullptr;
     Shape s{0, 0};
     int threads = 0, per_cu = 1;
     const int64_t cols = gated(epilogue) ? 2 * (int64_t)p.n : p.n;
-    const int64_t slots = layout == kMasked || layout == kBlocks ? groups : 1;
+    const int64_t slots = layout == kMasked ? groups : 1;
     // tiles that hold rows; a masked slot's row count is spread around the expected one
     auto tiles = [&](int bm, int bn) {
         const double tall = layout == kMasked ? expected_rows / (double)bm + 0.5
@@ -507,7 +480,7 @@ int launch_gemm(int operand, int layout, int epilogue, const MxParams& params, i
     const double small_us = small <= num_cus ? 0.77 * steps + 2
                                              : ceil(small / (2 * num_cus)) * (1.0 * steps + 5);
     const bool large = large_us <= small_us;
-    if (operand == kFp4 && epilogue != kGatedGrad && layout != kContiguous) {
+    if (epilogue != kGatedGrad && layout != kContiguous) {
         double best = large ? large_us : small_us;
         int best_tm = 0, best_tn = 0;
         for (int tm = 4; tm >= 1; tm /= 2) {               // (of equals the tallest: reads B least)
@@ -524,25 +497,19 @@ int launch_gemm(int operand, int layout, int epilogue, const MxParams& params, i
         }
         if (best_tm) return launch_stream(layout, epilogue, best_tm, best_tn, p, groups, expected_rows, stream);
     }
-#define MX_CASE(T, L, E)                                                     \
-    if (operand == T && layout == L && epilogue == E)                        \
-        pick<T, L, E>(large, &fn, &s, &threads, &per_cu);
-    MX_CASE(kFp4, kDense, kStore)
-    MX_CASE(kFp4, kContiguous, kStore)
-    MX_CASE(kFp4, kMasked, kStore)
-    MX_CASE(kFp4, kDense, kGated)
-    MX_CASE(kFp4, kContiguous, kGated)
-    MX_CASE(kFp4, kMasked, kGated)
-    MX_CASE(kFp4, kDense, kGatedQuant)
-    MX_CASE(kFp4, kContiguous, kGatedQuant)
-    MX_CASE(kFp4, kMasked, kGatedQuant)
-    MX_CASE(kFp4, kDense, kGatedGrad)
-    MX_CASE(kFp4, kContiguous, kGatedGrad)
-    MX_CASE(kBf16, kDense, kStore)
-    MX_CASE(kBf16, kDense, kStoreF32)
-    MX_CASE(kBf16, kContiguous, kStore)
-    MX_CASE(kBf16, kBlocks, kStore)
-    MX_CASE(kBf16, kBlocks, kStoreF32)
+#define MX_CASE(L, E) \
+    if (layout == L && epilogue == E) pick<L, E>(large, &fn, &s, &threads, &per_cu);
+    MX_CASE(kDense, kStore)
+    MX_CASE(kContiguous, kStore)
+    MX_CASE(kMasked, kStore)
+    MX_CASE(kDense, kGated)
+    MX_CASE(kContiguous, kGated)
+    MX_CASE(kMasked, kGated)
+    MX_CASE(kDense, kGatedQuant)
+    MX_CASE(kContiguous, kGatedQuant)
+    MX_CASE(kMasked, kGatedQuant)
+    MX_CASE(kDense, kGatedGrad)
+    MX_CASE(kContiguous, kGatedGrad)
 #undef MX_CASE
     if (!fn) return (int)hipErrorInvalidValue;
     const int bn_cols = gated(epilogue) ? s.bn / 2 : s.bn;

@@ -1,0 +1,410 @@
+// fp8bs_mx_grad.hip -- the two products of the gated block's backward pass on gfx950:
+//
+//     da = [dg | du] W        contraction over W's rows (2f), A as it lies
+//     db = [dg | du]^T X      contraction over the tokens, A transposed (a_t)
+//
+// [dg | du] in bf16, W and X in MXFP4 with their 4-bit blocks along the output columns, where
+// no matrix instruction can apply the scales: the values are widened to bf16 (exactly) on
+// their way into LDS, so the second operand is read from memory at 4.25 bits a value and no
+// widened or transposed copy of it exists.  FP32 accumulation, v_mfma_f32_16x16x32_bf16.
+//
+// A step is 64 rows of the contraction.  The second operand (and a transposed A) lies in LDS
+// as [64 rows][columns], and its fragments are read with the transpose load ds_read_b64_tr_b16
+// (lane s of 16 points at 8 bytes of row s / 4, piece s % 4; lane t gets column t of four
+// rows).  The 32-byte units of an LDS row are permuted by a key of the row so that the eight
+// rows a read touches fall into different banks.
+//
+// Widening: a thread loads 16 bytes of codes (one row, one 32-value block) and their exponent
+// a step ahead, turns them into pairs with v_cvt_scalef32_pk_bf16_fp4 and stores the 64 bytes.
+// Tiles, stages, barrier and copy schedule are those of fp8bs_mx_gemm.hip.
+#include <math.h>
+
+#include <type_traits>
+
+#include "fp8bs_mx_tile.h"
+
+namespace fp8bs {
+namespace mx {
+namespace {
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// permutation of a row's 32-byte units, 8 of which span the LDS banks: unit u of row k lies
+// at u ^ unit_key(k) (low three bits), with bit 1 turned by the unit's own bit 3
+__device__ __forceinline__ int unit_key(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+__device__ __forceinline__ int unit_at(int u, int key) {
+    const int high = u >> 3;
+    return high * 8 + ((u & 7) ^ key ^ ((high & 1) << 1));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
+    const int64_t n = bytes < 0 ? 0 : bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)n, 0x00020000);
+}
+
+template <int BM, int BN, int WM, int WN, bool AT, int LAYOUT, int EPI>
+__global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams p) {
+    constexpr int NW = WM * WN, TM = BM / WM / 16, TN = 4;
+    static_assert(BN / WN == 64 && BN / 32 == NW, "one 16-byte piece of codes per thread");
+    constexpr int A_COPIES = BM / 8 / NW;
+    constexpr int B_OFF = BM * 128, STAGE = B_OFF + BN * 128;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+    __shared__ uint32_t list[LAYOUT == kContiguous ? kMaxListed + 1 : 1];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int j = lane & 15, q = lane >> 4;
+
+    int m_tiles = p.m_tiles;
+    if constexpr (LAYOUT == kContiguous) {
+        if (wave == 0) {
+            const int n = list_tiles<BM, LAYOUT>(p, list);
+            if (lane == 0) list[kMaxListed] = (uint32_t)n;
+        }
+        __syncthreads();
+        m_tiles = __builtin_amdgcn_readfirstlane(list[kMaxListed]);
+    }
+    const int units = m_tiles * p.n_tiles * (LAYOUT == kBlocks ? p.num_groups : 1);
+    int u = logical_block();
+    if (u >= units) return;
+
+    // ---- A's copies: rows as in fp8bs_mx_gemm.hip, or 64 rows of BM columns (AT) ----
+    uint32_t a_row_at[A_COPIES];
+    int a_col[A_COPIES];
+#pragma unroll
+    for (int k = 0; k < A_COPIES; ++k) {
+        const int ins = wave * A_COPIES + k;
+        if constexpr (AT) {
+            const int pos = ins * 1024 + 16 * lane, row = pos / (2 * BM), in_row = pos % (2 * BM);
+            // (unit_at is its own inverse)
+            a_col[k] = unit_at(in_row >> 5, unit_key(row)) * 16 + ((in_row >> 4) & 1) * 8;
+            a_row_at[k] = (uint32_t)row * (uint32_t)p.a_row;
+        } else {
+            const int at = ins * 8 + (lane >> 3);
+            const int strip = at / (16 * TM), i = at / 16 % TM, r = at % 16;
+            a_col[k] = 8 * ((lane & 7) ^ (lane >> 3));
+            a_row_at[k] = (uint32_t)(strip * 16 * TM + TM * r + i) * (uint32_t)p.a_row;
+        }
+    }
+    // ---- the second operand: this thread's row and 32-value block of a step ----
+    const int b_row = (int)threadIdx.x / NW, b_block = (int)threadIdx.x % NW;
+    int b_to[2];                               // LDS offsets of its first and last 16 values
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        b_to[h] = B_OFF + b_row * 2 * BN + unit_at(2 * b_block + h, unit_key(b_row)) * 32;
+
+    const uint32_t lds0 = lds_offset(smem);
+    // A step: where its rows start, and this lane's offsets in the operands.
+    struct Step {
+        i32x4 a;
+        uint32_t a_at;                         // scalar offset of A's copies
+        int row0, rows;                        // first row of the contraction, rows that exist
+    };
+    Tile cur, nxt;
+    Step next = {};
+    uint32_t a_off[A_COPIES];
+    uint32_t b_off = 0;                        // byte of the codes within a row
+    int b_word = 0;                            // word row of the exponents
+    int nu = u, nc = 0;
+    int block = 0;                             // kBlocks: the block of step nc (read a step early)
+    auto open = [&] {
+        const int b = nxt.n0 + 32 * b_block < p.n ? b_block : 0;   // (past the last column: unused)
+        b_off = (uint32_t)(nxt.n0 / 2 + 16 * b);
+        b_word = nxt.n0 / 128 + b / 4;
+#pragma unroll
+        for (int k = 0; k < A_COPIES; ++k) {
+            if constexpr (AT)
+                a_off[k] = a_row_at[k] + 2u * (uint32_t)(nxt.m0 + a_col[k] < p.m ? a_col[k] : 0);
+            else
+                a_off[k] = a_row_at[k] + 2u * (uint32_t)a_col[k];
+        }
+    };
+    auto locate = [&] {
+        // (kBlocks: step nc of an expert is half nc % 2 of its 128-token block nc / 2)
+        if constexpr (LAYOUT == kBlocks) {
+            next.row0 = block * 128 + (nc & 1) * 64;
+            block = p.blocks[p.num_groups + 1 + ((nc + 1) >> 1)];      // for the step after
+        } else {
+            next.row0 = nc * 64;
+        }
+        next.rows = p.depth - next.row0;
+        if constexpr (AT) {
+            next.a = descriptor(p.a + (int64_t)next.row0 * p.a_row + 2 * (int64_t)nxt.m0,
+                                64 * p.a_row - 2 * (int64_t)nxt.m0);
+            next.a_at = 0;
+        } else {
+            next.a = descriptor(p.a + (int64_t)nxt.m0 * p.a_row, nxt.rows * p.a_row);
+            next.a_at = (uint32_t)nc * 128u;
+        }
+    };
+    auto seek = [&](int from) {
+        for (nu = from; nu < units; nu += gridDim.x) {
+            tile_at<BM, BN, LAYOUT>(p, list, m_tiles, nu, nxt);
+            if (nxt.c0 < nxt.c1) {
+                open();
+                nc = nxt.c0;
+                if constexpr (LAYOUT == kBlocks) block = p.blocks[p.num_groups + 1 + (nc >> 1)];
+                return true;
+            }
+        }
+        return false;
+    };
+    auto advance = [&] {
+        if (nu >= units || (++nc >= nxt.c1 && !seek(nu + gridDim.x))) return;
+        locate();
+    };
+    auto copy_part = [&](const Step& x, const uint32_t (&off)[A_COPIES], int stage, int k) {
+        copy16(x.a, off[k], x.a_at, lds0 + (uint32_t)(stage * STAGE + (wave * A_COPIES + k) * 1024));
+    };
+    int codes_g = 0;                           // the expert that the loaded codes serve
+    struct Codes {
+        u32x4 w;
+        uint32_t exponents;
+        int expert;                            // kBlocks: of the row; else whether it exists
+    };
+    auto live = [&](const Codes& x) { return LAYOUT == kBlocks ? x.expert == codes_g : x.expert != 0; };
+    // The codes of the next step.  Rows past the contraction's end, and rows that hold no token,
+    // meet rows of zeros in A: whatever they read as, they only have to be finite.
+    auto load_codes = [&](Codes& x) {
+        const int64_t group = AT ? 0 : nxt.g;
+        const int k = min(b_row, next.rows - 1);
+        const auto codes = buffer(p.b + (group * p.depth + next.row0) * p.b_row, 64 * p.b_row);
+        const auto words = buffer(p.sfb + group * p.kwords * p.sfb_ld + next.row0,
+                                  ((int64_t)p.kwords * p.sfb_ld - next.row0) * 4);
+        x.w = __builtin_amdgcn_raw_buffer_load_b128(codes, (uint32_t)k * (uint32_t)p.b_row + b_off, 0, 0);
+        x.exponents = __builtin_amdgcn_raw_buffer_load_b32(
+            words, ((uint32_t)b_word * (uint32_t)p.sfb_ld + (uint32_t)k) * 4u, 0, 0);
+        x.expert = LAYOUT == kBlocks ? p.group_data[next.row0 + k] : b_row < next.rows;
+        codes_g = nxt.g;
+    };
+    const int b_shift = 8 * (b_block & 3);
+    auto scale_of = [&](const Codes& x) {
+        const uint32_t e = (x.exponents >> b_shift) & 255u;
+        // 2^(e - 127): e = 0 is a subnormal, e = 255 not a number
+        const uint32_t bits = e == 0u ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23;
+        return __builtin_bit_cast(float, live(x) ? bits : 0x3F800000u);
+    };
+    // 16 of this thread's 32 values into LDS
+    auto widen_half = [&](const Codes& x, float scale, int stage, auto half_const) {
+        constexpr int HALF = decltype(half_const)::value;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w = x.w[2 * HALF + i];
+            u32x4 v;
+            v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+            v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+            v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+            v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+            *(u32x4*)(smem + stage * STAGE + b_to[HALF] + 16 * i) = v;
+        }
+    };
+    constexpr std::integral_constant<int, 0> kFirst{};
+    constexpr std::integral_constant<int, 1> kSecond{};
+
+    // ---- fragments: 8 values 32 h + 8 q .. + 7 of the contraction ----
+    const int read_key = (j >> 2) | ((q & 1) << 2);        // unit_key of every row a lane points at
+    const int read_row = 8 * q + (j >> 2);
+    int a_rd[AT ? TM : 2], b_rd[TN];
+    if constexpr (AT) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            a_rd[i] = read_row * 2 * BM + unit_at(wm * TM + i, read_key) * 32 + (j & 3) * 8;
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            a_rd[h] = (wm * 16 * TM + j) * 128 + (((4 * h + q) ^ (j & 7)) << 4);
+    }
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+        b_rd[n] = B_OFF + read_row * 2 * BN + unit_at(wn * 4 + n, read_key) * 32 + (j & 3) * 8;
+    auto read_columns = [&](int at, int width) {           // rows at .. at + 3 and at + 4 .. at + 7
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (LDS_AS i16x4*)(LDS_AS void*)(smem + at)));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (LDS_AS i16x4*)(LDS_AS void*)(smem + at + 4 * width)));
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
+    auto read_a = [&](int base, int h, int i) {
+        if constexpr (AT) return read_columns(base + a_rd[i] + h * 64 * BM, 2 * BM);
+        else return *(const u32x4*)(smem + base + a_rd[h] + 2048 * i);
+    };
+    auto read_b = [&](int base, int h, int n) {
+        return read_columns(base + b_rd[n] + h * 64 * BN, 2 * BN);
+    };
+
+    f32x4 acc[TM][TN];
+    auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int n = 0; n < TN; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    // Lane (j, q) holds rows m0 + 16 TM wm + (AT: 16 i + j, else TM j + i) and, in block n,
+    // columns n0 + 64 wn + 16 n + 4 q .. + 3.
+    auto store = [&](const Tile& t) {
+        const int64_t first = LAYOUT == kBlocks ? (int64_t)t.g * p.m : (int64_t)0;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = t.m0 + wm * 16 * TM + (AT ? 16 * i + j : TM * j + i);
+            bool ok = r - t.m0 < t.rows;
+            if constexpr (LAYOUT == kContiguous) ok = ok && p.group_data[r] == t.g;
+            if (!ok) continue;
+#pragma unroll
+            for (int n = 0; n < TN; ++n) {
+                const int col = t.n0 + wn * 64 + 16 * n + 4 * q;   // (k is a multiple of 128)
+                if (col >= p.n) continue;
+                const int64_t at = (first + r) * p.d_ld + col;
+                f32x4 v = acc[i][n];
+                if constexpr (EPI == kStore) {
+                    *(u32x2*)((uint16_t*)p.d + at) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                } else {
+                    float* d = (float*)p.d + at;
+                    if (p.accumulate) v += *(const f32x4*)d;
+                    *(f32x4*)d = v;
+                }
+            }
+        }
+    };
+
+    constexpr int GROUPS = 2 * TM, AHEAD = 3, LAST = GROUPS - AHEAD;
+    constexpr int PER = (A_COPIES + GROUPS / 2) / (GROUPS / 2 + 1);
+    clear();
+    const bool any = seek(u);                  // (no step at all: only zeros to store)
+    Codes codes = {};
+    if (any) {
+        locate();
+        load_codes(codes);
+#pragma unroll
+        for (int k = 0; k < A_COPIES; ++k) copy_part(next, a_off, 0, k);
+        const float scale = scale_of(codes);
+        widen_half(codes, scale, 0, kFirst);
+        widen_half(codes, scale, 0, kSecond);
+        advance();
+        load_codes(codes);
+    }
+    wait_and_meet();
+    float scale = 0.0f;
+    if (any) {
+#pragma unroll
+        for (int k = 0; k < PER * AHEAD && k < A_COPIES; ++k) copy_part(next, a_off, 1, k);
+        scale = scale_of(codes);
+        widen_half(codes, scale, 1, kFirst);
+        widen_half(codes, scale, 1, kSecond);
+    }
+    u32x4 fa[4], fb[2][TN];
+    int base = 0;
+#pragma unroll
+    for (int n = 0; n < TN; ++n) fb[0][n] = read_b(0, 0, n);
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) fa[g] = read_a(0, 0, g);
+
+    for (; u < units; u += gridDim.x) {
+        tile_at<BM, BN, LAYOUT>(p, list, m_tiles, u, cur);
+        for (int c = cur.c0; c < cur.c1; ++c) {
+            const int other = base ? 0 : STAGE;
+            const Step started = next;                     // its first copies are out
+            uint32_t started_off[A_COPIES];
+#pragma unroll
+            for (int k = 0; k < A_COPIES; ++k) started_off[k] = a_off[k];
+            advance();
+            load_codes(codes);
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const int h = g / TM, i = g % TM;
+                if (g == LAST) {
+                    wait_and_meet();
+                    // (the codes have landed with the copies; used any earlier, as the compiler
+                    // would have it, they stalled the step for their latency)
+                    asm volatile("" : "+v"(codes.w), "+v"(codes.exponents), "+v"(codes.expert));
+                }
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    if (g >= LAST) {
+                        if ((g - LAST) * PER + k < A_COPIES)
+                            copy_part(next, a_off, base ? 1 : 0, (g - LAST) * PER + k);
+                    } else if ((g + AHEAD) * PER + k < A_COPIES) {
+                        copy_part(started, started_off, base ? 0 : 1, (g + AHEAD) * PER + k);
+                    }
+                }
+                const int ahead = g + AHEAD;
+                fa[ahead % 4] = ahead < GROUPS ? read_a(base, ahead / TM, ahead % TM)
+                                               : read_a(other, 0, ahead - GROUPS);
+                if (g < TN) fb[1][g] = read_b(base, 1, g);
+                if (g == LAST) {
+#pragma unroll
+                    for (int n = 0; n < TN; ++n) fb[0][n] = read_b(other, 0, n);
+                    scale = scale_of(codes);
+                    widen_half(codes, scale, base ? 1 : 0, kFirst);
+                }
+                if (g == LAST + 1) widen_half(codes, scale, base ? 1 : 0, kSecond);
+#pragma unroll
+                for (int n = 0; n < TN; ++n)
+                    acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, fb[h][n]), __builtin_bit_cast(bf16x8, fa[g % 4]),
+                        acc[i][n], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            base = other;
+        }
+        store(cur);
+        clear();
+    }
+}
+
+typedef void (*KernelFn)(MxParams);
+
+}  // namespace
+
+int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int groups,
+                int num_cus, hipStream_t stream) {
+    MxParams p = params;
+    const int64_t slots = layout == kBlocks ? groups : 1;
+    auto tiles = [&](int b) {
+        return slots * ((p.m + b - 1) / b) * (int64_t)((p.n + b - 1) / b);
+    };
+    // 256x256 tiles, one workgroup per CU, or 128x128, two: the large ones take 1.6 us a step
+    // of 64 rows, the small ones 1.15 (0.9 alone on their CU).
+    const double large_us = ceil((double)tiles(256) / num_cus) * (1.6 * p.chunks + 6);
+    const double small_us = tiles(128) <= num_cus
+                                ? 0.9 * p.chunks + 3
+                                : ceil((double)tiles(128) / (2 * num_cus)) * (1.15 * p.chunks + 6);
+    const bool large = large_us <= small_us;
+    KernelFn fn = nullptr;
+#define MX_CASE(AT, L, E)                                                       \
+    if (a_t == AT && layout == L && epilogue == E)                              \
+        fn = large ? (KernelFn)mx_grad_kernel<256, 256, 2, 4, AT, L, E>         \
+                   : (KernelFn)mx_grad_kernel<128, 128, 2, 2, AT, L, E>;
+    MX_CASE(false, kDense, kStore)
+    MX_CASE(false, kContiguous, kStore)
+    MX_CASE(true, kDense, kStore)
+    MX_CASE(true, kDense, kStoreF32)
+    MX_CASE(true, kBlocks, kStore)
+    MX_CASE(true, kBlocks, kStoreF32)
+#undef MX_CASE
+    if (!fn) return (int)hipErrorInvalidValue;
+    const int side = large ? 256 : 128;
+    p.m_tiles = (p.m + side - 1) / side;
+    p.n_tiles = (p.n + side - 1) / side;
+    p.raster = 8;
+    const bool listed = layout == kContiguous;
+    const int64_t all = listed ? p.m / 128 : slots * p.m_tiles;
+    if (all * p.n_tiles > 0x7fffffff) return (int)hipErrorInvalidValue;
+    // a launch lists at most kMaxListed tiles along M
+    for (int64_t first = 0; first < all; first += kMaxListed) {
+        p.first = (int)first;
+        p.last = (int)(listed && first + kMaxListed < all ? first + kMaxListed : all);
+        int64_t grid = (int64_t)num_cus * (large ? 1 : 2);
+        const int64_t most = (p.last - p.first) * (int64_t)p.n_tiles;
+        if (grid > most) grid = most;
+        void* argv[] = {&p};
+        const hipError_t err = hipLaunchKernel((const void*)fn, dim3((unsigned)grid),
+                                               dim3(large ? 512 : 256), argv, 0, stream);
+        if (err != hipSuccess || !listed) return (int)err;
+    }
+    return (int)hipSuccess;
+}
+
+}  // namespace mx
+}  // namespace fp8bs

@@ -151,49 +151,6 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restri
     }
 }
 
-// Transposed widening.  Workgroup = 64 rows x 128 columns.  Thread t decodes 16 columns
-// (16 * (t % 8) ..) of the rows 2 (t / 8) and 2 (t / 8) + 1 and leaves them in LDS as pairs,
-// [column][row pair] with one word of padding; a column then goes out as one 128-byte line.
-__global__ void __launch_bounds__(256) mx_transpose_kernel(
-    const uint8_t* __restrict__ q, const uint32_t* __restrict__ sf, uint16_t* __restrict__ xt,
-    int rows, int k, int sf_ld, int64_t ld, int row_tiles, const int32_t* __restrict__ layout,
-    int experts) {
-    __shared__ uint32_t tile[128][33];
-    const int c = blockIdx.x % (k / 128);
-    const int rt = blockIdx.x / (k / 128) % row_tiles;
-    const int64_t slot = blockIdx.x / (k / 128) / row_tiles;
-    const int t = threadIdx.x, seg = t & 7, pair = t >> 3;
-    uint16_t v[2][16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = rt * 64 + 2 * pair + h;
-        bool ok = r < rows;
-        if (ok && layout) ok = layout[r] >= 0 && layout[r] < experts;
-        uint32_t lo = 0, hi = 0, word = 0;
-        if (ok) {
-            const uint2 w = *(const uint2*)(q + ((slot * rows + r) * (int64_t)k + 128 * c + 16 * seg) / 2);
-            lo = w.x;
-            hi = w.y;
-            word = sf[(slot * (k / 128) + c) * sf_ld + r];
-        }
-        float s0, s1;
-        scale_factors((word >> (8 * (seg >> 1))) & 255u, s0, s1);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            v[h][e] = to_bf16(code_value(((e < 8 ? lo : hi) >> (4 * (e & 7))) & 15u, s0, s1));
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) tile[16 * seg + e][pair] = v[0][e] | (uint32_t)v[1][e] << 16;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int col = (t >> 3) + 32 * i;
-        const uint32_t* w = &tile[col][4 * seg];
-        *(u32x4*)(xt + (slot * k + 128 * c + col) * ld + rt * 64 + 8 * seg) =
-            u32x4{w[0], w[1], w[2], w[3]};
-    }
-}
-
 // One workgroup; wavefront w takes the experts w, w + 16, ...: it counts their blocks 64 at a
 // time, then writes them in order behind the blocks of the experts before.
 __global__ void __launch_bounds__(1024) mx_block_order_kernel(const int32_t* __restrict__ layout,
@@ -241,18 +198,6 @@ int check(const void* x, int dtype, const void* q, const void* sf, int groups, i
 }
 
 }  // namespace
-
-int launch_transpose(const uint8_t* q, const int32_t* sf, uint16_t* xt, int groups, int rows,
-                     int k, int64_t ld, const int32_t* grouped_layout, int num_experts,
-                     hipStream_t stream) {
-    int sf_ld = (int)fp8bs_get_sfa_ld(rows), rt = (int)(ld / 64);
-    const int64_t grid = (int64_t)groups * rt * (k / 128);
-    if (grid > 0x7fffffff) return (int)hipErrorInvalidValue;
-    if (grid == 0) return (int)hipSuccess;
-    void* args[] = {&q, &sf, &xt, &rows, &k, &sf_ld, &ld, &rt, &grouped_layout, &num_experts};
-    return (int)hipLaunchKernel((const void*)mx_transpose_kernel, dim3((unsigned)grid), dim3(256),
-                                args, 0, stream);
-}
 
 int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups, int32_t* out,
                        hipStream_t stream) {
