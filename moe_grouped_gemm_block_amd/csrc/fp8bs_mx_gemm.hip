@@ -470,10 +470,10 @@ int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
     //   workgroup has a CU for itself.  28 steps, up to 256 tiles: 26 against 43 with 256x256;
     //   256 x 7168 x 2048: 11.5 against 19.6; 2048 x 7168 x 2048: 30 against 26; 16 slots of
     //   up to 256 rows, gated, f = 2048, k = 7168: 95 against 69, of 32 rows: 56 against 70.
-    // - few rows, dense or a few slots: a CU draws 27 GB/s into registers whatever the ring's
-    //   depth, so the bytes of its tiles' rows and columns count.  1 x 4096 x 7168: 6.5
-    //   (16x16) against 26; 64: 12.9 (32x32); 128: 16.6 (64x32); 256: 22 (64x64) against 26;
-    //   256 x 7168 x 2048: 17 against 11.5.
+    // - few rows, dense or a few slots: 1.3 a tile, and its rows' and columns' bytes at the 56
+    //   GB/s that a CU draws.  1 x 4096 x 7168: 5.9 (16x16 tiles) against 25; 48: 8.1 (32x32)
+    //   against 26; 128: 10.5 (64x32) against 26; 256: 13 (64x64) against 29; 512: 23 against
+    //   31; 256 x 7168 x 2048: 12.2 against 11.3; 16 slots of 16 rows: 34 against 32.5.
     const double steps = p.chunks;
     const double big = tiles(256, 256), small = tiles(128, 128);
     const double large_us = ceil(big / num_cus) * (1.4 * steps + 5);
@@ -485,9 +485,8 @@ int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
         int best_tm = 0, best_tn = 0;
         for (int tm = 4; tm >= 1; tm /= 2) {               // (of equals the tallest: reads B least)
             for (int tn = epilogue == kGatedQuant ? 4 : epilogue == kGated ? 2 : 1; tn <= 4; tn *= 2) {
-                const int rows = expected_rows < 16 * tm ? expected_rows : 16 * tm;
                 const double us = ceil(tiles(16 * tm, 16 * tn) / num_cus) *
-                                  (rows + 16 * tn) * (double)p.a_row / 27e3;
+                                  (1.3 + 16 * (tm + tn) * (double)p.a_row * 1.0625 / 56e3);
                 if (us < best) {
                     best = us;
                     best_tm = tm;

@@ -1,39 +1,56 @@
 // fp8bs_mx_stream.hip -- the MXFP4 product and gated block for few rows (single tokens,
-// decode batches, sparsely filled slots) on gfx950.
+// decode batches, a few slots) on gfx950.
 //
-// With few rows the weights' bytes are the work: they are read once, from HBM, and each is
-// used by one 16-row block or a few.  A workgroup takes a small tile (16 TM x 16 TN) and its
-// eight wavefronts share the contraction: wavefront w multiplies the 128-value steps of the
-// w-th eighth of K with operands loaded straight into registers, several steps ahead, so a
-// tile's whole weight strip is in flight at once and the grid has as many workgroups as the
-// columns allow.  The eight FP32 partial tiles meet in LDS and are added in a fixed order --
-// one launch, no workspace, no atomics.
+// With few rows the weights' bytes are the work, and what bounds it is how fast each CU draws
+// its tiles' rows and columns.  A workgroup takes a small tile (16 TM x 16 TN) and its
+// wavefronts share the contraction: each multiplies its own run of 256-value steps, brought
+// into a ring of its own in LDS by direct-to-LDS copies that read whole 128-byte lines (eight
+// rows a copy; fragments loaded straight into registers touch 16 half lines a load and drew
+// 27 GB/s per CU against 45: 128 x 4096 x 7168 took 16.9 us instead of 11).  Nothing is shared
+// until the end, so a wavefront waits for its own copies only; the FP32 partial tiles then
+// meet in LDS and are added in a fixed order -- one launch, no workspace, no atomics.
 //
-// Fragments: lane (j, q) = (l % 16, l / 16) holds the 16 bytes (one scale block) 16 q of row
-// j's step.  B row TN * r + n is row r of block n, so a lane owns 4 TN neighbouring columns;
-// a gated tile has TN / 2 blocks of the gate and as many of the up projection.
-#include "fp8bs_mx.h"
+// Tile row TM * j + i is row j of block i (columns likewise), as in fp8bs_mx_gemm.hip: a lane
+// owns 4 TN neighbouring columns and reads its scale words as vectors.  A gated tile has TN / 2
+// blocks of the gate and as many of the up projection.
+#include <math.h>
+
+#include "fp8bs_mx_tile.h"
 
 namespace fp8bs {
 namespace mx {
 namespace {
 
-constexpr int kWaves = 8;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)n, 0x00020000);
+// 16 bytes per lane from each lane's address to LDS bytes lds + 16 * lane
+__device__ __forceinline__ void copy16_from(const void* at, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(at), "s"(__builtin_amdgcn_readfirstlane(lds)));
+}
+// at most N of this wavefront's copies outstanding
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
 }
 
+template <int TM, int TN>
+struct Ring {
+    static constexpr int kWaves = TM + TN <= 4 ? 8 : 4;
+    static constexpr int kStep = (TM + TN) * 2048 + 1024;      // bytes: rows, then scale words
+    // as deep as 160 KB allow
+    static constexpr int kDepth = TM + TN <= 2 ? 3 : TM + TN <= 4 ? 2 : TM + TN <= 6 ? 3 : 2;
+    static_assert(kWaves * kStep * kDepth <= 160 * 1024, "LDS of a CU");
+};
+
 template <int TM, int TN, int LAYOUT, int EPI>
-__global__ void __launch_bounds__(64 * kWaves, TM + TN <= 5 ? 4 : 2)
-mx_stream_kernel(const MxParams p) {
+__global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kernel(const MxParams p) {
     constexpr bool GATED = gated(EPI);
     constexpr int BM = 16 * TM, COLS = GATED ? 8 * TN : 16 * TN;
-    // steps in flight: about 100 registers of operands (twice as many, with one workgroup per
-    // CU, measured 0-10% slower)
-    constexpr int RING = TM + TN <= 2 ? 8 : TM + TN <= 3 ? 6 : TM + TN <= 4 ? 4 : 3;
-    __shared__ f32x4 part[kWaves][TM * TN][64];
+    constexpr int WAVES = Ring<TM, TN>::kWaves, DEPTH = Ring<TM, TN>::kDepth, STEP = Ring<TM, TN>::kStep;
+    constexpr int HALF = TN / 2 > 0 ? TN / 2 : 1;
+    constexpr int B_OFF = TM * 2048, S_OFF = (TM + TN) * 2048;
+    constexpr int COPIES = 2 * (TM + TN) + 1;                  // of a step
+    constexpr int RING_BYTES = WAVES * STEP * DEPTH, PART_BYTES = WAVES * TM * TN * 1024;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING_BYTES > PART_BYTES ? RING_BYTES : PART_BYTES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, q = lane >> 4;
@@ -49,53 +66,61 @@ mx_stream_kernel(const MxParams p) {
     for (; mt * BM < limit; mt += p.m_tiles) {
         const int m0 = mt * BM, rows = limit - m0, slot = g;
 
-    // ---- operands ----
+    // ---- operands; rows and columns past the last one repeat it (never stored) ----
     const int64_t group = (int64_t)g * (GATED ? 2 * p.n : p.n);
-    const auto a = buffer(p.a + ((int64_t)slot * p.m + m0) * p.a_row, rows * p.a_row);
-    const auto b = buffer(p.b + (group + n0) * p.b_row, (int64_t)(p.n - n0) * p.b_row);
-    const auto up = buffer(p.b + (group + n0 + (GATED ? p.n : 0)) * p.b_row,
-                           (int64_t)(p.n - n0) * p.b_row);
-    const auto sa = buffer(p.sfa + (int64_t)slot * p.kwords * p.sfa_ld + m0,
-                           ((int64_t)p.kwords * p.sfa_ld - m0) * 4);
-    const auto sb = buffer(p.sfb + (int64_t)g * p.kwords * p.sfb_ld + n0,
-                           ((int64_t)p.kwords * p.sfb_ld - n0) * 4);
-    // A row past the last one is the last one again (its results are not stored), a column
-    // past the last one the last column: every read stays inside its operand.
-    uint32_t a_at[TM], b_at[TN], sa_at[TM], sb_at[TN];
+    const i32x4 a = descriptor(p.a + ((int64_t)slot * p.m + m0) * p.a_row, rows * p.a_row);
+    const i32x4 b = descriptor(p.b + (group + n0) * p.b_row, (int64_t)(p.n - n0) * p.b_row);
+    const i32x4 up = GATED ? descriptor(p.b + (group + n0 + p.n) * p.b_row, (int64_t)(p.n - n0) * p.b_row) : b;
+    // copy k of an operand fills LDS rows 8 k .. 8 k + 7: rows 8 (k % 2) .. of block k / 2; the
+    // lane's 16-byte unit is permuted by its row as in fp8bs_mx_gemm.hip
+    const uint32_t unit = (uint32_t)((lane & 7) ^ (lane >> 3));
+    const uint32_t tail_unit = unit >= 4 ? 64u : 0u;           // (see there: half a last step)
+    uint32_t a_at[2 * TM], b_at[2 * TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int r = min(16 * i + j, rows - 1);
-        a_at[i] = (uint32_t)r * (uint32_t)p.a_row + 16u * q;
-        sa_at[i] = 4u * r;
+    for (int k = 0; k < 2 * TM; ++k) {
+        const int r = min(TM * (8 * (k & 1) + (lane >> 3)) + k / 2, rows - 1);
+        a_at[k] = (uint32_t)r * (uint32_t)p.a_row + 16u * unit;
     }
 #pragma unroll
-    for (int n = 0; n < TN; ++n) {
-        constexpr int HALF = TN / 2 > 0 ? TN / 2 : 1;
-        const int r = min(GATED ? HALF * j + n % HALF : TN * j + n, p.n - 1 - n0);
-        b_at[n] = (uint32_t)r * (uint32_t)p.b_row + 16u * q;
-        sb_at[n] = 4u * (uint32_t)(GATED && n >= HALF ? r + p.n : r);
+    for (int k = 0; k < 2 * TN; ++k) {
+        const int n = k / 2, r = 8 * (k & 1) + (lane >> 3);
+        b_at[k] = (uint32_t)min(GATED ? HALF * r + n % HALF : TN * r + n, p.n - 1 - n0) * (uint32_t)p.b_row +
+                  16u * unit;
     }
-    struct Step {
-        i32x4 a[TM], b[TN];
-        int sa[TM], sb[TN];
-    };
-    auto load = [&](int c, Step& s) {
-        const uint32_t at = 64u * (uint32_t)c;
-        const uint32_t sa_row = 4u * (uint32_t)p.sfa_ld * (uint32_t)c;
-        const uint32_t sb_row = 4u * (uint32_t)p.sfb_ld * (uint32_t)c;
-#pragma unroll
-        for (int n = 0; n < TN; ++n)
-            s.b[n] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                GATED && n >= TN / 2 ? up : b, b_at[n], at, 2));      // 2: non-temporal
-#pragma unroll
-        for (int n = 0; n < TN; ++n)
-            s.sb[n] = __builtin_amdgcn_raw_buffer_load_b32(sb, sb_at[n], sb_row, 0);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            s.a[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                a, a_at[i], at, 0));
-            s.sa[i] = __builtin_amdgcn_raw_buffer_load_b32(sa, sa_at[i], sa_row, 0);
+    // scale words: lanes 0 .. 8 TM - 1 bring A's (two word rows of 16 TM), the next 8 TN B's,
+    // the rest repeat the first lane's; four words each
+    const int32_t* s_from;
+    int64_t s_ld;                                              // words from one word row to the next
+    bool s_second;
+    {
+        const bool mine_a = lane < 8 * TM || lane >= 8 * (TM + TN);
+        const int l = lane >= 8 * (TM + TN) ? 0 : mine_a ? lane : lane - 8 * TM;
+        const int per_row = mine_a ? 4 * TM : 4 * TN;          // lanes of a word row
+        s_second = l >= per_row;
+        int w = 4 * (l % per_row);
+        if (mine_a) {
+            s_ld = p.sfa_ld;
+            s_from = p.sfa + (int64_t)slot * p.kwords * p.sfa_ld + min(m0 + w, p.sfa_ld - 4);
+        } else {
+            // a gated tile's words: 8 TN of the gate, then of the up projection
+            if (GATED) w = w < COLS ? n0 + w : p.n + n0 + w - COLS;
+            else w += n0;
+            s_ld = p.sfb_ld;
+            s_from = p.sfb + (int64_t)g * p.kwords * p.sfb_ld + min(w, p.sfb_ld - 4);
         }
+    }
+    const uint32_t lds0 = lds_offset(smem) + (uint32_t)(wave * STEP * DEPTH);
+    auto copy_step = [&](int c, int buf) {
+        const uint32_t to = lds0 + (uint32_t)(buf * STEP), at = 128u * (uint32_t)c;
+        const bool half = 2 * c + 1 >= p.kwords;
+        const uint32_t back = half ? tail_unit : 0u;
+#pragma unroll
+        for (int k = 0; k < 2 * TN; ++k)
+            copy16<true>(GATED && k >= TN ? up : b, b_at[k] - back, at, to + (uint32_t)(B_OFF + k * 1024));
+        copy16_from(s_from + (2 * c + (s_second && !half ? 1 : 0)) * s_ld, to + (uint32_t)S_OFF);
+#pragma unroll
+        for (int k = 0; k < 2 * TM; ++k)
+            copy16(a, a_at[k] - back, at, to + (uint32_t)(k * 1024));
     };
 
     f32x4 acc[TM][TN];
@@ -104,52 +129,73 @@ mx_stream_kernel(const MxParams p) {
 #pragma unroll
         for (int n = 0; n < TN; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int c0 = (int)((int64_t)wave * p.kwords / kWaves);
-    const int c1 = (int)((int64_t)(wave + 1) * p.kwords / kWaves);
-    Step ring[RING];
+    const int c0 = (int)((int64_t)wave * p.chunks / WAVES);
+    const int c1 = (int)((int64_t)(wave + 1) * p.chunks / WAVES);
 #pragma unroll
-    for (int s = 0; s < RING - 1; ++s)
-        if (c0 + s < c1) load(c0 + s, ring[s]);
-    for (int c = c0; c < c1; c += RING) {
+    for (int d = 0; d < DEPTH; ++d)
+        if (c0 + d < c1) copy_step(c0 + d, d);
+    int buf = 0;
+    for (int c = c0; c < c1; ++c) {
+        // the copies of the steps after this one stay in flight
+        const int after = min(c1 - 1 - c, DEPTH - 1);
+        if (after == 0) wait_copies<0>();
+        else if (after == 1) wait_copies<COPIES>();
+        else wait_copies<2 * COPIES>();
+        const uint8_t* st = smem + (wave * DEPTH + buf) * STEP;
+        i32x4 fa[2][TM], fb[2][TN];
+        int ea[2][TM], eb[2][TN];
 #pragma unroll
-        for (int s = 0; s < RING; ++s) {
-            if (c + s < c1) {
-                if (c + s + RING - 1 < c1) load(c + s + RING - 1, ring[(s + RING - 1) % RING]);
-                int ea[TM], eb[TN];
+        for (int h = 0; h < 2; ++h) {
+            const int at = j * 128 + (((4 * h + q) ^ (j & 7)) << 4);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) ea[i] = (ring[s].sa[i] >> (8 * q)) & 255;
+            for (int i = 0; i < TM; ++i) fa[h][i] = *(const i32x4*)(st + at + 2048 * i);
 #pragma unroll
-                for (int n = 0; n < TN; ++n) eb[n] = (ring[s].sb[n] >> (8 * q)) & 255;
+            for (int n = 0; n < TN; ++n) fb[h][n] = *(const i32x4*)(st + B_OFF + at + 2048 * n);
+            const int* sa = (const int*)(st + S_OFF) + h * 16 * TM + TM * j;
+            const int* sb = (const int*)(st + S_OFF) + 32 * TM + h * 16 * TN + (GATED ? HALF * j : TN * j);
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
+            for (int i = 0; i < TM; ++i) ea[h][i] = sa[i];
 #pragma unroll
-                    for (int n = 0; n < TN; ++n) {
-                        const i32x4 x = ring[s].b[n], y = ring[s].a[i];
-                        acc[i][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            i32x8{x[0], x[1], x[2], x[3], 0, 0, 0, 0},
-                            i32x8{y[0], y[1], y[2], y[3], 0, 0, 0, 0}, acc[i][n], 4, 4, 0, eb[n],
-                            0, ea[i]);
-                    }
-            }
+            for (int n = 0; n < TN; ++n) eb[h][n] = sb[GATED ? n % HALF + n / HALF * COLS : n];
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read out before it is refilled
+        if (c + DEPTH < c1) copy_step(c + DEPTH, buf);
+        // (the second round of a row's last step does not exist when K / 128 is odd)
+        const int keep = 2 * c + 1 < p.kwords ? 255 : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    const i32x4 x = fb[h][n], y = fa[h][i];
+                    acc[i][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        i32x8{x[0], x[1], x[2], x[3], 0, 0, 0, 0},
+                        i32x8{y[0], y[1], y[2], y[3], 0, 0, 0, 0}, acc[i][n], 4, 4, 0,
+                        (eb[h][n] >> (8 * q)) & (h ? keep : 255), 0,
+                        (ea[h][i] >> (8 * q)) & (h ? keep : 255));
+                }
+        buf = buf + 1 == DEPTH ? 0 : buf + 1;
     }
 
-    // ---- the eight partial tiles, added in order by the first TM wavefronts ----
+    // ---- the partial tiles, in the rings' place, added in order by the first TM wavefronts ----
+    f32x4* part = (f32x4*)smem;                                // [wave][block][lane]
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int n = 0; n < TN; ++n) part[wave][i * TN + n][lane] = acc[i][n];
+        for (int n = 0; n < TN; ++n) part[(wave * TM * TN + i * TN + n) * 64 + lane] = acc[i][n];
     __syncthreads();
     if (wave < TM) {
     const int i = wave;
     f32x4 sum[TN];
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-        sum[n] = part[0][i * TN + n][lane];
+        sum[n] = part[(i * TN + n) * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum[n] += part[w][i * TN + n][lane];
+        for (int w = 1; w < WAVES; ++w) sum[n] += part[(w * TM * TN + i * TN + n) * 64 + lane];
     }
-    const int r = 16 * i + j;
+    const int r = TM * j + i;
     const bool ok = r < rows;
     const int64_t row = (int64_t)slot * p.m + m0 + r;
     if constexpr (!GATED) {
@@ -175,7 +221,7 @@ mx_stream_kernel(const MxParams p) {
         }
     } else {
         // columns n0 + HALF (4 q + v) + n of the gate (blocks below HALF) and the up projection
-        constexpr int HALF = TN / 2, MINE = 4 * HALF;
+        constexpr int MINE = 4 * HALF;
         const int col = n0 + MINE * q;
         float h[MINE];
 #pragma unroll
@@ -219,9 +265,10 @@ int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& para
                   int expected_rows, hipStream_t stream) {
     MxParams p = params;
     KernelFn fn = nullptr;
+    int threads = 0;
 #define MX_CASE(TM, TN, L, E)                                       \
     if (tm == TM && tn == TN && layout == L && epilogue == E)       \
-        fn = mx_stream_kernel<TM, TN, L, E>;
+        fn = mx_stream_kernel<TM, TN, L, E>, threads = 64 * Ring<TM, TN>::kWaves;
 #define MX_LAYOUTS(TM, TN, E)     \
     MX_CASE(TM, TN, kDense, E)    \
     MX_CASE(TM, TN, kMasked, E)
@@ -245,7 +292,7 @@ int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& para
     const int64_t grid = (int64_t)p.m_tiles * p.n_tiles * (layout == kMasked ? groups : 1);
     if (grid > 0x7fffffff) return (int)hipErrorInvalidValue;
     void* argv[] = {&p};
-    return (int)hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3(64 * kWaves), argv, 0,
+    return (int)hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3(threads), argv, 0,
                                 stream);
 }
 
