@@ -81,35 +81,11 @@ __device__ __forceinline__ uint32_t block_exponent(uint32_t amax_bits) {
     const uint32_t e = amax_bits >> 23;
     return e == 255u ? 255u : e > 2u ? e - 2u : 0u;
 }
-// 2^(127 - e), normal for every finite block's e (at most 252); multiplying by it is exact
-__device__ __forceinline__ float inverse_scale(uint32_t e) {
-    return __builtin_bit_cast(float, (254u - e) << 23);
-}
-
-// Value of code c (0..15) at exponent e, exact in FP32 and in bf16: the smallest magnitude
-// is 0.5 * 2^-127 (a subnormal of both), the largest 6 * 2^127 only reachable by hand-made
-// exponents (infinity then); e = 255 is not a number.
-__device__ __forceinline__ float code_value(uint32_t c, float scale_hi, float scale_lo) {
-    // magnitude as a float: exponent field 126 + (c >> 1 & 3), mantissa bit c & 1; codes 0
-    // and 1 are 0 and 0.5
-    const uint32_t mag = c & 7u;
-    const uint32_t bits = mag < 2u ? (mag ? 0x3F000000u : 0u)
-                                   : ((126u + (mag >> 1)) << 23) | ((mag & 1u) << 22);
-    return __builtin_bit_cast(float, bits | ((c & 8u) << 28)) * scale_hi * scale_lo;
-}
-// 2^(e - 127) as a product of two normal factors, the second a power of two that is exact
-// to multiply by last (one rounding at most, none for values that FP32 holds)
-__device__ __forceinline__ void scale_factors(uint32_t e, float& hi, float& lo) {
-    if (e == 255u) {
-        hi = __builtin_nanf("");
-        lo = 1.0f;
-    } else if (e < 64u) {
-        hi = __builtin_bit_cast(float, (e + 63u) << 23);        // 2^(e - 64)
-        lo = 0x1p-63f;
-    } else {
-        hi = __builtin_bit_cast(float, e << 23);
-        lo = 1.0f;
-    }
+// 2^(e - 127) as the conversion instructions take it: e = 0 is a subnormal, e = 255 not a number
+// (checked on MI355X: v_cvt_scalef32_pk_bf16_fp4 gives the exact value for every code and
+// exponent, in subnormals too, NaN for e = 255).
+__device__ __forceinline__ float scale_value(uint32_t e) {
+    return __builtin_bit_cast(float, e == 0u ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23);
 }
 
 // Activation of the gate and its derivative.  One exponential and one reciprocal each
@@ -146,12 +122,12 @@ __device__ __forceinline__ uint32_t quantise_row_block(const float (&h)[8], uint
     }
     exponent = block_exponent(top);
     if (exponent == 255u) return 0u;
-    const float inv = inverse_scale(exponent);
+    const float scale = scale_value(exponent);
     uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[0] * inv, h[1] * inv, 1.0f, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[2] * inv, h[3] * inv, 1.0f, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[4] * inv, h[5] * inv, 1.0f, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[6] * inv, h[7] * inv, 1.0f, 3);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[0], h[1], scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[2], h[3], scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[4], h[5], scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[6], h[7], scale, 3);
     return c;
 }
 

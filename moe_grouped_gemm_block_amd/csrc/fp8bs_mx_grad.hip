@@ -181,10 +181,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
     };
     const int b_shift = 8 * (b_block & 3);
     auto scale_of = [&](const Codes& x) {
-        const uint32_t e = (x.exponents >> b_shift) & 255u;
-        // 2^(e - 127): e = 0 is a subnormal, e = 255 not a number
-        const uint32_t bits = e == 0u ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23;
-        return __builtin_bit_cast(float, live(x) ? bits : 0x3F800000u);
+        return live(x) ? scale_value((x.exponents >> b_shift) & 255u) : 1.0f;
     };
     // 16 of this thread's 32 values into LDS
     auto widen_half = [&](const Codes& x, float scale, int stage, auto half_const) {

@@ -17,26 +17,57 @@ namespace {
 
 constexpr int kRows = 32, kCols = 256;
 
-// 8 consecutive inputs widened to FP32
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// 8 consecutive inputs as they lie: FP32 (two pieces of 16 bytes) or bf16 (one).  They are
+// read once, past the caches.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
-    if constexpr (BF16) {
-        const u32x4 w = *(const u32x4*)((const uint16_t*)x + at);
+struct Piece {
+    u32x4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void* x, int64_t at) {
+        const u32x4* from = (const u32x4*)((const uint8_t*)x + at * (BF16 ? 2 : 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = from_bf16(w[i] & 0xFFFFu);
-            v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
-        }
-    } else {
-        const f32x4 lo = *(const f32x4*)((const float*)x + at);
-        const f32x4 hi = *(const f32x4*)((const float*)x + at + 4);
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = __builtin_nontemporal_load(from + i);
+    }
+    // FP32 bits of the largest magnitude (bf16: their upper half, compared two at a time)
+    __device__ __forceinline__ uint32_t top() const {
+        if constexpr (BF16) {
+            u16x2 t = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = lo[i];
-            v[4 + i] = hi[i];
+            for (int i = 0; i < 4; ++i)
+                t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, w[0][i] & 0x7FFF7FFFu));
+            return (uint32_t)(t[0] > t[1] ? t[0] : t[1]) << 16;
+        } else {
+            uint32_t t = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = w[i >> 2][i & 3] & 0x7FFFFFFFu;
+                t = b > t ? b : t;
+            }
+            return t;
         }
     }
-}
+    // e2m1 codes of the values divided by scale (a power of two: exact before the rounding)
+    __device__ __forceinline__ uint32_t codes(float scale) const {
+        uint32_t c = 0;
+        if constexpr (BF16) {
+            const bf16x8 x = __builtin_bit_cast(bf16x8, w[0]);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2{x[0], x[1]}, scale, 0);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2{x[2], x[3]}, scale, 1);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2{x[4], x[5]}, scale, 2);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2{x[6], x[7]}, scale, 3);
+        } else {
+            const f32x4 a = __builtin_bit_cast(f32x4, w[0]), b = __builtin_bit_cast(f32x4, w[1]);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[0], a[1], scale, 0);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[2], a[3], scale, 1);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, b[0], b[1], scale, 2);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, b[2], b[3], scale, 3);
+        }
+        return c;
+    }
+};
 
 // Thread t of a workgroup: columns 8 * (t % 32) .. + 7 of rows t / 32 + 8 i.  Four
 // neighbouring lanes hold a 32-value block.
@@ -52,51 +83,31 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(const void* __restrict__ 
     const int t = threadIdx.x, seg = t & 31;
     const int col = ct * kCols + 8 * seg;
     const int64_t row0 = (int64_t)slot * rows;
-    float v[4][8];
+    Piece<BF16> v[4] = {};
     bool in[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = rt * kRows + (t >> 5) + 8 * i;
         in[i] = r < rows && col < k;
-        if (in[i]) load8<BF16>(x, (row0 + r) * k + col, v[i]);
+        if (in[i]) v[i].load(x, (row0 + r) * k + col);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int rr = (t >> 5) + 8 * i;
-        uint32_t top = 0;
-        if (in[i]) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t b = __builtin_bit_cast(uint32_t, v[i][e]) & 0x7FFFFFFFu;
-                top = b > top ? b : top;
-            }
-        }
-#pragma unroll
-        for (int w = 1; w <= 2; w <<= 1) {
-            const uint32_t o = __shfl_xor(top, w, 64);
-            top = o > top ? o : top;
-        }
+        // over the block's four lanes, then the four exponents of a 128-column group into one
+        // word: exchanges within 4 and 16 lanes (quad permutations, row rotations)
+        uint32_t top = v[i].top();
+        top = umax(top, __builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+        top = umax(top, __builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));   // lane ^ 2
         const uint32_t e = block_exponent(top);
-        if (in[i]) {
-            // A block that holds an infinity or a NaN is not a number as a whole (e2m1 has
-            // neither); its codes are zeros.
-            uint32_t codes = 0;
-            if (e != 255u) {
-                const float inv = inverse_scale(e);
-                float s[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) s[c] = v[i][c] * inv;
-                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[0], s[1], 1.0f, 0);
-                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[2], s[3], 1.0f, 1);
-                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[4], s[5], 1.0f, 2);
-                codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, s[6], s[7], 1.0f, 3);
-            }
-            *(uint32_t*)(q + ((row0 + rt * kRows + rr) * k + col) / 2) = codes;
-        }
-        // the four exponents of a 128-column group, one byte each
+        // A block that holds an infinity or a NaN is not a number as a whole (e2m1 has
+        // neither); its codes are zeros.
+        if (in[i])
+            *(uint32_t*)(q + ((row0 + rt * kRows + rr) * k + col) / 2) =
+                e == 255u ? 0u : v[i].codes(scale_value(e));
         uint32_t word = e << (8 * ((seg >> 2) & 3));
-        word |= __shfl_xor(word, 4, 64);
-        word |= __shfl_xor(word, 8, 64);
+        word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x124, 0xF, 0xF, true);   // rotate 4
+        word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x128, 0xF, 0xF, true);   // rotate 8
         if ((seg & 15) == 0) words[seg >> 4][rr] = word;
     }
     __syncthreads();
@@ -136,17 +147,21 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restri
         const int rr = (t >> 5) + 8 * i, r = rt * kRows + rr;
         if (r >= rows || col >= k) continue;
         const uint32_t e = (words[seg >> 4][rr] >> (8 * ((seg >> 2) & 3))) & 255u;
-        float hi, lo, v[8];
-        scale_factors(e, hi, lo);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = code_value((codes[i] >> (4 * c)) & 15u, hi, lo);
+        // bf16 holds every value exactly; FP32 values are those, widened
+        const float scale = scale_value(e);
+        u32x4 w;
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 0));
+        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 1));
+        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 2));
+        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 3));
         const int64_t at = (row0 + r) * k + col;
         if constexpr (BF16) {
-            *(u32x4*)((uint16_t*)x + at) = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            __builtin_nontemporal_store(w, (u32x4*)((uint16_t*)x + at));
         } else {
-            *(f32x4*)((float*)x + at) = f32x4{v[0], v[1], v[2], v[3]};
-            *(f32x4*)((float*)x + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            const u32x4 lo = {w[0] << 16, w[0] & 0xFFFF0000u, w[1] << 16, w[1] & 0xFFFF0000u};
+            const u32x4 hi = {w[2] << 16, w[2] & 0xFFFF0000u, w[3] << 16, w[3] & 0xFFFF0000u};
+            __builtin_nontemporal_store(lo, (u32x4*)((float*)x + at));
+            __builtin_nontemporal_store(hi, (u32x4*)((float*)x + at) + 1);
         }
     }
 }

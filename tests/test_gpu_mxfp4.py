@@ -194,6 +194,30 @@ def test_quantiser_ties_saturation_and_exponents():
     assert np.array_equal(code, want)
 
 
+def test_quantiser_of_every_bf16_value():
+    # each finite bf16 value twice: with nothing larger in its block, and two octaves below
+    # its block's largest
+    bits = np.arange(65536, dtype=np.uint32)
+    x = (bits << 16).view(np.float32)
+    x = x[np.isfinite(x)]
+    own = np.zeros((x.size, 32), np.float32)
+    own[:, 5] = x
+    beside = own.copy()
+    with np.errstate(over="ignore"):
+        big = x * np.float32(4)
+    beside[:, 9] = np.where(np.isfinite(big), big, 0)
+    v = np.concatenate([own, beside])
+    v = np.pad(v, ((0, -len(v) % 8), (0, 0))).reshape(-1, 256)
+    t = torch.from_numpy(v).bfloat16()
+    assert np.array_equal(t.float().numpy(), v)
+    want, want_e = quantise(v.astype(np.float64))
+    for inp in (t, torch.from_numpy(v)):
+        q, sf = fp8bs.quantize_mxfp4(inp.cuda())
+        code, e, _ = unpack(q, sf, len(v))
+        assert np.array_equal(e, want_e)
+        assert np.array_equal(code, want)
+
+
 def test_quantiser_infinities_nans_and_subnormals():
     x = np.random.default_rng(5).standard_normal((6, 256)).astype(np.float32)
     x[0, 3] = np.inf
