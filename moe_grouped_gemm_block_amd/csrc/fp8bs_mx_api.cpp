@@ -182,32 +182,29 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     p.a_row = 4 * (int64_t)f;
     p.n = k;
     p.d_ld = k;
-    if (da && m > 0) {
-        MxParams x = p;
-        x.depth = 2 * f;
-        x.chunks = f / 32;
-        x.d = da;
-        st = status(launch_grad(layout, false, kStore, x, groups, cus, stream));
+    MxParams xa = p, xb = p;
+    xa.depth = 2 * f;
+    xa.chunks = f / 32;
+    xa.d = da;
+    xb.b = (const uint8_t*)a;
+    xb.sfb = sfa;
+    xb.sfb_ld = p.sfa_ld;
+    xb.blocks = order;
+    xb.depth = m;
+    xb.chunks = (m + 63) / 64;
+    xb.m = 2 * f;
+    xb.d = db;
+    xb.accumulate = accumulate;
+    const int layout_b = layout == kContiguous ? kBlocks : kDense, epilogue_b = f32 ? kStoreF32 : kStore;
+    const bool want_da = da && m > 0;
+    if (db && layout == kContiguous) {
+        st = status(launch_block_order(group_data, m / 128, groups, order, stream));
         if (st != FP8BS_OK) return st;
     }
-    if (db) {
-        if (layout == kContiguous) {
-            st = status(launch_block_order(group_data, m / 128, groups, order, stream));
-            if (st != FP8BS_OK) return st;
-        }
-        MxParams x = p;
-        x.b = (const uint8_t*)a;
-        x.sfb = sfa;
-        x.sfb_ld = p.sfa_ld;
-        x.blocks = order;
-        x.depth = m;
-        x.chunks = (m + 63) / 64;
-        x.m = 2 * f;
-        x.d = db;
-        x.accumulate = accumulate;
-        st = status(launch_grad(layout == kContiguous ? kBlocks : kDense, true,
-                                f32 ? kStoreF32 : kStore, x, groups, cus, stream));
-    }
+    if (want_da && db && grad_pair_fits(layout, xa, xb, groups, cus))
+        return status(launch_grad_pair(layout, epilogue_b, xa, xb, groups, stream));
+    if (want_da) st = status(launch_grad(layout, false, kStore, xa, groups, cus, stream));
+    if (st == FP8BS_OK && db) st = status(launch_grad(layout_b, true, epilogue_b, xb, groups, cus, stream));
     return st;
 }
 

@@ -480,11 +480,11 @@ int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
     const double small_us = small <= num_cus ? 0.77 * steps + 2
                                              : ceil(small / (2 * num_cus)) * (1.0 * steps + 5);
     const bool large = large_us <= small_us;
-    if (epilogue != kGatedGrad && layout != kContiguous) {
+    if (layout != kContiguous) {
         double best = large ? large_us : small_us;
         int best_tm = 0, best_tn = 0;
         for (int tm = 4; tm >= 1; tm /= 2) {               // (of equals the tallest: reads B least)
-            for (int tn = epilogue == kGatedQuant ? 4 : epilogue == kGated ? 2 : 1; tn <= 4; tn *= 2) {
+            for (int tn = epilogue == kGatedQuant ? 4 : gated(epilogue) ? 2 : 1; tn <= 4; tn *= 2) {
                 const double us = ceil(tiles(16 * tm, 16 * tn) / num_cus) *
                                   (1.3 + 16 * (tm + tn) * (double)p.a_row * 1.0625 / 56e3);
                 if (us < best) {
@@ -494,7 +494,8 @@ int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
                 }
             }
         }
-        if (best_tm) return launch_stream(layout, epilogue, best_tm, best_tn, p, groups, expected_rows, stream);
+        const int rows = epilogue == kGatedGrad ? (p.m + 63) & -64 : expected_rows;
+        if (best_tm) return launch_stream(layout, epilogue, best_tm, best_tn, p, groups, rows, stream);
     }
 #define MX_CASE(L, E) \
     if (layout == L && epilogue == E) pick<L, E>(large, &fn, &s, &threads, &per_cu);

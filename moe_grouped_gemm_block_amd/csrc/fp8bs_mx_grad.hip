@@ -43,14 +43,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)n, 0x00020000);
 }
 
+// LDS of a workgroup with b x b tiles: two stages of both operands, the list of tiles.
+constexpr int grad_lds(int b, int layout) {
+    return 2 * 2 * b * 128 + (layout == kContiguous ? (kMaxListed + 1) * 4 : 0);
+}
+
+// One workgroup's work, `first` of `grid` persistent ones.
 template <int BM, int BN, int WM, int WN, bool AT, int LAYOUT, int EPI>
-__global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams p) {
+__device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int first, int grid) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = 4;
     static_assert(BN / WN == 64 && BN / 32 == NW, "one 16-byte piece of codes per thread");
     constexpr int A_COPIES = BM / 8 / NW;
     constexpr int B_OFF = BM * 128, STAGE = B_OFF + BN * 128;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
-    __shared__ uint32_t list[LAYOUT == kContiguous ? kMaxListed + 1 : 1];
+    uint32_t* list = (uint32_t*)(smem + 2 * STAGE);            // (contiguous only)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -67,7 +72,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
         m_tiles = __builtin_amdgcn_readfirstlane(list[kMaxListed]);
     }
     const int units = m_tiles * p.n_tiles * (LAYOUT == kBlocks ? p.num_groups : 1);
-    int u = logical_block();
+    int u = first;
     if (u >= units) return;
 
     // ---- A's copies: rows as in fp8bs_mx_gemm.hip, or 64 rows of BM columns (AT) ----
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
         }
     };
     auto seek = [&](int from) {
-        for (nu = from; nu < units; nu += gridDim.x) {
+        for (nu = from; nu < units; nu += grid) {
             tile_at<BM, BN, LAYOUT>(p, list, m_tiles, nu, nxt);
             if (nxt.c0 < nxt.c1) {
                 open();
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
         return false;
     };
     auto advance = [&] {
-        if (nu >= units || (++nc >= nxt.c1 && !seek(nu + gridDim.x))) return;
+        if (nu >= units || (++nc >= nxt.c1 && !seek(nu + grid))) return;
         locate();
     };
     auto copy_part = [&](const Step& x, const uint32_t (&off)[A_COPIES], int stage, int k) {
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
     // Lane (j, q) holds rows m0 + 16 TM wm + (AT: 16 i + j, else TM j + i) and, in block n,
     // columns n0 + 64 wn + 16 n + 4 q .. + 3.
     auto store = [&](const Tile& t) {
-        const int64_t first = LAYOUT == kBlocks ? (int64_t)t.g * p.m : (int64_t)0;
+        const int64_t row0 = LAYOUT == kBlocks ? (int64_t)t.g * p.m : (int64_t)0;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = t.m0 + wm * 16 * TM + (AT ? 16 * i + j : TM * j + i);
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
             for (int n = 0; n < TN; ++n) {
                 const int col = t.n0 + wn * 64 + 16 * n + 4 * q;   // (k is a multiple of 128)
                 if (col >= p.n) continue;
-                const int64_t at = (first + r) * p.d_ld + col;
+                const int64_t at = (row0 + r) * p.d_ld + col;
                 f32x4 v = acc[i][n];
                 if constexpr (EPI == kStore) {
                     *(u32x2*)((uint16_t*)p.d + at) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
 #pragma unroll
     for (int g = 0; g < AHEAD; ++g) fa[g] = read_a(0, 0, g);
 
-    for (; u < units; u += gridDim.x) {
+    for (; u < units; u += grid) {
         tile_at<BM, BN, LAYOUT>(p, list, m_tiles, u, cur);
         for (int c = cur.c0; c < cur.c1; ++c) {
             const int other = base ? 0 : STAGE;
@@ -350,9 +355,63 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
     }
 }
 
+template <int B, int WM, int WN, bool AT, int LAYOUT, int EPI>
+__global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[grad_lds(B, LAYOUT)];
+    grad_units<B, B, WM, WN, AT, LAYOUT, EPI>(p, smem, logical_block(), gridDim.x);
+}
+
+// Both products of a small problem side by side: workgroups below `split` work on da, the
+// others on db.
+template <int LAYOUT, int EPI>
+__global__ void __launch_bounds__(256, 2) mx_grad_pair_kernel(const MxParams a, const MxParams b,
+                                                              int split) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[grad_lds(128, LAYOUT)];
+    const int id = blockIdx.x;
+    if (id < split)
+        grad_units<128, 128, 2, 2, false, LAYOUT, kStore>(a, smem, id, split);
+    else
+        grad_units<128, 128, 2, 2, true, LAYOUT == kContiguous ? kBlocks : kDense, EPI>(
+            b, smem, id - split, gridDim.x - split);
+}
+
 typedef void (*KernelFn)(MxParams);
 
+// 128x128 tiles of a product's grid (an upper bound for the contiguous layout)
+int64_t small_tiles(const MxParams& p, int layout, int groups) {
+    return (layout == kBlocks ? groups : 1) * ((p.m + 127) / 128) * (int64_t)((p.n + 127) / 128);
+}
+void small_grid(MxParams& p, int layout) {
+    p.m_tiles = (p.m + 127) / 128;
+    p.n_tiles = (p.n + 127) / 128;
+    p.raster = 8;
+    p.first = 0;
+    p.last = layout == kContiguous ? p.m / 128 : p.m_tiles;
+}
+
 }  // namespace
+
+bool grad_pair_fits(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus) {
+    return small_tiles(a, layout, groups) +
+               small_tiles(b, layout == kContiguous ? kBlocks : kDense, groups) <= 2 * num_cus &&
+           (layout != kContiguous || a.m / 128 <= kMaxListed);
+}
+
+int launch_grad_pair(int layout, int epilogue, const MxParams& pa, const MxParams& pb, int groups,
+                     hipStream_t stream) {
+    MxParams a = pa, b = pb;
+    small_grid(a, layout);
+    small_grid(b, layout == kContiguous ? kBlocks : kDense);
+    int split = (int)small_tiles(a, layout, groups);
+    const int64_t grid = split + small_tiles(b, layout == kContiguous ? kBlocks : kDense, groups);
+    const void* fn = layout == kContiguous
+        ? (epilogue == kStore ? (const void*)mx_grad_pair_kernel<kContiguous, kStore>
+                              : (const void*)mx_grad_pair_kernel<kContiguous, kStoreF32>)
+        : (epilogue == kStore ? (const void*)mx_grad_pair_kernel<kDense, kStore>
+                              : (const void*)mx_grad_pair_kernel<kDense, kStoreF32>);
+    void* argv[] = {&a, &b, &split};
+    return (int)hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), argv, 0, stream);
+}
 
 int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int groups,
                 int num_cus, hipStream_t stream) {
@@ -371,8 +430,8 @@ int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int 
     KernelFn fn = nullptr;
 #define MX_CASE(AT, L, E)                                                       \
     if (a_t == AT && layout == L && epilogue == E)                              \
-        fn = large ? (KernelFn)mx_grad_kernel<256, 256, 2, 4, AT, L, E>         \
-                   : (KernelFn)mx_grad_kernel<128, 128, 2, 2, AT, L, E>;
+        fn = large ? (KernelFn)mx_grad_kernel<256, 2, 4, AT, L, E>              \
+                   : (KernelFn)mx_grad_kernel<128, 2, 2, AT, L, E>;
     MX_CASE(false, kDense, kStore)
     MX_CASE(false, kContiguous, kStore)
     MX_CASE(true, kDense, kStore)

@@ -61,14 +61,18 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     const int rest = id / p.m_tiles;
     const int n0 = rest % p.n_tiles * COLS;
     const int g = LAYOUT == kMasked ? rest / p.n_tiles : 0;
-    const int limit = LAYOUT == kMasked ? min(p.group_data[g], p.m) : p.m;
+    // (kGatedGrad stores zeros in the rows from m to the next multiple of 64)
+    const int limit = LAYOUT == kMasked ? min(p.group_data[g], p.m)
+                      : EPI == kGatedGrad ? (p.m + 63) & -64 : p.m;
     // (masked: the grid has tiles for the expected rows; a slot with more is walked through)
     for (; mt * BM < limit; mt += p.m_tiles) {
-        const int m0 = mt * BM, rows = limit - m0, slot = g;
+        const int m0 = mt * BM, slot = g;
+        const int from = EPI == kGatedGrad ? min(m0, p.m - 1) : m0;    // first row read
+        const int rows = (EPI == kGatedGrad ? p.m : limit) - from;
 
     // ---- operands; rows and columns past the last one repeat it (never stored) ----
     const int64_t group = (int64_t)g * (GATED ? 2 * p.n : p.n);
-    const i32x4 a = descriptor(p.a + ((int64_t)slot * p.m + m0) * p.a_row, rows * p.a_row);
+    const i32x4 a = descriptor(p.a + ((int64_t)slot * p.m + from) * p.a_row, rows * p.a_row);
     const i32x4 b = descriptor(p.b + (group + n0) * p.b_row, (int64_t)(p.n - n0) * p.b_row);
     const i32x4 up = GATED ? descriptor(p.b + (group + n0 + p.n) * p.b_row, (int64_t)(p.n - n0) * p.b_row) : b;
     // copy k of an operand fills LDS rows 8 k .. 8 k + 7: rows 8 (k % 2) .. of block k / 2; the
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
         for (int w = 1; w < WAVES; ++w) sum[n] += part[(w * TM * TN + i * TN + n) * 64 + lane];
     }
     const int r = TM * j + i;
-    const bool ok = r < rows;
+    const bool ok = EPI == kGatedGrad ? m0 + r < p.m : r < rows;
     const int64_t row = (int64_t)slot * p.m + m0 + r;
     if constexpr (!GATED) {
         // columns n0 + TN (4 q + v) + n: 4 TN neighbours
@@ -223,6 +227,31 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
         // columns n0 + HALF (4 q + v) + n of the gate (blocks below HALF) and the up projection
         constexpr int MINE = 4 * HALF;
         const int col = n0 + MINE * q;
+        if constexpr (EPI == kGatedGrad) {
+            if (m0 + r < limit && col < p.n) {
+                uint32_t dh[MINE / 2] = {}, dg[MINE / 2], du[MINE / 2];
+                if (ok) __builtin_memcpy(dh, p.dh + (int64_t)(m0 + r) * p.n + col, 2 * MINE);
+#pragma unroll
+                for (int e = 0; e < MINE; e += 2) {
+                    float gr[2], ur[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int n = (e + x) % HALF, v = (e + x) / HALF;
+                        const uint32_t w = dh[e / 2];
+                        const float d = __builtin_bit_cast(float, x ? w & 0xFFFF0000u : w << 16);
+                        float slope;
+                        const float value = activate<true>(p.act, sum[n][v], slope);
+                        gr[x] = d * sum[HALF + n][v] * slope;
+                        ur[x] = d * value;
+                    }
+                    dg[e / 2] = ok ? pack_bf16(gr[0], gr[1]) : 0u;
+                    du[e / 2] = ok ? pack_bf16(ur[0], ur[1]) : 0u;
+                }
+                uint16_t* to = (uint16_t*)p.d + (int64_t)(m0 + r) * p.d_ld + col;
+                __builtin_memcpy(to, dg, 2 * MINE);
+                __builtin_memcpy(to + (int64_t)p.n, du, 2 * MINE);
+            }
+        } else {
         float h[MINE];
 #pragma unroll
         for (int e = 0; e < MINE; ++e) {
@@ -250,6 +279,7 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
                     sf[col / 32 & 3] = (uint8_t)ex;
                 }
             }
+        }
         }
     }
     }
@@ -282,6 +312,12 @@ int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& para
     MX_ROWS(2, kGated)
     MX_ROWS(4, kGated)
     MX_ROWS(4, kGatedQuant)
+    MX_CASE(1, 2, kDense, kGatedGrad)
+    MX_CASE(2, 2, kDense, kGatedGrad)
+    MX_CASE(4, 2, kDense, kGatedGrad)
+    MX_CASE(1, 4, kDense, kGatedGrad)
+    MX_CASE(2, 4, kDense, kGatedGrad)
+    MX_CASE(4, 4, kDense, kGatedGrad)
 #undef MX_ROWS
 #undef MX_LAYOUTS
 #undef MX_CASE
