@@ -363,17 +363,37 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     int sa[4], sb[2][TN];                      // scale words as read
     int eb[TN];                                // this round's B exponents
     int base = 0;
+    auto read_first = [&] {                    // the fragments that a step finds read
 #pragma unroll
-    for (int n = 0; n < TN; ++n) fb[0][n] = read_b(0, 0, n);
-    read_sb(0, 0, sb[0]);
+        for (int n = 0; n < TN; ++n) fb[0][n] = read_b(base, 0, n);
+        read_sb(base, 0, sb[0]);
 #pragma unroll
-    for (int g = 0; g < AHEAD; ++g) {
-        fa[g] = read_a(0, 0, g);
-        sa[g] = read_sa(0, 0, g);
-    }
+        for (int g = 0; g < AHEAD; ++g) {
+            fa[g] = read_a(base, 0, g);
+            sa[g] = read_sa(base, 0, g);
+        }
+    };
+    read_first();
 
     for (; u < units; u += gridDim.x) {
         tile_at<BM, COLS, LAYOUT>(p, list, m_tiles, u, cur);
+        // A wavefront whose rows all lie past the tile's last one only copies and meets the
+        // others, which have the matrix cores to themselves (16 slots of up to 256 rows: 3-4%
+        // faster; the dense layout has at most one such row of tiles).
+        if (LAYOUT != kDense && wm * 16 * TM >= cur.rows) {
+            for (int c = 0; c < p.chunks; ++c) {
+                const Step started = next;
+                advance();
+#pragma unroll
+                for (int k = PER * AHEAD; k < COPIES; ++k) copy_part(started, base ? 0 : 1, k);
+                wait_and_meet();
+#pragma unroll
+                for (int k = 0; k < PER * AHEAD && k < COPIES; ++k) copy_part(next, base ? 1 : 0, k);
+                base = base ? 0 : STAGE;
+            }
+            read_first();
+            continue;
+        }
         for (int c = 0; c < p.chunks; ++c) {
             const int other = base ? 0 : STAGE;
             const int keep = 2 * c + 1 < p.kwords ? 255 : 0;

@@ -704,3 +704,144 @@ def test_results_do_not_change_from_call_to_call(m):
     assert all(torch.equal(x, y) for x, y in zip(*runs))
     if m == 0:
         assert (runs[0][3] == 0).all()
+
+
+# ---- every kernel, long lists, long operands ---------------------------------------
+
+# rows and columns at which the few-rows kernel takes each of its tile shapes and the LDS
+# kernel its two, with odd rests in every direction
+@pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 31, 33, 47, 64, 65, 100, 129, 250, 385, 700])
+@pytest.mark.parametrize("n,k", [(31, 128), (130, 640), (1000, 896), (2112, 256), (4097, 384)])
+def test_product_of_every_tile_shape(m, n, k):
+    rng = np.random.default_rng(m * 7 + n)
+    ca, ea, a = matrix(rng, (m, k))
+    cb, eb, b = matrix(rng, (n, k))
+    d = torch.full((m + 1, n), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    fp8bs.fp8bs_dense_nt_mxfp4(*pack(ca, ea, 255), *pack(cb, eb, 255), d[:m])
+    err, want = product_bound(a, b)
+    near(d[:m], want, rounded(want, err), f"{m}x{n}x{k}")
+    assert (d[m] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("max_m,masked,expected", [
+    (40, [40, 3, 0], 4), (90, [90, 1], 16), (300, [300, 0, 150, 17], 20), (64, [64], 64)])
+@pytest.mark.parametrize("n,k", [(100, 384), (320, 1152)])
+def test_slots_with_more_rows_than_expected(max_m, masked, expected, n, k):
+    # the hint only steers the choice of kernel; slots with more rows are walked through
+    rng = np.random.default_rng(max_m + n)
+    g = len(masked)
+    ca, ea, a = matrix(rng, (g, max_m, k))
+    cb, eb, b = matrix(rng, (g, n, k))
+    d = torch.full((g, max_m, n), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    fp8bs.fp8bs_grouped_masked_nt_mxfp4(*pack(ca, ea), *pack(cb, eb), d,
+                                        torch.tensor(masked, dtype=torch.int32, device="cuda"),
+                                        expected_m=expected)
+    for i, c in enumerate(masked):
+        err, want = product_bound(a[i, :c], b[i])
+        near(d[i, :c], want, rounded(want, err), f"slot {i}")
+        assert (d[i, c:] == SENTINEL).all()
+
+
+def _few(rng, total, few):
+    """a packed operand of `total` rows of 128 values, of which only `few` are not zero"""
+    code = np.zeros((len(few), 128), np.uint8)
+    code[:] = rng.integers(0, 16, code.shape)
+    e = rng.integers(120, 130, (len(few), 4)).astype(np.uint8)
+    q, sf = pack(code, e)
+    full_q = torch.zeros(total, 64, dtype=torch.uint8, device="cuda")
+    full_sf = torch.zeros(1, fp8bs.get_sfa_ld(total), dtype=torch.int32, device="cuda")
+    at = torch.tensor(few, device="cuda")
+    full_q[at] = q
+    full_sf[0, at] = sf[0, :len(few)]
+    return full_q, full_sf, values(code, e)
+
+
+def test_more_tiles_than_one_launch_lists():
+    # contiguous: 2050 blocks of 128 rows (a launch lists 2048), runs crossing the limit
+    rng = np.random.default_rng(21)
+    blocks, g, n, f = 2050, 3, 48, 32
+    few = [0, 127, 128, 2047 * 128 + 5, 2048 * 128, 2048 * 128 + 127, 2049 * 128 + 64]
+    a, sfa, va = _few(rng, blocks * 128, few)
+    index = np.full(blocks * 128, -1, np.int32)
+    index[:1000 * 128 + 77] = 0
+    index[1001 * 128:2049 * 128] = 2
+    index[2049 * 128:2049 * 128 + 100] = 1
+    layout = torch.from_numpy(index).cuda()
+    cb, eb, b = matrix(rng, (g, n, 128))
+    d = torch.full((blocks * 128, n), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    fp8bs.fp8bs_grouped_contiguous_nt_mxfp4(a, sfa, *pack(cb, eb), d, layout)
+    want = np.zeros((len(few), n))
+    err = np.zeros_like(want)
+    for i, r in enumerate(few):
+        err[i], want[i] = (x[0] for x in product_bound(va[i:i + 1], b[index[r]]))
+    near(d[torch.tensor(few, device="cuda")], want, rounded(want, err), "rows")
+    valid = layout >= 0
+    assert (d[~valid] == SENTINEL).all()
+    zero = valid.clone()
+    zero[torch.tensor(few, device="cuda")] = False
+    assert (d[zero] == 0).all()
+    # and the backward pass over them
+    cb, eb, b = matrix(rng, (g, 2 * f, 128), 0.1)
+    dh = torch.zeros(blocks * 128, f, dtype=torch.bfloat16, device="cuda")
+    rows = bf16(rng.standard_normal((len(few), f)))
+    dh[torch.tensor(few, device="cuda")] = rows.cuda()
+    da = torch.full((blocks * 128, 128), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    db = torch.full((g, 2 * f, 128), SENTINEL, device="cuda")
+    fp8bs.fp8bs_gated_contiguous_mxfp4_backward(a, sfa, *pack(cb, eb), dh, da, db, layout)
+    for e in range(g):
+        mine = [i for i, r in enumerate(few) if index[r] == e]
+        wa, ba, wb, bb = backward_bounds(va[mine], b[e], f, rows.double().numpy()[mine], "silu")
+        near(da[torch.tensor([few[i] for i in mine], device="cuda")], wa, ba, f"da of expert {e}")
+        near(db[e], wb, bb, f"db of expert {e}")
+    assert (da[zero] == 0).all() and (da[~valid] == SENTINEL).all()
+
+
+def test_more_slots_than_one_launch_lists():
+    g, max_m, n, k = 2100, 130, 16, 128
+    rng = np.random.default_rng(5)
+    code = torch.from_numpy(rng.integers(0, 256, (g, max_m, k // 2)).astype(np.uint8)).cuda()
+    sf = torch.full((g, 1, fp8bs.get_sfa_ld(max_m)), 0x7F7F7F7F, dtype=torch.int32, device="cuda")
+    cb, eb, b = matrix(rng, (g, n, k))
+    masked = rng.integers(0, max_m + 1, g).astype(np.int32)
+    d = torch.full((g, max_m, n), float("inf"), dtype=torch.bfloat16, device="cuda")
+    fp8bs.fp8bs_grouped_masked_nt_mxfp4(code, sf, *pack(cb, eb), d, torch.from_numpy(masked).cuda(),
+                                        expected_m=65)
+    q = code.cpu().numpy()
+    v = E2M1[np.stack((q & 15, q >> 4), -1).reshape(g, max_m, k)]
+    for i in (0, 1, 1023, 1024, 2047, 2048, 2099):
+        c = masked[i]
+        err, want = product_bound(v[i, :c], b[i])
+        near(d[i, :c], want, rounded(want, err), f"slot {i}")
+    rows = torch.arange(max_m, device="cuda")[None] >= torch.from_numpy(masked).cuda()[:, None]
+    assert torch.isinf(d[rows]).all() and torch.isfinite(d[~rows]).all()
+
+
+def test_operands_past_four_gigabytes():
+    # 4.6 GB of codes: the last rows' addresses need more than 32 bits
+    m, n, k = 560_003, 24, 16384
+    rng = np.random.default_rng(2)
+    a = torch.zeros(m, k // 2, dtype=torch.uint8, device="cuda")
+    sfa = torch.zeros(k // 128, fp8bs.get_sfa_ld(m), dtype=torch.int32, device="cuda")
+    tail = 70
+    ca, ea, va = matrix(rng, (tail, k))
+    q, sf = pack(ca, ea)
+    a[m - tail:] = q
+    sfa[:, m - tail:m] = sf[:, :tail]
+    cb, eb, b = matrix(rng, (n, k))
+    d = torch.full((m, n), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    fp8bs.fp8bs_dense_nt_mxfp4(a, sfa, *pack(cb, eb), d)
+    err, want = product_bound(va, b)
+    near(d[m - tail:], want, rounded(want, err), "last rows")
+    assert (d[:m - tail] == 0).all()
+    x = fp8bs.dequantize_mxfp4(a, sfa)                     # 18 GB
+    assert np.array_equal(x[m - tail:].cpu().double().numpy(), va)
+    q2, sf2 = fp8bs.quantize_mxfp4(x)
+    y = fp8bs.dequantize_mxfp4(q2[m - tail:].contiguous(), sf2[:, m - tail:].contiguous()
+                               if tail % 4 == 0 else _last(sf2, m, tail))
+    assert np.array_equal(y.cpu().double().numpy(), va)
+
+
+def _last(sf, m, tail):
+    out = torch.zeros(sf.shape[0], fp8bs.get_sfa_ld(tail), dtype=torch.int32, device="cuda")
+    out[:, :tail] = sf[:, m - tail:m]
+    return out
