@@ -11,8 +11,8 @@
 // A step is 64 rows of the contraction.  The second operand (and a transposed A) lies in LDS
 // as [64 rows][columns], and its fragments are read with the transpose load ds_read_b64_tr_b16
 // (lane s of 16 points at 8 bytes of row s / 4, piece s % 4; lane t gets column t of four
-// rows).  The 32-byte units of an LDS row are permuted by a key of the row so that the eight
-// rows a read touches fall into different banks.
+// rows).  The units of an LDS row are permuted by a key of the row so that what one read or
+// store touches falls into different banks.
 //
 // Widening: a thread loads 16 bytes of codes (one row, one 32-value block) and their exponent
 // a step ahead, turns them into pairs with v_cvt_scalef32_pk_bf16_fp4 and stores the 64 bytes.
@@ -30,12 +30,15 @@ namespace {
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// permutation of a row's 32-byte units, 8 of which span the LDS banks: unit u of row k lies
-// at u ^ unit_key(k) (low three bits), with bit 1 turned by the unit's own bit 3
-__device__ __forceinline__ int unit_key(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
-__device__ __forceinline__ int unit_at(int u, int key) {
-    const int high = u >> 3;
-    return high * 8 + ((u & 7) ^ key ^ ((high & 1) << 1));
+// Permutation of a row's 16-byte units, 16 of which span the LDS banks: unit x of row k lies at
+// x ^ unit_key(k), with bit 0 turned by bit 4 of x.  A transpose read takes 32 lanes at a time:
+// 8 rows (k % 4, and k / 8 even or odd) by two units, 16 places; a store of widened values 16
+// lanes: every fourth unit of two rows, 16 places too (without the turn of bit 0, two lanes to
+// a place: 43% of the LDS's busy cycles were conflicts).
+__device__ __forceinline__ int unit_key(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
+__device__ __forceinline__ int unit_at(int x, int key) {
+    const int high = x >> 4;
+    return high * 16 + ((x & 15) ^ key ^ (high & 1));
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
@@ -84,7 +87,7 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
         if constexpr (AT) {
             const int pos = ins * 1024 + 16 * lane, row = pos / (2 * BM), in_row = pos % (2 * BM);
             // (unit_at is its own inverse)
-            a_col[k] = unit_at(in_row >> 5, unit_key(row)) * 16 + ((in_row >> 4) & 1) * 8;
+            a_col[k] = unit_at(in_row >> 4, unit_key(row)) * 8;
             a_row_at[k] = (uint32_t)row * (uint32_t)p.a_row;
         } else {
             const int at = ins * 8 + (lane >> 3);
@@ -95,10 +98,10 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
     }
     // ---- the second operand: this thread's row and 32-value block of a step ----
     const int b_row = (int)threadIdx.x / NW, b_block = (int)threadIdx.x % NW;
-    int b_to[2];                               // LDS offsets of its first and last 16 values
+    int b_to[4];                               // LDS offsets of its values, eight by eight
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        b_to[h] = B_OFF + b_row * 2 * BN + unit_at(2 * b_block + h, unit_key(b_row)) * 32;
+    for (int h = 0; h < 4; ++h)
+        b_to[h] = B_OFF + b_row * 2 * BN + unit_at(4 * b_block + h, unit_key(b_row)) * 16;
 
     const uint32_t lds0 = lds_offset(smem);
     // A step: where its rows start, and this lane's offsets in the operands.
@@ -199,20 +202,21 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
             v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
             v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
             v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
-            *(u32x4*)(smem + stage * STAGE + b_to[HALF] + 16 * i) = v;
+            *(u32x4*)(smem + stage * STAGE + b_to[2 * HALF + i]) = v;
         }
     };
     constexpr std::integral_constant<int, 0> kFirst{};
     constexpr std::integral_constant<int, 1> kSecond{};
 
     // ---- fragments: 8 values 32 h + 8 q .. + 7 of the contraction ----
-    const int read_key = (j >> 2) | ((q & 1) << 2);        // unit_key of every row a lane points at
+    const int read_key = ((j >> 2) << 1) | ((q & 1) << 3); // unit_key of every row a lane points at
+    const int piece = (j & 3) >> 1;                        // unit of a block's two that it points at
     const int read_row = 8 * q + (j >> 2);
     int a_rd[AT ? TM : 2], b_rd[TN];
     if constexpr (AT) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-            a_rd[i] = read_row * 2 * BM + unit_at(wm * TM + i, read_key) * 32 + (j & 3) * 8;
+            a_rd[i] = read_row * 2 * BM + unit_at(2 * (wm * TM + i) + piece, read_key) * 16 + (j & 1) * 8;
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -220,7 +224,7 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
     }
 #pragma unroll
     for (int n = 0; n < TN; ++n)
-        b_rd[n] = B_OFF + read_row * 2 * BN + unit_at(wn * 4 + n, read_key) * 32 + (j & 3) * 8;
+        b_rd[n] = B_OFF + read_row * 2 * BN + unit_at(2 * (wn * 4 + n) + piece, read_key) * 16 + (j & 1) * 8;
     auto read_columns = [&](int at, int width) {           // rows at .. at + 3 and at + 4 .. at + 7
         const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (LDS_AS i16x4*)(LDS_AS void*)(smem + at)));
