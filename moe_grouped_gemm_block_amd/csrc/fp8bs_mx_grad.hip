@@ -17,6 +17,11 @@
 // Widening: a thread loads 16 bytes of codes (one row, one 32-value block) and their exponent
 // a step ahead, turns them into pairs with v_cvt_scalef32_pk_bf16_fp4 and stores the 64 bytes.
 // Tiles, stages, barrier and copy schedule are those of fp8bs_mx_gemm.hip.
+//
+// Bound by the matrix cores at the clock that power allows (2.1 GHz, busy 40-50% of the time),
+// by the widening (a tenth of a step) and by filling and storing a tile (12 us at 256x256).
+// 8192 rows, f = 2048, k = 7168: da 399 us, db 363 (1.21 and 1.33 PFLOP/s; the matrix cores fed
+// from registers alone, random operands: 2.15).
 #include <math.h>
 
 #include <type_traits>
@@ -256,17 +261,33 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
             const int r = t.m0 + wm * 16 * TM + (AT ? 16 * i + j : TM * j + i);
             bool ok = r - t.m0 < t.rows;
             if constexpr (LAYOUT == kContiguous) ok = ok && p.group_data[r] == t.g;
-            if (!ok) continue;
+            if constexpr (EPI == kStore) {
+                // Lanes q and q + 1 exchange pieces of two blocks, so that a lane holds 16
+                // consecutive bytes and a store writes 64 of every row (with 32 a store, 16384
+                // rows of eight experts took 2200 us instead of 2115, all kernels together).
 #pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                const int col = t.n0 + wn * 64 + 16 * n + 4 * q;   // (k is a multiple of 128)
-                if (col >= p.n) continue;
-                const int64_t at = (row0 + r) * p.d_ld + col;
-                f32x4 v = acc[i][n];
-                if constexpr (EPI == kStore) {
-                    *(u32x2*)((uint16_t*)p.d + at) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                } else {
-                    float* d = (float*)p.d + at;
+                for (int n = 0; n < TN; n += 2) {
+                    u32x4 w;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const f32x4 v = acc[i][n], x = acc[i][n + 1];
+                        const auto both = __builtin_amdgcn_permlane16_swap(
+                            pack_bf16(v[2 * h], v[2 * h + 1]), pack_bf16(x[2 * h], x[2 * h + 1]), false, false);
+                        w[h] = both[0];
+                        w[2 + h] = both[1];
+                    }
+                    const int col = t.n0 + wn * 64 + 16 * (n + (q & 1)) + 8 * (q >> 1);
+                    if (ok && col < p.n)                   // (k is a multiple of 128)
+                        *(u32x4*)((uint16_t*)p.d + (row0 + r) * p.d_ld + col) = w;
+                }
+            } else {
+                if (!ok) continue;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    const int col = t.n0 + wn * 64 + 16 * n + 4 * q;
+                    if (col >= p.n) continue;
+                    float* d = (float*)p.d + (row0 + r) * p.d_ld + col;
+                    f32x4 v = acc[i][n];
                     if (p.accumulate) v += *(const f32x4*)d;
                     *(f32x4*)d = v;
                 }
@@ -424,12 +445,16 @@ int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int 
     auto tiles = [&](int b) {
         return slots * ((p.m + b - 1) / b) * (int64_t)((p.n + b - 1) / b);
     };
-    // 256x256 tiles, one workgroup per CU, or 128x128, two: the large ones take 1.6 us a step
-    // of 64 rows, the small ones 1.15 (0.9 alone on their CU).
-    const double large_us = ceil((double)tiles(256) / num_cus) * (1.6 * p.chunks + 6);
+    // 256x256 tiles, one workgroup per CU: 1.5 us a step of 64 rows and 12 to fill and store.
+    // 128x128, two per CU: 1.0 and 9; 0.9 and 3 while every workgroup has a CU for itself.
+    // Measured, 256x256 against 128x128, 64 steps: 32 large tiles 103 against 60 us, 128: 100
+    // against 72, 256: 109 against 144, 448: 212 against 279, 896: 425 against 497; 32 steps,
+    // 128 tiles: 60 against 42, 224: 61 against 78; 128 steps, 448 tiles: 413 against 515.
+    const double steps = layout == kBlocks ? (double)p.chunks / groups : p.chunks;   // (on average)
+    const double large_us = ceil((double)tiles(256) / num_cus) * (1.5 * steps + 12);
     const double small_us = tiles(128) <= num_cus
-                                ? 0.9 * p.chunks + 3
-                                : ceil((double)tiles(128) / (2 * num_cus)) * (1.15 * p.chunks + 6);
+                                ? 0.9 * steps + 3
+                                : ceil((double)tiles(128) / (2 * num_cus)) * (1.0 * steps + 9);
     const bool large = large_us <= small_us;
     KernelFn fn = nullptr;
 #define MX_CASE(AT, L, E)                                                       \
