@@ -11,6 +11,10 @@ workspace included) and the stream.
 given).  ``dense_nt``, ``grouped_contiguous_nt`` and ``grouped_masked_nt`` are
 the workspace variants.
 
+``mxfp4`` holds the 4-bit operators (quantiser and inverse, products, gated
+feed-forward block with its backward pass, whole layer); its public names are
+re-exported here.
+
 The binding refuses to run without the compiled library; there is no fallback.
 Build it with ``python -m moe_grouped_gemm_block_amd.build``.
 """

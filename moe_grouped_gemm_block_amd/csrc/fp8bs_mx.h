@@ -1,5 +1,6 @@
 // fp8bs_mx.h -- device helpers and host types shared by the MXFP4 translation units
-// (fp8bs_mx_quant.hip, fp8bs_mx_gemm.hip, fp8bs_mx_stream.hip, fp8bs_mx_api.hip).
+// (fp8bs_mx_quant.hip, fp8bs_mx_gemm.hip, fp8bs_mx_stream.hip, fp8bs_mx_grad.hip,
+// fp8bs_mx_api.cpp; fp8bs_mx_tile.h holds what the matrix kernels alone share).
 // Not part of the public interface.
 #pragma once
 #include <hip/hip_runtime.h>

@@ -26,6 +26,13 @@
 // The grid is persistent: workgroup w takes units w, w + grid, ... in an order in which the
 // workgroups of an XCD (dealt round-robin) run neighbouring tiles, and copies the next
 // unit's first steps while it finishes and stores the present one.
+//
+// Bound by the clock that power allows (2.0 GHz; with zero operands everything runs 25%
+// faster) and by the products with their fragment reads: the barrier taken out is worth 2-3%,
+// the copies 2%, the stores 5% (15% with 8 steps a tile), the activation 1%.
+// 4096 x 7168 x 16384: 247 us, 3.9 PFLOP/s (the matrix cores fed from registers alone, random
+// operands: 7.0); gated, 33280 rows of eight experts, f = 2048, k = 7168: 500 us, 3.8;
+// 16 slots of up to 256 rows, 7168 x 2048: 45 us.
 #include <math.h>
 
 #include "fp8bs_mx_tile.h"

@@ -19,9 +19,9 @@
 // Tiles, stages, barrier and copy schedule are those of fp8bs_mx_gemm.hip.
 //
 // Bound by the matrix cores at the clock that power allows (2.1 GHz, busy 40-50% of the time),
-// by the widening (a tenth of a step) and by filling and storing a tile (12 us at 256x256).
-// 8192 rows, f = 2048, k = 7168: da 399 us, db 363 (1.21 and 1.33 PFLOP/s; the matrix cores fed
-// from registers alone, random operands: 2.15).
+// by the widening (a tenth of a step) and by filling and storing a tile (8 us at 256x256).
+// 8192 rows, f = 2048, k = 7168: da 399-445 us, db 363-450, by card (1.1-1.2 and 1.1-1.3
+// PFLOP/s; the matrix cores fed from registers alone, random operands: 2.15).
 #include <math.h>
 
 #include <type_traits>
@@ -445,16 +445,17 @@ int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int 
     auto tiles = [&](int b) {
         return slots * ((p.m + b - 1) / b) * (int64_t)((p.n + b - 1) / b);
     };
-    // 256x256 tiles, one workgroup per CU: 1.5 us a step of 64 rows and 12 to fill and store.
-    // 128x128, two per CU: 1.0 and 9; 0.9 and 3 while every workgroup has a CU for itself.
-    // Measured, 256x256 against 128x128, 64 steps: 32 large tiles 103 against 60 us, 128: 100
-    // against 72, 256: 109 against 144, 448: 212 against 279, 896: 425 against 497; 32 steps,
-    // 128 tiles: 60 against 42, 224: 61 against 78; 128 steps, 448 tiles: 413 against 515.
+    // 256x256 tiles, one workgroup per CU: 1.5 us a step of 64 rows and 8 to fill and store.
+    // 128x128, two per CU: 1.1 and 8; 0.9 and 3 while every workgroup has a CU for itself.
+    // Measured, 256x256 against 128x128 (one of the slower cards), 64 steps: 32 large tiles 98
+    // against 59 us, 128: 107 against 79, 256: 121 against 159, 448: 224 against 301, 896: 438
+    // against 536; 32 steps, 128 tiles: 57 against 46, 224: 57 against 77; 16 steps, 128: 32
+    // against 26; 128 steps, 448: 446 against 597.
     const double steps = layout == kBlocks ? (double)p.chunks / groups : p.chunks;   // (on average)
-    const double large_us = ceil((double)tiles(256) / num_cus) * (1.5 * steps + 12);
+    const double large_us = ceil((double)tiles(256) / num_cus) * (1.5 * steps + 8);
     const double small_us = tiles(128) <= num_cus
                                 ? 0.9 * steps + 3
-                                : ceil((double)tiles(128) / (2 * num_cus)) * (1.0 * steps + 9);
+                                : ceil((double)tiles(128) / (2 * num_cus)) * (1.1 * steps + 8);
     const bool large = large_us <= small_us;
     KernelFn fn = nullptr;
 #define MX_CASE(AT, L, E)                                                       \
