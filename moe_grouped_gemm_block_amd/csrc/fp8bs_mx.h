@@ -28,6 +28,10 @@ constexpr bool gated(int epi) { return epi == kGated || epi == kGatedQuant || ep
 // problems into several launches.
 constexpr int kMaxListed = 2048;
 
+// Largest K and most rows of an operand: copy offsets within a 256-row tile, and row and
+// column numbers of the last, partial tile, are 32-bit.
+constexpr int kMaxK = 1 << 24, kMaxRows = 0x7ffffe00;
+
 struct MxParams {
     const uint8_t* a;           // codes [rows] of a_row bytes; fp8bs_mx_grad.hip: bf16
     const uint8_t* b;           // codes [groups][B rows] of b_row bytes

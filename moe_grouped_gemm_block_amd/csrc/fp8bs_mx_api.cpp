@@ -36,12 +36,10 @@ bool aligned(const void* p, uintptr_t to) { return p && ((uintptr_t)p & (to - 1)
 int check_sizes(int layout, int64_t m, int64_t cols, int k, int groups) {
     if (k < 128 || k % 128 != 0 || m < 0 || cols < 1 || groups < 1) return FP8BS_ERR_SHAPE;
     if (layout == kContiguous && m % 128 != 0) return FP8BS_ERR_SHAPE;
-    // copy offsets within a 256-row tile and exponent words are 32-bit
-    if (k > (1 << 24)) return FP8BS_ERR_SHAPE;
-    const double words = k / 128.0;
+    if (k > kMaxK || m > kMaxRows || cols > kMaxRows) return FP8BS_ERR_SHAPE;
+    const double words = k / 128.0;                // an operand's exponents: 32-bit byte offsets
     if ((m + 3) * words * 4 >= 4294967296.0 || (cols + 3) * words * 4 >= 4294967296.0)
         return FP8BS_ERR_SHAPE;
-    if (m > 0x7ffffe00 || cols > 0x7ffffe00) return FP8BS_ERR_SHAPE;
     return FP8BS_OK;
 }
 

@@ -204,7 +204,8 @@ bool aligned(const void* p, uintptr_t to) { return p && ((uintptr_t)p & (to - 1)
 // Checks shared by both directions; *grid = workgroups.
 int check(const void* x, int dtype, const void* q, const void* sf, int groups, int rows, int k,
           int64_t* grid) {
-    if (k < 128 || k % 128 != 0 || rows < 0 || groups < 1) return FP8BS_ERR_SHAPE;
+    if (k < 128 || k % 128 != 0 || rows < 0 || groups < 1 || k > kMaxK || rows > kMaxRows)
+        return FP8BS_ERR_SHAPE;
     if (dtype != FP8BS_DTYPE_F32 && dtype != FP8BS_DTYPE_BF16) return FP8BS_ERR_UNSUPPORTED;
     if ((double)groups * rows * k >= 9.0e15) return FP8BS_ERR_SHAPE;
     *grid = (int64_t)groups * ((rows + kRows - 1) / kRows) * ((k + kCols - 1) / kCols);

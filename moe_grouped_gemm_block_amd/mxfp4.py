@@ -154,8 +154,8 @@ def _operands(a, sfa, b, sfb, masked, grouped):
     m, n, half = sa[-2], sb[-2], sa[-1]
     if sb[-1] != half:
         raise ValueError("shape mismatch between a and b")
-    if half & 63 or not half:
-        raise FP8BSError(1, "k must be a positive multiple of 128")
+    if half & 63 or not half or half > 1 << 23:
+        raise FP8BSError(1, "k must be a positive multiple of 128, at most 2^24")
     groups = sb[0] if grouped else 1
     words = half // 64
     return (index, pa, _scales(sfa, "sfa", (sa[0] if masked else 1) * words * ((m + 3) & -4), index),
@@ -199,6 +199,8 @@ def _values(x, name):
         _load()
     index = _first(x, name)
     s = x.shape
+    if s and s[-1] > 1 << 24:                  # (longer ones do not all fit the call's int)
+        raise FP8BSError(1, "k must be a positive multiple of 128, at most 2^24")
     if len(s) == 2:
         return index, 1, s[0], s[1]
     if len(s) != 3:

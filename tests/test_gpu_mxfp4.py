@@ -614,6 +614,20 @@ def test_gradient_against_differences():
         assert abs(num - got) <= (bdb * np.abs(db)).sum() + 1e-6 * abs(num)
 
 
+def test_k_past_32_bits_is_refused():
+    # (a call's k is an int: 2^32 + 256 would pass as 256)
+    k = (1 << 32) + 256
+    q = torch.empty(1, k // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.empty(k // 128, 4, dtype=torch.int32, device="cuda")
+    d = torch.full((1, 1), 5.0, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: fp8bs.fp8bs_dense_nt_mxfp4(q, sf, q, sf, d),
+                 lambda: fp8bs.dequantize_mxfp4(q, sf),
+                 lambda: fp8bs.quantize_mxfp4(q.view(torch.bfloat16)[:, :1 << 25])):
+        with pytest.raises(fp8bs.FP8BSError):
+            call()
+    assert d.item() == 5.0
+
+
 # ---- layer, streams, graphs ------------------------------------------------------
 
 @pytest.mark.parametrize("layout", ["dense", "contiguous", "masked"])

@@ -32,6 +32,10 @@ def test_quantiser_refusals(lib, p):
         assert call(p, 1, p, p, 1, -1, 128) == SHAPE
         assert call(p, 1, p, p, 0, 4, 128) == SHAPE
         assert call(p, 1, p, p, 1 << 20, 1 << 20, 1 << 20) == SHAPE
+        # tiles past the last column or row would have numbers past 32 bits
+        assert call(p, 1, p, p, 1, 1, (1 << 31) - 128) == SHAPE
+        assert call(p, 1, p, p, 1, 0, (1 << 24) + 128) == SHAPE
+        assert call(p, 1, p, p, 1, 0x7fffffff, 128) == SHAPE
         assert call(p, 2, p, p, 1, 4, 128) == UNSUPPORTED
         assert call(None, 1, p, p, 1, 4, 128) == POINTER
         assert call(p, 1, p + 4, p, 1, 4, 128) == POINTER
