@@ -167,9 +167,9 @@ int launch_gemm(int layout, int epilogue, const MxParams& p, int groups, int exp
 // D = A^T X, the contraction running over the rows of the second operand.
 int launch_grad(int layout, bool a_t, int epilogue, const MxParams& p, int groups, int num_cus,
                 hipStream_t stream);
-// da (layout dense or contiguous, parameters a) and db (b) in one launch, where every tile of
-// both finds a place at once.
-bool grad_pair_fits(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus);
+// da (layout dense or contiguous, parameters a) and db (b) in one launch, where that takes less
+// time than one after the other.
+bool grad_pair_pays(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus);
 int launch_grad_pair(int layout, int epilogue, const MxParams& a, const MxParams& b, int groups,
                      hipStream_t stream);
 // Few rows, dense and masked layouts: tiles of 16 tm x 16 tn (fp8bs_mx_stream.hip).

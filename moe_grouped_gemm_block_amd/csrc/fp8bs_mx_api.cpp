@@ -199,7 +199,7 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
         st = status(launch_block_order(group_data, m / 128, groups, order, stream));
         if (st != FP8BS_OK) return st;
     }
-    if (want_da && db && grad_pair_fits(layout, xa, xb, groups, cus))
+    if (want_da && db && grad_pair_pays(layout, xa, xb, groups, cus))
         return status(launch_grad_pair(layout, epilogue_b, xa, xb, groups, stream));
     if (want_da) st = status(launch_grad(layout, false, kStore, xa, groups, cus, stream));
     if (st == FP8BS_OK && db) st = status(launch_grad(layout_b, true, epilogue_b, xb, groups, cus, stream));

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams
     grad_units<B, B, WM, WN, AT, LAYOUT, EPI>(p, smem, logical_block(), gridDim.x);
 }
 
-// Both products of a small problem side by side: workgroups below `split` work on da, the
+// Both products of a small or medium problem side by side: workgroups below `split` work on da, the
 // others on db.
 template <int LAYOUT, int EPI>
 __global__ void __launch_bounds__(256, 2) mx_grad_pair_kernel(const MxParams a, const MxParams b,
@@ -414,12 +414,47 @@ void small_grid(MxParams& p, int layout) {
     p.last = layout == kContiguous ? p.m / 128 : p.m_tiles;
 }
 
+// Steps of a tile (kBlocks: of an expert, on average).
+double mean_steps(const MxParams& p, int layout, int groups) {
+    return layout == kBlocks ? (double)p.chunks / groups : p.chunks;
+}
+
+// 256x256 tiles, one workgroup per CU: 1.5 us a step of 64 rows and 8 to fill and store.
+// 128x128, two per CU: 1.1 and 8; 0.9 and 3 while every workgroup has a CU for itself.
+// Measured, 256x256 against 128x128 (one of the slower cards), 64 steps: 32 large tiles 98
+// against 59 us, 128: 107 against 79, 256: 121 against 159, 448: 224 against 301, 896: 438
+// against 536; 32 steps, 128 tiles: 57 against 46, 224: 57 against 77; 16 steps, 128: 32
+// against 26; 128 steps, 448: 446 against 597.
+struct Cost {
+    double large, small;                       // us
+    bool large_pays() const { return large <= small; }
+    double least() const { return large_pays() ? large : small; }
+};
+Cost cost(const MxParams& p, int layout, int groups, int num_cus) {
+    auto tiles = [&](int b) {
+        return (layout == kBlocks ? groups : 1) * ((p.m + b - 1) / b) * (double)((p.n + b - 1) / b);
+    };
+    const double steps = mean_steps(p, layout, groups);
+    return {ceil(tiles(256) / num_cus) * (1.5 * steps + 8),
+            tiles(128) <= num_cus ? 0.9 * steps + 3
+                                  : ceil(tiles(128) / (2 * num_cus)) * (1.1 * steps + 8)};
+}
+
 }  // namespace
 
-bool grad_pair_fits(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus) {
-    return small_tiles(a, layout, groups) +
-               small_tiles(b, layout == kContiguous ? kBlocks : kDense, groups) <= 2 * num_cus &&
-           (layout != kContiguous || a.m / 128 <= kMaxListed);
+// Side by side against one after the other, the whole backward pass: 300 x 704 x 1664 31 against
+// 40 us, 1024 x 2048 x 2048 78 against 102, 2048 x 1024 x 2048 57 against 80, eight experts 2048 x
+// 512 x 1024 38 against 50; 1024 x 2048 x 7168 172 against 164, 4096 x 2048 x 4096 355 against 280.
+bool grad_pair_pays(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus) {
+    const int layout_b = layout == kContiguous ? kBlocks : kDense;
+    const double ta = (double)small_tiles(a, layout, groups), tb = (double)small_tiles(b, layout_b, groups);
+    if (ta + tb > 0x7fffffff || (layout == kContiguous && a.m / 128 > kMaxListed)) return false;
+    const double sa = a.chunks, sb = mean_steps(b, layout_b, groups);
+    // the slots of 2 num_cus workgroups share all steps, but no tile ends before its own
+    const double all = (ta * sa + tb * sb) / (2 * num_cus) * 1.1 + 8 * ceil((ta + tb) / (2 * num_cus));
+    const double longest = (ta + tb <= num_cus ? 0.9 : 1.1) * (sa > sb ? sa : sb) + 8;
+    return (all > longest ? all : longest) <
+           cost(a, layout, groups, num_cus).least() + cost(b, layout_b, groups, num_cus).least() + 3;
 }
 
 int launch_grad_pair(int layout, int epilogue, const MxParams& pa, const MxParams& pb, int groups,
@@ -441,22 +476,8 @@ int launch_grad_pair(int layout, int epilogue, const MxParams& pa, const MxParam
 int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int groups,
                 int num_cus, hipStream_t stream) {
     MxParams p = params;
+    const bool large = cost(p, layout, groups, num_cus).large_pays();
     const int64_t slots = layout == kBlocks ? groups : 1;
-    auto tiles = [&](int b) {
-        return slots * ((p.m + b - 1) / b) * (int64_t)((p.n + b - 1) / b);
-    };
-    // 256x256 tiles, one workgroup per CU: 1.5 us a step of 64 rows and 8 to fill and store.
-    // 128x128, two per CU: 1.1 and 8; 0.9 and 3 while every workgroup has a CU for itself.
-    // Measured, 256x256 against 128x128 (one of the slower cards), 64 steps: 32 large tiles 98
-    // against 59 us, 128: 107 against 79, 256: 121 against 159, 448: 224 against 301, 896: 438
-    // against 536; 32 steps, 128 tiles: 57 against 46, 224: 57 against 77; 16 steps, 128: 32
-    // against 26; 128 steps, 448: 446 against 597.
-    const double steps = layout == kBlocks ? (double)p.chunks / groups : p.chunks;   // (on average)
-    const double large_us = ceil((double)tiles(256) / num_cus) * (1.5 * steps + 8);
-    const double small_us = tiles(128) <= num_cus
-                                ? 0.9 * steps + 3
-                                : ceil((double)tiles(128) / (2 * num_cus)) * (1.1 * steps + 8);
-    const bool large = large_us <= small_us;
     KernelFn fn = nullptr;
 #define MX_CASE(AT, L, E)                                                       \
     if (a_t == AT && layout == L && epilogue == E)                              \

@@ -614,6 +614,27 @@ def test_gradient_against_differences():
         assert abs(num - got) <= (bdb * np.abs(db)).sum() + 1e-6 * abs(num)
 
 
+@pytest.mark.parametrize("layout", ["dense", "contiguous"])
+def test_gradients_together_are_the_gradients_alone(layout):
+    # both in one launch (contiguous: of more 128x128 tiles, 16 x 8 + 16 x 8 for each of five
+    # experts, than run at once) against one after the other: every sum has the same order
+    rng = np.random.default_rng(61)
+    m, f, k, g = 2048, 1024, 1024, 5
+    lead = () if layout == "dense" else (g,)
+    a, b = pack(*matrix(rng, (m, k))[:2]), pack(*matrix(rng, lead + (2 * f, k), 0.1)[:2])
+    dh = bf16(rng.standard_normal((m, f))).cuda()
+    extra = () if layout == "dense" else (
+        torch.arange(m // 128, dtype=torch.int32).mul(7).remainder(g).repeat_interleave(128).cuda(),)
+    call = getattr(fp8bs, f"fp8bs_gated_{layout}_mxfp4_backward")
+    da, da2 = (torch.zeros(m, k, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    db, db2 = (torch.zeros(*lead, 2 * f, k, device="cuda") for _ in range(2))
+    call(*a, *b, dh, da, db, *extra)
+    call(*a, *b, dh, da2, None, *extra)
+    call(*a, *b, dh, None, db2, *extra)
+    assert torch.equal(da, da2) and torch.equal(db, db2)
+    assert bool(da.any(1).all()) and bool(db.any(-1).all())
+
+
 def test_k_past_32_bits_is_refused():
     # (a call's k is an int: 2^32 + 256 would pass as 256)
     k = (1 << 32) + 256
