@@ -56,6 +56,8 @@ struct MxParams {
     int raster;
     int act;
     int accumulate;
+    int splits;                 // fp8bs_mx_grad.hip: parts of the contraction, 1 where whole
+    float* part;                // splits > 1: [splits][rows of d][n]
 };
 
 #ifdef __HIPCC__
@@ -167,10 +169,13 @@ int launch_gemm(int layout, int epilogue, const MxParams& p, int groups, int exp
 // D = A^T X, the contraction running over the rows of the second operand.
 int launch_grad(int layout, bool a_t, int epilogue, const MxParams& p, int groups, int num_cus,
                 hipStream_t stream);
+// Into how many parts the contraction of a product is split (sizes only: the workspace holds
+// the parts).
+int grad_splits(int layout, const MxParams& p, int groups);
 // da (layout dense or contiguous, parameters a) and db (b) in one launch, where that takes less
-// time than one after the other.
+// time than one after the other; either may be null.  Adds the parts of split products.
 bool grad_pair_pays(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus);
-int launch_grad_pair(int layout, int epilogue, const MxParams& a, const MxParams& b, int groups,
+int launch_grad_pair(int layout, int epilogue, const MxParams* a, const MxParams* b, int groups,
                      hipStream_t stream);
 // Few rows, dense and masked layouts: tiles of 16 tm x 16 tn (fp8bs_mx_stream.hip).
 int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& p, int groups,

@@ -118,16 +118,39 @@ int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
                               stream));
 }
 
-// Workspace of the backward pass: dg | du, [rows up to a multiple of 64][2f], and for db of the
-// contiguous layout the blocks by expert.  Both parts start at a multiple of 256 bytes.
+// The backward pass's two products, sizes only: da over W's rows, db over the tokens.
+void gradient_sizes(MxParams& a, MxParams& b, int layout, int64_t m, int f, int k, int groups) {
+    a.m = (int)m;
+    a.depth = 2 * f;
+    a.chunks = f / 32;
+    b.m = 2 * f;
+    b.depth = (int)m;
+    b.chunks = (int)((m + 63) / 64);
+    a.n = b.n = k;
+    a.splits = grad_splits(layout, a, groups);
+    b.splits = grad_splits(layout == kContiguous ? kBlocks : kDense, b, groups);
+}
+
+// Workspace of the backward pass: dg | du, [rows up to a multiple of 64][2f]; for db of the
+// contiguous layout the blocks by expert; the parts of split products.  Each starts at a multiple
+// of 256 bytes.
 struct Parts {
-    int64_t order, total;
+    int64_t order, part_a, part_b, total;
 };
-Parts parts(int layout, int64_t m, int f, int groups, bool want_db) {
+Parts parts(int layout, int64_t m, int f, int k, int groups, bool want_da, bool want_db) {
+    auto whole = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
     Parts w;
-    w.order = ((m + 63) / 64 * 64 * 2 * f * 2 + 255) / 256 * 256;
+    w.order = whole((m + 63) / 64 * 64 * 2 * f * 2);
     // (four entries to spare: the copies look up to two steps past the last block)
     w.total = w.order + (want_db && layout == kContiguous ? (groups + 1 + m / 128 + 4) * 4 : 0);
+    MxParams a, b;
+    memset(&a, 0, sizeof a);
+    memset(&b, 0, sizeof b);
+    gradient_sizes(a, b, layout, m, f, k, groups);
+    w.part_a = w.part_b = whole(w.total);
+    if (want_da && a.splits > 1) w.total = w.part_b = w.part_a + whole(a.splits * m * k * 4);
+    if (want_db && b.splits > 1)
+        w.total = w.part_b + b.splits * (int64_t)(layout == kContiguous ? groups : 1) * 2 * f * k * 4;
     return w;
 }
 
@@ -157,7 +180,7 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     if (m > 0 && (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(dh, 16)))
         return FP8BS_ERR_POINTER;
     if (m == 0 && (!db || accumulate)) return FP8BS_OK;
-    const Parts w = parts(layout, m, f, groups, db != nullptr);
+    const Parts w = parts(layout, m, f, k, groups, da != nullptr, db != nullptr);
     if (w.total > 0 && workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
     if (w.total > 0 && !aligned(workspace, 16)) return FP8BS_ERR_POINTER;
     const int cus = device_cus();
@@ -178,20 +201,17 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     // both products: bf16 dg | du, 4-bit second operand with k columns
     p.a = grad;
     p.a_row = 4 * (int64_t)f;
-    p.n = k;
     p.d_ld = k;
     MxParams xa = p, xb = p;
-    xa.depth = 2 * f;
-    xa.chunks = f / 32;
+    gradient_sizes(xa, xb, layout, m, f, k, groups);
     xa.d = da;
+    xa.part = (float*)(grad + w.part_a);
     xb.b = (const uint8_t*)a;
     xb.sfb = sfa;
     xb.sfb_ld = p.sfa_ld;
     xb.blocks = order;
-    xb.depth = m;
-    xb.chunks = (m + 63) / 64;
-    xb.m = 2 * f;
     xb.d = db;
+    xb.part = (float*)(grad + w.part_b);
     xb.accumulate = accumulate;
     const int layout_b = layout == kContiguous ? kBlocks : kDense, epilogue_b = f32 ? kStoreF32 : kStore;
     const bool want_da = da && m > 0;
@@ -200,9 +220,13 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
         if (st != FP8BS_OK) return st;
     }
     if (want_da && db && grad_pair_pays(layout, xa, xb, groups, cus))
-        return status(launch_grad_pair(layout, epilogue_b, xa, xb, groups, stream));
-    if (want_da) st = status(launch_grad(layout, false, kStore, xa, groups, cus, stream));
-    if (st == FP8BS_OK && db) st = status(launch_grad(layout_b, true, epilogue_b, xb, groups, cus, stream));
+        return status(launch_grad_pair(layout, epilogue_b, &xa, &xb, groups, stream));
+    if (want_da)
+        st = status(xa.splits > 1 ? launch_grad_pair(layout, kStore, &xa, nullptr, groups, stream)
+                                  : launch_grad(layout, false, kStore, xa, groups, cus, stream));
+    if (st == FP8BS_OK && db)
+        st = status(xb.splits > 1 ? launch_grad_pair(layout, epilogue_b, nullptr, &xb, groups, stream)
+                                  : launch_grad(layout_b, true, epilogue_b, xb, groups, cus, stream));
     return st;
 }
 
@@ -357,7 +381,7 @@ int64_t fp8bs_gated_backward_workspace_size(int layout, int64_t m, int f, int k,
     const int st = check_backward(layout, m, f, k, layout == kDense ? 1 : num_groups);
     if (st != FP8BS_OK) return -(int64_t)st;
     if (!want_da && !want_db) return 0;
-    return parts(layout, m, f, layout == kDense ? 1 : num_groups, want_db != 0).total;
+    return parts(layout, m, f, k, layout == kDense ? 1 : num_groups, want_da != 0, want_db != 0).total;
 }
 
 int fp8bs_gated_dense_mxfp4_backward(const void* a, const int32_t* sfa, const void* b,

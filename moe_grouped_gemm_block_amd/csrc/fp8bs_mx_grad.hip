@@ -16,7 +16,9 @@
 //
 // Widening: a thread loads 16 bytes of codes (one row, one 32-value block) and their exponent
 // a step ahead, turns them into pairs with v_cvt_scalef32_pk_bf16_fp4 and stores the 64 bytes.
-// Tiles, stages, barrier and copy schedule are those of fp8bs_mx_gemm.hip.
+// Tiles, stages, barrier and copy schedule are those of fp8bs_mx_gemm.hip.  Problems of few tiles
+// run both products in one launch, and split a long contraction into parts, FP32, that a second
+// launch adds in their order (no atomics; the split depends on sizes only).
 //
 // Bound by the matrix cores at the clock that power allows (2.1 GHz, busy 40-50% of the time),
 // by the widening (a tenth of a step) and by filling and storing a tile (8 us at 256x256).
@@ -57,7 +59,7 @@ constexpr int grad_lds(int b, int layout) {
 }
 
 // One workgroup's work, `first` of `grid` persistent ones.
-template <int BM, int BN, int WM, int WN, bool AT, int LAYOUT, int EPI>
+template <int BM, int BN, int WM, int WN, bool AT, int LAYOUT, int EPI, bool SPLIT>
 __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int first, int grid) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = 4;
     static_assert(BN / WN == 64 && BN / 32 == NW, "one 16-byte piece of codes per thread");
@@ -79,7 +81,18 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
         __syncthreads();
         m_tiles = __builtin_amdgcn_readfirstlane(list[kMaxListed]);
     }
-    const int units = m_tiles * p.n_tiles * (LAYOUT == kBlocks ? p.num_groups : 1);
+    const int splits = SPLIT ? p.splits : 1;
+    const int units = m_tiles * p.n_tiles * (LAYOUT == kBlocks ? p.num_groups : 1) * splits;
+    // unit u: a tile, or part u % splits of its steps (which may be none)
+    auto work_at = [&](int u, Tile& t) {
+        tile_at<BM, BN, LAYOUT>(p, list, m_tiles, SPLIT ? u / splits : u, t);
+        if constexpr (SPLIT) {
+            const int part = u % splits, from = t.c0;
+            const int64_t steps = t.c1 - t.c0;
+            t.c0 = from + (int)(steps * part / splits);
+            t.c1 = from + (int)(steps * (part + 1) / splits);
+        }
+    };
     int u = first;
     if (u >= units) return;
 
@@ -154,7 +167,7 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
     };
     auto seek = [&](int from) {
         for (nu = from; nu < units; nu += grid) {
-            tile_at<BM, BN, LAYOUT>(p, list, m_tiles, nu, nxt);
+            work_at(nu, nxt);
             if (nxt.c0 < nxt.c1) {
                 open();
                 nc = nxt.c0;
@@ -254,14 +267,22 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
     };
     // Lane (j, q) holds rows m0 + 16 TM wm + (AT: 16 i + j, else TM j + i) and, in block n,
     // columns n0 + 64 wn + 16 n + 4 q .. + 3.
-    auto store = [&](const Tile& t) {
+    auto store = [&](const Tile& t, int part) {
         const int64_t row0 = LAYOUT == kBlocks ? (int64_t)t.g * p.m : (int64_t)0;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = t.m0 + wm * 16 * TM + (AT ? 16 * i + j : TM * j + i);
             bool ok = r - t.m0 < t.rows;
             if constexpr (LAYOUT == kContiguous) ok = ok && p.group_data[r] == t.g;
-            if constexpr (EPI == kStore) {
+            if (SPLIT && splits > 1) {
+                if (!ok) continue;
+                const int64_t all = (LAYOUT == kBlocks ? p.num_groups : 1) * (int64_t)p.m;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    const int col = t.n0 + wn * 64 + 16 * n + 4 * q;
+                    if (col < p.n) *(f32x4*)(p.part + (part * all + row0 + r) * p.n + col) = acc[i][n];
+                }
+            } else if constexpr (EPI == kStore) {
                 // Lanes q and q + 1 exchange pieces of two blocks, so that a lane holds 16
                 // consecutive bytes and a store writes 64 of every row (with 32 a store, 16384
                 // rows of eight experts took 2200 us instead of 2115, all kernels together).
@@ -328,7 +349,7 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
     for (int g = 0; g < AHEAD; ++g) fa[g] = read_a(0, 0, g);
 
     for (; u < units; u += grid) {
-        tile_at<BM, BN, LAYOUT>(p, list, m_tiles, u, cur);
+        work_at(u, cur);
         for (int c = cur.c0; c < cur.c1; ++c) {
             const int other = base ? 0 : STAGE;
             const Step started = next;                     // its first copies are out
@@ -375,7 +396,7 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
             }
             base = other;
         }
-        store(cur);
+        store(cur, u % splits);
         clear();
     }
 }
@@ -383,21 +404,47 @@ __device__ __forceinline__ void grad_units(const MxParams& p, uint8_t* smem, int
 template <int B, int WM, int WN, bool AT, int LAYOUT, int EPI>
 __global__ void __launch_bounds__(64 * WM * WN, 2) mx_grad_kernel(const MxParams p) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[grad_lds(B, LAYOUT)];
-    grad_units<B, B, WM, WN, AT, LAYOUT, EPI>(p, smem, logical_block(), gridDim.x);
+    grad_units<B, B, WM, WN, AT, LAYOUT, EPI, false>(p, smem, logical_block(), gridDim.x);
 }
 
 // Both products of a small or medium problem side by side: workgroups below `split` work on da, the
-// others on db.
-template <int LAYOUT, int EPI>
+// others on db.  (Without SPLIT both are whole: the arithmetic of parts costs 0.6 to 2.5 us.)
+template <int LAYOUT, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(256, 2) mx_grad_pair_kernel(const MxParams a, const MxParams b,
                                                               int split) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[grad_lds(128, LAYOUT)];
     const int id = blockIdx.x;
     if (id < split)
-        grad_units<128, 128, 2, 2, false, LAYOUT, kStore>(a, smem, id, split);
+        grad_units<128, 128, 2, 2, false, LAYOUT, kStore, SPLIT>(a, smem, id, split);
     else
-        grad_units<128, 128, 2, 2, true, LAYOUT == kContiguous ? kBlocks : kDense, EPI>(
+        grad_units<128, 128, 2, 2, true, LAYOUT == kContiguous ? kBlocks : kDense, EPI, SPLIT>(
             b, smem, id - split, gridDim.x - split);
+}
+
+// The parts of split products added in their order: four values a thread, the first `split`
+// workgroups those of a (bf16; contiguous: valid rows only), the others b's.
+template <int LAYOUT, int EPI>
+__global__ void __launch_bounds__(256) mx_grad_sum_kernel(const MxParams a, const MxParams b, int split) {
+    const bool first = (int)blockIdx.x < split;
+    const MxParams& p = first ? a : b;
+    const int64_t rows = (!first && LAYOUT == kContiguous ? p.num_groups : 1) * (int64_t)p.m;
+    const int64_t all = rows * p.n;
+    const int64_t at = ((int64_t)(first ? blockIdx.x : blockIdx.x - split) * 256 + threadIdx.x) * 4;
+    if (at >= all) return;
+    if (LAYOUT == kContiguous && first) {
+        const int64_t r = at / p.n;
+        const int e = expert_of(p, (int)(r >> 7));
+        if (e < 0 || p.group_data[r] != e) return;
+    }
+    f32x4 sum = *(const f32x4*)(p.part + at);
+    for (int s = 1; s < p.splits; ++s) sum += *(const f32x4*)(p.part + s * all + at);
+    if (EPI == kStoreF32 && !first) {
+        float* d = (float*)p.d + at;
+        if (p.accumulate) sum += *(const f32x4*)d;
+        *(f32x4*)d = sum;
+    } else {
+        *(u32x2*)((uint16_t*)p.d + at) = u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+    }
 }
 
 typedef void (*KernelFn)(MxParams);
@@ -435,6 +482,7 @@ Cost cost(const MxParams& p, int layout, int groups, int num_cus) {
         return (layout == kBlocks ? groups : 1) * ((p.m + b - 1) / b) * (double)((p.n + b - 1) / b);
     };
     const double steps = mean_steps(p, layout, groups);
+    if (p.splits > 1) return {1e30, 0.9 * steps / p.splits + 3 + 6};
     return {ceil(tiles(256) / num_cus) * (1.5 * steps + 8),
             tiles(128) <= num_cus ? 0.9 * steps + 3
                                   : ceil(tiles(128) / (2 * num_cus)) * (1.1 * steps + 8)};
@@ -442,35 +490,74 @@ Cost cost(const MxParams& p, int layout, int groups, int num_cus) {
 
 }  // namespace
 
+// Few tiles of a long contraction: as many parts as 256 workgroups take, of 8 steps at least,
+// where the steps saved are worth more than the second launch and the parts' bytes.  The whole
+// backward pass with and without: 16384 x 128 x 256 38 against 235 us, 8192 x 512 x 1024 77 against
+// 149, 128 x 4096 x 4096 63 against 175, 64 x 2048 x 2048 24 against 71, 1024 x 128 x 1024 21 against 24.
+int grad_splits(int layout, const MxParams& p, int groups) {
+    const int64_t tiles = small_tiles(p, layout, groups);
+    const double steps = mean_steps(p, layout, groups);
+    if (tiles < 1 || tiles > 128) return 1;
+    int n = (int)(256 / tiles);
+    if (n > steps / 8) n = (int)(steps / 8);
+    return n >= 2 && 0.9 * (steps - steps / n) > 6 + 0.03 * n * tiles ? n : 1;
+}
+
 // Side by side against one after the other, the whole backward pass: 300 x 704 x 1664 31 against
 // 40 us, 1024 x 2048 x 2048 78 against 102, 2048 x 1024 x 2048 57 against 80, eight experts 2048 x
 // 512 x 1024 38 against 50; 1024 x 2048 x 7168 172 against 164, 4096 x 2048 x 4096 355 against 280.
 bool grad_pair_pays(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus) {
     const int layout_b = layout == kContiguous ? kBlocks : kDense;
-    const double ta = (double)small_tiles(a, layout, groups), tb = (double)small_tiles(b, layout_b, groups);
+    const double ta = (double)small_tiles(a, layout, groups) * a.splits;
+    const double tb = (double)small_tiles(b, layout_b, groups) * b.splits;
     if (ta + tb > 0x7fffffff || (layout == kContiguous && a.m / 128 > kMaxListed)) return false;
-    const double sa = a.chunks, sb = mean_steps(b, layout_b, groups);
+    const double sa = (double)a.chunks / a.splits, sb = mean_steps(b, layout_b, groups) / b.splits;
     // the slots of 2 num_cus workgroups share all steps, but no tile ends before its own
     const double all = (ta * sa + tb * sb) / (2 * num_cus) * 1.1 + 8 * ceil((ta + tb) / (2 * num_cus));
-    const double longest = (ta + tb <= num_cus ? 0.9 : 1.1) * (sa > sb ? sa : sb) + 8;
+    const double longest = (ta + tb <= num_cus ? 0.9 : 1.1) * (sa > sb ? sa : sb) + 8 +
+                           (a.splits > 1 || b.splits > 1 ? 6 : 0);
     return (all > longest ? all : longest) <
            cost(a, layout, groups, num_cus).least() + cost(b, layout_b, groups, num_cus).least() + 3;
 }
 
-int launch_grad_pair(int layout, int epilogue, const MxParams& pa, const MxParams& pb, int groups,
+int launch_grad_pair(int layout, int epilogue, const MxParams* pa, const MxParams* pb, int groups,
                      hipStream_t stream) {
-    MxParams a = pa, b = pb;
-    small_grid(a, layout);
-    small_grid(b, layout == kContiguous ? kBlocks : kDense);
-    int split = (int)small_tiles(a, layout, groups);
-    const int64_t grid = split + small_tiles(b, layout == kContiguous ? kBlocks : kDense, groups);
-    const void* fn = layout == kContiguous
-        ? (epilogue == kStore ? (const void*)mx_grad_pair_kernel<kContiguous, kStore>
-                              : (const void*)mx_grad_pair_kernel<kContiguous, kStoreF32>)
-        : (epilogue == kStore ? (const void*)mx_grad_pair_kernel<kDense, kStore>
-                              : (const void*)mx_grad_pair_kernel<kDense, kStoreF32>);
+    const int layout_b = layout == kContiguous ? kBlocks : kDense;
+    MxParams a = {}, b = {};
+    int64_t na = 0, nb = 0, sum_a = 0, sum_b = 0;              // workgroups of both launches
+    if (pa) {
+        a = *pa;
+        small_grid(a, layout);
+        na = small_tiles(a, layout, groups) * a.splits;
+        if (a.splits > 1) sum_a = ((int64_t)a.m * a.n + 1023) / 1024;
+    }
+    if (pb) {
+        b = *pb;
+        small_grid(b, layout_b);
+        nb = small_tiles(b, layout_b, groups) * b.splits;
+        if (b.splits > 1) sum_b = ((layout_b == kBlocks ? groups : 1) * (int64_t)b.m * b.n + 1023) / 1024;
+    }
+    if (na + nb == 0) return (int)hipSuccess;
+    if (na + nb > 0x7fffffff) return (int)hipErrorInvalidValue;
+    const void *fn = nullptr, *add = nullptr;
+#define MX_CASE(L, E)                                                            \
+    if (layout == L && epilogue == E) {                                          \
+        fn = sum_a + sum_b > 0 ? (const void*)mx_grad_pair_kernel<L, E, true>    \
+                               : (const void*)mx_grad_pair_kernel<L, E, false>;  \
+        add = (const void*)mx_grad_sum_kernel<L, E>;                             \
+    }
+    MX_CASE(kDense, kStore)
+    MX_CASE(kDense, kStoreF32)
+    MX_CASE(kContiguous, kStore)
+    MX_CASE(kContiguous, kStoreF32)
+#undef MX_CASE
+    if (!fn) return (int)hipErrorInvalidValue;
+    int split = (int)na;
     void* argv[] = {&a, &b, &split};
-    return (int)hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), argv, 0, stream);
+    const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)(na + nb)), dim3(256), argv, 0, stream);
+    if (err != hipSuccess || sum_a + sum_b == 0) return (int)err;
+    split = (int)sum_a;
+    return (int)hipLaunchKernel(add, dim3((unsigned)(sum_a + sum_b)), dim3(256), argv, 0, stream);
 }
 
 int launch_grad(int layout, bool a_t, int epilogue, const MxParams& params, int groups,

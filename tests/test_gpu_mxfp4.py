@@ -550,6 +550,12 @@ def test_backward_dense(m, f, k, act):
     assert torch.equal(full, start + plain)
 
 
+# few tiles of a long contraction, in parts: db's (tokens), da's (columns of W), both
+@pytest.mark.parametrize("m,f,k", [(2085, 64, 256), (70, 1056, 128), (1300, 704, 128)])
+def test_backward_in_parts(m, f, k):
+    test_backward_dense(m, f, k, "silu")
+
+
 @pytest.mark.parametrize("case", range(len(CONTIGUOUS)))
 @pytest.mark.parametrize("f,k", [(96, 256), (640, 1152)])
 def test_backward_contiguous(case, f, k):
@@ -633,6 +639,30 @@ def test_gradients_together_are_the_gradients_alone(layout):
     call(*a, *b, dh, None, db2, *extra)
     assert torch.equal(da, da2) and torch.equal(db, db2)
     assert bool(da.any(1).all()) and bool(db.any(-1).all())
+
+
+def test_backward_in_parts_contiguous():
+    # experts of 42, 0 and 10 steps in two parts each; the middle one's are both empty
+    rng = np.random.default_rng(62)
+    f, k, g = 64, 256, 3
+    index, runs = contiguous_layout(rng, [(0, 21), (2, 5)], [3, 100])
+    ca, ea, a = matrix(rng, (index.size, k))
+    cb, eb, b = matrix(rng, (g, 2 * f, k), 2.0 / np.sqrt(k))
+    dh = bf16(rng.standard_normal((index.size, f)))
+    dh[torch.from_numpy(index < 0)] = float("nan")
+    start = torch.randn(g, 2 * f, k, device="cuda")
+    gb, plain = start.clone(), torch.empty_like(start)
+    size = fp8bs.gated_backward_workspace_size(fp8bs.LAYOUT_CONTIGUOUS, index.size, f, k, g)
+    ops = pack(ca, ea) + pack(cb, eb) + (dh.cuda(), None)
+    layout = torch.from_numpy(index).cuda()
+    for out, add in ((plain, False), (gb, True)):
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        fp8bs.fp8bs_gated_contiguous_mxfp4_backward(*ops, out, layout, accumulate=add, workspace=ws)
+    for lo, hi, e in runs:
+        _, _, db, bdb = backward_bounds(a[lo:hi], b[e], f, dh[lo:hi].double().numpy(), "silu")
+        near(plain[e], db, bdb, f"db of expert {e}")
+    assert (plain[1] == 0).all()
+    assert torch.equal(gb, start + plain)
 
 
 def test_k_past_32_bits_is_refused():
