@@ -52,6 +52,7 @@ struct MxParams {
     int sfa_ld, sfb_ld;
     int num_groups;
     int m_tiles, n_tiles;       // m_tiles: dense, and per slot for masked
+    int few;                    // masked: slots with at most so many rows are the few-rows kernel's
     int first, last;            // contiguous: blocks, masked: tiles, that this launch covers
     int raster;
     int act;
@@ -163,8 +164,9 @@ __device__ __forceinline__ int logical_block() {
 // order (a block belongs to the expert of its first row).
 int launch_block_order(const int32_t* grouped_layout, int blocks, int num_groups, int32_t* out,
                        hipStream_t stream);
+// (num_cus: under the process's cap, which changes tiles and grids, never results)
 int launch_gemm(int layout, int epilogue, const MxParams& p, int groups, int expected_rows,
-                int num_cus, hipStream_t stream);
+                int num_cus, int device_cus, hipStream_t stream);
 // Products of bf16 rows with widened codes (fp8bs_mx_grad.hip): D = A W, or with a_t
 // D = A^T X, the contraction running over the rows of the second operand.
 int launch_grad(int layout, bool a_t, int epilogue, const MxParams& p, int groups, int num_cus,

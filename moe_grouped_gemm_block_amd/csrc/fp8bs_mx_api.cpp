@@ -15,18 +15,21 @@ using namespace fp8bs::mx;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cus[kMaxDevices];           // 0: not asked yet
 
-// Compute units of the current device under the process's cap; 0 on error.
-int device_cus() {
+// Compute units of the current device (0 on error), and those under the process's cap.
+struct Cus {
+    int device, capped;
+};
+Cus compute_units() {
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (hipGetDevice(&dev) != hipSuccess) return {0, 0};
     int cus = dev >= 0 && dev < kMaxDevices ? g_cus[dev].load(std::memory_order_relaxed) : 0;
     if (cus == 0) {
         if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-            return 0;
+            return {0, 0};
         if (dev >= 0 && dev < kMaxDevices) g_cus[dev].store(cus, std::memory_order_relaxed);
     }
     const int cap = fp8bs_get_num_cus();
-    return cap > 0 && cap < cus ? cap : cus;
+    return {cus, cap > 0 && cap < cus ? cap : cus};
 }
 
 bool aligned(const void* p, uintptr_t to) { return p && ((uintptr_t)p & (to - 1)) == 0; }
@@ -81,14 +84,15 @@ int product(int layout, const void* a, const int32_t* sfa, const void* b, const 
     if (st != FP8BS_OK || m == 0) return st;
     if (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(d, 16))
         return FP8BS_ERR_POINTER;
-    const int cus = device_cus();
-    if (cus <= 0) return FP8BS_ERR_HIP;
+    const Cus cus = compute_units();
+    if (cus.capped <= 0) return FP8BS_ERR_HIP;
     MxParams p = base_params(a, sfa, b, sfb, group_data, m, n, k, groups);
     p.d = d;
     p.d_ld = n;
     p.n = n;
     const int rows = layout == kMasked && expected_m > 0 && expected_m < m ? expected_m : m;
-    return status(launch_gemm(layout, kStore, p, groups, rows, cus, stream));
+    return status(launch_gemm(layout, kStore, p, groups, rows, cus.capped,
+                              cus.device, stream));
 }
 
 int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
@@ -104,8 +108,8 @@ int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
     if (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(h, 16) ||
         (quantise && !aligned(sfh, 16)))
         return FP8BS_ERR_POINTER;
-    const int cus = device_cus();
-    if (cus <= 0) return FP8BS_ERR_HIP;
+    const Cus cus = compute_units();
+    if (cus.capped <= 0) return FP8BS_ERR_HIP;
     MxParams p = base_params(a, sfa, b, sfb, group_data, m, 2 * (int64_t)f, k, groups);
     p.d = h;
     p.d2 = sfh;
@@ -114,8 +118,8 @@ int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
     p.n = f;
     p.act = activation;
     const int rows = layout == kMasked && expected_m > 0 && expected_m < m ? expected_m : m;
-    return status(launch_gemm(layout, quantise ? kGatedQuant : kGated, p, groups, rows, cus,
-                              stream));
+    return status(launch_gemm(layout, quantise ? kGatedQuant : kGated, p, groups, rows,
+                              cus.capped, cus.device, stream));
 }
 
 // The backward pass's two products, sizes only: da over W's rows, db over the tokens.
@@ -183,8 +187,8 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     const Parts w = parts(layout, m, f, k, groups, da != nullptr, db != nullptr);
     if (w.total > 0 && workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
     if (w.total > 0 && !aligned(workspace, 16)) return FP8BS_ERR_POINTER;
-    const int cus = device_cus();
-    if (cus <= 0) return FP8BS_ERR_HIP;
+    const Cus cus = compute_units();
+    if (cus.capped <= 0) return FP8BS_ERR_HIP;
     uint8_t* grad = (uint8_t*)workspace;
     int32_t* order = (int32_t*)(grad + w.order);
 
@@ -195,7 +199,8 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
         p.dh = (const uint16_t*)dh;
         p.d = grad;
         p.d_ld = 2 * (int64_t)f;
-        st = status(launch_gemm(layout, kGatedGrad, p, groups, m, cus, stream));
+        st = status(launch_gemm(layout, kGatedGrad, p, groups, m, cus.capped, cus.device,
+                                stream));
         if (st != FP8BS_OK) return st;
     }
     // both products: bf16 dg | du, 4-bit second operand with k columns
@@ -219,14 +224,14 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
         st = status(launch_block_order(group_data, m / 128, groups, order, stream));
         if (st != FP8BS_OK) return st;
     }
-    if (want_da && db && grad_pair_pays(layout, xa, xb, groups, cus))
+    if (want_da && db && grad_pair_pays(layout, xa, xb, groups, cus.capped))
         return status(launch_grad_pair(layout, epilogue_b, &xa, &xb, groups, stream));
     if (want_da)
         st = status(xa.splits > 1 ? launch_grad_pair(layout, kStore, &xa, nullptr, groups, stream)
-                                  : launch_grad(layout, false, kStore, xa, groups, cus, stream));
+                                  : launch_grad(layout, false, kStore, xa, groups, cus.capped, stream));
     if (st == FP8BS_OK && db)
         st = status(xb.splits > 1 ? launch_grad_pair(layout, epilogue_b, nullptr, &xb, groups, stream)
-                                  : launch_grad(layout_b, true, epilogue_b, xb, groups, cus, stream));
+                                  : launch_grad(layout_b, true, epilogue_b, xb, groups, cus.capped, stream));
     return st;
 }
 

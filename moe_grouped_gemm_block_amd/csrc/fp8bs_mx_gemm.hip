@@ -475,55 +475,109 @@ void pick(bool large, KernelFn* fn, Shape* shape, int* threads, int* per_cu) {
     }
 }
 
+// What each kernel would take for `rows` rows (masked: of every slot) on `cus` CUs, in
+// microseconds; few: the few-rows kernel with its best tile, tm x tn blocks.
+struct Times {
+    double large, small, few;
+    int tm, tn;
+    double tiled() const { return large < small ? large : small; }
+};
+
+// MI355X, weights not in cache:
+// - 256x256 tiles, one workgroup per CU: 1.4 a step of 128 bytes, 5 to fill and store.
+// - 128x128, two per CU: 1.0 a step and 5 to fill and store; 0.77 and 2 while every
+//   workgroup has a CU for itself.  28 steps, up to 256 tiles: 26 against 43 with 256x256;
+//   256 x 7168 x 2048: 11.5 against 19.6; 2048 x 7168 x 2048: 30 against 26; 16 slots of up
+//   to 256 rows, gated, f = 2048, k = 7168, all full: 97 against 73, of 32 rows: 52 against 57.
+// - few rows, dense: 1.3 a tile, and its rows' and columns' bytes at the 56 GB/s that a CU
+//   draws.  1 x 4096 x 7168: 5.9 (16x16 tiles) against 25; 48: 8.1 (32x32) against 26; 128:
+//   10.5 (64x32) against 26; 256: 13 (64x64) against 29; 512: 23 against 31; 256 x 7168 x
+//   2048: 12.2 against 11.3.
+// - slots: tiles follow one another on a CU, which costs the few-rows kernel 3.3 a tile, and
+//   all CUs draw weights at once, 6 TB/s; the others take 1.2 times as long as dense and 2.5.
+//   Few-rows against 128x128 tiles, 16 rows a slot, 7168 x 2048: 2 slots 6 against 12, 4: 11
+//   against 13-16, 8: 21 against 18, 16: 36 against 33, 32: 68 against 61; gated, f = 2048, k =
+//   7168: 2 slots 9 against 33, 8: 26 against 37-46, 16: 48 against 52; 64 rows: 8: 30 against
+//   37-49, 16: 59 against 54; 128 rows: 4: 26 against 36, 8: 51 against 50, 16: 96 against 58.
+// A masked slot's row count is spread around the expected one; exact: all have just `rows`.
+Times times(int layout, int epilogue, const MxParams& p, int groups, int rows, int cus,
+            bool exact = false) {
+    const double cols = gated(epilogue) ? 2.0 * p.n : p.n, slots = layout == kMasked ? groups : 1;
+    auto tiles = [&](int bm, int bn) {                     // tiles that hold rows
+        double tall = ceil(rows / (double)bm);
+        if (layout == kMasked && !exact) {
+            tall = rows / (double)bm + 0.5;
+            const double most = ceil(p.m / (double)bm);
+            tall = tall < 1 ? 1 : tall > most ? most : tall;
+        }
+        return slots * tall * ceil(cols / bn);
+    };
+    const double steps = p.chunks, factor = layout == kMasked ? 1.2 : 1.0;
+    const double start = layout == kMasked ? 2.5 : 0;
+    const double big = tiles(256, 256), small = tiles(128, 128);
+    Times t;
+    t.large = start + factor * ceil(big / cus) * (1.4 * steps + 5);
+    t.small = start + factor * (small <= cus ? 0.77 * steps + 2
+                                             : ceil(small / (2.0 * cus)) * (1.0 * steps + 5));
+    t.few = 1e30;
+    t.tm = t.tn = 0;
+    if (layout == kContiguous) return t;
+    const double row_bytes = (double)p.a_row * 1.0625;     // with its exponents
+    const double weights = layout == kMasked ? slots * cols * row_bytes / 6e6 : 0;
+    for (int tm = 4; tm >= 1; tm /= 2) {                   // (of equals the tallest: reads B least)
+        for (int tn = epilogue == kGatedQuant ? 4 : gated(epilogue) ? 2 : 1; tn <= 4; tn *= 2) {
+            const double tile = (layout == kMasked ? 3.3 : 1.3) + 16 * (tm + tn) * row_bytes / 56e3;
+            const double us = ceil(tiles(16 * tm, 16 * tn) / cus) * tile;
+            if (us < t.few) {
+                t.few = us;
+                t.tm = tm;
+                t.tn = tn;
+            }
+        }
+    }
+    if (t.few < weights) t.few = weights;
+    return t;
+}
+
+// Up to how many rows the few-rows kernel takes: none or all (dense), or those slots that hold
+// no more (masked).  The two kernels add along K in different orders, so this follows from sizes
+// and the device alone: no result depends on the hint or on the cap on CUs, and which slots
+// go where on the counts themselves.  Both are launched where the limit lies between; an empty
+// launch costs 1.6 us.
+int few_rows_limit(int layout, int epilogue, const MxParams& p, int groups, int device_cus) {
+    auto gain = [&](int64_t rows) {
+        const Times t = times(layout, epilogue, p, groups, (int)(rows < p.m ? rows : p.m),
+                              device_cus, true);
+        return t.tiled() - t.few;
+    };
+    if (layout != kMasked) return gain(p.m) > 0 ? p.m : 0;
+    int64_t limit = 0;
+    for (int64_t rows = 16; limit < p.m && gain(rows) > 0; rows *= 2) limit = rows;
+    if (limit >= p.m) return p.m;
+    return limit > 0 && gain(16) > 2 ? (int)limit : 0;
+}
+
 }  // namespace
 
 int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
-                int expected_rows, int num_cus, hipStream_t stream) {
+                int expected_rows, int num_cus, int device_cus, hipStream_t stream) {
     MxParams p = params;
+    const int64_t slots = layout == kMasked ? groups : 1;
+    p.few = few_rows_limit(layout, epilogue, p, groups, device_cus);
+    if (p.few > 0) {
+        const int rows = expected_rows < p.few ? expected_rows : p.few;
+        // (dense: the tile decides how many parts of K are added)
+        const Times t = times(layout, epilogue, p, groups, rows, layout == kDense ? device_cus : num_cus);
+        const int err = launch_stream(layout, epilogue, t.tm, t.tn, p, groups,
+                                      epilogue == kGatedGrad ? (rows + 63) & -64 : rows, stream);
+        if (err != (int)hipSuccess || p.few >= p.m) return err;
+        if (expected_rows <= p.few) expected_rows = p.few + 1;
+    }
+    const Times t = times(layout, epilogue, p, groups, expected_rows, num_cus);
+    const bool large = t.large <= t.small;
     KernelFn fn = nullptr;
     Shape s{0, 0};
     int threads = 0, per_cu = 1;
-    const int64_t cols = gated(epilogue) ? 2 * (int64_t)p.n : p.n;
-    const int64_t slots = layout == kMasked ? groups : 1;
-    // tiles that hold rows; a masked slot's row count is spread around the expected one
-    auto tiles = [&](int bm, int bn) {
-        const double tall = layout == kMasked ? expected_rows / (double)bm + 0.5
-                                              : (double)((expected_rows + bm - 1) / bm);
-        return slots * (tall < 1 ? 1 : tall) * (double)((cols + bn - 1) / bn);
-    };
-    // Which kernel, by the time each would take (microseconds; MI355X, weights not in cache):
-    // - 256x256 tiles, one workgroup per CU: 1.4 a step of 128 bytes, 5 to fill and store.
-    // - 128x128, two per CU: 1.0 a step and 5 to fill and store; 0.77 and 2 while every
-    //   workgroup has a CU for itself.  28 steps, up to 256 tiles: 26 against 43 with 256x256;
-    //   256 x 7168 x 2048: 11.5 against 19.6; 2048 x 7168 x 2048: 30 against 26; 16 slots of
-    //   up to 256 rows, gated, f = 2048, k = 7168: 95 against 69, of 32 rows: 56 against 70.
-    // - few rows, dense or a few slots: 1.3 a tile, and its rows' and columns' bytes at the 56
-    //   GB/s that a CU draws.  1 x 4096 x 7168: 5.9 (16x16 tiles) against 25; 48: 8.1 (32x32)
-    //   against 26; 128: 10.5 (64x32) against 26; 256: 13 (64x64) against 29; 512: 23 against
-    //   31; 256 x 7168 x 2048: 12.2 against 11.3; 16 slots of 16 rows: 34 against 32.5.
-    const double steps = p.chunks;
-    const double big = tiles(256, 256), small = tiles(128, 128);
-    const double large_us = ceil(big / num_cus) * (1.4 * steps + 5);
-    const double small_us = small <= num_cus ? 0.77 * steps + 2
-                                             : ceil(small / (2 * num_cus)) * (1.0 * steps + 5);
-    const bool large = large_us <= small_us;
-    if (layout != kContiguous) {
-        double best = large ? large_us : small_us;
-        int best_tm = 0, best_tn = 0;
-        for (int tm = 4; tm >= 1; tm /= 2) {               // (of equals the tallest: reads B least)
-            for (int tn = epilogue == kGatedQuant ? 4 : gated(epilogue) ? 2 : 1; tn <= 4; tn *= 2) {
-                const double us = ceil(tiles(16 * tm, 16 * tn) / num_cus) *
-                                  (1.3 + 16 * (tm + tn) * (double)p.a_row * 1.0625 / 56e3);
-                if (us < best) {
-                    best = us;
-                    best_tm = tm;
-                    best_tn = tn;
-                }
-            }
-        }
-        const int rows = epilogue == kGatedGrad ? (p.m + 63) & -64 : expected_rows;
-        if (best_tm) return launch_stream(layout, epilogue, best_tm, best_tn, p, groups, rows, stream);
-    }
 #define MX_CASE(L, E) \
     if (layout == L && epilogue == E) pick<L, E>(large, &fn, &s, &threads, &per_cu);
     MX_CASE(kDense, kStore)

@@ -8,7 +8,11 @@
 // rows a copy; fragments loaded straight into registers touch 16 half lines a load and drew
 // 27 GB/s per CU against 56: 128 x 4096 x 7168 took 16.9 us instead of 10.5).  Nothing is shared
 // until the end, so a wavefront waits for its own copies only; the FP32 partial tiles then
-// meet in LDS and are added in a fixed order -- one launch, no workspace, no atomics.
+// meet in LDS and are added in a fixed order -- one launch, no workspace, no atomics.  Dense, a
+// wavefront takes one run of K; the tile shape, and with it their number, follows from sizes.  The
+// tile shape of slots follows from the caller's hint too, so there K is cut into eight runs whatever
+// the tile (each of four wavefronts takes two) and their sums are added in the same pairs: every
+// shape gives the same bits (0.1 to 1 us a launch slower than four runs).
 //
 // 1 x 4096 x 7168: 5.7 us, of which 3.7 are there at K = 128 too (launch, sum, store);
 // 128 x 2112 x 7168: 10 us; 64 x 2048 x 7168 gated, output quantised: 10 us.
@@ -65,8 +69,11 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     const int n0 = rest % p.n_tiles * COLS;
     const int g = LAYOUT == kMasked ? rest / p.n_tiles : 0;
     // (kGatedGrad stores zeros in the rows from m to the next multiple of 64)
-    const int limit = LAYOUT == kMasked ? min(p.group_data[g], p.m)
-                      : EPI == kGatedGrad ? (p.m + 63) & -64 : p.m;
+    int limit = EPI == kGatedGrad ? (p.m + 63) & -64 : p.m;
+    if constexpr (LAYOUT == kMasked) {                         // (slots with more rows: not here)
+        limit = min(p.group_data[g], p.m);
+        if (limit > p.few) limit = 0;
+    }
     // (masked: the grid has tiles for the expected rows; a slot with more is walked through)
     for (; mt * BM < limit; mt += p.m_tiles) {
         const int m0 = mt * BM, slot = g;
@@ -130,19 +137,22 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
             copy16(a, a_at[k] - back, at, to + (uint32_t)(k * 1024));
     };
 
-    f32x4 acc[TM][TN];
+    constexpr int RUNS = LAYOUT == kMasked ? 8 / WAVES : 1;    // of a wavefront
+    auto run_at = [&](int r) { return (int)((int64_t)r * p.chunks / (WAVES * RUNS)); };
+    // (accumulators for each: moved aside after the first run, they cost 0.4 us at 64 x 64)
+    f32x4 run_sum[RUNS][TM][TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int run = 0; run < RUNS; ++run)
 #pragma unroll
-        for (int n = 0; n < TN; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int c0 = (int)((int64_t)wave * p.chunks / WAVES);
-    const int c1 = (int)((int64_t)(wave + 1) * p.chunks / WAVES);
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int n = 0; n < TN; ++n) run_sum[run][i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int c0 = run_at(wave * RUNS), c1 = run_at((wave + 1) * RUNS);
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
         if (c0 + d < c1) copy_step(c0 + d, d);
     int buf = 0;
-    for (int c = c0; c < c1; ++c) {
+    auto multiply = [&](int c, f32x4 (&acc)[TM][TN]) {
         // the copies of the steps after this one stay in flight
         const int after = min(c1 - 1 - c, DEPTH - 1);
         if (after == 0) wait_copies<0>();
@@ -183,24 +193,35 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
                         (ea[h][i] >> (8 * q)) & (h ? keep : 255));
                 }
         buf = buf + 1 == DEPTH ? 0 : buf + 1;
-    }
+    };
+    int c = c0;
+    if constexpr (RUNS == 2)
+        for (const int end = run_at(wave * 2 + 1); c < end; ++c) multiply(c, run_sum[1]);
+    for (; c < c1; ++c) multiply(c, run_sum[0]);
 
-    // ---- the partial tiles, in the rings' place, added in order by the first TM wavefronts ----
+    // ---- the partial tiles, in the rings' place, added in order by the first TM wavefronts (slots:
+    // the runs' sums in pairs, (0 + 1) + (2 + 3) + ...) ----
     f32x4* part = (f32x4*)smem;                                // [wave][block][lane]
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int n = 0; n < TN; ++n) part[(wave * TM * TN + i * TN + n) * 64 + lane] = acc[i][n];
+        for (int n = 0; n < TN; ++n)
+            part[(wave * TM * TN + i * TN + n) * 64 + lane] =
+                RUNS == 2 ? run_sum[RUNS - 1][i][n] + run_sum[0][i][n] : run_sum[0][i][n];
     __syncthreads();
     if (wave < TM) {
+    constexpr bool PAIRED = LAYOUT == kMasked && RUNS == 1;
     const int i = wave;
     f32x4 sum[TN];
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-        sum[n] = part[(i * TN + n) * 64 + lane];
+        auto of = [&](int w) { return part[(w * TM * TN + i * TN + n) * 64 + lane]; };
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) sum[n] += part[(w * TM * TN + i * TN + n) * 64 + lane];
+        for (int w = 0; w < WAVES; w += PAIRED ? 2 : 1) {
+            const f32x4 next = PAIRED ? of(w) + of(w + 1) : of(w);
+            sum[n] = w ? sum[n] + next : next;
+        }
     }
     const int r = TM * j + i;
     const bool ok = EPI == kGatedGrad ? m0 + r < p.m : r < rows;

@@ -52,7 +52,7 @@ __device__ __forceinline__ int expert_of(const MxParams& p, int block) {
 // The tiles along M that hold a valid row, listed in LDS by one wavefront; returns how many.
 // Contiguous: block number * 2 + whether the next 128-row block, of the same expert, belongs
 // to the tile (256-row tiles pair the blocks of a run of one expert).  Masked: slot *
-// m_tiles + tile.
+// m_tiles + tile, of slots that the few-rows kernel leaves.
 template <int BM, int LAYOUT>
 __device__ int list_tiles(const MxParams& p, uint32_t* list) {
     const int lane = threadIdx.x & 63;
@@ -80,7 +80,8 @@ __device__ int list_tiles(const MxParams& p, uint32_t* list) {
         for (int w = p.first; w < p.last; w += 64) {
             const int i = w + lane;
             const int g = min(i, p.last - 1) / p.m_tiles;
-            const bool in = i < p.last && (i - g * p.m_tiles) * BM < min(p.group_data[g], p.m);
+            const int rows = min(p.group_data[g], p.m);
+            const bool in = i < p.last && rows > p.few && (i - g * p.m_tiles) * BM < rows;
             const uint64_t heads = __ballot(in);
             if (in) list[count + __popcll(heads & ((1ull << lane) - 1ull))] = (uint32_t)i;
             count += __popcll(heads);

@@ -1,0 +1,51 @@
+"""Which kernels the MXFP4 entry points launch, on the CPU (tests/_mx_launches.py)."""
+import pytest
+
+from _mx_launches import AVAILABLE, CONTIGUOUS, DENSE, MASKED, ask
+
+pytestmark = pytest.mark.skipif(not AVAILABLE, reason="no ROCm toolchain")
+
+# m (rows of a slot), n (f), k, groups
+SLOTS = [(256, 7168, 2048, 4), (256, 7168, 2048, 16), (16, 7168, 2048, 16), (256, 2048, 7168, 2),
+         (256, 2048, 7168, 8), (64, 2048, 7168, 16), (1024, 2048, 7168, 8), (300, 256, 384, 5),
+         (4096, 512, 1024, 32), (1, 128, 128, 1)]
+ROWS = [(1, 4096, 7168), (64, 4096, 7168), (256, 7168, 2048), (512, 4096, 7168), (600, 2048, 512),
+        (4096, 7168, 2048), (200, 416, 640)]
+
+
+def sums(result):
+    """the kernels whose order of summation differs, as launched; dense, the few-rows kernel's
+    with its tile (the number of wavefronts that share K follows from it)"""
+    assert result.status == 0
+    return [(x.kernel, x.args[:2] if x.kernel == "mx_stream_kernel" and x.args[2] == DENSE else None)
+            for x in result.launches if x.kernel in ("mx_stream_kernel", "mx_gemm_kernel")]
+
+
+@pytest.mark.parametrize("op", ["product", "gated", "gated_q", "layer"])
+def test_neither_hint_nor_cap_chooses_the_order_of_sums(op):
+    # include/fp8bs.h: expected_m "never changes results", nor does the cap on CUs
+    for m, n, k, g in SLOTS:
+        runs = [(op, MASKED, m, e, n, k, g, 256, cap) for cap in (0, 200, 64, 1)
+                for e in (0, 1, 16, 40, 65, 200, m, 2 * m)]
+        got = [sums(r) for r in ask(runs)]
+        assert all(x == got[0] for x in got), (m, n, k, g)
+    for m, n, k in ROWS:
+        if op in ("gated_q", "layer"):
+            n = n // 128 * 128
+        got = [sums(r) for r in ask([(op, DENSE, m, 0, n, k, 1, 256, cap) for cap in (0, 255, 64, 8, 1)])]
+        assert all(x == got[0] for x in got), (m, n, k)
+
+
+@pytest.mark.parametrize("layout", [DENSE, CONTIGUOUS])
+def test_the_cap_does_not_choose_how_gradients_are_summed(layout):
+    # the recomputed gate and up projections, and into how many parts a product is split (a
+    # launch of the kernel that adds parts; the 128x128 and 256x256 tiles sum alike)
+    for m, f, k, g in [(200, 416, 640, 1), (512, 2048, 2048, 4), (2048, 64, 256, 3), (4096, 2048, 7168, 8),
+                       (128, 4096, 4096, 2)]:
+        m = m if layout == DENSE else (m + 127) // 128 * 128
+        for flag in (1, 2, 3, 7, 15):
+            got = ask([("backward", layout, m, 0, f, k, g, flag, cap) for cap in (0, 200, 64, 1)])
+            for r in got:
+                assert sums(r) == sums(got[0])
+                assert (sum(x.kernel == "mx_grad_sum_kernel" for x in r.launches) > 0) == (
+                    sum(x.kernel == "mx_grad_sum_kernel" for x in got[0].launches) > 0)
