@@ -159,6 +159,12 @@ __device__ __forceinline__ int logical_block() {
 
 #endif  // __HIPCC__
 
+// Most workgroups of a launch of which per_cu share a CU, under the process's cap on CUs.
+inline int64_t most_workgroups(int per_cu) {
+    const int cap = fp8bs_get_num_cus();
+    return cap > 0 ? (int64_t)cap * per_cu : 0x7fffffff;
+}
+
 // Launchers; return a hipError_t value.
 // Contiguous layout: out = [num_groups + 1] offsets, then each expert's 128-row blocks in
 // order (a block belongs to the expert of its first row).

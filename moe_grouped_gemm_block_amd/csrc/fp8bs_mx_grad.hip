@@ -429,25 +429,35 @@ __global__ void __launch_bounds__(256) mx_grad_sum_kernel(const MxParams a, cons
     const MxParams& p = first ? a : b;
     const int64_t rows = (!first && LAYOUT == kContiguous ? p.num_groups : 1) * (int64_t)p.m;
     const int64_t all = rows * p.n;
-    const int64_t at = ((int64_t)(first ? blockIdx.x : blockIdx.x - split) * 256 + threadIdx.x) * 4;
-    if (at >= all) return;
-    if (LAYOUT == kContiguous && first) {
-        const int64_t r = at / p.n;
-        const int e = expert_of(p, (int)(r >> 7));
-        if (e < 0 || p.group_data[r] != e) return;
-    }
-    f32x4 sum = *(const f32x4*)(p.part + at);
-    for (int s = 1; s < p.splits; ++s) sum += *(const f32x4*)(p.part + s * all + at);
-    if (EPI == kStoreF32 && !first) {
-        float* d = (float*)p.d + at;
-        if (p.accumulate) sum += *(const f32x4*)d;
-        *(f32x4*)d = sum;
-    } else {
-        *(u32x2*)((uint16_t*)p.d + at) = u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+    const int64_t stride = (int64_t)(first ? split : gridDim.x - split) * 1024;
+    int64_t at = ((int64_t)(first ? blockIdx.x : blockIdx.x - split) * 256 + threadIdx.x) * 4;
+    for (; at < all; at += stride) {
+        if (LAYOUT == kContiguous && first) {
+            const int64_t r = at / p.n;
+            const int e = expert_of(p, (int)(r >> 7));
+            if (e < 0 || p.group_data[r] != e) continue;
+        }
+        f32x4 sum = *(const f32x4*)(p.part + at);
+        for (int s = 1; s < p.splits; ++s) sum += *(const f32x4*)(p.part + s * all + at);
+        if (EPI == kStoreF32 && !first) {
+            float* d = (float*)p.d + at;
+            if (p.accumulate) sum += *(const f32x4*)d;
+            *(f32x4*)d = sum;
+        } else {
+            *(u32x2*)((uint16_t*)p.d + at) = u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+        }
     }
 }
 
 typedef void (*KernelFn)(MxParams);
+
+// Workgroups of two jobs that share a launch, at most `most` (two or more; a job keeps one).
+void share(int64_t& a, int64_t& b, int64_t most) {
+    if (a + b <= most) return;
+    const int64_t part = (int64_t)(most * (double)a / (double)(a + b));
+    a = b == 0 ? most : a == 0 ? 0 : part < 1 ? 1 : part < most ? part : most - 1;
+    b = most - a;
+}
 
 // 128x128 tiles of a product's grid (an upper bound for the contiguous layout)
 int64_t small_tiles(const MxParams& p, int layout, int groups) {
@@ -552,10 +562,12 @@ int launch_grad_pair(int layout, int epilogue, const MxParams* pa, const MxParam
     MX_CASE(kContiguous, kStoreF32)
 #undef MX_CASE
     if (!fn) return (int)hipErrorInvalidValue;
+    share(na, nb, most_workgroups(2));
     int split = (int)na;
     void* argv[] = {&a, &b, &split};
     const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)(na + nb)), dim3(256), argv, 0, stream);
     if (err != hipSuccess || sum_a + sum_b == 0) return (int)err;
+    share(sum_a, sum_b, most_workgroups(8));
     split = (int)sum_a;
     return (int)hipLaunchKernel(add, dim3((unsigned)(sum_a + sum_b)), dim3(256), argv, 0, stream);
 }

@@ -77,46 +77,51 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) mx_quant_kernel(const void* __restrict__ x,
                                                        uint8_t* __restrict__ q,
                                                        uint32_t* __restrict__ sf, int rows, int k,
-                                                       int ld, int row_tiles, int col_tiles) {
+                                                       int ld, int row_tiles, int col_tiles,
+                                                       uint32_t tiles) {
     __shared__ uint32_t words[2][kRows];
-    const int ct = blockIdx.x % col_tiles;
-    const int rt = blockIdx.x / col_tiles % row_tiles;
-    const int slot = blockIdx.x / col_tiles / row_tiles;
     const int t = threadIdx.x, seg = t & 31;
-    const int col = ct * kCols + 8 * seg;
-    const int64_t row0 = (int64_t)slot * rows;
-    Piece<BF16> v[4] = {};
-    bool in[4];
+    // (a workgroup for each tile, unless the process's cap on CUs allows fewer)
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        if (tile != blockIdx.x) __syncthreads();           // before the words are replaced
+        const int ct = tile % col_tiles;
+        const int rt = tile / col_tiles % row_tiles;
+        const int slot = tile / col_tiles / row_tiles;
+        const int col = ct * kCols + 8 * seg;
+        const int64_t row0 = (int64_t)slot * rows;
+        Piece<BF16> v[4] = {};
+        bool in[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = rt * kRows + (t >> 5) + 8 * i;
-        in[i] = r < rows && col < k;
-        if (in[i]) v[i].load(x, (row0 + r) * k + col);
-    }
+        for (int i = 0; i < 4; ++i) {
+            const int r = rt * kRows + (t >> 5) + 8 * i;
+            in[i] = r < rows && col < k;
+            if (in[i]) v[i].load(x, (row0 + r) * k + col);
+        }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int rr = (t >> 5) + 8 * i;
-        // over the block's four lanes, then the four exponents of a 128-column group into one
-        // word: exchanges within 4 and 16 lanes (quad permutations, row rotations)
-        uint32_t top = v[i].top();
-        top = umax(top, __builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));   // lane ^ 1
-        top = umax(top, __builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));   // lane ^ 2
-        const uint32_t e = block_exponent(top);
-        // A block that holds an infinity or a NaN is not a number as a whole (e2m1 has
-        // neither); its codes are zeros.
-        if (in[i])
-            *(uint32_t*)(q + ((row0 + rt * kRows + rr) * k + col) / 2) =
-                e == 255u ? 0u : v[i].codes(scale_value(e));
-        uint32_t word = e << (8 * ((seg >> 2) & 3));
-        word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x124, 0xF, 0xF, true);   // rotate 4
-        word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x128, 0xF, 0xF, true);   // rotate 8
-        if ((seg & 15) == 0) words[seg >> 4][rr] = word;
-    }
-    __syncthreads();
-    if (t < 2 * kRows) {
-        const int c = ct * 2 + (t >> 5), r = rt * kRows + (t & 31);
-        if (r < rows && c < k / 128)
-            sf[((int64_t)slot * (k / 128) + c) * ld + r] = words[t >> 5][t & 31];
+        for (int i = 0; i < 4; ++i) {
+            const int rr = (t >> 5) + 8 * i;
+            // over the block's four lanes, then the four exponents of a 128-column group into one
+            // word: exchanges within 4 and 16 lanes (quad permutations, row rotations)
+            uint32_t top = v[i].top();
+            top = umax(top, __builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+            top = umax(top, __builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+            const uint32_t e = block_exponent(top);
+            // A block that holds an infinity or a NaN is not a number as a whole (e2m1 has
+            // neither); its codes are zeros.
+            if (in[i])
+                *(uint32_t*)(q + ((row0 + rt * kRows + rr) * k + col) / 2) =
+                    e == 255u ? 0u : v[i].codes(scale_value(e));
+            uint32_t word = e << (8 * ((seg >> 2) & 3));
+            word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x124, 0xF, 0xF, true);   // rotate 4
+            word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x128, 0xF, 0xF, true);   // rotate 8
+            if ((seg & 15) == 0) words[seg >> 4][rr] = word;
+        }
+        __syncthreads();
+        if (t < 2 * kRows) {
+            const int c = ct * 2 + (t >> 5), r = rt * kRows + (t & 31);
+            if (r < rows && c < k / 128)
+                sf[((int64_t)slot * (k / 128) + c) * ld + r] = words[t >> 5][t & 31];
+        }
     }
 }
 
@@ -124,46 +129,51 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restrict__ q,
                                                          const uint32_t* __restrict__ sf,
                                                          void* __restrict__ x, int rows, int k,
-                                                         int ld, int row_tiles, int col_tiles) {
+                                                         int ld, int row_tiles, int col_tiles,
+                                                         uint32_t tiles) {
     __shared__ uint32_t words[2][kRows];
-    const int ct = blockIdx.x % col_tiles;
-    const int rt = blockIdx.x / col_tiles % row_tiles;
-    const int slot = blockIdx.x / col_tiles / row_tiles;
     const int t = threadIdx.x, seg = t & 31;
-    const int col = ct * kCols + 8 * seg;
-    const int64_t row0 = (int64_t)slot * rows;
-    if (t < 2 * kRows) {
-        const int c = ct * 2 + (t >> 5), r = rt * kRows + (t & 31);
-        words[t >> 5][t & 31] =
-            (r < rows && c < k / 128) ? sf[((int64_t)slot * (k / 128) + c) * ld + r] : 0u;
-    }
-    uint32_t codes[4];
+    // (a workgroup for each tile, unless the process's cap on CUs allows fewer)
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        if (tile != blockIdx.x) __syncthreads();           // before the words are replaced
+        const int ct = tile % col_tiles;
+        const int rt = tile / col_tiles % row_tiles;
+        const int slot = tile / col_tiles / row_tiles;
+        const int col = ct * kCols + 8 * seg;
+        const int64_t row0 = (int64_t)slot * rows;
+        if (t < 2 * kRows) {
+            const int c = ct * 2 + (t >> 5), r = rt * kRows + (t & 31);
+            words[t >> 5][t & 31] =
+                (r < rows && c < k / 128) ? sf[((int64_t)slot * (k / 128) + c) * ld + r] : 0u;
+        }
+        uint32_t codes[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = rt * kRows + (t >> 5) + 8 * i;
-        codes[i] = (r < rows && col < k) ? *(const uint32_t*)(q + ((row0 + r) * k + col) / 2) : 0u;
-    }
-    __syncthreads();
+        for (int i = 0; i < 4; ++i) {
+            const int r = rt * kRows + (t >> 5) + 8 * i;
+            codes[i] = (r < rows && col < k) ? *(const uint32_t*)(q + ((row0 + r) * k + col) / 2) : 0u;
+        }
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int rr = (t >> 5) + 8 * i, r = rt * kRows + rr;
-        if (r >= rows || col >= k) continue;
-        const uint32_t e = (words[seg >> 4][rr] >> (8 * ((seg >> 2) & 3))) & 255u;
-        // bf16 holds every value exactly; FP32 values are those, widened
-        const float scale = scale_value(e);
-        u32x4 w;
-        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 0));
-        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 1));
-        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 2));
-        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 3));
-        const int64_t at = (row0 + r) * k + col;
-        if constexpr (BF16) {
-            __builtin_nontemporal_store(w, (u32x4*)((uint16_t*)x + at));
-        } else {
-            const u32x4 lo = {w[0] << 16, w[0] & 0xFFFF0000u, w[1] << 16, w[1] & 0xFFFF0000u};
-            const u32x4 hi = {w[2] << 16, w[2] & 0xFFFF0000u, w[3] << 16, w[3] & 0xFFFF0000u};
-            __builtin_nontemporal_store(lo, (u32x4*)((float*)x + at));
-            __builtin_nontemporal_store(hi, (u32x4*)((float*)x + at) + 1);
+        for (int i = 0; i < 4; ++i) {
+            const int rr = (t >> 5) + 8 * i, r = rt * kRows + rr;
+            if (r >= rows || col >= k) continue;
+            const uint32_t e = (words[seg >> 4][rr] >> (8 * ((seg >> 2) & 3))) & 255u;
+            // bf16 holds every value exactly; FP32 values are those, widened
+            const float scale = scale_value(e);
+            u32x4 w;
+            w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 0));
+            w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 1));
+            w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 2));
+            w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 3));
+            const int64_t at = (row0 + r) * k + col;
+            if constexpr (BF16) {
+                __builtin_nontemporal_store(w, (u32x4*)((uint16_t*)x + at));
+            } else {
+                const u32x4 lo = {w[0] << 16, w[0] & 0xFFFF0000u, w[1] << 16, w[1] & 0xFFFF0000u};
+                const u32x4 hi = {w[2] << 16, w[2] & 0xFFFF0000u, w[3] << 16, w[3] & 0xFFFF0000u};
+                __builtin_nontemporal_store(lo, (u32x4*)((float*)x + at));
+                __builtin_nontemporal_store(hi, (u32x4*)((float*)x + at) + 1);
+            }
         }
     }
 }
@@ -235,7 +245,9 @@ extern "C" int fp8bs_quantize_mxfp4(const void* x, int x_dtype, void* q, int32_t
     if (st != FP8BS_OK || rows == 0) return st;
     int ld = (int)fp8bs_get_sfa_ld(rows), rt = (rows + kRows - 1) / kRows,
         ct = (k + kCols - 1) / kCols;
-    void* args[] = {(void*)&x, (void*)&q, (void*)&sf, &rows, &k, &ld, &rt, &ct};
+    uint32_t tiles = (uint32_t)grid;
+    if (grid > most_workgroups(8)) grid = most_workgroups(8);
+    void* args[] = {(void*)&x, (void*)&q, (void*)&sf, &rows, &k, &ld, &rt, &ct, &tiles};
     const void* fn = x_dtype == FP8BS_DTYPE_BF16 ? (const void*)mx_quant_kernel<true>
                                                  : (const void*)mx_quant_kernel<false>;
     return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), args, 0, stream) == hipSuccess
@@ -250,7 +262,9 @@ extern "C" int fp8bs_dequantize_mxfp4(const void* q, const int32_t* sf, void* x,
     if (st != FP8BS_OK || rows == 0) return st;
     int ld = (int)fp8bs_get_sfa_ld(rows), rt = (rows + kRows - 1) / kRows,
         ct = (k + kCols - 1) / kCols;
-    void* args[] = {(void*)&q, (void*)&sf, (void*)&x, &rows, &k, &ld, &rt, &ct};
+    uint32_t tiles = (uint32_t)grid;
+    if (grid > most_workgroups(8)) grid = most_workgroups(8);
+    void* args[] = {(void*)&q, (void*)&sf, (void*)&x, &rows, &k, &ld, &rt, &ct, &tiles};
     const void* fn = x_dtype == FP8BS_DTYPE_BF16 ? (const void*)mx_dequant_kernel<true>
                                                  : (const void*)mx_dequant_kernel<false>;
     return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), args, 0, stream) == hipSuccess

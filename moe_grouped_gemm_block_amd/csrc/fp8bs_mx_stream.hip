@@ -63,7 +63,9 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     const int j = lane & 15, q = lane >> 4;
 
     // ---- the tile: tiles along M of one weight strip are neighbours on one XCD ----
-    const int id = logical_block();
+    // (a workgroup for each, unless the process's cap on CUs allows fewer)
+    const uint32_t units = (uint32_t)p.m_tiles * p.n_tiles * (LAYOUT == kMasked ? p.num_groups : 1);
+    for (uint32_t id = logical_block(); id < units; id += gridDim.x) {
     int mt = id % p.m_tiles;
     const int rest = id / p.m_tiles;
     const int n0 = rest % p.n_tiles * COLS;
@@ -309,6 +311,8 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     }
     if constexpr (LAYOUT == kMasked) __syncthreads();      // before the partials are replaced
     }
+    if (LAYOUT != kMasked && id + gridDim.x < units) __syncthreads();
+    }
 }
 
 typedef void (*KernelFn)(MxParams);
@@ -349,8 +353,9 @@ int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& para
     const int cols = gated(epilogue) ? 8 * tn : 16 * tn;
     p.m_tiles = (expected_rows + 16 * tm - 1) / (16 * tm);
     p.n_tiles = (p.n + cols - 1) / cols;
-    const int64_t grid = (int64_t)p.m_tiles * p.n_tiles * (layout == kMasked ? groups : 1);
+    int64_t grid = (int64_t)p.m_tiles * p.n_tiles * (layout == kMasked ? groups : 1);
     if (grid > 0x7fffffff) return (int)hipErrorInvalidValue;
+    if (grid > most_workgroups(1)) grid = most_workgroups(1);  // (one fits a CU's LDS)
     void* argv[] = {&p};
     return (int)hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3(threads), argv, 0,
                                 stream);

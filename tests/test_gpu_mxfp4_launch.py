@@ -80,3 +80,39 @@ def test_the_cap_changes_no_result(gen, cap, m, n, k):
         runs.append((d, h, da, db))
     for outs in runs[1:]:
         assert all(torch.equal(x, y) for x, y in zip(outs, runs[0]))
+
+
+def test_few_workgroups_do_all_of_the_work(gen, cap):
+    # each under a cap of 3 CUs against all of them: the quantiser and its inverse, slots, and the
+    # gradients side by side and in parts (dense; contiguous with an expert without rows)
+    x = torch.randn(3, 301, 1152, device="cuda", generator=gen).bfloat16()
+    a, sfa = operand(gen, 5, 70, 640)
+    b, sfb = operand(gen, 5, 520, 640)
+    masked = torch.tensor([70, 0, 3, 64, 17], dtype=torch.int32, device="cuda")
+    layout = torch.tensor([0, 0, 2, 0, 3, 3, 2], dtype=torch.int32, device="cuda").repeat_interleave(128)
+    layout[-60:] = -1
+    c, sfc = operand(gen, layout.numel(), 384)
+    w, sfw = operand(gen, 4, 832, 384)
+    long, sfl = operand(gen, 2085, 256)
+    v, sfv = operand(gen, 128, 256)
+    dh = torch.randn(layout.numel(), 416, device="cuda", generator=gen).bfloat16()
+    dl = torch.randn(2085, 64, device="cuda", generator=gen).bfloat16()
+    runs = []
+    for cus in (0, 3):
+        cap(cus)
+        print(f"[gpu] cap {cus}", flush=True)
+        q, sf = fp8bs.quantize_mxfp4(x)
+        sf[..., 301:] = 0                                  # (alignment padding is not written)
+        y = fp8bs.dequantize_mxfp4(q, sf, torch.float32)
+        d = torch.zeros(5, 70, 520, dtype=torch.bfloat16, device="cuda")
+        fp8bs.fp8bs_grouped_masked_nt_mxfp4(a, sfa, b, sfb, d, masked, expected_m=20)
+        da = torch.zeros(layout.numel(), 384, dtype=torch.bfloat16, device="cuda")
+        db = torch.zeros(4, 832, 384, device="cuda")
+        fp8bs.fp8bs_gated_contiguous_mxfp4_backward(c, sfc, w, sfw, dh, da, db, layout)
+        ga = torch.zeros(2085, 256, dtype=torch.bfloat16, device="cuda")
+        gb = torch.ones(128, 256, device="cuda")
+        fp8bs.fp8bs_gated_dense_mxfp4_backward(long, sfl, v, sfv, dl, ga, gb, accumulate=True)
+        runs.append((q, sf, y, d, da, db, ga, gb))
+    for i, (one, other) in enumerate(zip(*runs)):
+        assert torch.equal(one, other), i
+        assert one.any()

@@ -49,3 +49,29 @@ def test_the_cap_does_not_choose_how_gradients_are_summed(layout):
                 assert sums(r) == sums(got[0])
                 assert (sum(x.kernel == "mx_grad_sum_kernel" for x in r.launches) > 0) == (
                     sum(x.kernel == "mx_grad_sum_kernel" for x in got[0].launches) > 0)
+
+
+# workgroups of a kernel that share a CU (by LDS and threads)
+SHARE = {"mx_stream_kernel": 1, "mx_grad_pair_kernel": 2, "mx_grad_sum_kernel": 8, "mx_quant_kernel": 8,
+         "mx_dequant_kernel": 8, "mx_block_order_kernel": 1}
+
+
+def test_every_launch_keeps_to_the_cap():
+    calls = [("product", DENSE, 128, 0, 2112, 7168, 1), ("product", DENSE, 4096, 0, 7168, 2048, 1),
+             ("product", DENSE, 1, 0, 4096, 7168, 1), ("product", MASKED, 40, 9, 7168, 2048, 9),
+             ("gated", MASKED, 256, 16, 2048, 7168, 8), ("gated_q", CONTIGUOUS, 8192, 0, 512, 1024, 3),
+             ("layer", DENSE, 64, 0, 2048, 7168, 1, 7168), ("quantise", DENSE, 3000, 0, 0, 7168, 4, 1),
+             ("dequantise", DENSE, 3000, 0, 0, 7168, 4, 0), ("backward", DENSE, 200, 0, 416, 640, 1, 3),
+             ("backward", DENSE, 16384, 0, 128, 256, 1, 3), ("backward", DENSE, 8192, 0, 512, 1024, 1, 2),
+             ("backward", DENSE, 128, 0, 4096, 4096, 1, 1), ("backward", DENSE, 1024, 0, 2048, 2048, 1, 3),
+             ("backward", CONTIGUOUS, 2048, 0, 512, 1024, 8, 7),
+             ("backward", CONTIGUOUS, 16384, 0, 2048, 7168, 8, 3)]
+    seen = set()
+    for cap in (1, 7, 64):
+        for call, r in zip(calls, ask([(c + (0,) * (8 - len(c)) + (cap,)) for c in calls])):
+            assert r.status == 0, call
+            for x in r.launches:
+                per_cu = SHARE.get(x.kernel) or (1 if x.args[0] == 256 else 2)
+                assert 1 <= x.grid <= cap * per_cu, (call, cap, x)
+                seen.add(x.kernel)
+    assert seen == set(SHARE) | {"mx_gemm_kernel", "mx_grad_kernel"}
