@@ -159,10 +159,11 @@ __device__ __forceinline__ int logical_block() {
 
 #endif  // __HIPCC__
 
-// Most workgroups of a launch of which per_cu share a CU, under the process's cap on CUs.
+// Most workgroups of a launch of which per_cu share a CU: those of the process's cap on CUs;
+// without one, so many that their threads (at most 512 each) are a 32-bit number.
 inline int64_t most_workgroups(int per_cu) {
     const int cap = fp8bs_get_num_cus();
-    return cap > 0 ? (int64_t)cap * per_cu : 0x7fffffff;
+    return cap > 0 ? (int64_t)cap * per_cu : 1 << 22;
 }
 
 // Launchers; return a hipError_t value.

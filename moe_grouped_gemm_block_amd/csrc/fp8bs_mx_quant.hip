@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(const void* __restrict__ 
                                                        uint32_t tiles) {
     __shared__ uint32_t words[2][kRows];
     const int t = threadIdx.x, seg = t & 31;
-    // (a workgroup for each tile, unless the process's cap on CUs allows fewer)
+    // (a workgroup for each tile, unless a launch may not have so many)
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         if (tile != blockIdx.x) __syncthreads();           // before the words are replaced
         const int ct = tile % col_tiles;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restri
                                                          uint32_t tiles) {
     __shared__ uint32_t words[2][kRows];
     const int t = threadIdx.x, seg = t & 31;
-    // (a workgroup for each tile, unless the process's cap on CUs allows fewer)
+    // (a workgroup for each tile, unless a launch may not have so many)
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         if (tile != blockIdx.x) __syncthreads();           // before the words are replaced
         const int ct = tile % col_tiles;

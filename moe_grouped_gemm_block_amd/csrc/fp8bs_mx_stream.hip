@@ -63,7 +63,7 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     const int j = lane & 15, q = lane >> 4;
 
     // ---- the tile: tiles along M of one weight strip are neighbours on one XCD ----
-    // (a workgroup for each, unless the process's cap on CUs allows fewer)
+    // (a workgroup for each, unless a launch may not have so many)
     const uint32_t units = (uint32_t)p.m_tiles * p.n_tiles * (LAYOUT == kMasked ? p.num_groups : 1);
     for (uint32_t id = logical_block(); id < units; id += gridDim.x) {
     int mt = id % p.m_tiles;

@@ -116,3 +116,19 @@ def test_few_workgroups_do_all_of_the_work(gen, cap):
     for i, (one, other) in enumerate(zip(*runs)):
         assert torch.equal(one, other), i
         assert one.any()
+
+
+def test_more_tiles_than_a_launch_has_workgroups(gen):
+    # 17 million groups of one row: with a workgroup of 256 threads each, more threads than a
+    # launch may have
+    g = 17_000_000
+    print(f"[gpu] {g} groups", flush=True)
+    few = torch.randn(1000, 128, device="cuda", generator=gen).bfloat16()
+    x = few.repeat(g // 1000, 1).view(g, 1, 128)
+    q, sf = fp8bs.quantize_mxfp4(x)
+    want, words = fp8bs.quantize_mxfp4(few)
+    assert torch.equal(q.view(g // 1000, 1000, 64), want.expand(g // 1000, 1000, 64))
+    assert torch.equal(sf[:, 0, 0].view(g // 1000, 1000), words[:, :1000].expand(g // 1000, 1000))
+    y = fp8bs.dequantize_mxfp4(q, sf)
+    assert torch.equal(y.view(g // 1000, 1000, 128),
+                       fp8bs.dequantize_mxfp4(want, words).expand(g // 1000, 1000, 128))

@@ -75,3 +75,14 @@ def test_every_launch_keeps_to_the_cap():
                 assert 1 <= x.grid <= cap * per_cu, (call, cap, x)
                 seen.add(x.kernel)
     assert seen == set(SHARE) | {"mx_gemm_kernel", "mx_grad_kernel"}
+
+
+def test_no_launch_has_more_threads_than_a_32_bit_number():
+    # (the stand-in for the launch refuses such a grid, as the driver does)
+    calls = [("quantise", DENSE, 1, 0, 0, 128, 20_000_000, 1), ("quantise", DENSE, 600_000_000, 0, 0, 128, 1, 1),
+             ("dequantise", DENSE, 1, 0, 0, 128, 20_000_000), ("product", MASKED, 1, 0, 16, 128, 10_000_000),
+             ("product", DENSE, 1, 0, 1 << 29, 128, 1), ("gated", MASKED, 1, 0, 32, 128, 30_000_000),
+             ("backward", DENSE, 1 << 29, 0, 32, 128, 1, 3)]
+    for call, r in zip(calls, ask(calls)):
+        assert r.status == 0, (call, r)
+        assert all(x.grid * x.threads < 1 << 32 for x in r.launches), (call, r)
