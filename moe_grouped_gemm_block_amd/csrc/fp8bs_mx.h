@@ -110,7 +110,9 @@ __device__ __forceinline__ float activate(int act, float v, float& slope) {
     constexpr float c = 0.7978845608028654f;
     const float y = c * (v + 0.044715f * v * v * v);
     const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-2.0f * y));
-    if (GRAD) slope = sig + 2.0f * v * sig * (1.0f - sig) * c * (1.0f + 0.134145f * v * v);
+    // (beyond |v| = 1e15, where sig (1 - sig) is 0, the square stays finite: 0 times it is 0)
+    if (GRAD)
+        slope = sig + 2.0f * v * sig * (1.0f - sig) * c * (1.0f + 0.134145f * fminf(v * v, 1e30f));
     return v * sig;
 }
 
