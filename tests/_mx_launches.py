@@ -51,6 +51,21 @@ def _build():
     return exe
 
 
+def _kernel(name):
+    """(name, template arguments) of a kernel"""
+    kernel, _, args = name.removeprefix("void ").partition("<")
+    args = tuple(int(x) if x.strip().lstrip("-").isdigit() else x.strip() == "true"
+                 for x in args.rstrip("> ").split(",")) if args else ()
+    return kernel, args
+
+
+def instances():
+    """every compiled kernel of the operators"""
+    out = subprocess.run([_build(), "list"], capture_output=True, text=True, check=True,
+                         env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+    return {_kernel(line) for line in out.stdout.splitlines()}
+
+
 def ask(queries):
     """[Result] of [(op, layout, m, expected, n, k, groups, flag, cap)], the last ones optional"""
     lines = []
@@ -67,11 +82,7 @@ def ask(queries):
         launches = []
         for part in rest:
             name, grid, threads = part.rsplit(" ", 2)
-            name = name.removeprefix("void ")
-            kernel, _, args = name.partition("<")
-            args = tuple(int(x) if x.strip().lstrip("-").isdigit() else x.strip() == "true"
-                         for x in args.rstrip("> ").split(",")) if args else ()
-            launches.append(Launch(kernel, args, int(grid), int(threads)))
+            launches.append(Launch(*_kernel(name), int(grid), int(threads)))
         out.append(Result(int(head), launches))
     assert len(out) == len(lines)
     return out

@@ -1,7 +1,8 @@
 """Which kernels the MXFP4 entry points launch, on the CPU (tests/_mx_launches.py)."""
 import pytest
 
-from _mx_launches import AVAILABLE, CONTIGUOUS, DENSE, MASKED, ask
+from _mx_cases import CASES
+from _mx_launches import AVAILABLE, CONTIGUOUS, DENSE, MASKED, ask, instances
 
 pytestmark = pytest.mark.skipif(not AVAILABLE, reason="no ROCm toolchain")
 
@@ -86,3 +87,19 @@ def test_no_launch_has_more_threads_than_a_32_bit_number():
     for call, r in zip(calls, ask(calls)):
         assert r.status == 0, (call, r)
         assert all(x.grid * x.threads < 1 << 32 for x in r.launches), (call, r)
+
+
+def test_the_cases_compared_on_the_gpu_launch_every_kernel():
+    seen = {}
+    for case, r in zip(CASES, ask(CASES)):
+        assert r.status == 0, case
+        for x in r.launches:
+            seen.setdefault((x.kernel, x.args), []).append((case, x))
+    assert not instances() - set(seen)
+    # 256x256 tiles: also more of them than workgroups, and lists longer than a launch takes
+    for layout in (DENSE, CONTIGUOUS, MASKED):
+        for epilogue in (0, 2, 3):
+            assert any(x.grid == 256 for _, x in seen["mx_gemm_kernel", (256, 256, 2, 4, layout, epilogue)])
+    for kernel in ("mx_gemm_kernel", (256, 256, 2, 4, MASKED, 0)), ("mx_gemm_kernel", (128, 128, 2, 2, MASKED, 2)):
+        cases = [case for case, _ in seen[kernel]]
+        assert max(cases.count(c) for c in cases) > 1, kernel
