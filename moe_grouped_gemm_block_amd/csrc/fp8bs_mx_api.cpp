@@ -260,6 +260,8 @@ int check_layer(int layout, int64_t m, int f, int k, int groups) {
     if (layout != kDense && layout != kContiguous && layout != kMasked) return FP8BS_ERR_SHAPE;
     if (f < 128 || f % 128 != 0) return FP8BS_ERR_SHAPE;
     const int st = check_sizes(layout, m, 2 * (int64_t)f, k, groups);
+    // (as for the quantiser: sizes in bytes stay within 64 bits)
+    if ((layout == kMasked ? groups : 1.0) * m * (k > f ? k : f) >= 9.0e15) return FP8BS_ERR_SHAPE;
     return st != FP8BS_OK ? st : check_sizes(layout, m, 1, f, groups);
 }
 

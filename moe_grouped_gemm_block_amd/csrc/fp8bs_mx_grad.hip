@@ -461,7 +461,7 @@ void share(int64_t& a, int64_t& b, int64_t most) {
 
 // 128x128 tiles of a product's grid (an upper bound for the contiguous layout)
 int64_t small_tiles(const MxParams& p, int layout, int groups) {
-    return (layout == kBlocks ? groups : 1) * ((p.m + 127) / 128) * (int64_t)((p.n + 127) / 128);
+    return (int64_t)(layout == kBlocks ? groups : 1) * ((p.m + 127) / 128) * ((p.n + 127) / 128);
 }
 void small_grid(MxParams& p, int layout) {
     p.m_tiles = (p.m + 127) / 128;
@@ -489,7 +489,7 @@ struct Cost {
 };
 Cost cost(const MxParams& p, int layout, int groups, int num_cus) {
     auto tiles = [&](int b) {
-        return (layout == kBlocks ? groups : 1) * ((p.m + b - 1) / b) * (double)((p.n + b - 1) / b);
+        return (layout == kBlocks ? groups : 1.0) * ((p.m + b - 1) / b) * ((p.n + b - 1) / b);
     };
     const double steps = mean_steps(p, layout, groups);
     if (p.splits > 1) return {1e30, 0.9 * steps / p.splits + 3 + 6};

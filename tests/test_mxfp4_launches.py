@@ -103,3 +103,23 @@ def test_the_cases_compared_on_the_gpu_launch_every_kernel():
     for kernel in ("mx_gemm_kernel", (256, 256, 2, 4, MASKED, 0)), ("mx_gemm_kernel", (128, 128, 2, 2, MASKED, 2)):
         cases = [case for case, _ in seen[kernel]]
         assert max(cases.count(c) for c in cases) > 1, kernel
+
+
+def test_sizes_past_any_memory_are_refused_or_counted_right():
+    # (the host code runs with overflow checks here)
+    big, wide = 0x7fffffff, 1 << 21
+    layer, layer2, call, size, size2 = ask([
+        ("layer_size", MASKED, 1 << 20, 0, 1 << 14, 1 << 14, big), ("layer_size", MASKED, 1 << 20, 0, 128, 256, 1 << 12),
+        ("layer", MASKED, 1 << 20, 3, 1 << 14, 1 << 14, big, 5),
+        ("size", CONTIGUOUS, 1 << 20, 0, wide, 128, 1 << 20, 3), ("size", CONTIGUOUS, 1 << 20, 0, wide, 128, 1, 3)])
+    assert layer.status == -1 and call.status == 1 and not call.launches
+    assert layer2.status == (1 << 32) * (128 + 64) + (1 << 12) * (2 + 1) * (1 << 20) * 4
+    # dg and du of every row, and the blocks by expert; nothing is split
+    rows = (1 << 20) * 2 * wide * 2
+    assert size.status == rows + ((1 << 20) + 1 + (1 << 13) + 4) * 4
+    assert size2.status == rows + (1 + 1 + (1 << 13) + 4) * 4
+    refused = [("quantise", DENSE, big, 0, 0, 1 << 24, big, 1), ("product", MASKED, 0x7ffffe00, 5, 1 << 20, 128, big),
+               ("gated", MASKED, 0x7ffffe00, 5, 1 << 20, 128, big), ("product", DENSE, 1 << 29, 0, 1 << 29, 128, 1),
+               ("backward", DENSE, 1 << 26, 0, 1 << 20, 128, 1, 7)]
+    for call, r in zip(refused, ask(refused)):
+        assert r.status in (1, 3) and not r.launches, (call, r)
