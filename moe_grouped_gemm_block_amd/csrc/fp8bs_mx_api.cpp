@@ -46,6 +46,12 @@ int check_sizes(int layout, int64_t m, int64_t cols, int k, int groups) {
     return FP8BS_OK;
 }
 
+// Whether the 128x128 tiles of m x n in each of `slots` have 32-bit numbers: asked before a call
+// that launches several kernels launches the first.
+bool tiles_fit(int64_t m, int64_t n, int64_t slots) {
+    return (double)((m + 127) / 128) * ((n + 127) / 128) * slots <= 0x7fffffff;
+}
+
 // The parameters that every call shares.
 MxParams base_params(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
                      const int32_t* group_data, int m, int64_t cols, int k, int groups) {
@@ -84,6 +90,7 @@ int product(int layout, const void* a, const int32_t* sfa, const void* b, const 
     if (st != FP8BS_OK || m == 0) return st;
     if (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(d, 16))
         return FP8BS_ERR_POINTER;
+    if (!tiles_fit(m, n, layout == kMasked ? groups : 1)) return FP8BS_ERR_UNSUPPORTED;
     const Cus cus = compute_units();
     if (cus.capped <= 0) return FP8BS_ERR_HIP;
     MxParams p = base_params(a, sfa, b, sfb, group_data, m, n, k, groups);
@@ -108,6 +115,7 @@ int gated_forward(int layout, const void* a, const int32_t* sfa, const void* b,
     if (!pointers_ok(a, sfa, b, sfb, layout, group_data) || !aligned(h, 16) ||
         (quantise && !aligned(sfh, 16)))
         return FP8BS_ERR_POINTER;
+    if (!tiles_fit(m, 2 * (int64_t)f, layout == kMasked ? groups : 1)) return FP8BS_ERR_UNSUPPORTED;
     const Cus cus = compute_units();
     if (cus.capped <= 0) return FP8BS_ERR_HIP;
     MxParams p = base_params(a, sfa, b, sfb, group_data, m, 2 * (int64_t)f, k, groups);
@@ -187,6 +195,9 @@ int gated_backward(int layout, const void* a, const int32_t* sfa, const void* b,
     const Parts w = parts(layout, m, f, k, groups, da != nullptr, db != nullptr);
     if (w.total > 0 && workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
     if (w.total > 0 && !aligned(workspace, 16)) return FP8BS_ERR_POINTER;
+    if (!tiles_fit(m, 2 * (int64_t)f, 1) || (da && !tiles_fit(m, k, 1)) ||
+        (db && !tiles_fit(2 * (int64_t)f, k, layout == kContiguous ? groups : 1)))
+        return FP8BS_ERR_UNSUPPORTED;
     const Cus cus = compute_units();
     if (cus.capped <= 0) return FP8BS_ERR_HIP;
     uint8_t* grad = (uint8_t*)workspace;
@@ -282,6 +293,7 @@ int feed_forward(int layout, const void* x, int x_dtype, const void* b, const in
     const LayerParts w = layer_parts(slots, m, f, k);
     if (workspace_bytes < (size_t)w.total) return FP8BS_ERR_UNSUPPORTED;
     if (!aligned(workspace, 16)) return FP8BS_ERR_POINTER;
+    if (!tiles_fit(m, 2 * (int64_t)f, slots) || !tiles_fit(m, n, slots)) return FP8BS_ERR_UNSUPPORTED;
     uint8_t* ws = (uint8_t*)workspace;
     int32_t* sf = (int32_t*)(ws + w.sf);
     int32_t* sfh = (int32_t*)(ws + w.sfh);

@@ -123,3 +123,7 @@ def test_sizes_past_any_memory_are_refused_or_counted_right():
                ("backward", DENSE, 1 << 26, 0, 1 << 20, 128, 1, 7)]
     for call, r in zip(refused, ask(refused)):
         assert r.status in (1, 3) and not r.launches, (call, r)
+    # more tiles than a 32-bit number counts, of the last of several kernels: refused before the first
+    for r in ask([("backward", CONTIGUOUS, 1 << 20, 0, wide, 128, 1 << 20, 3),
+                  ("layer", MASKED, 1, 0, 128, 128, 1 << 30, 300)]):
+        assert r.status == 3 and not r.launches
