@@ -188,9 +188,10 @@ int grad_splits(int layout, const MxParams& p, int groups);
 bool grad_pair_pays(int layout, const MxParams& a, const MxParams& b, int groups, int num_cus);
 int launch_grad_pair(int layout, int epilogue, const MxParams* a, const MxParams* b, int groups,
                      hipStream_t stream);
-// Few rows, dense and masked layouts: tiles of 16 tm x 16 tn (fp8bs_mx_stream.hip).
+// Few rows, dense and masked layouts: tiles of 16 tm x 16 tn on at most `most` workgroups
+// (fp8bs_mx_stream.hip).
 int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& p, int groups,
-                  int expected_rows, hipStream_t stream);
+                  int expected_rows, int most, hipStream_t stream);
 
 }  // namespace mx
 }  // namespace fp8bs

@@ -479,8 +479,12 @@ void pick(bool large, KernelFn* fn, Shape* shape, int* threads, int* per_cu) {
 // microseconds; few: the few-rows kernel with its best tile, tm x tn blocks.
 struct Times {
     double large, small, few;
+    double drawn;                          // the tiled kernels' time to draw the slots' weights
     int tm, tn;
-    double tiled() const { return large < small ? large : small; }
+    double tiled() const {
+        const double us = large < small ? large : small;
+        return us > drawn ? us : drawn;
+    }
 };
 
 // MI355X, weights not in cache:
@@ -493,8 +497,9 @@ struct Times {
 //   draws.  1 x 4096 x 7168: 5.9 (16x16 tiles) against 25; 48: 8.1 (32x32) against 26; 128:
 //   10.5 (64x32) against 26; 256: 13 (64x64) against 29; 512: 23 against 31; 256 x 7168 x
 //   2048: 12.2 against 11.3.
-// - slots: tiles follow one another on a CU, which costs the few-rows kernel 3.3 a tile, and
-//   all CUs draw weights at once, 6 TB/s; the others take 1.2 times as long as dense and 2.5.
+// - slots: tiles follow one another on a CU, which costs the few-rows kernel 3.3 a tile; the
+//   others take 1.2 times as long as dense and 2.5.  All CUs draw weights at once, at 6 TB/s (few
+//   rows, whose rows come on top) or 4.9.
 //   Few-rows against 128x128 tiles, 16 rows a slot, 7168 x 2048: 2 slots 6 against 12, 4: 11
 //   against 13-16, 8: 21 against 18, 16: 36 against 33, 32: 68 against 61; gated, f = 2048, k =
 //   7168: 2 slots 9 against 33, 8: 26 against 37-46, 16: 48 against 52; 64 rows: 8: 30 against
@@ -514,20 +519,23 @@ Times times(int layout, int epilogue, const MxParams& p, int groups, int rows, i
     };
     const double steps = p.chunks, factor = layout == kMasked ? 1.2 : 1.0;
     const double start = layout == kMasked ? 2.5 : 0;
+    const double row_bytes = (double)p.a_row * 1.0625;     // with its exponents
+    const double weights = layout == kMasked ? slots * cols * row_bytes : 0;
     const double big = tiles(256, 256), small = tiles(128, 128);
     Times t;
     t.large = start + factor * ceil(big / cus) * (1.4 * steps + 5);
     t.small = start + factor * (small <= cus ? 0.77 * steps + 2
                                              : ceil(small / (2.0 * cus)) * (1.0 * steps + 5));
+    t.drawn = weights / 4.9e6;
     t.few = 1e30;
     t.tm = t.tn = 0;
     if (layout == kContiguous) return t;
-    const double row_bytes = (double)p.a_row * 1.0625;     // with its exponents
-    const double weights = layout == kMasked ? slots * cols * row_bytes / 6e6 : 0;
     for (int tm = 4; tm >= 1; tm /= 2) {                   // (of equals the tallest: reads B least)
         for (int tn = epilogue == kGatedQuant ? 4 : gated(epilogue) ? 2 : 1; tn <= 4; tn *= 2) {
-            const double tile = (layout == kMasked ? 3.3 : 1.3) + 16 * (tm + tn) * row_bytes / 56e3;
-            const double us = ceil(tiles(16 * tm, 16 * tn) / cus) * tile;
+            const double rounds = ceil(tiles(16 * tm, 16 * tn) / cus), a_us = 16 * tm * row_bytes / 56e3;
+            const double tile = (layout == kMasked ? 3.3 : 1.3) + a_us + 16 * tn * row_bytes / 56e3;
+            double us = rounds * tile;
+            if (us < weights / 6e6 + rounds * a_us) us = weights / 6e6 + rounds * a_us;
             if (us < t.few) {
                 t.few = us;
                 t.tm = tm;
@@ -535,7 +543,6 @@ Times times(int layout, int epilogue, const MxParams& p, int groups, int rows, i
             }
         }
     }
-    if (t.few < weights) t.few = weights;
     return t;
 }
 
@@ -543,7 +550,7 @@ Times times(int layout, int epilogue, const MxParams& p, int groups, int rows, i
 // no more (masked).  The two kernels add along K in different orders, so this follows from sizes
 // and the device alone: no result depends on the hint or on the cap on CUs, and which slots
 // go where on the counts themselves.  Both are launched where the limit lies between; an empty
-// launch costs 1.6 us.
+// launch costs 1.6 to 2.6 us.
 int few_rows_limit(int layout, int epilogue, const MxParams& p, int groups, int device_cus) {
     auto gain = [&](int64_t rows) {
         const Times t = times(layout, epilogue, p, groups, (int)(rows < p.m ? rows : p.m),
@@ -568,8 +575,11 @@ int launch_gemm(int layout, int epilogue, const MxParams& params, int groups,
         const int rows = expected_rows < p.few ? expected_rows : p.few;
         // (dense: the tile decides how many parts of K are added)
         const Times t = times(layout, epilogue, p, groups, rows, layout == kDense ? device_cus : num_cus);
+        // (slots expected not to be its: a workgroup a CU looks; 16 slots of 128 rows, gated, with one
+        // for each of 1024 tiles 67.5 us, so 65.4)
         const int err = launch_stream(layout, epilogue, t.tm, t.tn, p, groups,
-                                      epilogue == kGatedGrad ? (rows + 63) & -64 : rows, stream);
+                                      epilogue == kGatedGrad ? (rows + 63) & -64 : rows,
+                                      expected_rows > p.few ? num_cus : 0x7fffffff, stream);
         if (err != (int)hipSuccess || p.few >= p.m) return err;
         if (expected_rows <= p.few) expected_rows = p.few + 1;
     }

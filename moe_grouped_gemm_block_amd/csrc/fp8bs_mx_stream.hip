@@ -320,7 +320,7 @@ typedef void (*KernelFn)(MxParams);
 }  // namespace
 
 int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& params, int groups,
-                  int expected_rows, hipStream_t stream) {
+                  int expected_rows, int most, hipStream_t stream) {
     MxParams p = params;
     KernelFn fn = nullptr;
     int threads = 0;
@@ -356,6 +356,7 @@ int launch_stream(int layout, int epilogue, int tm, int tn, const MxParams& para
     int64_t grid = (int64_t)p.m_tiles * p.n_tiles * (layout == kMasked ? groups : 1);
     if (grid > 0x7fffffff) return (int)hipErrorInvalidValue;
     if (grid > most_workgroups(1)) grid = most_workgroups(1);  // (one fits a CU's LDS)
+    if (grid > most) grid = most;
     void* argv[] = {&p};
     return (int)hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3(threads), argv, 0,
                                 stream);
