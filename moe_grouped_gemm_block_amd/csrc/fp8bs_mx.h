@@ -52,7 +52,7 @@ struct MxParams {
     int sfa_ld, sfb_ld;
     int num_groups;
     int m_tiles, n_tiles;       // m_tiles: dense, and per slot for masked
-    int few;                    // masked: slots with at most so many rows are the few-rows kernel's
+    int few;                    // masked: slots of at most so many rows each are the few-rows kernel's
     int first, last;            // contiguous: blocks, masked: tiles, that this launch covers
     int raster;
     int act;

@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx_gemm_kernel(const MxParams
     int m_tiles = p.m_tiles;
     if constexpr (LISTED) {
         if (wave == 0) {
-            const int n = list_tiles<BM, LAYOUT>(p, list);
+            const bool none = LAYOUT == kMasked && p.few > 0 && !any_slot_over(p);
+            const int n = none ? 0 : list_tiles<BM, LAYOUT>(p, list);
             if (lane == 0) list[kMaxListed] = (uint32_t)n;
         }
         __syncthreads();
@@ -546,11 +547,12 @@ Times times(int layout, int epilogue, const MxParams& p, int groups, int rows, i
     return t;
 }
 
-// Up to how many rows the few-rows kernel takes: none or all (dense), or those slots that hold
-// no more (masked).  The two kernels add along K in different orders, so this follows from sizes
-// and the device alone: no result depends on the hint or on the cap on CUs, and which slots
-// go where on the counts themselves.  Both are launched where the limit lies between; an empty
-// launch costs 1.6 to 2.6 us.
+// Up to how many rows the few-rows kernel takes: none or all (dense); masked, slots of which none
+// holds more.  The two kernels add along K in different orders, so this follows from sizes and
+// the device alone, and where the limit lies below max_m from the counts themselves: both
+// kernels are launched and one of them finds that the slots are the other's, which costs it 1.6 to
+// 2.6 us.  No result depends on the hint or on the cap on CUs.  (Slot by slot, the two
+// kernels' times add: 16 slots of 0 to 256 rows, layer, took 139 us instead of 129.)
 int few_rows_limit(int layout, int epilogue, const MxParams& p, int groups, int device_cus) {
     auto gain = [&](int64_t rows) {
         const Times t = times(layout, epilogue, p, groups, (int)(rows < p.m ? rows : p.m),
@@ -558,6 +560,7 @@ int few_rows_limit(int layout, int epilogue, const MxParams& p, int groups, int 
         return t.tiled() - t.few;
     };
     if (layout != kMasked) return gain(p.m) > 0 ? p.m : 0;
+    if (groups > 4096) return gain(p.m) > 0 ? p.m : 0;     // (every workgroup reads all counts)
     int64_t limit = 0;
     for (int64_t rows = 16; limit < p.m && gain(rows) > 0; rows *= 2) limit = rows;
     if (limit >= p.m) return p.m;

@@ -62,6 +62,8 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, q = lane >> 4;
 
+    if (LAYOUT == kMasked && p.few < p.m && any_slot_over(p)) return;
+
     // ---- the tile: tiles along M of one weight strip are neighbours on one XCD ----
     // (a workgroup for each, unless a launch may not have so many)
     const uint32_t units = (uint32_t)p.m_tiles * p.n_tiles * (LAYOUT == kMasked ? p.num_groups : 1);
@@ -71,11 +73,8 @@ __global__ void __launch_bounds__((64 * Ring<TM, TN>::kWaves), 1) mx_stream_kern
     const int n0 = rest % p.n_tiles * COLS;
     const int g = LAYOUT == kMasked ? rest / p.n_tiles : 0;
     // (kGatedGrad stores zeros in the rows from m to the next multiple of 64)
-    int limit = EPI == kGatedGrad ? (p.m + 63) & -64 : p.m;
-    if constexpr (LAYOUT == kMasked) {                         // (slots with more rows: not here)
-        limit = min(p.group_data[g], p.m);
-        if (limit > p.few) limit = 0;
-    }
+    const int limit = LAYOUT == kMasked ? min(p.group_data[g], p.m)
+                      : EPI == kGatedGrad ? (p.m + 63) & -64 : p.m;
     // (masked: the grid has tiles for the expected rows; a slot with more is walked through)
     for (; mt * BM < limit; mt += p.m_tiles) {
         const int m0 = mt * BM, slot = g;

@@ -49,10 +49,21 @@ __device__ __forceinline__ int expert_of(const MxParams& p, int block) {
     return e >= 0 && e < p.num_groups ? e : -1;
 }
 
+// Masked: whether a slot holds more rows than the few-rows kernel takes (all slots then go to the
+// tiled kernels; asked by whole wavefronts).
+__device__ __forceinline__ bool any_slot_over(const MxParams& p) {
+    bool over = false;
+    for (int w = 0; w < p.num_groups; w += 64) {
+        const int g = w + (int)(threadIdx.x & 63);
+        over = over || __any(g < p.num_groups && min(p.group_data[g], p.m) > p.few);
+    }
+    return over;
+}
+
 // The tiles along M that hold a valid row, listed in LDS by one wavefront; returns how many.
 // Contiguous: block number * 2 + whether the next 128-row block, of the same expert, belongs
 // to the tile (256-row tiles pair the blocks of a run of one expert).  Masked: slot *
-// m_tiles + tile, of slots that the few-rows kernel leaves.
+// m_tiles + tile.
 template <int BM, int LAYOUT>
 __device__ int list_tiles(const MxParams& p, uint32_t* list) {
     const int lane = threadIdx.x & 63;
@@ -80,8 +91,7 @@ __device__ int list_tiles(const MxParams& p, uint32_t* list) {
         for (int w = p.first; w < p.last; w += 64) {
             const int i = w + lane;
             const int g = min(i, p.last - 1) / p.m_tiles;
-            const int rows = min(p.group_data[g], p.m);
-            const bool in = i < p.last && rows > p.few && (i - g * p.m_tiles) * BM < rows;
+            const bool in = i < p.last && (i - g * p.m_tiles) * BM < min(p.group_data[g], p.m);
             const uint64_t heads = __ballot(in);
             if (in) list[count + __popcll(heads & ((1ull << lane) - 1ull))] = (uint32_t)i;
             count += __popcll(heads);

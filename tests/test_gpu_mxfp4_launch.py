@@ -132,3 +132,24 @@ def test_more_tiles_than_a_launch_has_workgroups(gen):
     y = fp8bs.dequantize_mxfp4(q, sf)
     assert torch.equal(y.view(g // 1000, 1000, 128),
                        fp8bs.dequantize_mxfp4(want, words).expand(g // 1000, 1000, 128))
+
+
+@pytest.mark.parametrize("g,max_m,n,k", SLOTS + [(16, 256, 4096, 7168)])
+@pytest.mark.parametrize("most", [1, 16, 17, 32, 33, 64, 65, 128, 129])
+def test_the_hint_changes_no_result_of_slots_with_few_rows(gen, g, max_m, n, k, most):
+    # counts up to limits at which other kernels may take the slots, and one past them
+    if most > max_m:
+        pytest.skip("more rows than a slot has")
+    a, sfa = operand(gen, g, max_m, k)
+    b, sfb = operand(gen, g, n, k)
+    masked = torch.tensor([(37 * i + 11) % (most + 1) for i in range(g)], dtype=torch.int32, device="cuda")
+    masked[0] = most
+    runs = []
+    for expected in (0, 1, 40, max_m):
+        d = torch.zeros(g, max_m, n, dtype=torch.bfloat16, device="cuda")
+        fp8bs.fp8bs_grouped_masked_nt_mxfp4(a, sfa, b, sfb, d, masked, expected_m=expected)
+        runs.append(d)
+    assert all(torch.equal(d, runs[0]) for d in runs[1:])
+    assert runs[0][0, :most].any(-1).all() and not runs[0][0, most:].any()
+    rows = torch.arange(max_m, device="cuda")[None] < masked[:, None]
+    assert torch.equal(runs[0].any(-1), rows)
