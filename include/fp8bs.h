@@ -400,7 +400,8 @@ int fp8bs_quantize_128x128(const void* x, int x_dtype, void* q, float* sfb, int 
  * positive multiple of 128, at most 2^24.  Pointers are 16-byte aligned (grouped_layout and
  * masked_m 4-byte); sizes, valid rows, streams and errors are as for the FP8 calls above.
  * Neither expected_m nor the cap on CUs (fp8bs_set_num_cus) changes a result; every launch
- * of these calls keeps to the cap.
+ * of these calls keeps to the cap.  (The order in which K is summed follows from sizes and the
+ * device; of masked slots also from whether any masked_m passes a limit.)
  *
  * fp8bs_quantize_mxfp4 -- x f32 or bf16 [groups][rows][k] -> codes and exponents:
  *     e - 127 = floor(log2(max |x|)) - 2 over the block (at least -127; a block of zeros

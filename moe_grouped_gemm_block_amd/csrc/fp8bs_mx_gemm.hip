@@ -27,7 +27,7 @@
 // workgroups of an XCD (dealt round-robin) run neighbouring tiles, and copies the next
 // unit's first steps while it finishes and stores the present one.
 //
-// Bound by the clock that power allows (2.0 GHz; with zero operands everything runs 25%
+// Bound by the clock that power allows (1.9-1.95 GHz; with zero operands everything runs 25%
 // faster) and by the products with their fragment reads: the barrier taken out is worth 2-3%,
 // the copies 2%, the stores 5% (15% with 8 steps a tile), the activation 1%.
 // 4096 x 7168 x 16384: 247 us, 3.9 PFLOP/s (the matrix cores fed from registers alone, random
@@ -533,10 +533,10 @@ Times times(int layout, int epilogue, const MxParams& p, int groups, int rows, i
     if (layout == kContiguous) return t;
     for (int tm = 4; tm >= 1; tm /= 2) {                   // (of equals the tallest: reads B least)
         for (int tn = epilogue == kGatedQuant ? 4 : gated(epilogue) ? 2 : 1; tn <= 4; tn *= 2) {
-            const double rounds = ceil(tiles(16 * tm, 16 * tn) / cus), a_us = 16 * tm * row_bytes / 56e3;
-            const double tile = (layout == kMasked ? 3.3 : 1.3) + a_us + 16 * tn * row_bytes / 56e3;
-            double us = rounds * tile;
-            if (us < weights / 6e6 + rounds * a_us) us = weights / 6e6 + rounds * a_us;
+            const double rounds = ceil(tiles(16 * tm, 16 * tn) / cus), block = 16 * row_bytes / 56e3;
+            double us = rounds * ((layout == kMasked ? 3.3 : 1.3) + (tm + tn) * block);
+            const double drawn = weights / 6e6 + rounds * tm * block;
+            if (us < drawn) us = drawn;
             if (us < t.few) {
                 t.few = us;
                 t.tm = tm;

@@ -20,10 +20,10 @@
 // run both products in one launch, and split a long contraction into parts, FP32, that a second
 // launch adds in their order (no atomics; the split depends on sizes only).
 //
-// Bound by the matrix cores at the clock that power allows (2.1 GHz, busy 40-50% of the time),
-// by the widening (a tenth of a step) and by filling and storing a tile (8 us at 256x256).
-// 8192 rows, f = 2048, k = 7168: da 399-445 us, db 363-450, by card (1.1-1.2 and 1.1-1.3
-// PFLOP/s; the matrix cores fed from registers alone, random operands: 2.15).
+// Bound by the matrix cores at the clock that power allows (2.1-2.2 GHz; busy 53-57% of the CUs'
+// busy time in da, 45-58% in db), by the widening (a tenth of a step) and by filling and storing a
+// tile (8 us at 256x256).  8192 rows, f = 2048, k = 7168: da 399-445 us, db 363-450, by card
+// (1.1-1.2 and 1.1-1.3 PFLOP/s; the matrix cores fed from registers alone, random operands: 2.15).
 #include <math.h>
 
 #include <type_traits>

@@ -15,7 +15,9 @@
 // shape gives the same bits (0.1 to 1 us a launch slower than four runs).
 //
 // 1 x 4096 x 7168: 5.7 us, of which 3.7 are there at K = 128 too (launch, sum, store);
-// 128 x 2112 x 7168: 10 us; 64 x 2048 x 7168 gated, output quantised: 10 us.
+// 128 x 2112 x 7168: 10 us (132 tiles of 64 x 32: half of the CUs draw nothing, and K is not split
+// over workgroups); 64 x 2048 x 7168 gated, output quantised: 10 us (a quantised output fixes four
+// column blocks, so 16-row tiles draw every weight row four times).
 //
 // Tile row TM * j + i is row j of block i (columns likewise), as in fp8bs_mx_gemm.hip: a lane
 // owns 4 TN neighbouring columns and reads its scale words as vectors.  A gated tile has TN / 2
@@ -43,7 +45,8 @@ template <int TM, int TN>
 struct Ring {
     static constexpr int kWaves = TM + TN <= 4 ? 8 : 4;
     static constexpr int kStep = (TM + TN) * 2048 + 1024;      // bytes: rows, then scale words
-    // as deep as 160 KB allow
+    // steps in flight: as many as 160 KB hold, at most three (the waits below tell apart zero, one
+    // and two steps behind the one awaited; 16x16 tiles would have room for a fourth)
     static constexpr int kDepth = TM + TN <= 2 ? 3 : TM + TN <= 4 ? 2 : TM + TN <= 6 ? 3 : 2;
     static_assert(kWaves * kStep * kDepth <= 160 * 1024, "LDS of a CU");
 };

@@ -127,3 +127,10 @@ def test_sizes_past_any_memory_are_refused_or_counted_right():
     for r in ask([("backward", CONTIGUOUS, 1 << 20, 0, wide, 128, 1 << 20, 3),
                   ("layer", MASKED, 1, 0, 128, 128, 1 << 30, 300)]):
         assert r.status == 3 and not r.launches
+
+
+def test_of_equal_tiles_the_tallest():
+    # 64 rows, 7168 x 2048: 64x32 tiles and 32x64 ones draw as much and are as many rounds; the
+    # taller read the weights once (5.2 against 5.6 us)
+    (r,) = ask([("product", DENSE, 64, 0, 7168, 2048, 1)])
+    assert [x.args for x in r.launches] == [(4, 2, DENSE, 0)]
