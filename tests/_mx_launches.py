@@ -1,5 +1,6 @@
 """What the MXFP4 entry points launch for given sizes, asked on the CPU: builds
 tests/sanitize/mx_launches.cpp with the operators' host code (sanitizers on) and queries it."""
+import atexit
 import functools
 import os
 import shutil
@@ -29,6 +30,7 @@ def _run(cmd):
 @functools.lru_cache(None)
 def _build():
     tmp = tempfile.mkdtemp(prefix="mx_launches")
+    atexit.register(shutil.rmtree, tmp, True)
     sources = [os.path.join(CSRC, f) for f in (
         "fp8bs_mx_api.cpp", "fp8bs_mx_gemm.hip", "fp8bs_mx_stream.hip", "fp8bs_mx_grad.hip",
         "fp8bs_mx_quant.hip")] + [os.path.join(ROOT, "tests", "sanitize", "mx_launches.cpp")]
