@@ -79,7 +79,7 @@ def test_every_launch_keeps_to_the_cap():
 
 
 def test_no_launch_has_more_threads_than_a_32_bit_number():
-    # (the stand-in for the launch refuses such a grid, as the driver does)
+    # (the stand-in for the launch refuses such a grid, as HIP does)
     calls = [("quantise", DENSE, 1, 0, 0, 128, 20_000_000, 1), ("quantise", DENSE, 600_000_000, 0, 0, 128, 1, 1),
              ("dequantise", DENSE, 1, 0, 0, 128, 20_000_000), ("product", MASKED, 1, 0, 16, 128, 10_000_000),
              ("product", DENSE, 1, 0, 1 << 29, 128, 1), ("gated", MASKED, 1, 0, 32, 128, 30_000_000),
