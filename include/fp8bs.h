@@ -344,10 +344,12 @@ size_t fp8bs_noalloc_scratch_bytes(void);
 int64_t fp8bs_workspace_size(int layout, int64_t m, int n, int k, int num_groups,
                              int expected_m);
 
-/* Element types of quantiser inputs. */
+/* Element types of quantiser inputs, and of the calls between the products (further below);
+ * E4M3: codes with 1x128 scales. */
 typedef enum {
     FP8BS_DTYPE_F32 = 0,
-    FP8BS_DTYPE_BF16 = 1
+    FP8BS_DTYPE_BF16 = 1,
+    FP8BS_DTYPE_E4M3 = 2
 } fp8bs_dtype;
 
 /*
@@ -527,6 +529,140 @@ int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void*
                              const int32_t* group_data, int m, int expected_m, int f, int k,
                              int n, int num_groups, int activation, void* workspace,
                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Between the products of an FP8 mixture-of-experts layer: norm, dispatch and combine, gated
+ * activation, and the operands of the weight gradient.
+ *
+ * "1x128" is the form of fp8bs_quantize_1x128: codes [rows][k] and scales [k/128][ld(rows)],
+ * ld = fp8bs_get_sfa_ld; masked operands repeat both per slot.  "128x1" is the form that
+ * fp8bs_k_grouped_tn_contiguous reads: codes [R][n], R = rows rounded up to a multiple of 128,
+ * and scales f32 [R/128][ld(n)], one for each column and 128 rows.  Both quantise a block as
+ * fp8bs_quantize_1x128 does, from FP32 values (a NaN's code may have either sign).
+ * Sums are FP32 and each output is rounded once.  Optional buffers may be NULL.  Sizes,
+ * streams and errors are as for the calls above; pointers are 16-byte aligned, those to rstd, positions, weights, dweights, counts and group
+ * data 4-byte, ids as their type.  A workspace is device memory of at least the bytes that the
+ * size call gives, its contents ignored; less is refused with FP8BS_ERR_UNSUPPORTED, and two
+ * calls in flight must not share one.  Every launch keeps to the cap on CUs, which changes no
+ * result.
+ *
+ * fp8bs_rms_norm -- s = x + residual, rstd = 1 / sqrt(mean of s^2 over the row + eps),
+ * y = s * rstd * weight:
+ *   x         f32 or bf16 (x_dtype) [rows][k]; k a multiple of 8, of 128 with q; at most 32768
+ *   residual  f32 or bf16 (residual_dtype) [rows][k], optional (s = x without)
+ *   residual_out  s in residual_dtype, optional; may be residual
+ *   weight    f32 or bf16 (weight_dtype) [k]
+ *   y         f32 or bf16 (y_dtype) [rows][k], optional; may be x if of its type
+ *   q, sfa    y as e4m3, 1x128 (from y's FP32 values), optional
+ *   rstd      f32 [rows], optional
+ * At least one of residual_out, y and q is given; eps > 0.  The norm is that of the FP32 sum.
+ *
+ * fp8bs_rms_norm_backward -- with g = weight * dy and h = s * rstd:
+ *     dx = dresidual + rstd * (g - h * mean of g h over the row),  dweight = sum over rows of dy h
+ *   s         the norm's input (residual_out, or x without residual), rstd as it gave it
+ *   dy        f32 or bf16 (dy_dtype) [rows][k], the gradient of y
+ *   dresidual the gradient of residual_out, in dx's type (dx_dtype), optional
+ *   dx        the gradient of x and of residual; may be dresidual, dy or s if of its type
+ *   dweight   f32 [k], optional; accumulate != 0 adds to what it holds.  Written (zeros) for
+ *             rows == 0 too.  Without it no workspace is needed.
+ * Rows are added in an order that follows from the sizes alone.
+ */
+int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, void* residual_out,
+                   int residual_dtype, const void* weight, int weight_dtype, void* y, int y_dtype,
+                   void* q, float* sfa, float* rstd, int rows, int k, float eps,
+                   hipStream_t stream);
+int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k);
+int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd, const void* weight,
+                            int weight_dtype, const void* dy, int dy_dtype, const void* dresidual,
+                            void* dx, int dx_dtype, float* dweight, int accumulate, int rows,
+                            int k, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Dispatch: tokens' rows to the rows of their experts, in the contiguous or the masked layout.
+ *   ids        int32 or int64 (id_bytes 4 or 8) [tokens][topk]: the tokens' choices.  Choices
+ *              outside 0 .. num_groups-1 (experts elsewhere) take no part.  A token may choose an
+ *              expert twice.
+ *   x          [tokens][k] e4m3 with sfx (1x128), bf16 or f32 (x_dtype); k a multiple of 128 for
+ *              e4m3, else of 8
+ *   a, sfa     [m][k] (masked [num_groups][m][k]) in x's type, sfa for e4m3.  Rows that get no
+ *              token are not written.
+ *   group_data contiguous: grouped_layout [m], every entry written; masked: masked_m
+ *              [num_groups], the count or m if that is less
+ *   positions  int32 [tokens][topk]: the row of each choice (masked: slot * m + row), -1 for
+ *              none
+ *   counts     int32 [num_groups]: choices of each expert.  In the contiguous layout its segment
+ *              takes count rounded up to a multiple of 128 (a group size of
+ *              fp8bs_k_grouped_tn_contiguous).
+ * An expert's rows are in the order of its choices (token, then choice).  Contiguous: m is a
+ * multiple of 128 and at least fp8bs_moe_capacity(), which holds any choices; experts' segments
+ * follow each other from row 0 on.  Masked: choices past a slot's m rows are dropped.
+ * topk is at most 64, num_groups at most 1024, tokens * topk at most 2^30.
+ */
+int64_t fp8bs_moe_capacity(int64_t tokens, int topk, int num_groups);
+int64_t fp8bs_moe_dispatch_workspace_size(int layout, int64_t tokens, int topk, int num_groups,
+                                          int64_t m);
+int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, const void* x, int x_dtype,
+                       const float* sfx, void* a, float* sfa, int32_t* group_data,
+                       int32_t* positions, int32_t* counts, int tokens, int topk, int num_groups,
+                       int m, int k, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Combine: y[t] = sum over j of weights[t][j] * d[positions[t][j]], j ascending.
+ *   d          bf16 [rows][k] (masked: rows = num_groups * m); k a multiple of 8
+ *   positions  int32 [tokens][topk]; those outside 0 .. rows-1 are left out
+ *   weights    f32 [tokens][topk], NULL: ones (the gradient of dispatch with respect to x)
+ *   y          f32 or bf16 (y_dtype) [tokens][k]
+ *
+ * Its backward pass: with the products in FP32,
+ *     dd[positions[t][j]] = weights[t][j] * dy[t],  dweights[t][j] = <dy[t], d[positions[t][j]]>
+ *   dy         f32 or bf16 (dy_dtype) [tokens][k]
+ *   d          bf16 [slots * m][k], read for dweights only
+ *   dd         bf16 [slots * m][k], optional;  q, sfa: the same as e4m3, 1x128 per slot of m rows
+ *              (contiguous: slots = 1), k a multiple of 128, optional.  Rows of no choice are
+ *              not written.
+ *   dweights   f32 [tokens][topk], optional; 0 for a choice without a row
+ * At least one of dd, q and dweights is given.  No two positions may be the same row.
+ */
+int fp8bs_moe_combine(const void* d, const int32_t* positions, const float* weights, void* y,
+                      int y_dtype, int64_t rows, int tokens, int topk, int k, hipStream_t stream);
+int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const void* d,
+                               const int32_t* positions, const float* weights, void* dd, void* q,
+                               float* sfa, float* dweights, int slots, int m, int tokens, int topk,
+                               int k, hipStream_t stream);
+
+/*
+ * Gated activation h = act(gate) * up between two products, quantised for the second one.
+ *   layout     FP8BS_LAYOUT_DENSE, _CONTIGUOUS (group_data: grouped_layout) or _MASKED
+ *              (group_data: masked_m, num_groups slots of m rows)
+ *   g          bf16 [m][2f] (masked per slot), columns 0 .. f-1 gate, f .. 2f-1 up; f a multiple
+ *              of 128
+ *   hq, sfh    h as e4m3, 1x128, [m][f]
+ *   gq, sfg    g as e4m3, 1x128, [m][2f], optional: all that the backward pass needs of g
+ * Rows that are not valid (of the contiguous layout: a negative index) are not written.
+ *
+ * fp8bs_gated_quantize_backward -- at the values of g (e4m3 with sfg, or bf16: g_dtype):
+ *     dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ *   dh         bf16 [m][f]
+ *   d          [dgate dup] in bf16 [m][2f];  dq, sfd: as e4m3, 1x128;  dqt, sfdt: as e4m3, 128x1
+ *   hqt, sfht  h as e4m3, 128x1
+ * each optional, at least one of d, dq, dqt and hqt given.  grouped_layout int32 [m] or NULL
+ * (all rows valid; m then any).  Rows that are not valid are not read, nor written in d and dq;
+ * in dqt and hqt they, and the rows up to a multiple of 128, are zeros.
+ *
+ * fp8bs_quantize_128x1 -- x f32, bf16 or e4m3 with sfx (1x128) (x_dtype) [rows][n] -> q, sf
+ * (128x1); n a multiple of 16, of 128 for e4m3.  Rows with a negative grouped_layout entry
+ * (int32 [rows], optional; rows then a multiple of 128) are not read and count as zeros, as do
+ * the rows up to a multiple of 128.
+ */
+int fp8bs_gated_quantize(int layout, const void* g, void* hq, float* sfh, void* gq, float* sfg,
+                         const int32_t* group_data, int m, int f, int num_groups, int activation,
+                         hipStream_t stream);
+int fp8bs_gated_quantize_backward(const void* g, int g_dtype, const float* sfg, const void* dh,
+                                  void* d, void* dq, float* sfd, void* dqt, float* sfdt, void* hqt,
+                                  float* sfht, const int32_t* grouped_layout, int m, int f,
+                                  int activation, hipStream_t stream);
+int fp8bs_quantize_128x1(const void* x, int x_dtype, const float* sfx, void* q, float* sf,
+                         const int32_t* grouped_layout, int rows, int n, hipStream_t stream);
 
 /* Row alignment of expert segments in the contiguous layout (128).  Analogue
  * of get_mk_alignment_for_contiguous_layout (hada page, section "Tiện ích và

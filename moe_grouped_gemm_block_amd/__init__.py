@@ -826,3 +826,10 @@ from . import mxfp4 as _mxfp4  # noqa: E402  (needs the helpers above)
 from .mxfp4 import *  # noqa: E402,F401,F403
 
 __all__ += _mxfp4.__all__
+
+# ---- between the products (layer.py) --------------------------------------------
+
+from . import layer as _layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += _layer.__all__

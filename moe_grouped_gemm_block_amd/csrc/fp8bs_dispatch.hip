@@ -1,0 +1,567 @@
+// fp8bs_dispatch.hip -- tokens to their experts' rows and back, on gfx950.
+//
+// Assignment i = (token i / topk, choice i % topk) of expert e = ids[i] gets the rank r = number
+// of earlier assignments of e.  Its row: contiguous start[e] + r, start[e + 1] = start[e] +
+// roundup128(count[e]); masked e m + r, dropped if r >= m.  Ranks come from counts and ballots
+// alone, so they do not depend on scheduling.
+//
+//   dispatch  a[row] = x[token]                      (e4m3 rows with their scales, or values)
+//   combine   y[token] = sum_j w[j] d[row_j]         (FP32, j ascending)
+//   combine's backward  dd[row_j] = w[j] dy[token],  dw[j] = <dy[token], d[row_j]>
+//
+// All are bound by HBM: a token's row is read once and written topk times, or the other way.
+#include "fp8bs_layer.h"
+
+namespace fp8bs {
+namespace layer {
+namespace {
+
+constexpr int kMostGroups = 1024;
+constexpr int kMostTopk = 64;
+constexpr int kMostAssignments = 1 << 30;
+constexpr int kMostChunks = 256;
+
+struct DispatchParams {
+    const void* ids;            // int32 or int64 [tokens * topk]
+    const uint8_t* x;           // rows of row_bytes
+    const float* sfx;           // e4m3: [groups of columns][sfx_ld], else nullptr
+    uint8_t* a;
+    float* sfa;
+    int32_t* group_data;        // contiguous: the rows' experts; masked: the slots' rows
+    int32_t* positions;
+    int32_t* counts;
+    int32_t* chunk_counts;      // workspace [chunks][groups]
+    int32_t* source;            // workspace [rows]: the row's token
+    int ids64, masked;
+    int n, topk, tokens;        // n = tokens * topk
+    int groups, m;              // m: rows (contiguous) or rows of a slot
+    int vectors;                // 16-byte pieces of a row
+    int kb;                     // scales of a row (0: none)
+    int sfx_ld, sfa_ld;
+    int chunk, chunks;          // assignments of a chunk (a multiple of 256)
+    uint32_t units;
+};
+
+__device__ __forceinline__ int expert_of(const DispatchParams& p, int i) {
+    const int64_t e = p.ids64 ? ((const int64_t*)p.ids)[i] : (int64_t)((const int32_t*)p.ids)[i];
+    return e >= 0 && e < p.groups ? (int)e : -1;
+}
+
+// Lanes whose expert is this lane's (bits of the group number one by one).
+__device__ __forceinline__ uint64_t same_expert(int e, int groups) {
+    uint64_t same = ~0ull;
+    for (int b = 1; b < groups; b <<= 1) {
+        const uint64_t set = __ballot(e & b);
+        same &= (e & b) ? set : ~set;
+    }
+    return same & __ballot(e >= 0);
+}
+
+// start[0 .. groups]: first rows of the experts' segments from their counts (contiguous), by
+// 256 threads.
+__device__ __forceinline__ void segment_starts(const int* counts, int groups, int* start,
+                                               int* wave_sums) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int each = (groups + 255) / 256;     // at most 4
+    int own = 0;
+    for (int i = 0; i < each; ++i) {
+        const int e = t * each + i;
+        if (e < groups) own += (counts[e] + 127) & ~127;
+    }
+    int before = own;
+#pragma unroll
+    for (int w = 1; w < 64; w <<= 1) {
+        const int o = __shfl_up(before, w, 64);
+        if (lane >= w) before += o;
+    }
+    if (lane == 63) wave_sums[wave] = before;
+    __syncthreads();
+    before -= own;
+    for (int w = 0; w < wave; ++w) before += wave_sums[w];
+    for (int i = 0; i < each; ++i) {
+        const int e = t * each + i;
+        if (e < groups) {
+            start[e] = before;
+            before += (counts[e] + 127) & ~127;
+            if (e == groups - 1) start[groups] = before;
+        }
+    }
+    __syncthreads();
+}
+
+// Outputs that follow from the counts: this workgroup's share of the rows' experts, and by
+// workgroup 0 the counts.  256 threads.
+__device__ __forceinline__ void write_group_data(const DispatchParams& p, const int* counts,
+                                                 const int* start, int block, int blocks) {
+    if (block == 0)
+        for (int e = threadIdx.x; e < p.groups; e += 256) {
+            p.counts[e] = counts[e];
+            if (p.masked) p.group_data[e] = counts[e] < p.m ? counts[e] : p.m;
+        }
+    if (p.masked) return;
+    for (int64_t r = (int64_t)block * 256 + threadIdx.x; r < p.m; r += (int64_t)blocks * 256) {
+        int lo = 0, hi = p.groups;             // the last segment that starts at or before r
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= r) lo = mid; else hi = mid;
+        }
+        p.group_data[r] = r - start[lo] < counts[lo] ? lo : -1;
+    }
+}
+
+__device__ __forceinline__ int row_of(const DispatchParams& p, const int* start, int e, int rank) {
+    if (e < 0) return -1;
+    if (p.masked) return rank < p.m ? e * p.m + rank : -1;
+    return start[e] + rank;
+}
+
+// ---- many assignments: counts of chunks, ranks, rows -----------------------------
+
+__global__ void __launch_bounds__(256) dispatch_count_kernel(DispatchParams p) {
+    __shared__ int hist[kMostGroups];
+    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        for (int e = threadIdx.x; e < p.groups; e += 256) hist[e] = 0;
+        __syncthreads();
+        const int64_t end = (int64_t)(c + 1) * p.chunk < p.n ? (int64_t)(c + 1) * p.chunk : p.n;
+        for (int64_t i = (int64_t)c * p.chunk + threadIdx.x; i < end; i += 256) {
+            const int e = expert_of(p, (int)i);
+            if (e >= 0) atomicAdd(&hist[e], 1);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.groups; e += 256)
+            p.chunk_counts[(int64_t)c * p.groups + e] = hist[e];
+        __syncthreads();
+    }
+}
+
+// A chunk's four wavefronts take a quarter each, in order.
+__global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
+    __shared__ int total[kMostGroups], start[kMostGroups + 1], wave_sums[4];
+    __shared__ int next[4][kMostGroups];       // the wavefront's next rank of each expert
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        for (int e = t; e < p.groups; e += 256) {
+            total[e] = 0;
+            for (int w = 0; w < 4; ++w) next[w][e] = 0;
+        }
+        __syncthreads();
+        // (assignments of earlier chunks go into next[0], those of the chunk's earlier
+        // wavefronts below)
+        const int64_t all = (int64_t)p.chunks * p.groups;
+        for (int64_t i = t; i < all; i += 256) {
+            const int of = (int)(i / p.groups), e = (int)(i - (int64_t)of * p.groups);
+            const int v = p.chunk_counts[i];
+            if (v) {
+                atomicAdd(&total[e], v);
+                if (of < c) atomicAdd(&next[0][e], v);
+            }
+        }
+        const int quarter = p.chunk / 4;
+        const int64_t first = (int64_t)c * p.chunk + (int64_t)wave * quarter;
+        const int64_t end = first + quarter < p.n ? first + quarter : p.n;
+        if (wave < 3)
+            for (int64_t i = first + lane; i < end; i += 64) {
+                const int e = expert_of(p, (int)i);
+                if (e >= 0) atomicAdd(&next[wave + 1][e], 1);
+            }
+        __syncthreads();
+        for (int e = t; e < p.groups; e += 256)
+            for (int w = 1; w < 4; ++w) next[w][e] += next[w - 1][e];
+        segment_starts(total, p.groups, start, wave_sums);
+        write_group_data(p, total, start, c, p.chunks);
+        for (int64_t base = first; base < end; base += 64) {
+            const int64_t i = base + lane;
+            const int e = i < end ? expert_of(p, (int)i) : -1;
+            const uint64_t same = same_expert(e, p.groups);
+            const uint64_t below = same & ((1ull << lane) - 1ull);
+            const int rank = e < 0 ? 0 : next[wave][e] + __popcll(below);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (e >= 0 && below == 0) next[wave][e] += __popcll(same);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (i < end) {
+                const int row = row_of(p, start, e, rank);
+                p.positions[i] = row;
+                if (row >= 0 && p.kb) p.source[row] = (int)(i / p.topk);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int kRowPieces = 8;                  // 16-byte pieces of a lane at a time
+
+// A wavefront copies up to 8 KB of a token's row to the rows of its assignments.
+__device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int piece0, int lane,
+                                         const int32_t* rows) {
+    u32x4 v[kRowPieces];
+    const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
+#pragma unroll
+    for (int i = 0; i < kRowPieces; ++i) {
+        const int at = piece0 + 64 * i + lane;
+        if (at < p.vectors) v[i] = __builtin_nontemporal_load(from + at);
+    }
+    for (int j = 0; j < p.topk; ++j) {
+        const int row = rows[j];
+        if (row < 0) continue;
+        u32x4* to = (u32x4*)p.a + (int64_t)row * p.vectors;
+#pragma unroll
+        for (int i = 0; i < kRowPieces; ++i) {
+            const int at = piece0 + 64 * i + lane;
+            if (at < p.vectors) to[at] = v[i];
+        }
+    }
+}
+
+// Scales lie column-group-major, so they go by rows: a wavefront 64 neighbouring rows of the
+// output, whose scales it writes in runs of 256 bytes, reading where the rows' tokens are.
+__device__ __forceinline__ void copy_scales(const DispatchParams& p, uint32_t block, int lane) {
+    const uint32_t blocks = (uint32_t)((p.m + 63) / 64);
+    const int slot = (int)(block / blocks);
+    const int r = (int)(block - slot * blocks) * 64 + lane;
+    if (r >= p.m) return;
+    const bool held = p.masked ? r < p.group_data[slot] : p.group_data[r] >= 0;
+    if (!held) return;
+    const int token = p.source[(int64_t)slot * p.m + r];
+    float* to = p.sfa + (int64_t)slot * p.kb * p.sfa_ld + r;
+#pragma unroll 8
+    for (int c = 0; c < p.kb; ++c) to[(int64_t)c * p.sfa_ld] = p.sfx[(int64_t)c * p.sfx_ld + token];
+}
+
+__global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchParams p, int pieces,
+                                                            uint32_t scale_units) {
+    const int lane = threadIdx.x & 63;
+    // (uniform over the wavefront)
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    for (uint32_t unit = wave; unit < p.units; unit += gridDim.x * 4) {
+        if (unit < scale_units) {
+            copy_scales(p, unit, lane);
+            continue;
+        }
+        const uint32_t u = unit - scale_units;
+        const int token = (int)(u / pieces), piece = (int)(u - (uint32_t)token * pieces);
+        copy_row(p, token, piece * 64 * kRowPieces, lane, p.positions + (int64_t)token * p.topk);
+    }
+}
+
+// ---- few assignments: one launch ---------------------------------------------------
+
+constexpr int kFewAssignments = 4096;
+
+// Workgroup = one token at a time.  Each counts all assignments for itself.
+__global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
+    __shared__ int16_t ids[kFewAssignments];
+    __shared__ int total[kMostGroups], start[kMostGroups + 1], wave_sums[4];
+    __shared__ int32_t rows[kMostTopk];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int e = t; e < p.groups; e += 256) total[e] = 0;
+    __syncthreads();
+    for (int i = t; i < p.n; i += 256) {
+        const int e = expert_of(p, i);
+        ids[i] = (int16_t)e;
+        if (e >= 0) atomicAdd(&total[e], 1);
+    }
+    __syncthreads();
+    segment_starts(total, p.groups, start, wave_sums);
+    write_group_data(p, total, start, blockIdx.x, gridDim.x);
+    for (int token = blockIdx.x; token < p.tokens; token += gridDim.x) {
+        for (int j = wave; j < p.topk; j += 4) {
+            const int i = token * p.topk + j, e = ids[i];
+            int rank = 0;
+            for (int base = 0; base < i; base += 64)
+                rank += __popcll(__ballot(base + lane < i && ids[base + lane] == e));
+            const int row = row_of(p, start, e, rank);
+            if (lane == 0) {
+                rows[j] = row;
+                p.positions[i] = row;
+            }
+        }
+        __syncthreads();
+        for (int piece = wave; piece * 64 * kRowPieces < p.vectors; piece += 4)
+            copy_row(p, token, piece * 64 * kRowPieces, lane, rows);
+        for (int i = t; i < p.kb * p.topk; i += 256) {
+            const int j = i / p.kb, c = i - j * p.kb, row = rows[j];
+            if (row < 0) continue;
+            const int slot = p.masked ? row / p.m : 0;
+            p.sfa[((int64_t)slot * p.kb + c) * p.sfa_ld + row - slot * p.m] =
+                p.sfx[(int64_t)c * p.sfx_ld + token];
+        }
+        __syncthreads();
+    }
+}
+
+// ---- the way back ------------------------------------------------------------------
+
+struct CombineParams {
+    const uint16_t* d;
+    const int32_t* positions;
+    const float* weights;       // nullptr: ones
+    void* y;
+    int64_t rows;
+    int tokens, topk, k, pieces;
+    uint32_t units;
+};
+
+// A wavefront: 512 columns of a token.
+template <bool YB>
+__global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    for (uint32_t unit = wave; unit < p.units; unit += gridDim.x * 4) {
+        const int token = (int)(unit / p.pieces);
+        const int col = (int)(unit - (uint32_t)token * p.pieces) * 512 + lane * 8;
+        if (col >= p.k) continue;
+        const int32_t* at = p.positions + (int64_t)token * p.topk;
+        const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
+        float y[8] = {};
+        for (int j0 = 0; j0 < p.topk; j0 += 4) {
+            Eight<true> v[4];
+            float f[4];
+            bool in[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = j0 + j < p.topk ? at[j0 + j] : -1;
+                in[j] = row >= 0 && row < p.rows;
+                f[j] = in[j] && w ? w[j0 + j] : 1.0f;
+                if (in[j]) v[j].load(p.d, (int64_t)row * p.k + col);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in[j])
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] += f[j] * v[j][e];
+        }
+        store8(p.y, YB, (int64_t)token * p.k + col, y);
+    }
+}
+
+struct CombineBackwardParams {
+    const void* dy;
+    const uint16_t* d;
+    const int32_t* positions;
+    const float* weights;
+    uint16_t* dd;
+    uint8_t* q;
+    float* sfa;
+    float* dw;
+    int64_t rows;
+    int m, ld, tokens, topk, k;
+};
+
+// Workgroup = one token: 2048 columns at a time, eight a lane, 16 lanes a group of 128.  A
+// group's largest |w dy| is |w| times that of |dy| (rounding keeps the order), found once.
+template <bool GB>
+__global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardParams p) {
+    __shared__ float dots[4][kMostTopk];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (uint32_t unit = blockIdx.x; unit < (uint32_t)p.tokens; unit += gridDim.x) {
+        const uint32_t token = xcd_order(unit, (uint32_t)p.tokens);
+        const int32_t* at = p.positions + (int64_t)token * p.topk;
+        const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
+        for (int col0 = 0; col0 < p.k; col0 += 2048) {
+            const int col = col0 + t * 8;
+            const bool in = col < p.k;
+            Eight<GB> g;
+            g.zero();
+            if (in) g.load(p.dy, (int64_t)token * p.k + col);
+            float dy[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dy[e] = g[e];
+            const float top = max16(max8(dy));
+            for (int j = 0; j < p.topk; ++j) {
+                const int row = at[j];
+                if (row < 0 || row >= p.rows) {
+                    if (lane == 0 && col0 == 0) dots[wave][j] = 0.0f;
+                    continue;
+                }
+                const float f = w ? w[j] : 1.0f;
+                const int64_t to = (int64_t)row * p.k + col;
+                if (p.dw) {
+                    Eight<true> v;
+                    v.zero();
+                    if (in) v.load(p.d, to);
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot += dy[e] * v[e];
+                    dot = sum_wave(dot);
+                    if (lane == 0) dots[wave][j] = col0 == 0 ? dot : dots[wave][j] + dot;
+                }
+                if (in) {
+                    float dd[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dd[e] = f * dy[e];
+                    if (p.dd) store8(p.dd, true, to, dd);
+                    if (p.q) {
+                        float inv;             // (a NaN product is no maximum)
+                        const float sc =
+                            block_scale(__builtin_fmaxf(__builtin_fabsf(f) * top, 0.0f), inv);
+                        *(u32x2*)(p.q + to) = codes8(dd, inv);
+                        if ((lane & 15) == 0) {
+                            const int slot = row / p.m;
+                            p.sfa[((int64_t)slot * (p.k >> 7) + (col >> 7)) * p.ld + row -
+                                  slot * p.m] = sc;
+                        }
+                    }
+                }
+            }
+        }
+        if (p.dw) {
+            __syncthreads();
+            for (int j = t; j < p.topk; j += 256)
+                p.dw[(int64_t)token * p.topk + j] =
+                    (dots[0][j] + dots[1][j]) + (dots[2][j] + dots[3][j]);
+            __syncthreads();
+        }
+    }
+}
+
+// ---- launches -----------------------------------------------------------------
+
+bool counts_fit(int64_t tokens, int topk, int num_groups) {
+    return tokens >= 0 && topk >= 1 && topk <= kMostTopk && num_groups >= 1 &&
+           num_groups <= kMostGroups && tokens <= kMostAssignments / topk;
+}
+int64_t capacity_of(int64_t n, int num_groups) {
+    return (n + 127 * (n < num_groups ? n : (int64_t)num_groups)) / 128 * 128;
+}
+int chunk_of(int64_t n) {
+    const int64_t each = (n + kMostChunks - 1) / kMostChunks;
+    return each <= 1024 ? 1024 : (int)((each + 255) / 256 * 256);
+}
+bool few(int64_t n) { return n <= kFewAssignments; }
+
+}  // namespace
+}  // namespace layer
+}  // namespace fp8bs
+
+extern "C" int64_t fp8bs_moe_capacity(int64_t tokens, int topk, int num_groups) {
+    using namespace fp8bs::layer;
+    if (!counts_fit(tokens, topk, num_groups)) return -FP8BS_ERR_SHAPE;
+    return capacity_of(tokens * topk, num_groups);
+}
+
+extern "C" int64_t fp8bs_moe_dispatch_workspace_size(int layout, int64_t tokens, int topk,
+                                                     int num_groups, int64_t m) {
+    using namespace fp8bs::layer;
+    if (layout != FP8BS_LAYOUT_CONTIGUOUS && layout != FP8BS_LAYOUT_MASKED)
+        return -FP8BS_ERR_UNSUPPORTED;
+    if (!counts_fit(tokens, topk, num_groups) || m < 0 || m > kMaxRows) return -FP8BS_ERR_SHAPE;
+    const int64_t n = tokens * topk;
+    if (few(n)) return 0;
+    const int64_t rows = layout == FP8BS_LAYOUT_MASKED ? m * num_groups : m;
+    return (int64_t)kMostChunks * num_groups * 4 + (rows + 3) / 4 * 16;
+}
+
+extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, const void* x,
+                                  int x_dtype, const float* sfx, void* a, float* sfa,
+                                  int32_t* group_data, int32_t* positions, int32_t* counts,
+                                  int tokens, int topk, int num_groups, int m, int k,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    using namespace fp8bs::layer;
+    const int64_t need = fp8bs_moe_dispatch_workspace_size(layout, tokens, topk, num_groups, m);
+    if (need < 0) return (int)-need;
+    const bool masked = layout == FP8BS_LAYOUT_MASKED, e4m3 = x_dtype == FP8BS_DTYPE_E4M3;
+    if (!e4m3 && !value_type(x_dtype)) return FP8BS_ERR_UNSUPPORTED;
+    if (id_bytes != 4 && id_bytes != 8) return FP8BS_ERR_UNSUPPORTED;
+    if (k < 8 || k > kMaxK || k % (e4m3 ? 128 : 8) != 0) return FP8BS_ERR_SHAPE;
+    const int64_t n = (int64_t)tokens * topk;
+    if (masked ? (int64_t)m * num_groups > kMaxRows
+               : m % 128 != 0 || m < capacity_of(n, num_groups))
+        return FP8BS_ERR_SHAPE;
+    const int64_t rows = masked ? (int64_t)m * num_groups : m;
+    if (!aligned(counts, 4) || ((masked || m > 0) && !aligned(group_data, 4)))
+        return FP8BS_ERR_POINTER;
+    if (n > 0 && (!aligned(ids, (uintptr_t)id_bytes) || !aligned(positions, 4) || !aligned(x)))
+        return FP8BS_ERR_POINTER;
+    if (n > 0 && rows > 0 && (!aligned(a) || (e4m3 && (!aligned(sfx) || !aligned(sfa)))))
+        return FP8BS_ERR_POINTER;
+    if (need > 0 && !aligned(workspace)) return FP8BS_ERR_POINTER;
+    if (workspace_bytes < (size_t)need) return FP8BS_ERR_UNSUPPORTED;
+    DispatchParams p = {};
+    p.ids = ids;
+    p.x = (const uint8_t*)x;
+    p.sfx = sfx;
+    p.a = (uint8_t*)a;
+    p.sfa = sfa;
+    p.group_data = group_data;
+    p.positions = positions;
+    p.counts = counts;
+    p.ids64 = id_bytes == 8;
+    p.masked = masked;
+    p.n = (int)n;
+    p.topk = topk;
+    p.tokens = tokens;
+    p.groups = num_groups;
+    p.m = m;
+    p.vectors = k / (e4m3 ? 16 : x_dtype == FP8BS_DTYPE_BF16 ? 8 : 4);
+    p.kb = e4m3 ? k / 128 : 0;
+    p.sfx_ld = (int)fp8bs_get_sfa_ld(tokens);
+    p.sfa_ld = (int)fp8bs_get_sfa_ld(m);
+    if (few(n)) {
+        // (without tokens: the group data alone)
+        const int64_t units = tokens > 0 ? tokens : (m + 1023) / 1024 + 1;
+        return launch((const void*)dispatch_few_kernel, workgroups(units, 4), 256, p, stream);
+    }
+    p.chunk_counts = (int32_t*)workspace;
+    p.source = p.chunk_counts + (int64_t)kMostChunks * num_groups;
+    p.chunk = chunk_of(n);
+    p.chunks = (int)((n + p.chunk - 1) / p.chunk);
+    const int pieces = (p.vectors + 64 * kRowPieces - 1) / (64 * kRowPieces);
+    const int64_t scale_units = e4m3 ? (int64_t)((m + 63) / 64) * (masked ? num_groups : 1) : 0;
+    const int64_t units = scale_units + (int64_t)tokens * pieces;
+    if (units > 0x7fffffff) return FP8BS_ERR_UNSUPPORTED;
+    p.units = (uint32_t)units;
+    int st = launch((const void*)dispatch_count_kernel, workgroups(p.chunks, 4), 256, p, stream);
+    if (st != FP8BS_OK) return st;
+    st = launch((const void*)dispatch_rank_kernel, workgroups(p.chunks, 4), 256, p, stream);
+    if (st != FP8BS_OK || rows == 0) return st;
+    uint32_t su = (uint32_t)scale_units;
+    int pc = pieces;
+    void* args[] = {(void*)&p, (void*)&pc, (void*)&su};
+    return hipLaunchKernel((const void*)dispatch_rows_kernel, dim3(workgroups((units + 3) / 4, 8)),
+                           dim3(256), args, 0, stream) == hipSuccess ? FP8BS_OK : FP8BS_ERR_HIP;
+}
+
+extern "C" int fp8bs_moe_combine(const void* d, const int32_t* positions, const float* weights,
+                                 void* y, int y_dtype, int64_t rows, int tokens, int topk, int k,
+                                 hipStream_t stream) {
+    using namespace fp8bs::layer;
+    if (!counts_fit(tokens, topk, 1) || rows < 0 || rows > 0x7fffffff || k < 8 || k % 8 != 0 ||
+        k > kMaxK)
+        return FP8BS_ERR_SHAPE;
+    if (!value_type(y_dtype)) return FP8BS_ERR_UNSUPPORTED;
+    if (tokens == 0) return FP8BS_OK;
+    if ((rows > 0 ? !aligned(d) : false) || !aligned(positions, 4) || !aligned_or_null(weights, 4) ||
+        !aligned(y))
+        return FP8BS_ERR_POINTER;
+    const int pieces = (k + 511) / 512;
+    const int64_t units = (int64_t)tokens * pieces;
+    if (units > 0x7fffffff) return FP8BS_ERR_UNSUPPORTED;
+    CombineParams p = {(const uint16_t*)d, positions, weights, y, rows, tokens, topk, k, pieces,
+                       (uint32_t)units};
+    return launch(y_dtype == FP8BS_DTYPE_BF16 ? (const void*)combine_kernel<true>
+                                              : (const void*)combine_kernel<false>,
+                  workgroups((units + 3) / 4, 8), 256, p, stream);
+}
+
+extern "C" int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const void* d,
+                                          const int32_t* positions, const float* weights, void* dd,
+                                          void* q, float* sfa, float* dweights, int slots, int m,
+                                          int tokens, int topk, int k, hipStream_t stream) {
+    using namespace fp8bs::layer;
+    if (!counts_fit(tokens, topk, 1) || slots < 1 || m < 0 || (int64_t)slots * m > kMaxRows ||
+        k < 8 || k > kMaxK || k % (q ? 128 : 8) != 0)
+        return FP8BS_ERR_SHAPE;
+    if (!value_type(dy_dtype)) return FP8BS_ERR_UNSUPPORTED;
+    if (tokens == 0) return FP8BS_OK;
+    const int64_t rows = (int64_t)slots * m;
+    if (!aligned(dy) || !aligned(positions, 4) || !aligned_or_null(weights, 4) ||
+        !aligned_or_null(dd) || !aligned_or_null(q) || !aligned_or_null(dweights, 4) ||
+        (rows > 0 && ((dweights && !aligned(d)) || (q && !aligned(sfa)))) || !(dd || q || dweights))
+        return FP8BS_ERR_POINTER;
+    CombineBackwardParams p = {dy, (const uint16_t*)d, positions, weights, (uint16_t*)dd,
+                               (uint8_t*)q, sfa, dweights, rows, m > 0 ? m : 1,
+                               (int)fp8bs_get_sfa_ld(m), tokens, topk, k};
+    return launch(dy_dtype == FP8BS_DTYPE_BF16 ? (const void*)combine_backward_kernel<true>
+                                               : (const void*)combine_backward_kernel<false>,
+                  workgroups(tokens, 8), 256, p, stream);
+}

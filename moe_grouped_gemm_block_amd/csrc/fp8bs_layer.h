@@ -1,0 +1,226 @@
+// fp8bs_layer.h -- what the operators between the FP8 products share (norm, dispatch and
+// combine, gated activation, quantiser along tokens): checks, launches, and the device code of
+// loads, exchanges between lanes and e4m3 quantisation.
+#ifndef FP8BS_LAYER_H
+#define FP8BS_LAYER_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8bs.h"
+
+namespace fp8bs {
+namespace layer {
+
+constexpr int kMaxK = 1 << 24;                 // columns of an operand
+constexpr int kMaxRows = 0x7fffff00;           // rows, with room to round up
+
+inline bool aligned(const void* p, uintptr_t to = 16) { return p && ((uintptr_t)p & (to - 1)) == 0; }
+// an optional buffer
+inline bool aligned_or_null(const void* p, uintptr_t to = 16) { return ((uintptr_t)p & (to - 1)) == 0; }
+inline bool value_type(int dtype) { return dtype == FP8BS_DTYPE_F32 || dtype == FP8BS_DTYPE_BF16; }
+
+// Workgroups for `units` units of work when `per_cu` workgroups share a CU: one a unit, within
+// the process's cap on CUs and so few that their threads (at most 1024 each) are a 32-bit number.
+// Kernels go on to further units.
+inline unsigned workgroups(int64_t units, int per_cu) {
+    const int cap = fp8bs_get_num_cus();
+    const int64_t most = cap > 0 ? (int64_t)cap * per_cu : 1 << 21;
+    return (unsigned)(units < most ? units : most);
+}
+
+template <class P>
+int launch(const void* kernel, unsigned grid, int threads, P& params, hipStream_t stream,
+           size_t lds = 0) {
+    void* args[] = {(void*)&params};
+    return hipLaunchKernel(kernel, dim3(grid), dim3(threads), args, lds, stream) == hipSuccess
+               ? FP8BS_OK : FP8BS_ERR_HIP;
+}
+
+#ifdef __HIPCC__
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// (by value: a bit cast of a vector's element in place takes element 0)
+__device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
+__device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// Eight consecutive values as they lie: bf16 in 16 bytes, FP32 in 32.
+template <bool BF16>
+struct Eight {
+    u32x4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = u32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void load(const void* x, int64_t at) {
+        const u32x4* from = (const u32x4*)((const uint8_t*)x + at * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = from[i];
+    }
+    // read once, past the caches
+    __device__ __forceinline__ void stream(const void* x, int64_t at) {
+        const u32x4* from = (const u32x4*)((const uint8_t*)x + at * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = __builtin_nontemporal_load(from + i);
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (BF16) {
+            const uint32_t u = w[0][i >> 1];
+            return as_float((i & 1) ? u & 0xFFFF0000u : u << 16);
+        } else {
+            return as_float(w[i >> 2][i & 3]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        if constexpr (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[0][i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = as_bits(v[i]);
+        }
+    }
+    __device__ __forceinline__ void store(void* x, int64_t at) const {
+        u32x4* to = (u32x4*)((uint8_t*)x + at * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) to[i] = w[i];
+    }
+};
+
+__device__ __forceinline__ void store8(void* x, bool bf16, int64_t at, const float (&v)[8]) {
+    if (bf16) {
+        Eight<true> p;
+        p.set(v);
+        p.store(x, at);
+    } else {
+        Eight<false> p;
+        p.set(v);
+        p.store(x, at);
+    }
+}
+
+// Eight e4m3 codes, widened.
+__device__ __forceinline__ void widen_e4m3(u32x2 w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        v[4 * i] = lo[0];
+        v[4 * i + 1] = lo[1];
+        v[4 * i + 2] = hi[0];
+        v[4 * i + 3] = hi[1];
+    }
+}
+
+// ---- exchanges ----------------------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+    return as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_bits(x), CTRL, 0xF, 0xF, true));
+}
+// over 16 neighbouring lanes: quad permutations, then mirrors of 8 and 16 lanes
+__device__ __forceinline__ float max16(float x) {
+    x = __builtin_fmaxf(x, moved<0xB1>(x));
+    x = __builtin_fmaxf(x, moved<0x4E>(x));
+    x = __builtin_fmaxf(x, moved<0x141>(x));
+    return __builtin_fmaxf(x, moved<0x140>(x));
+}
+__device__ __forceinline__ float sum16(float x) {
+    x += moved<0xB1>(x);
+    x += moved<0x4E>(x);
+    x += moved<0x141>(x);
+    return x + moved<0x140>(x);
+}
+// v_permlane16_swap exchanges the odd rows (of 16 lanes) of its first operand with the even rows
+// of its second, v_permlane32_swap the upper half of the first with the lower half of the second.
+__device__ __forceinline__ void swap_rows(float& x, float& y) {
+    const auto a = __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(y), false, false);
+    x = as_float(a[0]);
+    y = as_float(a[1]);
+}
+__device__ __forceinline__ void swap_halves(float& x, float& y) {
+    const auto a = __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(y), false, false);
+    x = as_float(a[0]);
+    y = as_float(a[1]);
+}
+__device__ __forceinline__ float sum_wave(float x) {
+    x = sum16(x);
+    float y = x;
+    swap_rows(x, y);
+    x += y;
+    y = x;
+    swap_halves(x, y);
+    return x + y;
+}
+// Largest of eight values each over the lanes l, l + 16, l + 32, l + 48, two values an exchange:
+// lane l is left with those numbered first_of(l) and the one after.
+__device__ __forceinline__ f32x2 max_rows(float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        swap_rows(v[e], v[e + 4]);
+        v[e] = __builtin_fmaxf(v[e], v[e + 4]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        swap_halves(v[e], v[e + 2]);
+        v[e] = __builtin_fmaxf(v[e], v[e + 2]);
+    }
+    return f32x2{v[0], v[1]};
+}
+__device__ __forceinline__ int first_of(int lane) {
+    return ((lane >> 4) & 1) * 4 + (lane >> 5) * 2;
+}
+
+// ---- quantisation ---------------------------------------------------------------
+
+// Scale of a block whose largest magnitude is amax, and what its values are multiplied by; each
+// step one IEEE operation, as for fp8bs_quantize_1x128.
+__device__ __forceinline__ float block_scale(float amax, float& inv) {
+    const float a = amax < 1e-4f ? 1e-4f : amax;
+    inv = 448.0f / a;
+    return a / 448.0f;
+}
+// A NaN leaves the maximum as it is: the operand that is a number wins.
+__device__ __forceinline__ float max8(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+    return m;
+}
+// e4m3 codes of v * inv.  No clamp: |v| is at most the block's maximum, so the product passes
+// 448 by a rounding of FP32 at most, and the conversion gives 448 up to 464 (checked on MI355X;
+// it gives 0xFF for every NaN).
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], float inv) {
+    u32x2 out;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
+        out[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv,
+                                                           w, true);
+    }
+    return out;
+}
+
+// Workgroup b runs on XCD b % 8, each with an L2 of its own: XCD x takes a contiguous eighth of
+// the units, so that neighbouring units' parts of a cache line meet in one L2.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t unit, uint32_t units) {
+    const uint32_t each = units >> 3;
+    return unit < each * 8 ? (unit & 7) * each + (unit >> 3) : unit;
+}
+
+#endif  // __HIPCC__
+
+}  // namespace layer
+}  // namespace fp8bs
+
+#endif  // FP8BS_LAYER_H
