@@ -559,10 +559,11 @@ int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void*
  *
  * fp8bs_rms_norm_backward -- with g = weight * dy and h = s * rstd:
  *     dx = dresidual + rstd * (g - h * mean of g h over the row),  dweight = sum over rows of dy h
- *   s         the norm's input (residual_out, or x without residual), rstd as it gave it
+ *   s         the norm's input (residual_out, or x without residual; s_dtype), rstd as it gave it
  *   dy        f32 or bf16 (dy_dtype) [rows][k], the gradient of y
- *   dresidual the gradient of residual_out, in dx's type (dx_dtype), optional
- *   dx        the gradient of x and of residual; may be dresidual, dy or s if of its type
+ *   dresidual the gradient of residual_out, in s's type, optional
+ *   dx        the gradient of x and of residual, in s's type; may be dresidual, s or (of its
+ *             type) dy
  *   dweight   f32 [k], optional; accumulate != 0 adds to what it holds.  Written (zeros) for
  *             rows == 0 too.  Without it no workspace is needed.
  * Rows are added in an order that follows from the sizes alone.
@@ -574,8 +575,8 @@ int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, void* resid
 int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k);
 int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd, const void* weight,
                             int weight_dtype, const void* dy, int dy_dtype, const void* dresidual,
-                            void* dx, int dx_dtype, float* dweight, int accumulate, int rows,
-                            int k, void* workspace, size_t workspace_bytes, hipStream_t stream);
+                            void* dx, float* dweight, int accumulate, int rows, int k,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Dispatch: tokens' rows to the rows of their experts, in the contiguous or the masked layout.

@@ -39,6 +39,7 @@ struct DispatchParams {
     int kb;                     // scales of a row (0: none)
     int sfx_ld, sfa_ld;
     int chunk, chunks;          // assignments of a chunk (a multiple of 256)
+    int far;
     uint32_t units;
 };
 
@@ -188,18 +189,19 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
     }
 }
 
-constexpr int kRowPieces = 8;                  // 16-byte pieces of a lane at a time
+constexpr int kRowPieces = 4;                  // 16-byte pieces of a lane at a time
 
-// A wavefront copies up to 8 KB of a token's row to the rows of its assignments.
+// A wavefront copies up to 4 KB of a token's row to the rows of its assignments.
 __device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int piece0, int lane,
                                          const int32_t* rows) {
     u32x4 v[kRowPieces];
     const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
 #pragma unroll
-    for (int i = 0; i < kRowPieces; ++i) {
+    for (int i = 0; i < kRowPieces; ++i) {     // (past the row's end: its last piece again)
         const int at = piece0 + 64 * i + lane;
-        if (at < p.vectors) v[i] = __builtin_nontemporal_load(from + at);
+        v[i] = __builtin_nontemporal_load(from + (at < p.vectors ? at : p.vectors - 1));
     }
+#pragma unroll 1
     for (int j = 0; j < p.topk; ++j) {
         const int row = rows[j];
         if (row < 0) continue;
@@ -207,7 +209,9 @@ __device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int
 #pragma unroll
         for (int i = 0; i < kRowPieces; ++i) {
             const int at = piece0 + 64 * i + lane;
-            if (at < p.vectors) to[at] = v[i];
+            if (at >= p.vectors) continue;
+            if (p.far) __builtin_nontemporal_store(v[i], to + at);
+            else to[at] = v[i];
         }
     }
 }
@@ -344,72 +348,90 @@ struct CombineBackwardParams {
     float* sfa;
     float* dw;
     int64_t rows;
-    int m, ld, tokens, topk, k;
+    int m, ld, tokens, topk, k, far;
 };
 
-// Workgroup = one token: 2048 columns at a time, eight a lane, 16 lanes a group of 128.  A
-// group's largest |w dy| is |w| times that of |dy| (rounding keeps the order), found once.
+// Workgroup = one token, two choices at a time; a lane eight columns of each 2048, 16 lanes a group
+// of 128, two such runs at a time, their loads issued together.  A group's largest |w dy| is |w|
+// times that of |dy| (rounding keeps the order).
 template <bool GB>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardParams p) {
-    __shared__ float dots[4][kMostTopk];
+    __shared__ float dots[2][2][4];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (uint32_t unit = blockIdx.x; unit < (uint32_t)p.tokens; unit += gridDim.x) {
-        const uint32_t token = xcd_order(unit, (uint32_t)p.tokens);
+    int turn = 0;
+    for (uint32_t token = blockIdx.x; token < (uint32_t)p.tokens; token += gridDim.x) {
         const int32_t* at = p.positions + (int64_t)token * p.topk;
         const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
-        for (int col0 = 0; col0 < p.k; col0 += 2048) {
-            const int col = col0 + t * 8;
-            const bool in = col < p.k;
-            Eight<GB> g;
-            g.zero();
-            if (in) g.load(p.dy, (int64_t)token * p.k + col);
-            float dy[8];
+        for (int j0 = 0; j0 < p.topk; j0 += 2, turn ^= 1) {
+            int row[2];
+            bool in[2];
+            const uint16_t* from[2];
+            float f[2], dot[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dy[e] = g[e];
-            const float top = max16(max8(dy));
-            for (int j = 0; j < p.topk; ++j) {
-                const int row = at[j];
-                if (row < 0 || row >= p.rows) {
-                    if (lane == 0 && col0 == 0) dots[wave][j] = 0.0f;
-                    continue;
+            for (int j = 0; j < 2; ++j) {
+                row[j] = j0 + j < p.topk ? at[j0 + j] : -1;
+                in[j] = row[j] >= 0 && row[j] < p.rows;
+                f[j] = in[j] && w ? w[j0 + j] : 1.0f;
+                // (a choice without a row reads dy in its place)
+                from[j] = in[j] ? p.d + (int64_t)row[j] * p.k
+                                : (const uint16_t*)p.dy + (int64_t)token * p.k;
+            }
+            for (int col0 = t * 8; col0 < p.k; col0 += 4096) {
+                Eight<GB> g[2];
+                Eight<true> d[2][2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // (past the row's end: its last columns again)
+                    const int col = col0 + 2048 * i < p.k ? col0 + 2048 * i : p.k - 8;
+                    g[i].load(p.dy, (int64_t)token * p.k + col);
+                    if (p.dw)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            d[i][j].stream(from[j], col);
                 }
-                const float f = w ? w[j] : 1.0f;
-                const int64_t to = (int64_t)row * p.k + col;
-                if (p.dw) {
-                    Eight<true> v;
-                    v.zero();
-                    if (in) v.load(p.d, to);
-                    float dot = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dot += dy[e] * v[e];
-                    dot = sum_wave(dot);
-                    if (lane == 0) dots[wave][j] = col0 == 0 ? dot : dots[wave][j] + dot;
-                }
-                if (in) {
-                    float dd[8];
+                for (int i = 0; i < 2; ++i) {
+                    const int col = col0 + 2048 * i;
+                    if (col >= p.k) continue;
+                    float dy[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dd[e] = f * dy[e];
-                    if (p.dd) store8(p.dd, true, to, dd);
-                    if (p.q) {
-                        float inv;             // (a NaN product is no maximum)
-                        const float sc =
-                            block_scale(__builtin_fmaxf(__builtin_fabsf(f) * top, 0.0f), inv);
-                        *(u32x2*)(p.q + to) = codes8(dd, inv);
-                        if ((lane & 15) == 0) {
-                            const int slot = row / p.m;
-                            p.sfa[((int64_t)slot * (p.k >> 7) + (col >> 7)) * p.ld + row -
-                                  slot * p.m] = sc;
+                    for (int e = 0; e < 8; ++e) dy[e] = g[i][e];
+                    const float top = p.q ? max16(max8(dy)) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (!in[j]) continue;
+                        if (p.dw)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) dot[j] += dy[e] * d[i][j][e];
+                        float dd[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dd[e] = f[j] * dy[e];
+                        const int64_t to = (int64_t)row[j] * p.k + col;
+                        if (p.dd) put_values(p.dd, true, to, dd, p.far);
+                        if (p.q) {
+                            float inv;         // (a NaN product is no maximum)
+                            const float sc = block_scale(
+                                __builtin_fmaxf(__builtin_fabsf(f[j]) * top, 0.0f), inv);
+                            put_codes(p.q + to, codes8(dd, inv), p.far);
+                            if ((lane & 15) == 0) {
+                                const int slot = row[j] / p.m;
+                                p.sfa[((int64_t)slot * (p.k >> 7) + (col >> 7)) * p.ld + row[j] -
+                                      slot * p.m] = sc;
+                            }
                         }
                     }
                 }
             }
-        }
-        if (p.dw) {
-            __syncthreads();
-            for (int j = t; j < p.topk; j += 256)
-                p.dw[(int64_t)token * p.topk + j] =
-                    (dots[0][j] + dots[1][j]) + (dots[2][j] + dots[3][j]);
-            __syncthreads();
+            if (p.dw) {                        // (two buffers: one barrier a turn)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float sum = sum_wave(dot[j]);
+                    if (lane == 0) dots[turn][j][wave] = sum;
+                }
+                __syncthreads();
+                if (t < 2 && j0 + t < p.topk)
+                    p.dw[(int64_t)token * p.topk + j0 + t] =
+                        (dots[turn][t][0] + dots[turn][t][1]) + (dots[turn][t][2] + dots[turn][t][3]);
+            }
         }
     }
 }
@@ -423,9 +445,12 @@ bool counts_fit(int64_t tokens, int topk, int num_groups) {
 int64_t capacity_of(int64_t n, int num_groups) {
     return (n + 127 * (n < num_groups ? n : (int64_t)num_groups)) / 128 * 128;
 }
-int chunk_of(int64_t n) {
-    const int64_t each = (n + kMostChunks - 1) / kMostChunks;
-    return each <= 1024 ? 1024 : (int)((each + 255) / 256 * 256);
+// Assignments of a chunk, a multiple of 256.  A workgroup of the ranks' launch goes through all
+// chunks' counts, so there are fewer chunks where there are many experts.
+int chunk_of(int64_t n, int num_groups) {
+    int64_t chunks = 8192 / num_groups;
+    chunks = chunks < kMostChunks ? chunks : kMostChunks;
+    return (int)(((n + chunks - 1) / chunks + 255) / 256 * 256);
 }
 bool few(int64_t n) { return n <= kFewAssignments; }
 
@@ -496,6 +521,7 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     p.kb = e4m3 ? k / 128 : 0;
     p.sfx_ld = (int)fp8bs_get_sfa_ld(tokens);
     p.sfa_ld = (int)fp8bs_get_sfa_ld(m);
+    p.far = far_outputs((double)n * p.vectors * 16);
     if (few(n)) {
         // (without tokens: the group data alone)
         const int64_t units = tokens > 0 ? tokens : (m + 1023) / 1024 + 1;
@@ -503,7 +529,7 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     }
     p.chunk_counts = (int32_t*)workspace;
     p.source = p.chunk_counts + (int64_t)kMostChunks * num_groups;
-    p.chunk = chunk_of(n);
+    p.chunk = chunk_of(n, num_groups);
     p.chunks = (int)((n + p.chunk - 1) / p.chunk);
     const int pieces = (p.vectors + 64 * kRowPieces - 1) / (64 * kRowPieces);
     const int64_t scale_units = e4m3 ? (int64_t)((m + 63) / 64) * (masked ? num_groups : 1) : 0;
@@ -560,7 +586,8 @@ extern "C" int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const vo
         return FP8BS_ERR_POINTER;
     CombineBackwardParams p = {dy, (const uint16_t*)d, positions, weights, (uint16_t*)dd,
                                (uint8_t*)q, sfa, dweights, rows, m > 0 ? m : 1,
-                               (int)fp8bs_get_sfa_ld(m), tokens, topk, k};
+                               (int)fp8bs_get_sfa_ld(m), tokens, topk, k,
+                               far_outputs((double)tokens * topk * k * ((dd ? 2 : 0) + (q ? 1 : 0)))};
     return launch(dy_dtype == FP8BS_DTYPE_BF16 ? (const void*)combine_backward_kernel<true>
                                                : (const void*)combine_backward_kernel<false>,
                   workgroups(tokens, 8), 256, p, stream);

@@ -13,46 +13,80 @@ namespace fp8bs {
 namespace layer {
 namespace {
 
-// exp(-x) of x >= 0, within an ulp or so: v_exp_f32 of the product with log2 e and what that
-// product rounds away (104 is past the last result above 0).
-__device__ __forceinline__ float exp_minus(float x) {
+// The logistic function s of v and, where asked for, 1 - s, each within two or three units in the
+// last place: v_exp_f32 of the product with -log2 e, times what that product's rounding leaves
+// out, and v_rcp_f32.  (-v is cut off where the exponential is infinite and s 0.)
+template <bool GRAD>
+__device__ __forceinline__ float logistic(float v, float& rest) {
     constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float a = -__builtin_fminf(x, 104.0f);
+    const float a = __builtin_fminf(-v, 200.0f);
     const float hi = a * kHi;
     const float lo = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi);
-    return __builtin_fmaf(e, lo * kLn2, e);
-}
-
-// The logistic function s of v and 1 - s, neither by a difference.
-__device__ __forceinline__ void logistic(float v, float& s, float& rest) {
-    const float e = exp_minus(__builtin_fabsf(v));
-    const float d = 1.0f + e;
-    float r = __builtin_amdgcn_rcpf(d);
-    r = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);     // one step of Newton's
-    const float small = e * r;
-    s = v < 0.0f ? small : r;
-    rest = v < 0.0f ? r : small;
+    const float e = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    if (GRAD) rest = __builtin_fminf(e, 3.0e38f) * s;      // (0 where s is)
+    return s;
 }
 
 // act(v), and its derivative.
-template <bool GRAD>
-__device__ __forceinline__ float activate(int act, float v, float& slope) {
-    float s, rest;
-    if (act == FP8BS_ACT_SILU) {
-        logistic(v, s, rest);
-        if (GRAD) slope = s * (1.0f + v * rest);
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float activate(float v, float& slope) {
+    float rest;
+    if constexpr (ACT == FP8BS_ACT_SILU) {
+        const float s = logistic<GRAD>(v, rest), a = v * s;
+        if (GRAD) slope = __builtin_fmaf(a, rest, s);      // s (1 + v (1 - s))
+        return a;
+    } else {
+        // (1 + tanh(y)) / 2 is the logistic function of 2 y,  y = sqrt(2/pi) (v + 0.044715 v^3)
+        constexpr float c = 0.7978845608028654f;
+        const float v2 = v * v;
+        const float s = logistic<GRAD>(2.0f * c * v * __builtin_fmaf(0.044715f, v2, 1.0f), rest);
+        // (beyond |v| = 1e15, where s (1 - s) is 0, the square stays finite: 0 times it is 0)
+        if (GRAD)
+            slope = __builtin_fmaf(2.0f * c * v * s * rest,
+                                   __builtin_fmaf(0.134145f, __builtin_fminf(v2, 1e30f), 1.0f), s);
         return v * s;
     }
-    // (1 + tanh(y)) / 2 is the logistic function of 2 y,  y = sqrt(2/pi) (v + 0.044715 v^3)
-    constexpr float c = 0.7978845608028654f;
-    const float v2 = v * v;
-    logistic(2.0f * c * v * (1.0f + 0.044715f * v2), s, rest);
-    // (beyond |v| = 1e15, where s (1 - s) is 0, the square stays finite: 0 times it is 0)
-    if (GRAD)
-        slope = s + 2.0f * v * s * rest * c * (1.0f + 0.134145f * __builtin_fminf(v2, 1e30f));
-    return v * s;
 }
+
+__device__ __forceinline__ u32x2 take8(const uint8_t* base, uint32_t at) {
+    return __builtin_nontemporal_load((const u32x2*)(base + at));
+}
+// Eight bf16 or FP32 values
+template <bool BF16>
+__device__ __forceinline__ void take(const void* base, uint32_t at, Eight<BF16>& v) {
+    const u32x4* from = (const u32x4*)((const uint8_t*)base + at);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) v.w[i] = __builtin_nontemporal_load(from + i);
+}
+// Byte offset in a tile: row r (at most 127) of rows of `bytes` (less than 2^24), and on.
+__device__ __forceinline__ uint32_t place(int r, int bytes, int on) {
+    return __umul24((uint32_t)r, (uint32_t)bytes) + (uint32_t)on;
+}
+
+// Entries of grouped_layout for a lane's rows r0, r0 + 4, ...  Kept as they come (held() looks at
+// them when they are needed): a test here would wait for each before the loads behind it.
+__device__ __forceinline__ int clipped(int r, int last) { return r < last ? +r : +last; }
+template <int ROWS>
+struct Held {
+    int32_t entry[ROWS];
+    __device__ __forceinline__ void load(const int32_t* layout, int r0, int last) {
+        if (layout) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) entry[i] = layout[clipped(r0 + 4 * i, last)];
+        } else {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) entry[i] = 0;
+        }
+    }
+    // bit i: the i-th row holds a token
+    __device__ __forceinline__ uint32_t held(int r0, int last) const {
+        uint32_t in = 0;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) in |= (r0 + 4 * i <= last && entry[i] >= 0 ? 1u : 0u) << i;
+        return in;
+    }
+};
 
 struct GatedParams {
     const uint16_t* g;          // bf16 [slots][m][2f]
@@ -61,18 +95,21 @@ struct GatedParams {
     uint8_t* gq;                // or nullptr
     float* sfg;
     const int32_t* group_data;
-    int layout, m, f, ld, act;
-    int row_tiles;
+    int layout, m, f, ld;
+    int row_tiles, far;
     uint32_t tiles;
 };
 
-constexpr int kTileRows = 64;
+constexpr int kLaneRows = 2, kTileRows = 16 * kLaneRows;
 
 // Workgroup: 64 rows x a group of 128 columns, of gate and up; a lane eight columns of each, of
-// four rows, all loads issued before any arithmetic.
+// four rows, all loads issued before any arithmetic.  The lane divides for one of its group's
+// blocks (block_scales): h, gate and up of each of the four rows.
+template <int ACT, bool KEEP>
 __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
+    constexpr int kBlocks = KEEP ? 3 * kLaneRows : kLaneRows;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int seg = lane & 15, sub = lane >> 4;
+    const int seg = lane & 15, lane_row = wave * 4 * kLaneRows + (lane >> 4);
     const int fb = p.f >> 7;
     for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
         const int c = (int)(tile % fb);
@@ -81,46 +118,63 @@ __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
         const int held = p.layout == FP8BS_LAYOUT_MASKED && p.group_data[slot] < p.m
                              ? p.group_data[slot] : p.m;
         if (rt * kTileRows >= held) continue;
-        const int64_t slot_row = (int64_t)slot * p.m;
-        const int col = 128 * c + 8 * seg;
-        Eight<true> gate[4], up[4];
-        bool in[4];
+        const int64_t row0 = (int64_t)slot * p.m + rt * kTileRows;
+        const int last = held - 1 - rt * kTileRows;
+        const int32_t* layout =
+            p.layout == FP8BS_LAYOUT_CONTIGUOUS ? p.group_data + rt * kTileRows : nullptr;
+        const uint16_t* from = p.g + row0 * 2 * p.f + 128 * c;
+        Eight<true> gate[kLaneRows], up[kLaneRows];
+        Held<kLaneRows> rows;
+        rows.load(layout, lane_row, last);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = rt * kTileRows + wave * 16 + 4 * i + sub;
-            in[i] = r < held && (p.layout != FP8BS_LAYOUT_CONTIGUOUS || p.group_data[r] >= 0);
-            gate[i].zero();
-            up[i].zero();
-            if (in[i]) {
-                const int64_t at = (slot_row + r) * 2 * p.f + col;
-                gate[i].stream(p.g, at);
-                up[i].stream(p.g, at + p.f);
-            }
+        for (int i = 0; i < kLaneRows; ++i) {          // (rows past the last: that one again)
+            const int r = clipped(lane_row + 4 * i, last);
+            take(from, place(r, 4 * p.f, 16 * seg), gate[i]);
+            take(from + p.f, place(r, 4 * p.f, 16 * seg), up[i]);
         }
+        float h[kLaneRows][8], top[kBlocks], inv[kBlocks], unused;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = rt * kTileRows + wave * 16 + 4 * i + sub;
-            float h[8], unused;
+        for (int i = 0; i < kLaneRows; ++i) {
+            float g[8], u[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = activate<false>(p.act, gate[i][e], unused) * up[i][e];
-            float inv;
-            float s = block_scale(max16(max8(h)), inv);
-            if (in[i]) {
-                *(u32x2*)(p.hq + (slot_row + r) * p.f + col) = codes8(h, inv);
-                if (seg == 0) p.sfh[((int64_t)slot * fb + c) * p.ld + r] = s;
+            for (int e = 0; e < 8; ++e) {
+                g[e] = gate[i][e];
+                u[e] = up[i][e];
+                h[i][e] = activate<ACT, false>(g[e], unused) * u[e];
             }
-            if (!p.gq) continue;
+            top[i] = max8(h[i]);
+            if constexpr (KEEP) {
+                top[kLaneRows + i] = max8(g);
+                top[2 * kLaneRows + i] = max8(u);
+            }
+            // (widened again below: held as they came, they take half of the registers)
+            asm("" : "+v"(gate[i].w[0]), "+v"(up[i].w[0]));
+        }
+        const float scale = block_scales(top, seg, inv);
+        const uint32_t in = rows.held(lane_row, last);
+        const int block = block_of<kBlocks>(seg), of = block % kLaneRows;
+        if (seg < kBlocks && (in >> of & 1)) {
+            const int which = block / kLaneRows;
+            float* to = which == 0 ? p.sfh + ((int64_t)slot * fb + c) * p.ld
+                                   : p.sfg + ((int64_t)(slot * 2 + which - 1) * fb + c) * p.ld;
+            to[rt * kTileRows + lane_row + 4 * of] = scale;
+        }
+        uint8_t* const hq = p.hq + row0 * p.f + 128 * c;
+        uint8_t* const gq = p.gq + row0 * 2 * p.f + 128 * c;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+        for (int i = 0; i < kLaneRows; ++i) {
+            if (!(in >> i & 1)) continue;
+            const int r = lane_row + 4 * i;
+            put_codes(hq + place(r, p.f, 8 * seg), codes8(h[i], inv[i]), p.far);
+            if constexpr (KEEP) {
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = half ? up[i][e] : gate[i][e];
-                s = block_scale(max16(max8(v)), inv);
-                if (in[i]) {
-                    *(u32x2*)(p.gq + (slot_row + r) * 2 * p.f + half * p.f + col) = codes8(v, inv);
-                    if (seg == 0)
-                        p.sfg[((int64_t)slot * 2 * fb + half * fb + c) * p.ld + r] = s;
-                }
+                for (int e = 0; e < 8; ++e) v[e] = gate[i][e];
+                put_codes(gq + place(r, 2 * p.f, 8 * seg), codes8(v, inv[kLaneRows + i]), p.far);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = up[i][e];
+                put_codes(gq + p.f + place(r, 2 * p.f, 8 * seg), codes8(v, inv[2 * kLaneRows + i]),
+                          p.far);
             }
         }
     }
@@ -128,20 +182,21 @@ __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
 
 // ---- 128 rows x 128 columns: blocks both ways -----------------------------------
 
-// A tile's workgroup: eight wavefronts of 16 rows, a lane eight columns (8 (lane % 16) ..) of the
-// rows 16 wave + 4 i + lane / 16, i = 0 .. 3.
+// A tile's workgroup: kWaves wavefronts of 128 / kWaves rows, a lane eight columns
+// (8 (lane % 16) ..) of the rows first_row(wave) + 4 i + lane / 16.
 constexpr int kBlock = 128;
 
-// Scales of the tile's 128-row blocks, and what their columns are multiplied by.  top: largest
-// magnitudes of the lane's columns over its four rows.  N arrays at a time.
-template <int N>
+template <int N, int WAVES>
 struct ColumnScales {
-    float most[N][8][kBlock];   // the wavefronts' largest magnitudes
+    float most[N][WAVES][kBlock];   // the wavefronts' largest magnitudes
     float inv[N][kBlock];
 };
-template <int N>
-__device__ __forceinline__ void column_scales(ColumnScales<N>& lds, float (&top)[N][8],
-                                              float* const (&to)[N], const int (&cols)[N]) {
+// Scales of the tile's 128-row blocks, and what their columns are multiplied by, of N arrays.
+// top: largest magnitudes of the lane's columns over its rows.  (The first barrier also keeps
+// inv until every wavefront has read the tile's before.)
+template <int N, int WAVES>
+__device__ __forceinline__ void column_scales(ColumnScales<N, WAVES>& lds, float (&top)[N][8],
+                                              float* const (&to)[N], int cols) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, seg = lane & 15;
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -151,13 +206,13 @@ __device__ __forceinline__ void column_scales(ColumnScales<N>& lds, float (&top)
         const int n = t >> 7, col = t & 127;
         float m = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) m = __builtin_fmaxf(m, lds.most[n][w][col]);
+        for (int w = 0; w < WAVES; ++w) m = larger(m, lds.most[n][w][col]);
         float inv;
         const float s = block_scale(m, inv);
         lds.inv[n][col] = inv;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i == n && to[i] && col < cols[i]) to[i][col] = s;
+            if (i == n && to[i] && col < cols) to[i][col] = s;
     }
     __syncthreads();
 }
@@ -185,102 +240,152 @@ struct GatedBackwardParams {
     uint8_t* hqt;               // 128x1, or nullptr
     float* sfht;
     const int32_t* grouped_layout;
-    int m, f, ld, act;
+    int m, f, ld, far;
     uint32_t tiles;
 };
 
+constexpr int kGradWaves = 16, kGradRows = 32 / kGradWaves;   // rows of a lane
+
+// A lane's inputs as they lie.
 template <bool KEPT>
-__global__ void __launch_bounds__(512) gated_backward_kernel(GatedBackwardParams p) {
-    __shared__ ColumnScales<3> lds;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int seg = lane & 15, sub = lane >> 4;
+struct GradInputs {
+    Eight<true> dh[kGradRows];
+    u32x2 gate_q[KEPT ? kGradRows : 1], up_q[KEPT ? kGradRows : 1];
+    float gate_s[KEPT ? kGradRows : 1], up_s[KEPT ? kGradRows : 1];
+    Eight<true> gate[KEPT ? 1 : kGradRows], up[KEPT ? 1 : kGradRows];
+    Held<kGradRows> rows;
+};
+
+template <bool KEPT>
+__device__ __forceinline__ void fetch(const GatedBackwardParams& p, uint32_t tile, int lane_row,
+                                      int seg, GradInputs<KEPT>& v) {
     const int fb = p.f >> 7;
+    const int c = (int)(tile % fb), rt = (int)(tile / fb);
+    const int64_t row0 = (int64_t)rt * kBlock;
+    const int last = p.m - 1 - row0 < kBlock - 1 ? (int)(p.m - 1 - row0) : kBlock - 1;
+    const int32_t* layout = p.grouped_layout ? p.grouped_layout + row0 : nullptr;
+    const uint16_t* dh = p.dh + row0 * p.f + kBlock * c;
+    const int64_t at = row0 * 2 * p.f + kBlock * c;
+    v.rows.load(layout, lane_row, last);
+#pragma unroll
+    for (int i = 0; i < kGradRows; ++i) {      // (rows past the last: that one again)
+        const int r = clipped(lane_row + 4 * i, last);
+        take(dh, place(r, 2 * p.f, 16 * seg), v.dh[i]);
+        if constexpr (KEPT) {
+            const uint8_t* g = (const uint8_t*)p.g + at;
+            v.gate_q[i] = take8(g, place(r, 2 * p.f, 8 * seg));
+            v.up_q[i] = take8(g + p.f, place(r, 2 * p.f, 8 * seg));
+            v.gate_s[i] = (p.sfg + (int64_t)c * p.ld + row0)[r];
+            v.up_s[i] = (p.sfg + (int64_t)(fb + c) * p.ld + row0)[r];
+        } else {
+            const uint16_t* g = (const uint16_t*)p.g + at;
+            take(g, place(r, 4 * p.f, 16 * seg), v.gate[i]);
+            take(g + p.f, place(r, 4 * p.f, 16 * seg), v.up[i]);
+        }
+    }
+}
+
+template <int ACT, bool KEPT>
+__global__ void __launch_bounds__(64 * kGradWaves)
+    gated_backward_kernel(GatedBackwardParams p) {
+    __shared__ ColumnScales<3, kGradWaves> lds;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int seg = lane & 15, lane_row = wave * 4 * kGradRows + (lane >> 4);
+    const int fb = p.f >> 7;
+    GradInputs<KEPT> v;
+    fetch<KEPT>(p, blockIdx.x, lane_row, seg, v);
     for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
         const int c = (int)(tile % fb), rt = (int)(tile / fb);
-        const int col = kBlock * c + 8 * seg;
-        float dg[4][8], du[4][8], h[4][8];
+        const int64_t row0 = (int64_t)rt * kBlock;
+        const int last = p.m - 1 - row0 < kBlock - 1 ? (int)(p.m - 1 - row0) : kBlock - 1;
+        const uint32_t held = v.rows.held(lane_row, last);
+        float dg[kGradRows][8], du[kGradRows][8], h[kGradRows][8];
         float top[3][8] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)rt * kBlock + wave * 16 + 4 * i + sub;
-            const bool in = r < p.m && (!p.grouped_layout || p.grouped_layout[r] >= 0);
-            const int64_t at = r * 2 * p.f + col;
-            float gate[8] = {}, up[8] = {};
-            Eight<true> dh;
-            dh.zero();
-            if (in) {
-                dh.stream(p.dh, r * p.f + col);
-                if constexpr (KEPT) {
-                    widen_e4m3(__builtin_nontemporal_load((const u32x2*)((const uint8_t*)p.g + at)),
-                               gate);
-                    widen_e4m3(__builtin_nontemporal_load(
-                                   (const u32x2*)((const uint8_t*)p.g + at + p.f)), up);
-                    const float sg = p.sfg[(int64_t)c * p.ld + r];
-                    const float su = p.sfg[(int64_t)(fb + c) * p.ld + r];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        gate[e] *= sg;
-                        up[e] *= su;
-                    }
-                } else {
-                    Eight<true> a, b;
-                    a.stream(p.g, at);
-                    b.stream(p.g, at + p.f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        gate[e] = a[e];
-                        up[e] = b[e];
-                    }
-                }
+        for (int i = 0; i < kGradRows; ++i) {
+            // a row that holds no token is zeros
+            const bool in = (held >> i) & 1;
+            float gate[8], up[8];
+            if constexpr (KEPT) {
+                widen_e4m3(in ? v.gate_q[i] : u32x2{0, 0}, gate);
+                widen_e4m3(in ? v.up_q[i] : u32x2{0, 0}, up);
+                v.gate_s[i] = in ? v.gate_s[i] : 0.0f;
+                v.up_s[i] = in ? v.up_s[i] : 0.0f;
+            } else {
+                if (!in) v.gate[i].zero();
+                if (!in) v.up[i].zero();
             }
+            if (!in) v.dh[i].zero();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                if constexpr (KEPT) {
+                    gate[e] *= v.gate_s[i];
+                    up[e] *= v.up_s[i];
+                } else {
+                    gate[e] = v.gate[i][e];
+                    up[e] = v.up[i][e];
+                }
+                const float dh = v.dh[i][e];
                 float slope;
-                const float act = activate<true>(p.act, gate[e], slope);
-                // (zeros in a row that holds no token)
-                dg[i][e] = dh[e] * up[e] * slope;
-                du[i][e] = dh[e] * act;
+                const float act = activate<ACT, true>(gate[e], slope);
+                dg[i][e] = dh * up[e] * slope;
+                du[i][e] = dh * act;
                 h[i][e] = act * up[e];
                 top[0][e] = __builtin_fmaxf(top[0][e], __builtin_fabsf(dg[i][e]));
                 top[1][e] = __builtin_fmaxf(top[1][e], __builtin_fabsf(du[i][e]));
                 top[2][e] = __builtin_fmaxf(top[2][e], __builtin_fabsf(h[i][e]));
             }
-            if (p.d && in) {
-                store8(p.d, true, at, dg[i]);
-                store8(p.d, true, at + p.f, du[i]);
-            }
-            if (p.dq) {
-                float inv_g, inv_u;
-                const float sg = block_scale(max16(max8(dg[i])), inv_g);
-                const float su = block_scale(max16(max8(du[i])), inv_u);
-                if (in) {
-                    *(u32x2*)(p.dq + at) = codes8(dg[i], inv_g);
-                    *(u32x2*)(p.dq + at + p.f) = codes8(du[i], inv_u);
-                    if (seg == 0) {
-                        p.sfd[(int64_t)c * p.ld + r] = sg;
-                        p.sfd[(int64_t)(fb + c) * p.ld + r] = su;
-                    }
-                }
-            }
         }
+        if (tile + gridDim.x < p.tiles) fetch<KEPT>(p, tile + gridDim.x, lane_row, seg, v);
+        if (p.dq) {
+            float most[2 * kGradRows], inv[2 * kGradRows];
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i) {
+                most[i] = max8(dg[i]);
+                most[kGradRows + i] = max8(du[i]);
+            }
+            const float scale = block_scales(most, seg, inv);
+            if (seg < 2 * kGradRows && (held >> (seg % kGradRows) & 1))
+                p.sfd[(int64_t)(seg / kGradRows * fb + c) * p.ld + row0 + lane_row +
+                      4 * (seg % kGradRows)] = scale;
+            uint8_t* const to = p.dq + row0 * 2 * p.f + kBlock * c;
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i)
+                if (held >> i & 1) {
+                    const uint32_t at = place(lane_row + 4 * i, 2 * p.f, 8 * seg);
+                    put_codes(to + at, codes8(dg[i], inv[i]), p.far);
+                    put_codes(to + p.f + at, codes8(du[i], inv[kGradRows + i]), p.far);
+                }
+        }
+        if (p.d)
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i)
+                if (held >> i & 1) {
+                    const int64_t at =
+                        (row0 + lane_row + 4 * i) * 2 * p.f + kBlock * c + 8 * seg;
+                    store8(p.d, true, at, dg[i]);
+                    store8(p.d, true, at + p.f, du[i]);
+                }
         if (!p.dqt && !p.hqt) continue;
         float* const to[3] = {
             p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + kBlock * c : nullptr,
             p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + p.f + kBlock * c : nullptr,
             p.hqt ? p.sfht + (int64_t)rt * p.f + kBlock * c : nullptr};
-        const int cols[3] = {kBlock, kBlock, kBlock};
-        column_scales<3>(lds, top, to, cols);
+        column_scales(lds, top, to, kBlock);
+        uint8_t* const dqt = p.dqt + row0 * 2 * p.f + kBlock * c;
+        uint8_t* const hqt = p.hqt + row0 * p.f + kBlock * c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)rt * kBlock + wave * 16 + 4 * i + sub;
+        for (int i = 0; i < kGradRows; ++i) {
+            const int r = lane_row + 4 * i;
             if (p.dqt) {
-                *(u32x2*)(p.dqt + r * 2 * p.f + col) = column_codes(dg[i], &lds.inv[0][8 * seg]);
-                *(u32x2*)(p.dqt + r * 2 * p.f + p.f + col) =
-                    column_codes(du[i], &lds.inv[1][8 * seg]);
+                const uint32_t at = place(r, 2 * p.f, 8 * seg);
+                put_codes(dqt + at, column_codes(dg[i], &lds.inv[0][8 * seg]), p.far);
+                put_codes(dqt + p.f + at, column_codes(du[i], &lds.inv[1][8 * seg]), p.far);
             }
-            if (p.hqt) *(u32x2*)(p.hqt + r * p.f + col) = column_codes(h[i], &lds.inv[2][8 * seg]);
+            if (p.hqt)
+                put_codes(hqt + place(r, p.f, 8 * seg), column_codes(h[i], &lds.inv[2][8 * seg]),
+                          p.far);
         }
-        __syncthreads();                       // before lds is written again
     }
 }
 
@@ -290,60 +395,90 @@ struct ColumnParams {
     uint8_t* q;
     float* sf;
     const int32_t* grouped_layout;
-    int rows, n, ldx, ld, col_tiles;
+    int rows, n, ldx, ld, col_tiles, far;
     uint32_t tiles;
 };
 
+constexpr int kColumnWaves = 8, kColumnRows = 32 / kColumnWaves;
+
+template <int DTYPE>
+struct ColumnInputs {
+    static constexpr bool kKept = DTYPE == FP8BS_DTYPE_E4M3;
+    u32x2 q[kKept ? kColumnRows : 1];
+    float s[kKept ? kColumnRows : 1];
+    Eight<DTYPE == FP8BS_DTYPE_BF16> x[kKept ? 1 : kColumnRows];
+    Held<kColumnRows> rows;
+};
+template <int DTYPE>
+__device__ __forceinline__ void fetch(const ColumnParams& p, uint32_t tile, int lane_row, int seg,
+                                      ColumnInputs<DTYPE>& v) {
+    const int c = (int)(tile % p.col_tiles), rt = (int)(tile / p.col_tiles);
+    const int64_t row0 = (int64_t)rt * kBlock;
+    const int last = p.rows - 1 - row0 < kBlock - 1 ? (int)(p.rows - 1 - row0) : kBlock - 1;
+    const int32_t* layout = p.grouped_layout ? p.grouped_layout + row0 : nullptr;
+    const int64_t at = row0 * p.n + kBlock * c;
+    const int col = clipped(8 * seg, p.n - kBlock * c - 8);
+    v.rows.load(layout, lane_row, last);
+#pragma unroll
+    for (int i = 0; i < kColumnRows; ++i) {    // (rows past the last: that one again; columns alike)
+        const int r = clipped(lane_row + 4 * i, last);
+        if constexpr (DTYPE == FP8BS_DTYPE_E4M3) {
+            v.q[i] = take8((const uint8_t*)p.x + at, place(r, p.n, col));
+            v.s[i] = (p.sfx + (int64_t)c * p.ldx + row0)[r];
+        } else if constexpr (DTYPE == FP8BS_DTYPE_BF16) {
+            take((const uint16_t*)p.x + at, place(r, 2 * p.n, 2 * col), v.x[i]);
+        } else {
+            take((const float*)p.x + at, place(r, 4 * p.n, 4 * col), v.x[i]);
+        }
+    }
+}
+
 // Tile of 128 x 128 as above; n need not be a multiple of 128.
 template <int DTYPE>
-__global__ void __launch_bounds__(512) quant_128x1_kernel(ColumnParams p) {
-    __shared__ ColumnScales<1> lds;
+__global__ void __launch_bounds__(64 * kColumnWaves) quant_128x1_kernel(ColumnParams p) {
+    __shared__ ColumnScales<1, kColumnWaves> lds;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int seg = lane & 15, sub = lane >> 4;
-    for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const int seg = lane & 15, lane_row = wave * 4 * kColumnRows + (lane >> 4);
+    for (uint32_t unit = blockIdx.x; unit < p.tiles; unit += gridDim.x) {
+        const uint32_t tile = xcd_order(unit, p.tiles);
         const int c = (int)(tile % p.col_tiles), rt = (int)(tile / p.col_tiles);
-        const int col = kBlock * c + 8 * seg;
-        float v[4][8] = {};
+        const int64_t row0 = (int64_t)rt * kBlock;
+        ColumnInputs<DTYPE> x;
+        fetch<DTYPE>(p, tile, lane_row, seg, x);
+        const uint32_t held = x.rows.held(
+            lane_row, p.rows - 1 - row0 < kBlock - 1 ? (int)(p.rows - 1 - row0) : kBlock - 1);
+        float v[kColumnRows][8];
         float top[1][8] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)rt * kBlock + wave * 16 + 4 * i + sub;
-            const bool in = r < p.rows && col < p.n &&
-                            (!p.grouped_layout || p.grouped_layout[r] >= 0);
-            if (in) {
-                const int64_t at = r * p.n + col;
-                if constexpr (DTYPE == FP8BS_DTYPE_E4M3) {
-                    widen_e4m3(__builtin_nontemporal_load((const u32x2*)((const uint8_t*)p.x + at)),
-                               v[i]);
-                    const float s = p.sfx[(int64_t)c * p.ldx + r];
+        for (int i = 0; i < kColumnRows; ++i) {
+            const bool in = (held >> i) & 1;
+            if constexpr (DTYPE == FP8BS_DTYPE_E4M3) {
+                widen_e4m3(in ? x.q[i] : u32x2{0, 0}, v[i]);
+                const float s = in ? x.s[i] : 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] *= s;
-                } else {
-                    Eight<DTYPE == FP8BS_DTYPE_BF16> x;
-                    x.stream(p.x, at);
+                for (int e = 0; e < 8; ++e) v[i][e] *= s;
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] = x[e];
-                }
+                for (int e = 0; e < 8; ++e) v[i][e] = in ? x.x[i][e] : 0.0f;
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kColumnRows; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 top[0][e] = __builtin_fmaxf(top[0][e], __builtin_fabsf(v[i][e]));
         float* const to[1] = {p.sf + (int64_t)rt * p.ld + kBlock * c};
-        const int cols[1] = {p.n - kBlock * c};
-        column_scales<1>(lds, top, to, cols);
-        if (col < p.n)
+        column_scales(lds, top, to, p.n - kBlock * c);
+        uint8_t* const q = p.q + (int64_t)rt * kBlock * p.n + kBlock * c;
+        if (kBlock * c + 8 * seg < p.n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t r = (int64_t)rt * kBlock + wave * 16 + 4 * i + sub;
-                *(u32x2*)(p.q + r * p.n + col) = column_codes(v[i], &lds.inv[0][8 * seg]);
-            }
-        __syncthreads();                       // before lds is written again
+            for (int i = 0; i < kColumnRows; ++i)
+                put_codes(q + place(lane_row + 4 * i, p.n, 8 * seg),
+                     column_codes(v[i], &lds.inv[0][8 * seg]), p.far);
     }
 }
 
+constexpr int kMostColumns = 1 << 20;
 bool activation_known(int act) { return act == FP8BS_ACT_SILU || act == FP8BS_ACT_GELU_TANH; }
 
 }  // namespace
@@ -358,7 +493,7 @@ extern "C" int fp8bs_gated_quantize(int layout, const void* g, void* hq, float* 
         layout != FP8BS_LAYOUT_MASKED)
         return FP8BS_ERR_UNSUPPORTED;
     const int slots = layout == FP8BS_LAYOUT_MASKED ? num_groups : 1;
-    if (m < 0 || m > kMaxRows || f < 128 || f % 128 != 0 || f > kMaxK / 2 || slots < 1 ||
+    if (m < 0 || m > kMaxRows || f < 128 || f % 128 != 0 || f > kMostColumns || slots < 1 ||
         (layout == FP8BS_LAYOUT_CONTIGUOUS && m % 128 != 0))
         return FP8BS_ERR_SHAPE;
     if (!activation_known(activation)) return FP8BS_ERR_UNSUPPORTED;
@@ -370,8 +505,15 @@ extern "C" int fp8bs_gated_quantize(int layout, const void* g, void* hq, float* 
         (gq && !aligned(sfg)) || (layout != FP8BS_LAYOUT_DENSE && !aligned(group_data, 4)))
         return FP8BS_ERR_POINTER;
     GatedParams p = {(const uint16_t*)g, (uint8_t*)hq, sfh, (uint8_t*)gq, sfg, group_data, layout,
-                     m, f, (int)fp8bs_get_sfa_ld(m), activation, row_tiles, (uint32_t)tiles};
-    return launch((const void*)gated_quant_kernel, workgroups(p.tiles, 8), 256, p, stream);
+                     m, f, (int)fp8bs_get_sfa_ld(m), row_tiles,
+                     far_outputs((double)slots * m * f * (gq ? 3 : 1)), (uint32_t)tiles};
+    const void* fn =
+        activation == FP8BS_ACT_SILU
+            ? gq ? (const void*)gated_quant_kernel<FP8BS_ACT_SILU, true>
+                 : (const void*)gated_quant_kernel<FP8BS_ACT_SILU, false>
+            : gq ? (const void*)gated_quant_kernel<FP8BS_ACT_GELU_TANH, true>
+                 : (const void*)gated_quant_kernel<FP8BS_ACT_GELU_TANH, false>;
+    return launch(fn, workgroups(p.tiles, 8), 256, p, stream);
 }
 
 extern "C" int fp8bs_gated_quantize_backward(const void* g, int g_dtype, const float* sfg,
@@ -380,7 +522,7 @@ extern "C" int fp8bs_gated_quantize_backward(const void* g, int g_dtype, const f
                                              const int32_t* grouped_layout, int m, int f,
                                              int activation, hipStream_t stream) {
     using namespace fp8bs::layer;
-    if (m < 0 || m > kMaxRows || f < 128 || f % 128 != 0 || f > kMaxK / 2 ||
+    if (m < 0 || m > kMaxRows || f < 128 || f % 128 != 0 || f > kMostColumns ||
         (grouped_layout && m % 128 != 0))
         return FP8BS_ERR_SHAPE;
     if ((g_dtype != FP8BS_DTYPE_E4M3 && g_dtype != FP8BS_DTYPE_BF16) || !activation_known(activation))
@@ -396,10 +538,19 @@ extern "C" int fp8bs_gated_quantize_backward(const void* g, int g_dtype, const f
         return FP8BS_ERR_POINTER;
     GatedBackwardParams p = {g, sfg, (const uint16_t*)dh, (uint16_t*)d, (uint8_t*)dq, sfd,
                              (uint8_t*)dqt, sfdt, (uint8_t*)hqt, sfht, grouped_layout, m, f,
-                             (int)fp8bs_get_sfa_ld(m), activation, (uint32_t)tiles};
-    return launch(kept ? (const void*)gated_backward_kernel<true>
-                       : (const void*)gated_backward_kernel<false>,
-                  workgroups(p.tiles, 2), 512, p, stream);
+                             (int)fp8bs_get_sfa_ld(m),
+                             far_outputs((double)m * f * ((d ? 4 : 0) + (dq ? 2 : 0) +
+                                                          (dqt ? 2 : 0) + (hqt ? 1 : 0))),
+                             (uint32_t)tiles};
+    const int cus = compute_units();
+    if (cus <= 0) return FP8BS_ERR_HIP;
+    const void* fn =
+        activation == FP8BS_ACT_SILU
+            ? kept ? (const void*)gated_backward_kernel<FP8BS_ACT_SILU, true>
+                   : (const void*)gated_backward_kernel<FP8BS_ACT_SILU, false>
+            : kept ? (const void*)gated_backward_kernel<FP8BS_ACT_GELU_TANH, true>
+                   : (const void*)gated_backward_kernel<FP8BS_ACT_GELU_TANH, false>;
+    return launch(fn, p.tiles < (uint32_t)cus ? p.tiles : (unsigned)cus, 64 * kGradWaves, p, stream);
 }
 
 extern "C" int fp8bs_quantize_128x1(const void* x, int x_dtype, const float* sfx, void* q,
@@ -408,7 +559,7 @@ extern "C" int fp8bs_quantize_128x1(const void* x, int x_dtype, const float* sfx
     using namespace fp8bs::layer;
     const bool kept = x_dtype == FP8BS_DTYPE_E4M3;
     if (!kept && !value_type(x_dtype)) return FP8BS_ERR_UNSUPPORTED;
-    if (rows < 0 || rows > kMaxRows || n < 16 || n > kMaxK || n % (kept ? 128 : 16) != 0 ||
+    if (rows < 0 || rows > kMaxRows || n < 16 || n > kMostColumns || n % (kept ? 128 : 16) != 0 ||
         (grouped_layout && rows % 128 != 0))
         return FP8BS_ERR_SHAPE;
     const int col_tiles = (n + 127) / 128;
@@ -419,9 +570,10 @@ extern "C" int fp8bs_quantize_128x1(const void* x, int x_dtype, const float* sfx
         !aligned_or_null(grouped_layout, 4))
         return FP8BS_ERR_POINTER;
     ColumnParams p = {x, sfx, (uint8_t*)q, sf, grouped_layout, rows, n, (int)fp8bs_get_sfa_ld(rows),
-                      (int)fp8bs_get_sfa_ld(n), col_tiles, (uint32_t)tiles};
+                      (int)fp8bs_get_sfa_ld(n), col_tiles, far_outputs((double)rows * n),
+                      (uint32_t)tiles};
     const void* fn = kept ? (const void*)quant_128x1_kernel<FP8BS_DTYPE_E4M3>
                      : x_dtype == FP8BS_DTYPE_BF16 ? (const void*)quant_128x1_kernel<FP8BS_DTYPE_BF16>
                                                    : (const void*)quant_128x1_kernel<FP8BS_DTYPE_F32>;
-    return launch(fn, workgroups(p.tiles, 4), 512, p, stream);
+    return launch(fn, workgroups(p.tiles, 4), 64 * kColumnWaves, p, stream);
 }

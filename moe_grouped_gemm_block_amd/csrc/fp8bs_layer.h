@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fp8bs.h"
 
 namespace fp8bs {
@@ -28,6 +30,27 @@ inline unsigned workgroups(int64_t units, int per_cu) {
     const int64_t most = cap > 0 ? (int64_t)cap * per_cu : 1 << 21;
     return (unsigned)(units < most ? units : most);
 }
+
+// Compute units of the current device under the process's cap; 0 on error.
+inline int compute_units() {
+    static std::atomic<int> known[64];             // 0: not asked yet
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    const bool kept = dev >= 0 && dev < 64;
+    if (kept) cus = known[dev].load(std::memory_order_relaxed);
+    if (cus == 0) {
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            return 0;
+        if (kept) known[dev].store(cus, std::memory_order_relaxed);
+    }
+    const int cap = fp8bs_get_num_cus();
+    return cap > 0 && cap < cus ? cap : cus;
+}
+
+// Whether outputs of so many bytes are written past the caches: they would not stay there for the
+// next kernel (the last level holds 256 MB), and streaming runs 5-10% faster past them (norm of
+// 16384 x 7168: 180 us through them, 172 past them; its gradients 192 and 170).
+inline int far_outputs(double bytes) { return bytes > 64e6; }
 
 template <class P>
 int launch(const void* kernel, unsigned grid, int threads, P& params, hipStream_t stream,
@@ -109,6 +132,27 @@ __device__ __forceinline__ void store8(void* x, bool bf16, int64_t at, const flo
     }
 }
 
+// The same past the caches (far): for outputs that are too large for them.
+__device__ __forceinline__ void put_values(void* x, bool bf16, int64_t at, const float (&v)[8],
+                                           bool far) {
+    if (!far) {
+        store8(x, bf16, at, v);
+    } else if (bf16) {
+        Eight<true> p;
+        p.set(v);
+        __builtin_nontemporal_store(p.w[0], (u32x4*)((uint8_t*)x + at * 2));
+    } else {
+        Eight<false> p;
+        p.set(v);
+        __builtin_nontemporal_store(p.w[0], (u32x4*)((uint8_t*)x + at * 4));
+        __builtin_nontemporal_store(p.w[1], (u32x4*)((uint8_t*)x + at * 4) + 1);
+    }
+}
+__device__ __forceinline__ void put_codes(uint8_t* to, u32x2 codes, bool far) {
+    if (far) __builtin_nontemporal_store(codes, (u32x2*)to);
+    else *(u32x2*)to = codes;
+}
+
 // Eight e4m3 codes, widened.
 __device__ __forceinline__ void widen_e4m3(u32x2 w, float (&v)[8]) {
 #pragma unroll
@@ -128,12 +172,18 @@ template <int CTRL>
 __device__ __forceinline__ float moved(float x) {
     return as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_bits(x), CTRL, 0xF, 0xF, true));
 }
-// over 16 neighbouring lanes: quad permutations, then mirrors of 8 and 16 lanes
+// Largest of two numbers >= 0, by their bits: for floats from exchanges the compiler would make
+// sure first that they are no signalling NaN.
+__device__ __forceinline__ float larger(float a, float b) {
+    const uint32_t x = as_bits(a), y = as_bits(b);
+    return as_float(x > y ? x : y);
+}
+// (magnitudes) over 16 neighbouring lanes: quad permutations, then mirrors of 8 and 16 lanes
 __device__ __forceinline__ float max16(float x) {
-    x = __builtin_fmaxf(x, moved<0xB1>(x));
-    x = __builtin_fmaxf(x, moved<0x4E>(x));
-    x = __builtin_fmaxf(x, moved<0x141>(x));
-    return __builtin_fmaxf(x, moved<0x140>(x));
+    x = larger(x, moved<0xB1>(x));
+    x = larger(x, moved<0x4E>(x));
+    x = larger(x, moved<0x141>(x));
+    return larger(x, moved<0x140>(x));
 }
 __device__ __forceinline__ float sum16(float x) {
     x += moved<0xB1>(x);
@@ -162,18 +212,18 @@ __device__ __forceinline__ float sum_wave(float x) {
     swap_halves(x, y);
     return x + y;
 }
-// Largest of eight values each over the lanes l, l + 16, l + 32, l + 48, two values an exchange:
+// Largest of eight magnitudes each over the lanes l, l + 16, l + 32, l + 48, two values an exchange:
 // lane l is left with those numbered first_of(l) and the one after.
 __device__ __forceinline__ f32x2 max_rows(float (&v)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         swap_rows(v[e], v[e + 4]);
-        v[e] = __builtin_fmaxf(v[e], v[e + 4]);
+        v[e] = larger(v[e], v[e + 4]);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         swap_halves(v[e], v[e + 2]);
-        v[e] = __builtin_fmaxf(v[e], v[e + 2]);
+        v[e] = larger(v[e], v[e + 2]);
     }
     return f32x2{v[0], v[1]};
 }
@@ -189,6 +239,61 @@ __device__ __forceinline__ float block_scale(float amax, float& inv) {
     const float a = amax < 1e-4f ? 1e-4f : amax;
     inv = 448.0f / a;
     return a / 448.0f;
+}
+// Two blocks' maxima over a pair of lanes: the lane whose bit is set goes on with b, the other
+// with a.  (Unary plus: a conditional of two variables would be one of their addresses.)
+template <int CTRL>
+__device__ __forceinline__ float join(float a, float b, bool bit) {
+    const float own = bit ? +b : +a, other = bit ? +a : +b;
+    return larger(own, moved<CTRL>(other));
+}
+// Largest magnitudes of N blocks that 16 neighbouring lanes share, from the lanes' own: lane seg is
+// left with block_of<N>(seg)'s.  Neighbours 1 and 2 away by quad permutations, 4 and 8 by
+// rotations, which keep the lower bits.
+template <int N>
+__device__ __forceinline__ float block_max(const float (&m)[N], int seg) {
+    static_assert(N == 1 || N == 2 || N == 4 || N == 6, "");
+    float z;
+    if constexpr (N == 1) {
+        z = larger(m[0], moved<0xB1>(m[0]));
+        z = larger(z, moved<0x4E>(z));
+    } else if constexpr (N == 2) {
+        z = join<0xB1>(m[0], m[1], seg & 1);
+        z = larger(z, moved<0x4E>(z));
+    } else {
+        z = join<0x4E>(join<0xB1>(m[0], m[1], seg & 1), join<0xB1>(m[2], m[3], seg & 1), seg & 2);
+    }
+    if constexpr (N == 6) {
+        float y = join<0xB1>(m[4], m[5], seg & 1);
+        y = larger(y, moved<0x4E>(y));
+        z = join<0x124>(z, y, seg & 4);
+    } else {
+        z = larger(z, moved<0x124>(z));
+    }
+    return larger(z, moved<0x128>(z));
+}
+// The block of which lane seg holds the maximum above; each is in one lane below N.
+template <int N>
+__device__ __forceinline__ int block_of(int seg) {
+    return N == 6 ? ((seg & 4) ? 4 + (seg & 1) : seg & 3) : seg & (N - 1);
+}
+
+template <int N, int J = 0>
+__device__ __forceinline__ void factors(float inv, float (&all)[N]) {
+    if constexpr (J < N) {
+        all[J] = moved<0x150 + J>(inv);        // lane J's, to all 16
+        factors<N, J + 1>(inv, all);
+    }
+}
+// Scales of N blocks that 16 neighbouring lanes share, top[j] the lane's own largest magnitude in
+// block j.  A lane divides for its block_of() alone, so that a division is made once and not N
+// times.  Gives that block's scale, and all blocks' factors.
+template <int N>
+__device__ __forceinline__ float block_scales(const float (&top)[N], int seg, float (&inv)[N]) {
+    float f;
+    const float s = block_scale(block_max(top, seg), f);
+    factors<N>(f, inv);
+    return s;
 }
 // A NaN leaves the maximum as it is: the operand that is a number wins.
 __device__ __forceinline__ float max8(const float (&v)[8]) {

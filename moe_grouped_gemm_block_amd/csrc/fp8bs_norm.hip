@@ -25,24 +25,9 @@ struct NormParams {
     float* rstd;                // or nullptr
     int rows, k, ld;
     float eps;
-    int w_bf16, y_bf16;
-    int tile_rows;              // rows of a unit (their scales leave together)
-    uint32_t tiles;
+    int out_bf16, y_bf16, far;
+    uint32_t units;
 };
-
-__device__ __forceinline__ void load_weights(const void* w, int bf16, int col, float (&v)[8]) {
-    if (bf16) {
-        Eight<true> t;
-        t.load(w, col);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = t[e];
-    } else {
-        Eight<false> t;
-        t.load(w, col);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = t[e];
-    }
-}
 
 // Sum over the lanes of a row: W wavefronts.  `part` alternates between two buffers, so one
 // barrier a sum is enough.
@@ -61,96 +46,86 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[16], int& turn) 
     return v;
 }
 
-// Workgroup = one row at a time on W = 4 or 16 wavefronts, or four rows (W = 1, a wavefront
-// each); a lane holds NV runs of eight columns, 512 W apart, 16 lanes a 128-column group.  A unit
-// is tile_rows rows, one after another, the next one's loads issued before this one's sum; their
-// scales meet in LDS and leave as runs of tile_rows floats (they lie K-group-major).
-template <int W, int NV, bool XB, bool RB>
+// Workgroup = one row on W = 4 or 16 wavefronts, or four rows (W = 1, a wavefront each).  A lane
+// holds NV runs of eight columns, 512 W apart, 16 lanes a 128-column group.  RES: type of residual
+// (0 none, 1 bf16, 2 FP32).  16384 x 7168 in bf16 takes 141 us (5.9 TB/s; a copy past the caches
+// runs at 6.2): loads issued together, the weight's before the sum, a division for NV groups.  Eight rows
+// a workgroup, the next one's loads before this one's sum and scales written together, took 150.
+template <int W, int NV, bool XB, int RES, bool WB>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormParams p) {
-    extern __shared__ float scales[];          // [k/128][tile_rows]
     __shared__ float part[2][16];
     constexpr int kThreads = W == 16 ? 1024 : 256, kAtOnce = kThreads / 64 / W;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wr = wave % W, sub = wave / W;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, seg = lane & 15;
+    const int wr = wave % W;
     const float over_k = 1.0f / (float)p.k;
     int turn = 0;
-    int col[NV];
+    int col[NV], from[NV];                     // (past the last column: the last ones again)
+    Eight<WB> w[NV];                           // as they come, for all rows
 #pragma unroll
-    for (int i = 0; i < NV; ++i) col[i] = ((i * W + wr) * 64 + lane) * 8;
-
-    for (uint32_t unit = blockIdx.x; unit < p.tiles; unit += gridDim.x) {
-        const uint32_t tile = xcd_order(unit, p.tiles);
-        const int64_t row0 = (int64_t)tile * p.tile_rows;
+    for (int i = 0; i < NV; ++i) {
+        col[i] = ((i * W + wr) * 64 + lane) * 8;
+        from[i] = col[i] < p.k ? +col[i] : p.k - 8;
+        w[i].load(p.w, from[i]);
+    }
+    for (uint32_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+        const int64_t row = (int64_t)unit * kAtOnce + wave / W;
+        const bool in = row < p.rows;
+        const int64_t at = (in ? +row : (int64_t)p.rows - 1) * p.k;
         Eight<XB> x[NV];
-        Eight<RB> r[NV];
-        auto fetch = [&](int64_t row) {
+        Eight<RES != 2> r[RES ? NV : 1];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                x[i].zero();
-                r[i].zero();
-                if (row < p.rows && col[i] < p.k) {
-                    x[i].load(p.x, row * p.k + col[i]);
-                    if (p.res) r[i].load(p.res, row * p.k + col[i]);
-                }
+        for (int i = 0; i < NV; ++i) {
+            x[i].stream(p.x, at + from[i]);
+            if constexpr (RES) r[i].stream(p.res, at + from[i]);
+        }
+        float s[NV][8];
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[i][e] = x[i][e];
+                if constexpr (RES) s[i][e] += r[i][e];
+                if (col[i] >= p.k) s[i][e] = 0.0f;
+                sq += s[i][e] * s[i][e];
             }
-        };
-        fetch(row0 + sub);
-        for (int rr = sub; rr < p.tile_rows; rr += kAtOnce) {
-            const int64_t row = row0 + rr;
-            float s[NV][8];
-            float sq = 0.0f;
+        if (p.out && in)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (col[i] < p.k) put_values(p.out, p.out_bf16, at + col[i], s[i], p.far);
+        const float ms = row_sum<W>(sq, part, turn) * over_k;
+        float rstd = 1.0f / sqrtf(ms + p.eps), told = rstd;
+        if (ms > 3.0e38f) {                    // the squares overflow: those of s 2^-96 do not
+            sq = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    s[i][e] = x[i][e] + r[i][e];
+                    s[i][e] *= 0x1p-96f;
                     sq += s[i][e] * s[i][e];
                 }
-            if (rr + kAtOnce < p.tile_rows) fetch(row + kAtOnce);
-            const bool in = row < p.rows;
-            if (p.out && in)
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (col[i] < p.k) store8(p.out, RB, row * p.k + col[i], s[i]);
-            float ms = row_sum<W>(sq, part, turn) * over_k;
-            float rstd = 1.0f / sqrtf(ms + p.eps), told = rstd;
-            if (ms > 3.0e38f) {                // the squares overflow: of s 2^-96 they do not
-                sq = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        s[i][e] *= 0x1p-96f;
-                        sq += s[i][e] * s[i][e];
-                    }
-                rstd = 1.0f / sqrtf(row_sum<W>(sq, part, turn) * over_k);
-                told = rstd * 0x1p-96f;
-            }
-            if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (col[i] >= p.k) continue;
-                float y[8], w[8];
-                load_weights(p.w, p.w_bf16, col[i], w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = s[i][e] * rstd * w[e];
-                if (p.y && in) store8(p.y, p.y_bf16, row * p.k + col[i], y);
-                if (p.q) {
-                    float inv;
-                    const float sc = block_scale(max16(max8(y)), inv);
-                    if (in) *(u32x2*)(p.q + row * p.k + col[i]) = codes8(y, inv);
-                    if ((lane & 15) == 0) scales[(col[i] >> 7) * p.tile_rows + rr] = sc;
-                }
-            }
+            rstd = 1.0f / sqrtf(row_sum<W>(sq, part, turn) * over_k);
+            told = rstd * 0x1p-96f;
         }
+        if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
+        float top[NV], inv[NV], y[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[i][e] = s[i][e] * rstd * w[i][e];
+            top[i] = max8(y[i]);
+        }
+        if (p.y && in)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (col[i] < p.k) put_values(p.y, p.y_bf16, at + col[i], y[i], p.far);
         if (p.q) {
-            __syncthreads();
-            const int n = (p.k >> 7) * p.tile_rows;
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-                const int c = i / p.tile_rows, rr = i - c * p.tile_rows;
-                if (row0 + rr < p.rows) p.sfa[(int64_t)c * p.ld + row0 + rr] = scales[i];
-            }
-            __syncthreads();
+            const float scale = block_scales(top, seg, inv);
+            const int group = (block_of<NV>(seg) * W + wr) * 4 + (lane >> 4);
+            if (in && seg < NV && group < (p.k >> 7)) p.sfa[(int64_t)group * p.ld + row] = scale;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in && col[i] < p.k) put_codes(p.q + at + col[i], codes8(y[i], inv[i]), p.far);
         }
     }
 }
@@ -163,12 +138,11 @@ struct BackwardParams {
     const void* dres;           // nullptr: none
     void* dx;
     float* part;                // [units x rows at once][k] sums of dy h, or nullptr
-    int rows, k;
-    int w_bf16;
+    int rows, k, far;
     uint32_t units;             // unit u takes the rows u, u + units, ... (times rows at once)
 };
 
-template <int W, int NV, bool SB, bool GB, bool DB>
+template <int W, int NV, bool SB, bool GB, bool WB>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel(BackwardParams p) {
     __shared__ float part[2][16];
     constexpr int kThreads = W == 16 ? 1024 : 256, kAtOnce = kThreads / 64 / W;
@@ -179,10 +153,9 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
     int col[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) col[i] = ((i * W + wr) * 64 + lane) * 8;
-    float w[NV][8] = {};
+    Eight<WB> w[NV];                           // (as they come, for all rows)
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (col[i] < p.k) load_weights(p.w, p.w_bf16, col[i], w[i]);
+    for (int i = 0; i < NV; ++i) w[i].load(p.w, col[i] < p.k ? +col[i] : p.k - 8);
 
     for (uint32_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
         float acc[NV][8] = {};
@@ -191,29 +164,27 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
         // (every wavefront of a workgroup makes the same number of turns)
         for (int64_t first = (int64_t)unit * kAtOnce; first < p.rows; first += step, row += step) {
             const bool in = row < p.rows;
+            const int64_t from = in ? +row : (int64_t)p.rows - 1;
             Eight<SB> s[NV];
             Eight<GB> g[NV];
-            Eight<DB> d[NV];
-            const float r = in ? p.rstd[row] : 0.0f;
+            Eight<SB> d[NV];
+            const float r = p.rstd[from];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                s[i].zero();
-                g[i].zero();
-                d[i].zero();
-                if (in && col[i] < p.k) {
-                    s[i].load(p.s, row * p.k + col[i]);
-                    g[i].load(p.dy, row * p.k + col[i]);
-                    if (p.dres) d[i].load(p.dres, row * p.k + col[i]);
-                }
+            for (int i = 0; i < NV; ++i) {     // (past the last row or column: that one again)
+                const int64_t at = from * p.k + (col[i] < p.k ? +col[i] : p.k - 8);
+                s[i].stream(p.s, at);
+                g[i].stream(p.dy, at);
+                if (p.dres) d[i].stream(p.dres, at);
             }
             float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float h = s[i][e] * r;
-                    dot += g[i][e] * w[i][e] * h;
-                    acc[i][e] += g[i][e] * h;
+                    const float t = g[i][e] * (s[i][e] * r);
+                    const float own = in && col[i] < p.k ? +t : 0.0f;
+                    dot += own * w[i][e];
+                    acc[i][e] += own;
                 }
             const float mean = row_sum<W>(dot, part, turn) * over_k;
             if (in)
@@ -223,8 +194,9 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
                     float dx[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        dx[e] = d[i][e] + r * (g[i][e] * w[i][e] - s[i][e] * r * mean);
-                    store8(p.dx, DB, row * p.k + col[i], dx);
+                        dx[e] = (p.dres ? d[i][e] : 0.0f) +
+                                r * (g[i][e] * w[i][e] - s[i][e] * r * mean);
+                    put_values(p.dx, SB, row * p.k + col[i], dx, p.far);
                 }
         }
         if (p.part)
@@ -282,25 +254,27 @@ Shape shape_of(int k, bool few_rows) {
     return {0, 0};
 }
 
-template <int W, int NV>
-const void* norm_kernel(bool xb, bool rb) {
-    if (xb) return rb ? (const void*)rms_norm_kernel<W, NV, true, true>
-                      : (const void*)rms_norm_kernel<W, NV, true, false>;
-    return rb ? (const void*)rms_norm_kernel<W, NV, false, true>
-              : (const void*)rms_norm_kernel<W, NV, false, false>;
+template <int W, int NV, bool XB, bool WB>
+const void* norm_kernel(int res) {
+    return res == 0   ? (const void*)rms_norm_kernel<W, NV, XB, 0, WB>
+           : res == 1 ? (const void*)rms_norm_kernel<W, NV, XB, 1, WB>
+                      : (const void*)rms_norm_kernel<W, NV, XB, 2, WB>;
 }
 template <int W, int NV>
-const void* backward_kernel(bool sb, bool gb, bool db) {
-    if (sb) {
-        if (gb) return db ? (const void*)rms_norm_backward_kernel<W, NV, true, true, true>
-                          : (const void*)rms_norm_backward_kernel<W, NV, true, true, false>;
-        return db ? (const void*)rms_norm_backward_kernel<W, NV, true, false, true>
-                  : (const void*)rms_norm_backward_kernel<W, NV, true, false, false>;
-    }
-    if (gb) return db ? (const void*)rms_norm_backward_kernel<W, NV, false, true, true>
-                      : (const void*)rms_norm_backward_kernel<W, NV, false, true, false>;
-    return db ? (const void*)rms_norm_backward_kernel<W, NV, false, false, true>
-              : (const void*)rms_norm_backward_kernel<W, NV, false, false, false>;
+const void* norm_kernel(bool xb, int res, bool wb) {
+    if (xb) return wb ? norm_kernel<W, NV, true, true>(res) : norm_kernel<W, NV, true, false>(res);
+    return wb ? norm_kernel<W, NV, false, true>(res) : norm_kernel<W, NV, false, false>(res);
+}
+template <int W, int NV, bool SB>
+const void* backward_kernel(bool gb, bool wb) {
+    if (gb) return wb ? (const void*)rms_norm_backward_kernel<W, NV, SB, true, true>
+                      : (const void*)rms_norm_backward_kernel<W, NV, SB, true, false>;
+    return wb ? (const void*)rms_norm_backward_kernel<W, NV, SB, false, true>
+              : (const void*)rms_norm_backward_kernel<W, NV, SB, false, false>;
+}
+template <int W, int NV>
+const void* backward_kernel(bool sb, bool gb, bool wb) {
+    return sb ? backward_kernel<W, NV, true>(gb, wb) : backward_kernel<W, NV, false>(gb, wb);
 }
 
 #define FP8BS_BY_SHAPE(call, s, ...)                                                             \
@@ -315,7 +289,7 @@ int threads_of(Shape s) { return s.waves == 16 ? 1024 : 256; }
 int at_once(Shape s) { return s.waves == 1 ? 4 : 1; }
 
 constexpr int kFewRows = 512;
-constexpr int kMostUnits = 1024;               // of the backward pass: parts of dw
+constexpr int kMostUnits = 512;               // of the backward pass: parts of dw
 
 Shape backward_shape(int64_t rows, int k) { return shape_of(k, rows < kFewRows); }
 // By sizes alone, not by the device or the cap on CUs: the units' sums are added in order.
@@ -346,14 +320,13 @@ extern "C" int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, 
         return FP8BS_ERR_POINTER;
     const Shape s = shape_of(k, rows < kFewRows);
     NormParams p = {x, residual, residual_out, weight, y, (uint8_t*)q, sfa, rstd, rows, k,
-                    (int)fp8bs_get_sfa_ld(rows), eps, weight_dtype == FP8BS_DTYPE_BF16,
-                    y_dtype == FP8BS_DTYPE_BF16, 0, 0};
-    p.tile_rows = rows >= 8192 ? 8 : 4;
-    if (rows < kFewRows) p.tile_rows = at_once(s);
-    p.tiles = (uint32_t)((rows + p.tile_rows - 1) / p.tile_rows);
-    const bool xb = x_dtype == FP8BS_DTYPE_BF16, rb = residual_dtype == FP8BS_DTYPE_BF16;
-    return launch(FP8BS_BY_SHAPE(norm_kernel, s, xb, rb), workgroups(p.tiles, s.waves == 16 ? 2 : 8),
-                  threads_of(s), p, stream, q ? (size_t)(k / 128) * p.tile_rows * 4 : 0);
+                    (int)fp8bs_get_sfa_ld(rows), eps, residual_dtype == FP8BS_DTYPE_BF16,
+                    y_dtype == FP8BS_DTYPE_BF16, far_outputs((double)rows * k * (q ? 1 : 2)),
+                    (uint32_t)(((int64_t)rows + at_once(s) - 1) / at_once(s))};
+    const int res = !residual ? 0 : residual_dtype == FP8BS_DTYPE_BF16 ? 1 : 2;
+    return launch(FP8BS_BY_SHAPE(norm_kernel, s, x_dtype == FP8BS_DTYPE_BF16, res,
+                                 weight_dtype == FP8BS_DTYPE_BF16), workgroups(p.units, s.waves == 16 ? 2 : 8),
+                  threads_of(s), p, stream);
 }
 
 extern "C" int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k) {
@@ -365,15 +338,14 @@ extern "C" int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k) {
 
 extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd,
                                        const void* weight, int weight_dtype, const void* dy,
-                                       int dy_dtype, const void* dresidual, void* dx, int dx_dtype,
-                                       float* dweight, int accumulate, int rows, int k,
+                                       int dy_dtype, const void* dresidual, void* dx, float* dweight,
+                                       int accumulate, int rows, int k,
                                        void* workspace, size_t workspace_bytes,
                                        hipStream_t stream) {
     using namespace fp8bs::layer;
     const int64_t need = fp8bs_rms_norm_backward_workspace_size(rows, k);
     if (need < 0) return FP8BS_ERR_SHAPE;
-    if (!value_type(s_dtype) || !value_type(weight_dtype) || !value_type(dy_dtype) ||
-        !value_type(dx_dtype))
+    if (!value_type(s_dtype) || !value_type(weight_dtype) || !value_type(dy_dtype))
         return FP8BS_ERR_UNSUPPORTED;
     if (!aligned_or_null(dweight)) return FP8BS_ERR_POINTER;
     const Shape shape = backward_shape(rows, k);
@@ -383,11 +355,11 @@ extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* 
             return FP8BS_ERR_POINTER;
         if (dweight && workspace_bytes < (size_t)need) return FP8BS_ERR_UNSUPPORTED;
         BackwardParams p = {s, rstd, weight, dy, dresidual, dx, dweight ? (float*)workspace : nullptr,
-                            rows, k, weight_dtype == FP8BS_DTYPE_BF16,
+                            rows, k, far_outputs((double)rows * k * 2),
                             (uint32_t)backward_units(rows, shape)};
         const int st = launch(FP8BS_BY_SHAPE(backward_kernel, shape, s_dtype == FP8BS_DTYPE_BF16,
                                              dy_dtype == FP8BS_DTYPE_BF16,
-                                             dx_dtype == FP8BS_DTYPE_BF16),
+                                             weight_dtype == FP8BS_DTYPE_BF16),
                               workgroups(p.units, shape.waves == 16 ? 1 : 4), threads_of(shape), p,
                               stream);
         if (st != FP8BS_OK) return st;

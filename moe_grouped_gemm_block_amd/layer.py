@@ -49,7 +49,7 @@ def _load():
     P, I, I64, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     for name, args in {
         "fp8bs_rms_norm": [P, I, P, P, I, P, I, P, I, P, P, P, I, I, ctypes.c_float, P],
-        "fp8bs_rms_norm_backward": [P, I, P, P, I, P, I, P, P, I, P, I, I, I, P, S, P],
+        "fp8bs_rms_norm_backward": [P, I, P, P, I, P, I, P, P, P, I, I, I, P, S, P],
         "fp8bs_moe_dispatch": [I, P, I, P, I] + [P] * 6 + [I] * 5 + [P, S, P],
         "fp8bs_moe_combine": [P] * 4 + [I, I64, I, I, I, P],
         "fp8bs_moe_combine_backward": [P, I] + [P] * 7 + [I] * 5 + [P],
@@ -198,9 +198,9 @@ def rms_norm_backward_workspace_size(rows: int, k: int) -> int:
 def fp8bs_rms_norm_backward(s, rstd, weight, dy, dx, dresidual=None, dweight=None,
                             accumulate: bool = False, workspace=None, stream=None):
     """Gradients of the norm: s bf16 or f32 [rows][k] (residual_out, or x without a residual) and
-    rstd as the forward call gave it, dy bf16 or f32 -> dx (bf16 or f32; of x and of residual) and
+    rstd as the forward call gave it, dy bf16 or f32 -> dx in s's type (of x and of residual) and
     dweight f32 [k] (accumulate: added to what it holds), which may be None.  dresidual: the
-    gradient of residual_out, in dx's type; dx may be dresidual, dy or s.  workspace: uint8 tensor
+    gradient of residual_out, in s's type; dx may be dresidual, s or dy.  workspace: uint8 tensor
     of rms_norm_backward_workspace_size() bytes, or None to allocate one."""
     index = _start(s, "s")
     sp, rows, k = _matrix(s, "s", _FLOAT, index)
@@ -208,16 +208,15 @@ def fp8bs_rms_norm_backward(s, rstd, weight, dy, dx, dresidual=None, dweight=Non
     tp = _like(rstd, "rstd", _F32, (rows,), index)
     wp = _like(weight, "weight", _FLOAT, (k,), index)
     gp = _like(dy, "dy", _FLOAT, shape, index)
-    xp = _like(dx, "dx", _FLOAT, shape, index)
-    rp = _optional(dresidual, "dresidual", (dx.dtype,), shape, index)
+    xp = _like(dx, "dx", (s.dtype,), shape, index)
+    rp = _optional(dresidual, "dresidual", (s.dtype,), shape, index)
     dwp = _optional(dweight, "dweight", _F32, (k,), index)
     p, n, _keep = None, 0, None
     if dwp is not None:
         p, n, _keep = _space(workspace, lambda: rms_norm_backward_workspace_size(rows, k), index,
                              stream)
     _call("fp8bs_rms_norm_backward", index, stream, sp, _CODE[s.dtype], tp, wp,
-          _CODE[weight.dtype], gp, _CODE[dy.dtype], rp, xp, _CODE[dx.dtype], dwp,
-          1 if accumulate else 0, rows, k, p, n)
+          _CODE[weight.dtype], gp, _CODE[dy.dtype], rp, xp, dwp, 1 if accumulate else 0, rows, k, p, n)
 
 
 # ---- dispatch and combine ----------------------------------------------------------
