@@ -210,8 +210,7 @@ __device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int
         for (int i = 0; i < kRowPieces; ++i) {
             const int at = piece0 + 64 * i + lane;
             if (at >= p.vectors) continue;
-            if (p.far) __builtin_nontemporal_store(v[i], to + at);
-            else to[at] = v[i];
+            put16(to + at, v[i], p.far);
         }
     }
 }

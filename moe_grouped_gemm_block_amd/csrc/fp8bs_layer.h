@@ -132,25 +132,38 @@ __device__ __forceinline__ void store8(void* x, bool bf16, int64_t at, const flo
     }
 }
 
-// The same past the caches (far): for outputs that are too large for them.
+// Stores past the caches (far) or through them: outputs that are too large to stay there.  The
+// empty asm on both sides keeps the compiler from making one ordinary store of the branches.
+__device__ __forceinline__ void put16(void* to, u32x4 v, bool far) {
+    if (far) {
+        asm volatile("");
+        __builtin_nontemporal_store(v, (u32x4*)to);
+        asm volatile("");
+    } else {
+        *(u32x4*)to = v;
+    }
+}
 __device__ __forceinline__ void put_values(void* x, bool bf16, int64_t at, const float (&v)[8],
                                            bool far) {
-    if (!far) {
-        store8(x, bf16, at, v);
-    } else if (bf16) {
+    if (bf16) {
         Eight<true> p;
         p.set(v);
-        __builtin_nontemporal_store(p.w[0], (u32x4*)((uint8_t*)x + at * 2));
+        put16((uint8_t*)x + at * 2, p.w[0], far);
     } else {
         Eight<false> p;
         p.set(v);
-        __builtin_nontemporal_store(p.w[0], (u32x4*)((uint8_t*)x + at * 4));
-        __builtin_nontemporal_store(p.w[1], (u32x4*)((uint8_t*)x + at * 4) + 1);
+        put16((uint8_t*)x + at * 4, p.w[0], far);
+        put16((uint8_t*)x + at * 4 + 16, p.w[1], far);
     }
 }
 __device__ __forceinline__ void put_codes(uint8_t* to, u32x2 codes, bool far) {
-    if (far) __builtin_nontemporal_store(codes, (u32x2*)to);
-    else *(u32x2*)to = codes;
+    if (far) {
+        asm volatile("");
+        __builtin_nontemporal_store(codes, (u32x2*)to);
+        asm volatile("");
+    } else {
+        *(u32x2*)to = codes;
+    }
 }
 
 // Eight e4m3 codes, widened.
