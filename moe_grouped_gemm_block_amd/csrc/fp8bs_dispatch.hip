@@ -39,6 +39,7 @@ struct DispatchParams {
     int kb;                     // scales of a row (0: none)
     int sfx_ld, sfa_ld;
     int chunk, chunks;          // assignments of a chunk (a multiple of 256)
+    int rank_units;             // at least the chunks
     int far;
     uint32_t units;
 };
@@ -135,12 +136,13 @@ __global__ void __launch_bounds__(256) dispatch_count_kernel(DispatchParams p) {
     }
 }
 
-// A chunk's four wavefronts take a quarter each, in order.
+// A chunk's four wavefronts take a quarter each, in order.  (More workgroups than chunks: the
+// others write their share of the rows' experts alone.)
 __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
     __shared__ int total[kMostGroups], start[kMostGroups + 1], wave_sums[4];
     __shared__ int next[4][kMostGroups];       // the wavefront's next rank of each expert
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+    for (int c = blockIdx.x; c < p.rank_units; c += gridDim.x) {
         for (int e = t; e < p.groups; e += 256) {
             total[e] = 0;
             for (int w = 0; w < 4; ++w) next[w][e] = 0;
@@ -159,7 +161,8 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
         }
         const int quarter = p.chunk / 4;
         const int64_t first = (int64_t)c * p.chunk + (int64_t)wave * quarter;
-        const int64_t end = first + quarter < p.n ? first + quarter : p.n;
+        const int64_t end =
+            c >= p.chunks ? first : first + quarter < p.n ? first + quarter : (int64_t)p.n;
         if (wave < 3)
             for (int64_t i = first + lane; i < end; i += 64) {
                 const int e = expert_of(p, (int)i);
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
         for (int e = t; e < p.groups; e += 256)
             for (int w = 1; w < 4; ++w) next[w][e] += next[w - 1][e];
         segment_starts(total, p.groups, start, wave_sums);
-        write_group_data(p, total, start, c, p.chunks);
+        write_group_data(p, total, start, c, p.rank_units);
         for (int64_t base = first; base < end; base += 64) {
             const int64_t i = base + lane;
             const int e = i < end ? expert_of(p, (int)i) : -1;
@@ -248,25 +251,46 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchParams p, in
 
 // ---- few assignments: one launch ---------------------------------------------------
 
-constexpr int kFewAssignments = 4096;
+constexpr int kFewAssignments = 2048;
+// Up to so many assignments: the time grows with their square (every workgroup goes through them),
+// that of the three launches with the groups.  e4m3 rows of 2048 and 7168, eight choices, 8 to 16
+// groups: 1024 assignments 7.8-11.8 us against 9.6-15.1, 2048 12-16.9 against 9.9-16.2; 256 groups:
+// 2048 assignments 13.9-17 against 13.7-30.
+constexpr int few_assignments(int groups) { return groups < 64 ? 1024 : kFewAssignments; }
 
-// Workgroup = one token at a time.  Each counts all assignments for itself.
+// Workgroup = one token at a time.  Each ranks its own choices by going through all earlier ones;
+// the token's row and scales are on their way meanwhile.  64 tokens, eight choices each, e4m3 rows
+// of 7168 into slots: 6.7 us, most of it the latency of one load after the other.
 __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
     __shared__ int16_t ids[kFewAssignments];
     __shared__ int total[kMostGroups], start[kMostGroups + 1], wave_sums[4];
     __shared__ int32_t rows[kMostTopk];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int e = t; e < p.groups; e += 256) total[e] = 0;
-    __syncthreads();
+    // (slots start at their number: the counts are outputs alone, of workgroup 0)
+    const bool count = !p.masked || blockIdx.x == 0;
+    if (count) {
+        for (int e = t; e < p.groups; e += 256) total[e] = 0;
+        __syncthreads();
+    }
     for (int i = t; i < p.n; i += 256) {
         const int e = expert_of(p, i);
         ids[i] = (int16_t)e;
-        if (e >= 0) atomicAdd(&total[e], 1);
+        if (count && e >= 0) atomicAdd(&total[e], 1);
     }
-    __syncthreads();
-    segment_starts(total, p.groups, start, wave_sums);
-    write_group_data(p, total, start, blockIdx.x, gridDim.x);
     for (int token = blockIdx.x; token < p.tokens; token += gridDim.x) {
+        u32x4 v[4];
+        const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {          // (past the row's end: its last piece again)
+            const int at = t + 256 * i;
+            v[i] = __builtin_nontemporal_load(from + (at < p.vectors ? +at : p.vectors - 1));
+        }
+        const float scale = t < p.kb ? p.sfx[(int64_t)t * p.sfx_ld + token] : 0.0f;
+        __syncthreads();
+        if (token == (int)blockIdx.x && count) {
+            if (!p.masked) segment_starts(total, p.groups, start, wave_sums);
+            write_group_data(p, total, start, blockIdx.x, gridDim.x);
+        }
         for (int j = wave; j < p.topk; j += 4) {
             const int i = token * p.topk + j, e = ids[i];
             int rank = 0;
@@ -279,16 +303,25 @@ __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
             }
         }
         __syncthreads();
-        for (int piece = wave; piece * 64 * kRowPieces < p.vectors; piece += 4)
-            copy_row(p, token, piece * 64 * kRowPieces, lane, rows);
-        for (int i = t; i < p.kb * p.topk; i += 256) {
-            const int j = i / p.kb, c = i - j * p.kb, row = rows[j];
+        for (int j = 0; j < p.topk; ++j) {
+            const int row = rows[j];
             if (row < 0) continue;
+            u32x4* to = (u32x4*)p.a + (int64_t)row * p.vectors;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t + 256 * i < p.vectors) put16(to + t + 256 * i, v[i], p.far);
+            for (int at = t + 1024; at < p.vectors; at += 256) put16(to + at, from[at], p.far);
             const int slot = p.masked ? row / p.m : 0;
-            p.sfa[((int64_t)slot * p.kb + c) * p.sfa_ld + row - slot * p.m] =
-                p.sfx[(int64_t)c * p.sfx_ld + token];
+            float* sf = p.sfa + (int64_t)slot * p.kb * p.sfa_ld + row - slot * p.m;
+            if (t < p.kb) sf[(int64_t)t * p.sfa_ld] = scale;
+            for (int c = t + 256; c < p.kb; c += 256)
+                sf[(int64_t)c * p.sfa_ld] = p.sfx[(int64_t)c * p.sfx_ld + token];
         }
+    }
+    if (p.tokens == 0) {                       // (group data alone)
         __syncthreads();
+        if (!p.masked) segment_starts(total, p.groups, start, wave_sums);
+        if (count) write_group_data(p, total, start, blockIdx.x, gridDim.x);
     }
 }
 
@@ -348,20 +381,26 @@ struct CombineBackwardParams {
     float* dw;
     int64_t rows;
     int m, ld, tokens, topk, k, far;
+    uint32_t units;
 };
 
-// Workgroup = one token, two choices at a time; a lane eight columns of each 2048, 16 lanes a group
-// of 128, two such runs at a time, their loads issued together.  A group's largest |w dy| is |w|
-// times that of |dy| (rounding keeps the order).
+// Workgroup = two choices of a token; a lane eight columns of each 2048, 16 lanes a group of 128, two
+// such runs at a time, their loads issued together.  A group's largest |w dy| is |w| times that of
+// |dy| (rounding keeps the order).  Workgroups go round the 8 XCDs: eight tokens' first pairs are
+// followed by their second ones, so that a token's pairs find its dy in one L2.  16384 tokens of
+// two choices, 7168 columns: 170 us (5.6 TB/s); one load at a time took 205.
 template <bool GB>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardParams p) {
     __shared__ float dots[2][2][4];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     int turn = 0;
-    for (uint32_t token = blockIdx.x; token < (uint32_t)p.tokens; token += gridDim.x) {
-        const int32_t* at = p.positions + (int64_t)token * p.topk;
-        const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
-        for (int j0 = 0; j0 < p.topk; j0 += 2, turn ^= 1) {
+    const uint32_t pairs = (uint32_t)(p.topk + 1) / 2;
+    for (uint32_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+        const int token = (int)(unit / (8 * pairs) * 8 + unit % 8);
+        const int j0 = (int)(unit / 8 % pairs) * 2;
+        if (token < p.tokens) {
+            const int32_t* at = p.positions + (int64_t)token * p.topk;
+            const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
             int row[2];
             bool in[2];
             const uint16_t* from[2];
@@ -420,7 +459,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardPa
                     }
                 }
             }
-            if (p.dw) {                        // (two buffers: one barrier a turn)
+            if (p.dw) {                        // (two buffers: one barrier a unit)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float sum = sum_wave(dot[j]);
@@ -430,6 +469,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardPa
                 if (t < 2 && j0 + t < p.topk)
                     p.dw[(int64_t)token * p.topk + j0 + t] =
                         (dots[turn][t][0] + dots[turn][t][1]) + (dots[turn][t][2] + dots[turn][t][3]);
+                turn ^= 1;
             }
         }
     }
@@ -451,7 +491,7 @@ int chunk_of(int64_t n, int num_groups) {
     chunks = chunks < kMostChunks ? chunks : kMostChunks;
     return (int)(((n + chunks - 1) / chunks + 255) / 256 * 256);
 }
-bool few(int64_t n) { return n <= kFewAssignments; }
+bool few(int64_t n, int groups) { return n <= few_assignments(groups); }
 
 }  // namespace
 }  // namespace layer
@@ -470,7 +510,7 @@ extern "C" int64_t fp8bs_moe_dispatch_workspace_size(int layout, int64_t tokens,
         return -FP8BS_ERR_UNSUPPORTED;
     if (!counts_fit(tokens, topk, num_groups) || m < 0 || m > kMaxRows) return -FP8BS_ERR_SHAPE;
     const int64_t n = tokens * topk;
-    if (few(n)) return 0;
+    if (few(n, num_groups)) return 0;
     const int64_t rows = layout == FP8BS_LAYOUT_MASKED ? m * num_groups : m;
     return (int64_t)kMostChunks * num_groups * 4 + (rows + 3) / 4 * 16;
 }
@@ -521,7 +561,7 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     p.sfx_ld = (int)fp8bs_get_sfa_ld(tokens);
     p.sfa_ld = (int)fp8bs_get_sfa_ld(m);
     p.far = far_outputs((double)n * p.vectors * 16);
-    if (few(n)) {
+    if (few(n, num_groups)) {
         // (without tokens: the group data alone)
         const int64_t units = tokens > 0 ? tokens : (m + 1023) / 1024 + 1;
         return launch((const void*)dispatch_few_kernel, workgroups(units, 4), 256, p, stream);
@@ -530,6 +570,9 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     p.source = p.chunk_counts + (int64_t)kMostChunks * num_groups;
     p.chunk = chunk_of(n, num_groups);
     p.chunks = (int)((n + p.chunk - 1) / p.chunk);
+    p.rank_units = p.chunks;
+    if (!masked && m / 512 > p.chunks) p.rank_units = m / 512 < 256 ? m / 512 : 256;
+    if (p.rank_units < p.chunks) p.rank_units = p.chunks;
     const int pieces = (p.vectors + 64 * kRowPieces - 1) / (64 * kRowPieces);
     const int64_t scale_units = e4m3 ? (int64_t)((m + 63) / 64) * (masked ? num_groups : 1) : 0;
     const int64_t units = scale_units + (int64_t)tokens * pieces;
@@ -537,7 +580,7 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     p.units = (uint32_t)units;
     int st = launch((const void*)dispatch_count_kernel, workgroups(p.chunks, 4), 256, p, stream);
     if (st != FP8BS_OK) return st;
-    st = launch((const void*)dispatch_rank_kernel, workgroups(p.chunks, 4), 256, p, stream);
+    st = launch((const void*)dispatch_rank_kernel, workgroups(p.rank_units, 4), 256, p, stream);
     if (st != FP8BS_OK || rows == 0) return st;
     uint32_t su = (uint32_t)scale_units;
     int pc = pieces;
@@ -583,11 +626,14 @@ extern "C" int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const vo
         !aligned_or_null(dd) || !aligned_or_null(q) || !aligned_or_null(dweights, 4) ||
         (rows > 0 && ((dweights && !aligned(d)) || (q && !aligned(sfa)))) || !(dd || q || dweights))
         return FP8BS_ERR_POINTER;
+    const int64_t units = ((int64_t)tokens + 7) / 8 * 8 * ((topk + 1) / 2);
+    if (units > 0x7fffffff) return FP8BS_ERR_UNSUPPORTED;
     CombineBackwardParams p = {dy, (const uint16_t*)d, positions, weights, (uint16_t*)dd,
                                (uint8_t*)q, sfa, dweights, rows, m > 0 ? m : 1,
                                (int)fp8bs_get_sfa_ld(m), tokens, topk, k,
-                               far_outputs((double)tokens * topk * k * ((dd ? 2 : 0) + (q ? 1 : 0)))};
+                               far_outputs((double)tokens * topk * k * ((dd ? 2 : 0) + (q ? 1 : 0))),
+                               (uint32_t)units};
     return launch(dy_dtype == FP8BS_DTYPE_BF16 ? (const void*)combine_backward_kernel<true>
                                                : (const void*)combine_backward_kernel<false>,
-                  workgroups(tokens, 8), 256, p, stream);
+                  workgroups(units, 8), 256, p, stream);
 }

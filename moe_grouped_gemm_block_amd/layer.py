@@ -12,6 +12,7 @@ checks and marshalling only.  Operands in e4m3 are pairs of codes, uint8 (or
 from __future__ import annotations
 
 import ctypes
+import functools
 from collections import namedtuple
 
 import moe_grouped_gemm_block_amd as _pkg
@@ -35,11 +36,12 @@ _lib = None
 
 def _load():
     """The library with this module's prototypes."""
-    global _lib, _FP8, _BF16, _F32, _FLOAT, _INT32, _IDS, _KEPT, _ROWS, _CODE, _bf16, _u8, _f32
+    global _lib, _Tensor, _FP8, _BF16, _F32, _FLOAT, _INT32, _IDS, _KEPT, _ROWS, _CODE, _bf16, _u8, _f32
     if _lib is not None:
         return _lib
     lib = _mx._load()
     torch = _torch()
+    _Tensor = torch.Tensor
     _bf16, _u8, _f32 = torch.bfloat16, torch.uint8, torch.float32
     _FP8, _BF16, _F32 = _pkg._fp8_dtypes(), _pkg._bf16_dtypes(), (torch.float32,)
     _FLOAT, _INT32, _IDS = (_bf16, _f32), (torch.int32,), (torch.int32, torch.int64)
@@ -80,6 +82,10 @@ def _start(t, name):
 
 def _like(t, name, dtypes, shape, index):
     """Address of a tensor of a given shape."""
+    # (the common case in few attribute reads: these run on every call of a decode step)
+    if (type(t) is _Tensor and t.get_device() == index and t.dtype in dtypes and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     p = _ptr(t, name, dtypes, len(shape), index)
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
@@ -94,7 +100,10 @@ def _scales(t, name, count, index):
     """Address of `count` float32 scales."""
     if t is None:
         raise ValueError(f"{name} is missing: codes come with their scales")
-    p = _ptr(t, name, _F32, t.ndim if isinstance(t, _mx._Tensor) else 0, index)
+    if (type(t) is _Tensor and t.get_device() == index and t.dtype is _f32 and t.numel() == count
+            and t.is_contiguous()):
+        return t.data_ptr()
+    p = _ptr(t, name, _F32, t.ndim if isinstance(t, _Tensor) else 0, index)
     if t.numel() != count:
         raise ValueError(f"{name}: scale tensor sizes do not match the shapes")
     return p
@@ -191,6 +200,7 @@ def rms_norm_1x128(x, weight, residual=None, eps: float = 1e-6, stream=None):
     return q, sfa, x if s is None else s, rstd
 
 
+@functools.lru_cache(256)
 def rms_norm_backward_workspace_size(rows: int, k: int) -> int:
     return _size("fp8bs_rms_norm_backward_workspace_size", rows, k)
 
@@ -226,6 +236,7 @@ def moe_capacity(tokens: int, topk: int, num_groups: int) -> int:
     return _size("fp8bs_moe_capacity", tokens, topk, num_groups)
 
 
+@functools.lru_cache(256)
 def moe_dispatch_workspace_size(layout: int, tokens: int, topk: int, num_groups: int,
                                 m: int) -> int:
     """Workspace bytes of ``fp8bs_moe_dispatch`` (layout: LAYOUT_CONTIGUOUS or LAYOUT_MASKED; m:
@@ -252,7 +263,7 @@ def fp8bs_moe_dispatch(ids, x, a, group_data, positions, counts, sfx=None, sfa=N
     cp = _ptr(counts, "counts", _INT32, 1, index)
     g = counts.shape[0]
     kind = _CODE[x.dtype]
-    masked = isinstance(a, _mx._Tensor) and a.ndim == 3
+    masked = isinstance(a, _Tensor) and a.ndim == 3
     ap = _ptr(a, "a", _FP8 if kind == DTYPE_E4M3 else (x.dtype,), 3 if masked else 2, index)
     m = a.shape[-2]
     if a.shape[-1] != k or (masked and a.shape[0] != g):
