@@ -15,11 +15,11 @@ namespace {
 
 // The logistic function s of v and, where asked for, 1 - s, each within two or three units in the
 // last place: v_exp_f32 of the product with -log2 e, times what that product's rounding leaves
-// out, and v_rcp_f32.  (-v is cut off where the exponential is infinite and s 0.)
+// out, and v_rcp_f32.  (v is cut off where s is 0 or 1 already, before its products overflow.)
 template <bool GRAD>
 __device__ __forceinline__ float logistic(float v, float& rest) {
     constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float a = __builtin_fminf(-v, 200.0f);
+    const float a = __builtin_amdgcn_fmed3f(-v, -200.0f, 200.0f);
     const float hi = a * kHi;
     const float lo = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -hi));
     const float e = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
@@ -41,9 +41,9 @@ __device__ __forceinline__ float activate(float v, float& slope) {
         constexpr float c = 0.7978845608028654f;
         const float v2 = v * v;
         const float s = logistic<GRAD>(2.0f * c * v * __builtin_fmaf(0.044715f, v2, 1.0f), rest);
-        // (beyond |v| = 1e15, where s (1 - s) is 0, the square stays finite: 0 times it is 0)
+        // (where s (1 - s) is 0, far out, its factors stay finite: 0 times them is 0)
         if (GRAD)
-            slope = __builtin_fmaf(2.0f * c * v * s * rest,
+            slope = __builtin_fmaf(s * rest * v * (2.0f * c),
                                    __builtin_fmaf(0.134145f, __builtin_fminf(v2, 1e30f), 1.0f), s);
         return v * s;
     }
