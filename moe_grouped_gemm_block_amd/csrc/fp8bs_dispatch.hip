@@ -563,7 +563,7 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     p.far = far_outputs((double)n * p.vectors * 16);
     if (few(n, num_groups)) {
         // (without tokens: the group data alone)
-        const int64_t units = tokens > 0 ? tokens : (m + 1023) / 1024 + 1;
+        const int64_t units = tokens > 0 ? tokens : m / 1024 + 1;
         return launch((const void*)dispatch_few_kernel, workgroups(units, 4), 256, p, stream);
     }
     p.chunk_counts = (int32_t*)workspace;
