@@ -137,7 +137,7 @@ struct BackwardParams {
     const void* dy;
     const void* dres;           // nullptr: none
     void* dx;
-    float* part;                // [units x rows at once][k] sums of dy h, or nullptr
+    float* part;                // [units][k] sums of dy h, or nullptr
     int rows, k, far;
     uint32_t units;             // unit u takes the rows u, u + units, ... (times rows at once)
 };
@@ -199,11 +199,23 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
                     put_values(p.dx, SB, row * p.k + col[i], dx, p.far);
                 }
         }
-        if (p.part)
+        if (!p.part) continue;
+        if constexpr (W == 1) {                // the four rows' sums: one part
+            __shared__ float sums[kAtOnce][NV * 512];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                store8(sums[sub], false, col[i], acc[i]);
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.k; c += kThreads)
+                p.part[(int64_t)unit * p.k + c] =
+                    (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+            __syncthreads();
+        } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (col[i] < p.k)
-                    store8(p.part, false, ((int64_t)unit * kAtOnce + sub) * p.k + col[i], acc[i]);
+                if (col[i] < p.k) store8(p.part, false, (int64_t)unit * p.k + col[i], acc[i]);
+        }
     }
 }
 
@@ -214,25 +226,27 @@ struct SumParams {
     uint32_t tiles;
 };
 
-// dw = the parts' sum: a workgroup 64 columns, 16 wavefronts every 16th part each, then those
-// sixteen in order.
+// dw = the parts' sum: a workgroup 32 columns, in 32 chains of every 32nd part each, then those in
+// order.  (Of 512 parts x 7168, with the kernel before it: 32 columns 45.7 us for 4096 rows, 16
+// columns, reads of half a line, 48.3.)
+constexpr int kSumCols = 32;
 __global__ void __launch_bounds__(1024) rms_norm_sum_kernel(SumParams p) {
-    __shared__ float sums[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int kCols = kSumCols, kChains = 1024 / kCols;
+    __shared__ float sums[kChains][kCols];
+    const int t = threadIdx.x, c = t % kCols, chain = t / kCols;
     for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-        const int col = (int)tile * 64 + lane;
+        const int col = (int)tile * kCols + c;
         float v = 0.0f;
         if (col < p.k)
 #pragma unroll 8
-            for (int i = wave; i < p.parts; i += 16) v += p.part[(int64_t)i * p.k + col];
-        sums[wave][lane] = v;
+            for (int i = chain; i < p.parts; i += kChains) v += p.part[(int64_t)i * p.k + col];
+        sums[chain][c] = v;
         __syncthreads();
-        if (wave == 0 && col < p.k) {
-            v = p.accumulate ? p.dw[col] : 0.0f;
+        if (chain == 0 && col < p.k) {
             float all = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) all += sums[i][lane];
-            p.dw[col] = v + all;
+            for (int i = 0; i < kChains; ++i) all += sums[i][c];
+            p.dw[col] = p.accumulate ? p.dw[col] + all : all;
         }
         __syncthreads();
     }
@@ -240,19 +254,32 @@ __global__ void __launch_bounds__(1024) rms_norm_sum_kernel(SumParams p) {
 
 // ---- launches -----------------------------------------------------------------
 
-// How a row is laid over a workgroup: wavefronts and eights a lane.
+// How a row is laid over a workgroup: wavefronts and eights a lane.  A short row is one wavefront's,
+// four rows a workgroup; longer ones take 4 wavefronts, then 16.  Few rows leave CUs idle, so there
+// a row takes more wavefronts instead of more eights a lane (bf16, both layouts measured):
+//   2048 columns, 4 x 1 against 1 x 4: 64 rows 2.8 us against 3.5, 512 rows 3.2 and 3.8, 2048 rows
+//   6.2 and 5.8; the gradients 4096 rows 18.5 and 27
+//   7168 columns, 16 x 1 against 4 x 4: 64 rows 3.5 us against 3.9, 256 rows 4.1 and 4.4, 512 rows 6.3
+//   and 6.2, 1024 rows 12.2 and 11.1; the gradients 256 rows 10.1 and 10.6, 512 rows 16.5 and 16.5
 struct Shape {
     int waves, eights;
 };
-Shape shape_of(int k, bool few_rows) {
-    // A row of up to 512 columns is one eight a lane of one wavefront; longer ones take up to four
-    // eights a lane.  Few rows leave CUs idle, so there a row takes as many wavefronts as it fills.
-    for (int waves : {1, 4, 16})
-        for (int eights : {1, 2, 4})
-            if (k <= 512 * waves * eights && (!few_rows || eights == 1 || waves == 16))
-                return {waves, eights};
-    return {0, 0};
+constexpr int kFewRows = 512;
+Shape shape_of(int64_t rows, int k, bool backward) {
+    const bool few = rows < kFewRows;
+    if (k <= 512) return {1, 1};
+    if (k <= 2048 && !few && !backward) return {1, k <= 1024 ? 2 : 4};
+    if (k <= 2048) return {4, 1};
+    if (k <= 4096) return {4, 2};
+    if (k <= 8192) return few ? Shape{16, 1} : Shape{4, 4};
+    return {16, k <= 16384 ? 2 : 4};
 }
+
+#define FP8BS_BY_SHAPE(call, s, ...)                                                             \
+    ((s).waves == 4 ? (s).eights == 1   ? call<4, 1>(__VA_ARGS__)                              \
+                        : (s).eights == 2 ? call<4, 2>(__VA_ARGS__) : call<4, 4>(__VA_ARGS__)    \
+     : (s).eights == 1 ? call<16, 1>(__VA_ARGS__)                                                \
+     : (s).eights == 2 ? call<16, 2>(__VA_ARGS__) : call<16, 4>(__VA_ARGS__))
 
 template <int W, int NV, bool XB, bool WB>
 const void* norm_kernel(int res) {
@@ -276,26 +303,27 @@ template <int W, int NV>
 const void* backward_kernel(bool sb, bool gb, bool wb) {
     return sb ? backward_kernel<W, NV, true>(gb, wb) : backward_kernel<W, NV, false>(gb, wb);
 }
-
-#define FP8BS_BY_SHAPE(call, s, ...)                                                             \
-    ((s).waves == 1   ? (s).eights == 1   ? call<1, 1>(__VA_ARGS__)                              \
-                        : (s).eights == 2 ? call<1, 2>(__VA_ARGS__) : call<1, 4>(__VA_ARGS__)    \
-     : (s).waves == 4 ? (s).eights == 1   ? call<4, 1>(__VA_ARGS__)                              \
-                        : (s).eights == 2 ? call<4, 2>(__VA_ARGS__) : call<4, 4>(__VA_ARGS__)    \
-     : (s).eights == 1 ? call<16, 1>(__VA_ARGS__)                                                \
-     : (s).eights == 2 ? call<16, 2>(__VA_ARGS__) : call<16, 4>(__VA_ARGS__))
+const void* norm_kernel(Shape s, bool xb, int res, bool wb) {
+    if (s.waves == 1)
+        return s.eights == 1   ? norm_kernel<1, 1>(xb, res, wb)
+               : s.eights == 2 ? norm_kernel<1, 2>(xb, res, wb) : norm_kernel<1, 4>(xb, res, wb);
+    return FP8BS_BY_SHAPE(norm_kernel, s, xb, res, wb);
+}
+const void* backward_kernel(Shape s, bool sb, bool gb, bool wb) {
+    return s.waves == 1 ? backward_kernel<1, 1>(sb, gb, wb)
+                        : FP8BS_BY_SHAPE(backward_kernel, s, sb, gb, wb);
+}
 
 int threads_of(Shape s) { return s.waves == 16 ? 1024 : 256; }
 int at_once(Shape s) { return s.waves == 1 ? 4 : 1; }
 
-constexpr int kFewRows = 512;
-constexpr int kMostUnits = 512;               // of the backward pass: parts of dw
-
-Shape backward_shape(int64_t rows, int k) { return shape_of(k, rows < kFewRows); }
-// By sizes alone, not by the device or the cap on CUs: the units' sums are added in order.
+// Units of the backward pass: parts of dweight.  By sizes alone, not by the device or the cap on CUs:
+// the units' sums are added in order.  512 at most: 16384 x 7168 takes 160 us, with 256 185 (too
+// few loads in flight), with 1024 165 (twice the parts).  256 up to 1024 turns: 512 x 7168 takes
+// 13.6 us, with a unit a row 16.3.
 int64_t backward_units(int64_t rows, Shape s) {
-    const int64_t n = (rows + at_once(s) - 1) / at_once(s);
-    return n < kMostUnits ? n : kMostUnits;
+    const int64_t turns = (rows + at_once(s) - 1) / at_once(s);
+    return turns < 256 ? turns : turns < 1024 ? 256 : turns < 2048 ? turns / 4 : 512;
 }
 
 }  // namespace
@@ -318,22 +346,20 @@ extern "C" int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, 
         !aligned(weight) || !aligned_or_null(y) || !aligned_or_null(q) || (q && !aligned(sfa)) ||
         !aligned_or_null(rstd, 4) || !(y || q || residual_out))
         return FP8BS_ERR_POINTER;
-    const Shape s = shape_of(k, rows < kFewRows);
+    const Shape s = shape_of(rows, k, false);
     NormParams p = {x, residual, residual_out, weight, y, (uint8_t*)q, sfa, rstd, rows, k,
                     (int)fp8bs_get_sfa_ld(rows), eps, residual_dtype == FP8BS_DTYPE_BF16,
                     y_dtype == FP8BS_DTYPE_BF16, far_outputs((double)rows * k * (q ? 1 : 2)),
                     (uint32_t)(((int64_t)rows + at_once(s) - 1) / at_once(s))};
     const int res = !residual ? 0 : residual_dtype == FP8BS_DTYPE_BF16 ? 1 : 2;
-    return launch(FP8BS_BY_SHAPE(norm_kernel, s, x_dtype == FP8BS_DTYPE_BF16, res,
-                                 weight_dtype == FP8BS_DTYPE_BF16), workgroups(p.units, s.waves == 16 ? 2 : 8),
+    return launch(norm_kernel(s, x_dtype == FP8BS_DTYPE_BF16, res, weight_dtype == FP8BS_DTYPE_BF16), workgroups(p.units, s.waves == 16 ? 2 : 8),
                   threads_of(s), p, stream);
 }
 
 extern "C" int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k) {
     using namespace fp8bs::layer;
     if (rows < 0 || rows > kMaxRows || k < 8 || k % 8 != 0 || k > kMostCols) return -FP8BS_ERR_SHAPE;
-    const Shape s = backward_shape(rows, k);
-    return backward_units(rows, s) * at_once(s) * k * 4;
+    return backward_units(rows, shape_of(rows, k, true)) * k * 4;
 }
 
 extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd,
@@ -348,7 +374,7 @@ extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* 
     if (!value_type(s_dtype) || !value_type(weight_dtype) || !value_type(dy_dtype))
         return FP8BS_ERR_UNSUPPORTED;
     if (!aligned_or_null(dweight)) return FP8BS_ERR_POINTER;
-    const Shape shape = backward_shape(rows, k);
+    const Shape shape = shape_of(rows, k, true);
     if (rows > 0) {
         if (!aligned(s) || !aligned(rstd, 4) || !aligned(weight) || !aligned(dy) ||
             !aligned_or_null(dresidual) || !aligned(dx) || (dweight && !aligned(workspace)))
@@ -357,16 +383,16 @@ extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* 
         BackwardParams p = {s, rstd, weight, dy, dresidual, dx, dweight ? (float*)workspace : nullptr,
                             rows, k, far_outputs((double)rows * k * 2),
                             (uint32_t)backward_units(rows, shape)};
-        const int st = launch(FP8BS_BY_SHAPE(backward_kernel, shape, s_dtype == FP8BS_DTYPE_BF16,
-                                             dy_dtype == FP8BS_DTYPE_BF16,
-                                             weight_dtype == FP8BS_DTYPE_BF16),
+        const int st = launch(backward_kernel(shape, s_dtype == FP8BS_DTYPE_BF16,
+                                              dy_dtype == FP8BS_DTYPE_BF16,
+                                              weight_dtype == FP8BS_DTYPE_BF16),
                               workgroups(p.units, shape.waves == 16 ? 1 : 4), threads_of(shape), p,
                               stream);
         if (st != FP8BS_OK) return st;
     }
     if (!dweight) return FP8BS_OK;
     SumParams p = {(const float*)workspace, dweight,
-                   rows > 0 ? (int)(backward_units(rows, shape) * at_once(shape)) : 0, k,
-                   accumulate != 0, (uint32_t)((k + 63) / 64)};
+                   rows > 0 ? (int)backward_units(rows, shape) : 0, k,
+                   accumulate != 0, (uint32_t)((k + kSumCols - 1) / kSumCols)};
     return launch((const void*)rms_norm_sum_kernel, workgroups(p.tiles, 2), 1024, p, stream);
 }
