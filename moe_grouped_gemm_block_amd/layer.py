@@ -73,17 +73,23 @@ def _load():
 
 # ---- argument checks -----------------------------------------------------------
 
+# These run on every call of a decode step: the common case -- contiguous tensors of the right type
+# and shape on the device -- is a few attribute reads; _ptr names what is wrong otherwise.
+
 def _start(t, name):
     """Device index of a call's first operand."""
     if _lib is None:
         _load()
+    if type(t) is _Tensor:
+        index = t.get_device()
+        if index >= 0:
+            return index
     return _first(t, name)
 
 
 def _like(t, name, dtypes, shape, index):
     """Address of a tensor of a given shape."""
-    # (the common case in few attribute reads: these run on every call of a decode step)
-    if (type(t) is _Tensor and t.get_device() == index and t.dtype in dtypes and t.shape == shape
+    if (isinstance(t, _Tensor) and t.dtype in dtypes and t.get_device() == index and t.shape == shape
             and t.is_contiguous()):
         return t.data_ptr()
     p = _ptr(t, name, dtypes, len(shape), index)
@@ -92,17 +98,13 @@ def _like(t, name, dtypes, shape, index):
     return p
 
 
-def _optional(t, name, dtypes, shape, index):
-    return None if t is None else _like(t, name, dtypes, shape, index)
-
-
 def _scales(t, name, count, index):
     """Address of `count` float32 scales."""
+    if (isinstance(t, _Tensor) and t.dtype is _f32 and t.get_device() == index
+            and t.numel() == count and t.is_contiguous()):
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is missing: codes come with their scales")
-    if (type(t) is _Tensor and t.get_device() == index and t.dtype is _f32 and t.numel() == count
-            and t.is_contiguous()):
-        return t.data_ptr()
     p = _ptr(t, name, _F32, t.ndim if isinstance(t, _Tensor) else 0, index)
     if t.numel() != count:
         raise ValueError(f"{name}: scale tensor sizes do not match the shapes")
@@ -153,11 +155,12 @@ def _space(workspace, size, index, stream):
 
 def _matrix(t, name, dtypes, index):
     """(address, rows, columns) of a matrix."""
-    p = _ptr(t, name, dtypes, 2, index)
-    rows, k = t.shape
-    if k > 1 << 24:                            # (longer ones do not all fit the call's int)
-        raise FP8BSError(1, f"{name}: at most 2^24 columns")
-    return p, rows, k
+    if isinstance(t, _Tensor) and t.dtype in dtypes and t.get_device() == index:
+        shape = t.shape
+        if len(shape) == 2 and shape[1] <= 1 << 24 and t.is_contiguous():
+            return t.data_ptr(), *shape
+    _ptr(t, name, dtypes, 2, index)
+    raise FP8BSError(1, f"{name}: at most 2^24 columns")   # (longer ones do not all fit the call's int)
 
 
 # ---- norm ------------------------------------------------------------------------
@@ -173,14 +176,14 @@ def fp8bs_rms_norm(x, weight, residual=None, residual_out=None, y=None, q=None, 
     xp, rows, k = _matrix(x, "x", _FLOAT, index)
     shape = x.shape
     wp = _like(weight, "weight", _FLOAT, (k,), index)
-    rp = _optional(residual, "residual", _FLOAT, shape, index)
-    op = _optional(residual_out, "residual_out", _FLOAT, shape, index)
+    rp = None if residual is None else _like(residual, "residual", _FLOAT, shape, index)
+    op = None if residual_out is None else _like(residual_out, "residual_out", _FLOAT, shape, index)
     rt = residual if residual is not None else residual_out
     if rp is not None and op is not None and residual.dtype is not residual_out.dtype:
         raise TypeError("residual and residual_out must have the same dtype")
-    yp = _optional(y, "y", _FLOAT, shape, index)
+    yp = None if y is None else _like(y, "y", _FLOAT, shape, index)
     qp, sp = _codes(q, sfa, ("q", "sfa"), 1, rows, k, shape, index)
-    tp = _optional(rstd, "rstd", _F32, (rows,), index)
+    tp = None if rstd is None else _like(rstd, "rstd", _F32, (rows,), index)
     if yp is None and qp is None and op is None and rows:
         raise ValueError("no output given: residual_out, y or q")
     _call("fp8bs_rms_norm", index, stream, xp, _CODE[x.dtype], rp, op,
@@ -219,8 +222,8 @@ def fp8bs_rms_norm_backward(s, rstd, weight, dy, dx, dresidual=None, dweight=Non
     wp = _like(weight, "weight", _FLOAT, (k,), index)
     gp = _like(dy, "dy", _FLOAT, shape, index)
     xp = _like(dx, "dx", (s.dtype,), shape, index)
-    rp = _optional(dresidual, "dresidual", (s.dtype,), shape, index)
-    dwp = _optional(dweight, "dweight", _F32, (k,), index)
+    rp = None if dresidual is None else _like(dresidual, "dresidual", (s.dtype,), shape, index)
+    dwp = None if dweight is None else _like(dweight, "dweight", _F32, (k,), index)
     p, n, _keep = None, 0, None
     if dwp is not None:
         p, n, _keep = _space(workspace, lambda: rms_norm_backward_workspace_size(rows, k), index,
@@ -318,7 +321,8 @@ def _assigned(positions, weights, tokens, index):
     pp = _ptr(positions, "positions", _INT32, 2, index)
     if positions.shape[0] != tokens:
         raise ValueError("positions must have one row per token")
-    return pp, _optional(weights, "weights", _F32, positions.shape, index), positions.shape[1]
+    wp = None if weights is None else _like(weights, "weights", _F32, positions.shape, index)
+    return pp, wp, positions.shape[1]
 
 
 def fp8bs_moe_combine(d, positions, y, weights=None, stream=None):
@@ -352,10 +356,10 @@ def fp8bs_moe_combine_backward(dy, positions, d=None, weights=None, dd=None, q=N
     if len(shape) not in (2, 3) or shape[-1] != k:
         raise ValueError(f"dd, q and d must be [m][{k}] or [g][m][{k}], got {tuple(shape)}")
     slots, m = shape[0] if len(shape) == 3 else 1, shape[-2]
-    dp = _optional(d, "d", (_bf16,), shape, index)
-    ddp = _optional(dd, "dd", (_bf16,), shape, index)
+    dp = None if d is None else _like(d, "d", (_bf16,), shape, index)
+    ddp = None if dd is None else _like(dd, "dd", (_bf16,), shape, index)
     qp, sp = _codes(q, sfa, ("q", "sfa"), slots, m, k, shape, index)
-    dwp = _optional(dweights, "dweights", _F32, positions.shape, index)
+    dwp = None if dweights is None else _like(dweights, "dweights", _F32, positions.shape, index)
     _call("fp8bs_moe_combine_backward", index, stream, gp, _CODE[dy.dtype], dp, pp, wp, ddp, qp, sp,
           dwp, slots, m, tokens, topk, k)
 
@@ -413,13 +417,13 @@ def fp8bs_gated_quantize_backward(g, dh, sfg=None, d=None, dq=None, sfd=None, dq
     elif sfg is not None:
         raise ValueError("sfg belongs to an e4m3 g")
     dhp = _like(dh, "dh", (_bf16,), (m, f), index)
-    dp = _optional(d, "d", (_bf16,), g.shape, index)
+    dp = None if d is None else _like(d, "d", (_bf16,), g.shape, index)
     qp, qs = _codes(dq, sfd, ("dq", "sfd"), 1, m, two_f, g.shape, index)
     tp, ts = _columns(dqt, sfdt, ("dqt", "sfdt"), m, two_f, index)
     hp, hs = _columns(hqt, sfht, ("hqt", "sfht"), m, f, index)
     if dp is None and qp is None and tp is None and hp is None and m:
         raise ValueError("no output given: d, dq, dqt or hqt")
-    lp = _optional(grouped_layout, "grouped_layout", _INT32, (m,), index)
+    lp = None if grouped_layout is None else _like(grouped_layout, "grouped_layout", _INT32, (m,), index)
     _call("fp8bs_gated_quantize_backward", index, stream, gp, kind, sp, dhp, dp, qp, qs, tp, ts, hp,
           hs, lp, m, f, act)
 
@@ -441,7 +445,7 @@ def fp8bs_quantize_128x1(x, q, sf, sfx=None, grouped_layout=None, stream=None):
     qp, sp = _columns(q, sf, ("q", "sf"), rows, n, index)
     if qp is None:
         raise ValueError("q is missing")
-    lp = _optional(grouped_layout, "grouped_layout", _INT32, (rows,), index)
+    lp = None if grouped_layout is None else _like(grouped_layout, "grouped_layout", _INT32, (rows,), index)
     _call("fp8bs_quantize_128x1", index, stream, xp, kind, sxp, qp, sp, lp, rows, n)
 
 
