@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
         Eight<true> gate[kLaneRows], up[kLaneRows];
         Held<kLaneRows> rows;
         rows.load(layout, lane_row, last);
+        // (no row of the wavefront holds a token, as past the last expert's: nothing to read)
+        if (layout && !__ballot(rows.held(lane_row, last))) continue;
 #pragma unroll
         for (int i = 0; i < kLaneRows; ++i) {          // (rows past the last: that one again)
             const int r = clipped(lane_row + 4 * i, last);
