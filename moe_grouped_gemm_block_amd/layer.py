@@ -153,14 +153,24 @@ def _space(workspace, size, index, stream):
     return _ptr(workspace, "workspace", (_u8,), 1, index), workspace.shape[0], workspace
 
 
+_MOST = 0x7FFFFFFF                                  # (the calls take sizes as int: more would wrap)
+
+
+def _within(name, *sizes):
+    for n in sizes:
+        if n > _MOST:
+            raise FP8BSError(1, f"{name}: sizes are at most 2^31 - 1")
+
+
 def _matrix(t, name, dtypes, index):
     """(address, rows, columns) of a matrix."""
-    if isinstance(t, _Tensor) and t.dtype in dtypes and t.get_device() == index:
-        shape = t.shape
-        if len(shape) == 2 and shape[1] <= 1 << 24 and t.is_contiguous():
-            return t.data_ptr(), *shape
-    _ptr(t, name, dtypes, 2, index)
-    raise FP8BSError(1, f"{name}: at most 2^24 columns")   # (longer ones do not all fit the call's int)
+    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.get_device() == index
+            and t.ndim == 2 and t.is_contiguous()):
+        _ptr(t, name, dtypes, 2, index)
+    rows, columns = t.shape
+    if columns > 1 << 24 or rows > _MOST:
+        raise FP8BSError(1, f"{name}: at most 2^24 columns and 2^31 - 1 rows")
+    return t.data_ptr(), rows, columns
 
 
 # ---- norm ------------------------------------------------------------------------
@@ -205,6 +215,7 @@ def rms_norm_1x128(x, weight, residual=None, eps: float = 1e-6, stream=None):
 
 @functools.lru_cache(256)
 def rms_norm_backward_workspace_size(rows: int, k: int) -> int:
+    _within("rms_norm_backward_workspace_size", k)
     return _size("fp8bs_rms_norm_backward_workspace_size", rows, k)
 
 
@@ -236,6 +247,7 @@ def fp8bs_rms_norm_backward(s, rstd, weight, dy, dx, dresidual=None, dweight=Non
 
 def moe_capacity(tokens: int, topk: int, num_groups: int) -> int:
     """Rows of the contiguous layout that hold any choices."""
+    _within("moe_capacity", topk, num_groups)
     return _size("fp8bs_moe_capacity", tokens, topk, num_groups)
 
 
@@ -244,6 +256,7 @@ def moe_dispatch_workspace_size(layout: int, tokens: int, topk: int, num_groups:
                                 m: int) -> int:
     """Workspace bytes of ``fp8bs_moe_dispatch`` (layout: LAYOUT_CONTIGUOUS or LAYOUT_MASKED; m:
     rows, of a slot if masked)."""
+    _within("moe_dispatch_workspace_size", layout, topk, num_groups)
     return _size("fp8bs_moe_dispatch_workspace_size", layout, tokens, topk, num_groups, m)
 
 
@@ -269,6 +282,7 @@ def fp8bs_moe_dispatch(ids, x, a, group_data, positions, counts, sfx=None, sfa=N
     masked = isinstance(a, _Tensor) and a.ndim == 3
     ap = _ptr(a, "a", _FP8 if kind == DTYPE_E4M3 else (x.dtype,), 3 if masked else 2, index)
     m = a.shape[-2]
+    _within("a", g, m, topk)
     if a.shape[-1] != k or (masked and a.shape[0] != g):
         raise ValueError("shape mismatch between x, a and counts")
     gp = _like(group_data, "group_data", _INT32, (g,) if masked else (m,), index)
@@ -296,6 +310,7 @@ def moe_dispatch(ids, x, num_groups: int, sfx=None, max_m=None, stream=None):
     _, tokens, k = _matrix(x, "x", _ROWS, index)
     if ids.ndim != 2:
         raise ValueError("ids must be [tokens][topk]")
+    _within("ids", ids.shape[1], int(num_groups))
     g = int(num_groups)
     if g < 1:
         raise ValueError("num_groups must be at least 1")
@@ -321,6 +336,7 @@ def _assigned(positions, weights, tokens, index):
     pp = _ptr(positions, "positions", _INT32, 2, index)
     if positions.shape[0] != tokens:
         raise ValueError("positions must have one row per token")
+    _within("positions", positions.shape[1])
     wp = None if weights is None else _like(weights, "weights", _F32, positions.shape, index)
     return pp, wp, positions.shape[1]
 
@@ -356,6 +372,7 @@ def fp8bs_moe_combine_backward(dy, positions, d=None, weights=None, dd=None, q=N
     if len(shape) not in (2, 3) or shape[-1] != k:
         raise ValueError(f"dd, q and d must be [m][{k}] or [g][m][{k}], got {tuple(shape)}")
     slots, m = shape[0] if len(shape) == 3 else 1, shape[-2]
+    _within("d", slots, m)
     dp = None if d is None else _like(d, "d", (_bf16,), shape, index)
     ddp = None if dd is None else _like(dd, "dd", (_bf16,), shape, index)
     qp, sp = _codes(q, sfa, ("q", "sfa"), slots, m, k, shape, index)
@@ -383,6 +400,7 @@ def fp8bs_gated_quantize(g, hq, sfh, gq=None, sfg=None, grouped_layout=None, mas
     masked = masked_m is not None
     gp = _ptr(g, "g", (_bf16,), 3 if masked else 2, index)
     slots, m = g.shape[0] if masked else 1, g.shape[-2]
+    _within("g", slots, m)
     f = _gated_columns(g.shape[-1])
     if f > 1 << 23:
         raise FP8BSError(1, "g: at most 2^24 columns")

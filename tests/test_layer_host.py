@@ -232,6 +232,25 @@ def test_the_binding_refuses_host_tensors_and_other_types():
         fp8bs.fp8bs_quantize_128x1(x, x, x)
 
 
+def test_sizes_that_an_int_does_not_hold_are_refused():
+    """they would wrap to small ones: 2^32 + 1 rows to one row (the pages of the tensors here are
+    never touched)"""
+    m = fp8bs.layer
+    m._load()
+    many = (1 << 32) + 1
+    tall = torch.empty(many, 1, dtype=torch.uint8)
+    with pytest.raises(fp8bs.FP8BSError, match="2.31"):
+        m._matrix(tall, "x", m._ROWS, tall.get_device())
+    for t in (torch.empty(8, 16, dtype=torch.uint8), torch.empty(0, 16, dtype=torch.uint8)):
+        assert m._matrix(t, "x", m._ROWS, t.get_device())[1:] == tuple(t.shape)
+    for call in (lambda: m.moe_capacity(1, many, 8), lambda: m.moe_capacity(1, 1, many),
+                 lambda: m.moe_dispatch_workspace_size(CONTIGUOUS, 1, many, 8, 128),
+                 lambda: m.rms_norm_backward_workspace_size(8, (1 << 32) + 8),
+                 lambda: m._within("g", 1, many)):
+        with pytest.raises(fp8bs.FP8BSError):
+            call()
+
+
 def test_the_reference_quantiser():
     """the tests' own quantiser against torch's cast, and its half step"""
     rng = np.random.default_rng(1)
