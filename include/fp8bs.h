@@ -540,8 +540,9 @@ int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void*
  * and scales f32 [R/128][ld(n)], one for each column and 128 rows.  Both quantise a block as
  * fp8bs_quantize_1x128 does, from FP32 values (a NaN's code may have either sign).
  * Sums are FP32 and each output is rounded once.  Optional buffers may be NULL.  Sizes,
- * streams and errors are as for the calls above; pointers are 16-byte aligned, those to rstd, positions, weights, dweights, counts and group
- * data 4-byte, ids as their type.  A workspace is device memory of at least the bytes that the
+ * streams and errors are as for the calls above (rows, of all slots for dispatch and the gradient of
+ * combine, are at most 2^31 - 256); pointers are 16-byte aligned, those to rstd, positions,
+ * weights, dweights, counts and group data 4-byte, ids as their type.  A workspace is device memory of at least the bytes that the
  * size call gives, its contents ignored; less is refused with FP8BS_ERR_UNSUPPORTED, and two
  * calls in flight must not share one.  Every launch keeps to the cap on CUs, which changes no
  * result.
@@ -597,7 +598,7 @@ int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd, const
  * An expert's rows are in the order of its choices (token, then choice).  Contiguous: m is a
  * multiple of 128 and at least fp8bs_moe_capacity(), which holds any choices; experts' segments
  * follow each other from row 0 on.  Masked: choices past a slot's m rows are dropped.
- * topk is at most 64, num_groups at most 1024, tokens * topk at most 2^30.
+ * topk is at most 64, num_groups at most 1024, tokens * topk at most 2^30, k at most 2^24.
  */
 int64_t fp8bs_moe_capacity(int64_t tokens, int topk, int num_groups);
 int64_t fp8bs_moe_dispatch_workspace_size(int layout, int64_t tokens, int topk, int num_groups,
@@ -609,7 +610,7 @@ int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, const void* x,
 
 /*
  * Combine: y[t] = sum over j of weights[t][j] * d[positions[t][j]], j ascending.
- *   d          bf16 [rows][k] (masked: rows = num_groups * m); k a multiple of 8
+ *   d          bf16 [rows][k] (masked: rows = num_groups * m); k a multiple of 8, at most 2^24
  *   positions  int32 [tokens][topk]; those outside 0 .. rows-1 are left out
  *   weights    f32 [tokens][topk], NULL: ones (the gradient of dispatch with respect to x)
  *   y          f32 or bf16 (y_dtype) [tokens][k]
@@ -636,7 +637,7 @@ int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const void* d,
  *   layout     FP8BS_LAYOUT_DENSE, _CONTIGUOUS (group_data: grouped_layout) or _MASKED
  *              (group_data: masked_m, num_groups slots of m rows)
  *   g          bf16 [m][2f] (masked per slot), columns 0 .. f-1 gate, f .. 2f-1 up; f a multiple
- *              of 128
+ *              of 128, at most 2^20
  *   hq, sfh    h as e4m3, 1x128, [m][f]
  *   gq, sfg    g as e4m3, 1x128, [m][2f], optional: all that the backward pass needs of g
  * Rows that are not valid (of the contiguous layout: a negative index) are not written.
@@ -651,7 +652,7 @@ int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const void* d,
  * in dqt and hqt they, and the rows up to a multiple of 128, are zeros.
  *
  * fp8bs_quantize_128x1 -- x f32, bf16 or e4m3 with sfx (1x128) (x_dtype) [rows][n] -> q, sf
- * (128x1); n a multiple of 16, of 128 for e4m3.  Rows with a negative grouped_layout entry
+ * (128x1); n a multiple of 16, of 128 for e4m3, at most 2^20.  Rows with a negative grouped_layout entry
  * (int32 [rows], optional; rows then a multiple of 128) are not read and count as zeros, as do
  * the rows up to a multiple of 128.
  */

@@ -13,7 +13,10 @@ the workspace variants.
 
 ``mxfp4`` holds the 4-bit operators (quantiser and inverse, products, gated
 feed-forward block with its backward pass, whole layer); its public names are
-re-exported here.
+re-exported here.  ``layer`` holds what stands between the products of an FP8
+mixture-of-experts layer (norm with quantised output, dispatch and combine,
+gated activation with an e4m3 checkpoint, quantiser along tokens, and their
+backward passes); re-exported likewise.
 
 The binding refuses to run without the compiled library; there is no fallback.
 Build it with ``python -m moe_grouped_gemm_block_amd.build``.

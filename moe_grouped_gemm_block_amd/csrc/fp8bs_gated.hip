@@ -13,18 +13,20 @@ namespace fp8bs {
 namespace layer {
 namespace {
 
-// The logistic function s of v and, where asked for, 1 - s, each within two or three units in the
-// last place: v_exp_f32 of the product with -log2 e, times what that product's rounding leaves
-// out, and v_rcp_f32.  (v is cut off where s is 0 or 1 already, before its products overflow.)
+// The logistic function s of v and, where asked for, 1 - s.  With e = exp(-v): v_exp_f32 of the
+// product h with log2 e, and what that product's rounding leaves out of -v by the first term of its
+// own exponential (ln 2's rounding is h 1.9e-9: 4 2^-24 at the most); v_rcp_f32 of 1 + e.  s and
+// 1 - s are within 10 2^-24, below |v| = 20 within 7 2^-24.  (-v is cut off at 88, where e is finite
+// and the reciprocal 0 already, and where e is 0, before its products overflow.)
 template <bool GRAD>
 __device__ __forceinline__ float logistic(float v, float& rest) {
-    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float a = __builtin_amdgcn_fmed3f(-v, -200.0f, 200.0f);
-    const float hi = a * kHi;
-    const float lo = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
+    constexpr float kLog2 = 1.44269502f, kLn2 = 0.693147182f;
+    const float a = __builtin_amdgcn_fmed3f(-v, -200.0f, 88.0f);
+    const float h = a * kLog2;
+    const float power = __builtin_amdgcn_exp2f(h);
+    const float e = __builtin_fmaf(power, __builtin_fmaf(h, -kLn2, a), power);
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
-    if (GRAD) rest = __builtin_fminf(e, 3.0e38f) * s;      // (0 where s is)
+    if (GRAD) rest = e * s;
     return s;
 }
 
@@ -102,9 +104,11 @@ struct GatedParams {
 
 constexpr int kLaneRows = 2, kTileRows = 16 * kLaneRows;
 
-// Workgroup: 64 rows x a group of 128 columns, of gate and up; a lane eight columns of each, of
-// four rows, all loads issued before any arithmetic.  The lane divides for one of its group's
-// blocks (block_scales): h, gate and up of each of the four rows.
+// Workgroup: 32 rows x a group of 128 columns, of gate and up; a lane eight columns of each, of
+// two rows, all loads issued before any arithmetic.  The lane divides for one of its group's
+// blocks (block_scales): h, gate and up of each of the two rows.  33280 x 2048 with the checkpoint
+// takes 83 us (476 MB: 5.7 TB/s), without 58; 64 slots' rows of 16 x 256 x 2048 4.1 us.  HBM bounds
+// it, the vector units are busy for two thirds of the time.
 template <int ACT, bool KEEP>
 __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
     constexpr int kBlocks = KEEP ? 3 * kLaneRows : kLaneRows;
@@ -287,6 +291,12 @@ __device__ __forceinline__ void fetch(const GatedBackwardParams& p, uint32_t til
     }
 }
 
+// A workgroup a CU, which goes from tile to tile: the next tile's inputs are on their way while this
+// one's scales are exchanged, which is what two barriers a tile cost most.  Gradients are FP32 until
+// their codes; each is quantised both ways from the registers, so that nothing is read twice.  33280 x
+// 2048 from the checkpoint takes 127 us (622 MB: 4.9 TB/s); the vector units are busy for two thirds of
+// that, some 50 instructions a value.  Without the inputs ahead it took 164 when it took 133 with
+// them, two workgroups of 8 wavefronts a CU 148 (there are no registers to keep inputs ahead).
 template <int ACT, bool KEPT>
 __global__ void __launch_bounds__(64 * kGradWaves)
     gated_backward_kernel(GatedBackwardParams p) {
@@ -303,21 +313,28 @@ __global__ void __launch_bounds__(64 * kGradWaves)
         const uint32_t held = v.rows.held(lane_row, last);
         float dg[kGradRows][8], du[kGradRows][8], h[kGradRows][8];
         float top[3][8] = {};
+        // a row that holds no token is zeros
+        if (__ballot(held != (1u << kGradRows) - 1)) {
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i) {
+                if ((held >> i) & 1) continue;
+                v.dh[i].zero();
+                if constexpr (KEPT) {
+                    v.gate_q[i] = v.up_q[i] = u32x2{0, 0};
+                    v.gate_s[i] = v.up_s[i] = 0.0f;
+                } else {
+                    v.gate[i].zero();
+                    v.up[i].zero();
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i) {
-            // a row that holds no token is zeros
-            const bool in = (held >> i) & 1;
             float gate[8], up[8];
             if constexpr (KEPT) {
-                widen_e4m3(in ? v.gate_q[i] : u32x2{0, 0}, gate);
-                widen_e4m3(in ? v.up_q[i] : u32x2{0, 0}, up);
-                v.gate_s[i] = in ? v.gate_s[i] : 0.0f;
-                v.up_s[i] = in ? v.up_s[i] : 0.0f;
-            } else {
-                if (!in) v.gate[i].zero();
-                if (!in) v.up[i].zero();
+                widen_e4m3(v.gate_q[i], gate);
+                widen_e4m3(v.up_q[i], up);
             }
-            if (!in) v.dh[i].zero();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if constexpr (KEPT) {
@@ -435,7 +452,11 @@ __device__ __forceinline__ void fetch(const ColumnParams& p, uint32_t tile, int 
     }
 }
 
-// Tile of 128 x 128 as above; n need not be a multiple of 128.
+// Tile of 128 x 128 as above; n need not be a multiple of 128.  33280 x 7168 from e4m3 takes 90 us
+// (488 MB: 5.4 TB/s; a copy of the same tiles, whose rows are single lines, 84 to 93), bf16 16384 x 7168
+// 64, FP32 16384 x 4096 63.  A workgroup a tile, three a CU, hide its barriers better than one that goes
+// on with the next tile's inputs ahead (101 to 106).  Neighbouring tiles on one XCD, as the scales of
+// four tiles lie in one line: 3% of the time.
 template <int DTYPE>
 __global__ void __launch_bounds__(64 * kColumnWaves) quant_128x1_kernel(ColumnParams p) {
     __shared__ ColumnScales<1, kColumnWaves> lds;

@@ -48,9 +48,10 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[16], int& turn) 
 
 // Workgroup = one row on W = 4 or 16 wavefronts, or four rows (W = 1, a wavefront each).  A lane
 // holds NV runs of eight columns, 512 W apart, 16 lanes a 128-column group.  RES: type of residual
-// (0 none, 1 bf16, 2 FP32).  16384 x 7168 in bf16 takes 141 us (5.9 TB/s; a copy past the caches
-// runs at 6.2): loads issued together, the weight's before the sum, a division for NV groups.  Eight rows
-// a workgroup, the next one's loads before this one's sum and scales written together, took 150.
+// (0 none, 1 bf16, 2 FP32).  16384 x 7168 in bf16 takes 140 us (5.9 TB/s; a copy past the caches
+// runs at 6.4): loads issued together, the weight's before the sum, a division for NV groups.  Eight rows
+// a workgroup, the next one's loads before this one's sum and scales written together, took 150.  One
+// row of 7168: 2.9 us, a launch and three latencies.
 template <int W, int NV, bool XB, int RES, bool WB>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormParams p) {
     __shared__ float part[2][16];
@@ -142,6 +143,8 @@ struct BackwardParams {
     uint32_t units;             // unit u takes the rows u, u + units, ... (times rows at once)
 };
 
+// A workgroup goes through rows and keeps its part of dweight in registers; the parts are written
+// once and added by the kernel below.  16384 x 7168 in bf16 takes 156 + 5 us (940 MB: 5.9 TB/s, HBM).
 template <int W, int NV, bool SB, bool GB, bool WB>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel(BackwardParams p) {
     __shared__ float part[2][16];
@@ -352,8 +355,8 @@ extern "C" int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, 
                     y_dtype == FP8BS_DTYPE_BF16, far_outputs((double)rows * k * (q ? 1 : 2)),
                     (uint32_t)(((int64_t)rows + at_once(s) - 1) / at_once(s))};
     const int res = !residual ? 0 : residual_dtype == FP8BS_DTYPE_BF16 ? 1 : 2;
-    return launch(norm_kernel(s, x_dtype == FP8BS_DTYPE_BF16, res, weight_dtype == FP8BS_DTYPE_BF16), workgroups(p.units, s.waves == 16 ? 2 : 8),
-                  threads_of(s), p, stream);
+    return launch(norm_kernel(s, x_dtype == FP8BS_DTYPE_BF16, res, weight_dtype == FP8BS_DTYPE_BF16),
+                  workgroups(p.units, s.waves == 16 ? 2 : 8), threads_of(s), p, stream);
 }
 
 extern "C" int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k) {
