@@ -148,6 +148,12 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
             total[e] = 0;
             for (int w = 0; w < 4; ++w) next[w][e] = 0;
         }
+        const int quarter = p.chunk / 4;
+        const int64_t first = (int64_t)c * p.chunk + (int64_t)wave * quarter;
+        const int64_t end =
+            c >= p.chunks ? first : first + quarter < p.n ? first + quarter : (int64_t)p.n;
+        // (the first choices are on their way while the counts are added)
+        const int e0 = first + lane < end ? expert_of(p, (int)first + lane) : -1;
         __syncthreads();
         // (assignments of earlier chunks go into next[0], those of the chunk's earlier
         // wavefronts below)
@@ -160,13 +166,9 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
                 if (of < c) atomicAdd(&next[0][e], v);
             }
         }
-        const int quarter = p.chunk / 4;
-        const int64_t first = (int64_t)c * p.chunk + (int64_t)wave * quarter;
-        const int64_t end =
-            c >= p.chunks ? first : first + quarter < p.n ? first + quarter : (int64_t)p.n;
         if (wave < 3)
             for (int64_t i = first + lane; i < end; i += 64) {
-                const int e = expert_of(p, (int)i);
+                const int e = i == first + lane ? e0 : expert_of(p, (int)i);
                 if (e >= 0) atomicAdd(&next[wave + 1][e], 1);
             }
         __syncthreads();
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
         write_group_data(p, total, start, c, p.rank_units);
         for (int64_t base = first; base < end; base += 64) {
             const int64_t i = base + lane;
-            const int e = i < end ? expert_of(p, (int)i) : -1;
+            const int e = base == first ? e0 : i < end ? expert_of(p, (int)i) : -1;
             const uint64_t same = same_expert(e, p.groups);
             const uint64_t below = same & ((1ull << lane) - 1ull);
             const int rank = e < 0 ? 0 : next[wave][e] + __popcll(below);
@@ -193,30 +195,13 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
     }
 }
 
-constexpr int kRowPieces = 4;                  // 16-byte pieces of a lane at a time
-
-// A wavefront copies up to 4 KB of a token's row to the rows of its assignments.
-__device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int piece0, int lane,
+// A wavefront copies 1 KB of a token's row to the rows of its assignments (2 KB: 4% slower, 4 KB 6%).
+__device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int at,
                                          const int32_t* rows) {
-    u32x4 v[kRowPieces];
-    const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
-#pragma unroll
-    for (int i = 0; i < kRowPieces; ++i) {     // (past the row's end: its last piece again)
-        const int at = piece0 + 64 * i + lane;
-        v[i] = __builtin_nontemporal_load(from + (at < p.vectors ? at : p.vectors - 1));
-    }
-#pragma unroll 1
-    for (int j = 0; j < p.topk; ++j) {
-        const int row = rows[j];
-        if (row < 0) continue;
-        u32x4* to = (u32x4*)p.a + (int64_t)row * p.vectors;
-#pragma unroll
-        for (int i = 0; i < kRowPieces; ++i) {
-            const int at = piece0 + 64 * i + lane;
-            if (at >= p.vectors) continue;
-            put16(to + at, v[i], p.far);
-        }
-    }
+    if (at >= p.vectors) return;
+    const u32x4 v = __builtin_nontemporal_load((const u32x4*)p.x + (int64_t)token * p.vectors + at);
+    for (int j = 0; j < p.topk; ++j)
+        if (rows[j] >= 0) put16((u32x4*)p.a + (int64_t)rows[j] * p.vectors + at, v, p.far);
 }
 
 // Scales lie column-group-major, so they go by rows: a wavefront 64 neighbouring rows of the
@@ -234,8 +219,8 @@ __device__ __forceinline__ void copy_scales(const DispatchParams& p, uint32_t bl
     for (int c = 0; c < p.kb; ++c) to[(int64_t)c * p.sfa_ld] = p.sfx[(int64_t)c * p.sfx_ld + token];
 }
 
-// Scales first: their units are the longer ones.  16384 tokens of two choices, e4m3 rows of 7168: 69
-// us (364 MB: 5.3 TB/s); a row is read once, its copies written past the caches.
+// Scales first, as their units are the longer ones (last: 13% slower).  16384 tokens of two choices,
+// e4m3 rows of 7168: 62 us (364 MB: 5.9 TB/s); a row is read once, its copies written past the caches.
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchParams p, int pieces,
                                                             uint32_t scale_units) {
     const int lane = threadIdx.x & 63;
@@ -248,7 +233,7 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchParams p, in
         }
         const uint32_t u = unit - scale_units;
         const int token = (int)(u / pieces), piece = (int)(u - (uint32_t)token * pieces);
-        copy_row(p, token, piece * 64 * kRowPieces, lane, p.positions + (int64_t)token * p.topk);
+        copy_row(p, token, piece * 64 + lane, p.positions + (int64_t)token * p.topk);
     }
 }
 
@@ -577,7 +562,7 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     p.rank_units = p.chunks;
     if (!masked && m / 512 > p.chunks) p.rank_units = m / 512 < 256 ? m / 512 : 256;
     if (p.rank_units < p.chunks) p.rank_units = p.chunks;
-    const int pieces = (p.vectors + 64 * kRowPieces - 1) / (64 * kRowPieces);
+    const int pieces = (p.vectors + 63) / 64;
     const int64_t scale_units = e4m3 ? (int64_t)((m + 63) / 64) * (masked ? num_groups : 1) : 0;
     const int64_t units = scale_units + (int64_t)tokens * pieces;
     if (units > 0x7fffffff) return FP8BS_ERR_UNSUPPORTED;

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(64 * kGradWaves)
                 top[2][e] = __builtin_fmaxf(top[2][e], __builtin_fabsf(h[i][e]));
             }
         }
-        if (tile + gridDim.x < p.tiles) fetch<KEPT>(p, tile + gridDim.x, lane_row, seg, v);
+        
         if (p.dq) {
             float most[2 * kGradRows], inv[2 * kGradRows];
 #pragma unroll
@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(64 * kGradWaves)
                     store8(p.d, true, at, dg[i]);
                     store8(p.d, true, at + p.f, du[i]);
                 }
+        if (tile + gridDim.x < p.tiles) fetch<KEPT>(p, tile + gridDim.x, lane_row, seg, v);
         if (!p.dqt && !p.hqt) continue;
         float* const to[3] = {
             p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + kBlock * c : nullptr,
