@@ -321,13 +321,13 @@ struct CombineParams {
     const float* weights;       // nullptr: ones
     void* y;
     int64_t rows;
-    int tokens, topk, k, pieces;
+    int tokens, topk, k, pieces, far;
     uint32_t units;
 };
 
 // A wavefront: 512 columns of a token, four choices' rows on their way at a time.  16384 tokens of two
-// choices, 7168 columns: 127 us (705 MB: 5.6 TB/s, HBM); 64 tokens of eight choices 3.8.
-template <bool YB>
+// choices, 7168 columns: 117 us (705 MB: 6 TB/s, HBM); 64 tokens of eight choices 3.8.
+template <bool YB, bool FAR>
 __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
     const int lane = threadIdx.x & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
                 const int row = j0 + j < p.topk ? at[j0 + j] : -1;
                 in[j] = row >= 0 && row < p.rows;
                 f[j] = in[j] && w ? w[j0 + j] : 1.0f;
-                if (in[j]) v[j].load(p.d, (int64_t)row * p.k + col);
+                if (in[j]) v[j].take<FAR>(p.d, (int64_t)row * p.k + col);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] += f[j] * v[j][e];
         }
-        store8(p.y, YB, (int64_t)token * p.k + col, y);
+        put_values(p.y, YB, (int64_t)token * p.k + col, y, p.far);
     }
 }
 
@@ -373,12 +373,12 @@ struct CombineBackwardParams {
     uint32_t units;
 };
 
-// Workgroup = two choices of a token; a lane eight columns of each 2048, 16 lanes a group of 128, two
-// such runs at a time, their loads issued together.  A group's largest |w dy| is |w| times that of
-// |dy| (rounding keeps the order).  Workgroups go round the 8 XCDs: eight tokens' first pairs are
-// followed by their second ones, so that a token's pairs find its dy in one L2.  16384 tokens of
-// two choices, 7168 columns: 170 us (5.6 TB/s); one load at a time took 205.
-template <bool GB>
+// Workgroup = two choices of a token; a lane eight columns of each 2048, 16 lanes a group of 128.  A
+// group's largest |w dy| is |w| times that of |dy| (rounding keeps the order).  Workgroups go round
+// the 8 XCDs: eight tokens' first pairs are followed by their second ones, so that a token's pairs
+// find its dy in one L2.  16384 tokens of two choices, 7168 columns: 166 us (947 MB: 5.7 TB/s; reads
+// alone run at 6.9); 512 threads take the same.
+template <bool GB, bool FAR>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardParams p) {
     __shared__ float dots[2][2][4];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -387,79 +387,68 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardPa
     for (uint32_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
         const int token = (int)(unit / (8 * pairs) * 8 + unit % 8);
         const int j0 = (int)(unit / 8 % pairs) * 2;
-        if (token < p.tokens) {
-            const int32_t* at = p.positions + (int64_t)token * p.topk;
-            const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
-            int row[2];
-            bool in[2];
-            const uint16_t* from[2];
-            float f[2], dot[2] = {0.0f, 0.0f};
+        if (token >= p.tokens) continue;
+        const int32_t* at = p.positions + (int64_t)token * p.topk;
+        const float* w = p.weights ? p.weights + (int64_t)token * p.topk : nullptr;
+        int row[2];
+        bool in[2];
+        const uint16_t* from[2];
+        float f[2], dot[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            row[j] = j0 + j < p.topk ? at[j0 + j] : -1;
+            in[j] = row[j] >= 0 && row[j] < p.rows;
+            f[j] = in[j] && w ? w[j0 + j] : 1.0f;
+            // (a choice without a row reads dy in its place)
+            from[j] = in[j] ? p.d + (int64_t)row[j] * p.k
+                            : (const uint16_t*)p.dy + (int64_t)token * p.k;
+        }
+        for (int col = t * 8; col < p.k; col += 2048) {
+            Eight<GB> g;
+            Eight<true> d[2];
+            g.template take<FAR>(p.dy, (int64_t)token * p.k + col);
+            if (p.dw)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) d[j].take<FAR>(from[j], col);
+            float dy[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dy[e] = g[e];
+            const float top = p.q ? max16(max8(dy)) : 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                row[j] = j0 + j < p.topk ? at[j0 + j] : -1;
-                in[j] = row[j] >= 0 && row[j] < p.rows;
-                f[j] = in[j] && w ? w[j0 + j] : 1.0f;
-                // (a choice without a row reads dy in its place)
-                from[j] = in[j] ? p.d + (int64_t)row[j] * p.k
-                                : (const uint16_t*)p.dy + (int64_t)token * p.k;
-            }
-            for (int col0 = t * 8; col0 < p.k; col0 += 4096) {
-                Eight<GB> g[2];
-                Eight<true> d[2][2];
+                if (!in[j]) continue;
+                if (p.dw)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {  // (past the row's end: its last columns again)
-                    const int col = col0 + 2048 * i < p.k ? col0 + 2048 * i : p.k - 8;
-                    g[i].load(p.dy, (int64_t)token * p.k + col);
-                    if (p.dw)
+                    for (int e = 0; e < 8; ++e) dot[j] += dy[e] * d[j][e];
+                float dd[8];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            d[i][j].stream(from[j], col);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = col0 + 2048 * i;
-                    if (col >= p.k) continue;
-                    float dy[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dy[e] = g[i][e];
-                    const float top = p.q ? max16(max8(dy)) : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (!in[j]) continue;
-                        if (p.dw)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) dot[j] += dy[e] * d[i][j][e];
-                        float dd[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dd[e] = f[j] * dy[e];
-                        const int64_t to = (int64_t)row[j] * p.k + col;
-                        if (p.dd) put_values(p.dd, true, to, dd, p.far);
-                        if (p.q) {
-                            float inv;         // (a NaN product is no maximum)
-                            const float sc = block_scale(
-                                __builtin_fmaxf(__builtin_fabsf(f[j]) * top, 0.0f), inv);
-                            put_codes(p.q + to, codes8(dd, inv), p.far);
-                            if ((lane & 15) == 0) {
-                                const int slot = row[j] / p.m;
-                                p.sfa[((int64_t)slot * (p.k >> 7) + (col >> 7)) * p.ld + row[j] -
-                                      slot * p.m] = sc;
-                            }
-                        }
+                for (int e = 0; e < 8; ++e) dd[e] = f[j] * dy[e];
+                const int64_t to = (int64_t)row[j] * p.k + col;
+                if (p.dd) put_values(p.dd, true, to, dd, p.far);
+                if (p.q) {
+                    float inv;             // (a NaN product is no maximum)
+                    const float sc =
+                        block_scale(__builtin_fmaxf(__builtin_fabsf(f[j]) * top, 0.0f), inv);
+                    put_codes(p.q + to, codes8(dd, inv), p.far);
+                    if ((lane & 15) == 0) {
+                        const int slot = row[j] / p.m;
+                        p.sfa[((int64_t)slot * (p.k >> 7) + (col >> 7)) * p.ld + row[j] -
+                              slot * p.m] = sc;
                     }
                 }
             }
-            if (p.dw) {                        // (two buffers: one barrier a unit)
+        }
+        if (p.dw) {                        // (two buffers: one barrier a unit)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float sum = sum_wave(dot[j]);
-                    if (lane == 0) dots[turn][j][wave] = sum;
-                }
-                __syncthreads();
-                if (t < 2 && j0 + t < p.topk)
-                    p.dw[(int64_t)token * p.topk + j0 + t] =
-                        (dots[turn][t][0] + dots[turn][t][1]) + (dots[turn][t][2] + dots[turn][t][3]);
-                turn ^= 1;
+            for (int j = 0; j < 2; ++j) {
+                const float sum = sum_wave(dot[j]);
+                if (lane == 0) dots[turn][j][wave] = sum;
             }
+            __syncthreads();
+            if (t < 2 && j0 + t < p.topk)
+                p.dw[(int64_t)token * p.topk + j0 + t] =
+                    (dots[turn][t][0] + dots[turn][t][1]) + (dots[turn][t][2] + dots[turn][t][3]);
+            turn ^= 1;
         }
     }
 }
@@ -590,13 +579,17 @@ extern "C" int fp8bs_moe_combine(const void* d, const int32_t* positions, const 
     if ((rows > 0 ? !aligned(d) : false) || !aligned(positions, 4) || !aligned_or_null(weights, 4) ||
         !aligned(y))
         return FP8BS_ERR_POINTER;
+    const bool bf16 = y_dtype == FP8BS_DTYPE_BF16;
     const int pieces = (k + 511) / 512;
     const int64_t units = (int64_t)tokens * pieces;
     if (units > 0x7fffffff) return FP8BS_ERR_UNSUPPORTED;
     CombineParams p = {(const uint16_t*)d, positions, weights, y, rows, tokens, topk, k, pieces,
-                       (uint32_t)units};
-    return launch(y_dtype == FP8BS_DTYPE_BF16 ? (const void*)combine_kernel<true>
-                                              : (const void*)combine_kernel<false>,
+                       far_outputs((double)tokens * k * (bf16 ? 2 : 4)), (uint32_t)units};
+    const bool far = far_inputs((double)tokens * k * (topk * 2 + (bf16 ? 2 : 4)));
+    return launch(bf16  ? far ? (const void*)combine_kernel<true, true>
+                              : (const void*)combine_kernel<true, false>
+                  : far ? (const void*)combine_kernel<false, true>
+                        : (const void*)combine_kernel<false, false>,
                   workgroups((units + 3) / 4, 8), 256, p, stream);
 }
 
@@ -622,7 +615,12 @@ extern "C" int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const vo
                                (int)fp8bs_get_sfa_ld(m), tokens, topk, k,
                                far_outputs((double)tokens * topk * k * ((dd ? 2 : 0) + (q ? 1 : 0))),
                                (uint32_t)units};
-    return launch(dy_dtype == FP8BS_DTYPE_BF16 ? (const void*)combine_backward_kernel<true>
-                                               : (const void*)combine_backward_kernel<false>,
+    const bool bf16 = dy_dtype == FP8BS_DTYPE_BF16;
+    const bool far = far_inputs(
+        (double)tokens * k * ((bf16 ? 2 : 4) + topk * ((dd ? 2 : 0) + (q ? 1 : 0) + (dweights ? 2 : 0))));
+    return launch(bf16  ? far ? (const void*)combine_backward_kernel<true, true>
+                              : (const void*)combine_backward_kernel<true, false>
+                  : far ? (const void*)combine_backward_kernel<false, true>
+                        : (const void*)combine_backward_kernel<false, false>,
                   workgroups(units, 8), 256, p, stream);
 }

@@ -51,15 +51,18 @@ __device__ __forceinline__ float activate(float v, float& slope) {
     }
 }
 
+template <bool FAR>
 __device__ __forceinline__ u32x2 take8(const uint8_t* base, uint32_t at) {
-    return __builtin_nontemporal_load((const u32x2*)(base + at));
+    const u32x2* from = (const u32x2*)(base + at);
+    return FAR ? __builtin_nontemporal_load(from) : *from;
 }
 // Eight bf16 or FP32 values
-template <bool BF16>
+template <bool FAR, bool BF16>
 __device__ __forceinline__ void take(const void* base, uint32_t at, Eight<BF16>& v) {
     const u32x4* from = (const u32x4*)((const uint8_t*)base + at);
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 1 : 2); ++i) v.w[i] = __builtin_nontemporal_load(from + i);
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+        v.w[i] = FAR ? __builtin_nontemporal_load(from + i) : from[i];
 }
 // Byte offset in a tile: row r (at most 127) of rows of `bytes` (less than 2^24), and on.
 __device__ __forceinline__ uint32_t place(int r, int bytes, int on) {
@@ -108,8 +111,8 @@ constexpr int kLaneRows = 2, kTileRows = 16 * kLaneRows;
 // two rows, all loads issued before any arithmetic.  The lane divides for one of its group's
 // blocks (block_scales): h, gate and up of each of the two rows.  33280 x 2048 with the checkpoint
 // takes 83 us (476 MB: 5.7 TB/s), without 58; 64 slots' rows of 16 x 256 x 2048 4.1 us.  HBM bounds
-// it, the vector units are busy for two thirds of the time.
-template <int ACT, bool KEEP>
+// it, the vector units are busy for two thirds of the time.  One row a lane: 4% slower.
+template <int ACT, bool KEEP, bool FAR>
 __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
     constexpr int kBlocks = KEEP ? 3 * kLaneRows : kLaneRows;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -135,8 +138,8 @@ __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {
 #pragma unroll
         for (int i = 0; i < kLaneRows; ++i) {          // (rows past the last: that one again)
             const int r = clipped(lane_row + 4 * i, last);
-            take(from, place(r, 4 * p.f, 16 * seg), gate[i]);
-            take(from + p.f, place(r, 4 * p.f, 16 * seg), up[i]);
+            take<FAR>(from, place(r, 4 * p.f, 16 * seg), gate[i]);
+            take<FAR>(from + p.f, place(r, 4 * p.f, 16 * seg), up[i]);
         }
         float h[kLaneRows][8], top[kBlocks], inv[kBlocks], unused;
 #pragma unroll
@@ -276,17 +279,17 @@ __device__ __forceinline__ void fetch(const GatedBackwardParams& p, uint32_t til
 #pragma unroll
     for (int i = 0; i < kGradRows; ++i) {      // (rows past the last: that one again)
         const int r = clipped(lane_row + 4 * i, last);
-        take(dh, place(r, 2 * p.f, 16 * seg), v.dh[i]);
+        take<false>(dh, place(r, 2 * p.f, 16 * seg), v.dh[i]);
         if constexpr (KEPT) {
             const uint8_t* g = (const uint8_t*)p.g + at;
-            v.gate_q[i] = take8(g, place(r, 2 * p.f, 8 * seg));
-            v.up_q[i] = take8(g + p.f, place(r, 2 * p.f, 8 * seg));
+            v.gate_q[i] = take8<false>(g, place(r, 2 * p.f, 8 * seg));
+            v.up_q[i] = take8<false>(g + p.f, place(r, 2 * p.f, 8 * seg));
             v.gate_s[i] = (p.sfg + (int64_t)c * p.ld + row0)[r];
             v.up_s[i] = (p.sfg + (int64_t)(fb + c) * p.ld + row0)[r];
         } else {
             const uint16_t* g = (const uint16_t*)p.g + at;
-            take(g, place(r, 4 * p.f, 16 * seg), v.gate[i]);
-            take(g + p.f, place(r, 4 * p.f, 16 * seg), v.up[i]);
+            take<false>(g, place(r, 4 * p.f, 16 * seg), v.gate[i]);
+            take<false>(g + p.f, place(r, 4 * p.f, 16 * seg), v.up[i]);
         }
     }
 }
@@ -294,8 +297,9 @@ __device__ __forceinline__ void fetch(const GatedBackwardParams& p, uint32_t til
 // A workgroup a CU, which goes from tile to tile: the next tile's inputs are on their way while this
 // one's scales are exchanged, which is what two barriers a tile cost most.  Gradients are FP32 until
 // their codes; each is quantised both ways from the registers, so that nothing is read twice.  33280 x
-// 2048 from the checkpoint takes 127 us (622 MB: 4.9 TB/s); the vector units are busy for two thirds of
-// that, some 50 instructions a value.  Without the inputs ahead it took 164 when it took 133 with
+// 2048 from the checkpoint takes 129 us (622 MB: 4.8 TB/s); the vector units are busy for two thirds of
+// that, some 50 instructions a value.  Inputs are read through the caches at every size: 129 us against
+// 127 past them, 8192 x 2048 29.7 against 35.4.  Without the inputs ahead it took 164 when it took 133 with
 // them, two workgroups of 8 wavefronts a CU 148 (there are no registers to keep inputs ahead).
 template <int ACT, bool KEPT>
 __global__ void __launch_bounds__(64 * kGradWaves)
@@ -429,7 +433,7 @@ struct ColumnInputs {
     Eight<DTYPE == FP8BS_DTYPE_BF16> x[kKept ? 1 : kColumnRows];
     Held<kColumnRows> rows;
 };
-template <int DTYPE>
+template <int DTYPE, bool FAR>
 __device__ __forceinline__ void fetch(const ColumnParams& p, uint32_t tile, int lane_row, int seg,
                                       ColumnInputs<DTYPE>& v) {
     const int c = (int)(tile % p.col_tiles), rt = (int)(tile / p.col_tiles);
@@ -443,12 +447,12 @@ __device__ __forceinline__ void fetch(const ColumnParams& p, uint32_t tile, int 
     for (int i = 0; i < kColumnRows; ++i) {    // (rows past the last: that one again; columns alike)
         const int r = clipped(lane_row + 4 * i, last);
         if constexpr (DTYPE == FP8BS_DTYPE_E4M3) {
-            v.q[i] = take8((const uint8_t*)p.x + at, place(r, p.n, col));
+            v.q[i] = take8<FAR>((const uint8_t*)p.x + at, place(r, p.n, col));
             v.s[i] = (p.sfx + (int64_t)c * p.ldx + row0)[r];
         } else if constexpr (DTYPE == FP8BS_DTYPE_BF16) {
-            take((const uint16_t*)p.x + at, place(r, 2 * p.n, 2 * col), v.x[i]);
+            take<FAR>((const uint16_t*)p.x + at, place(r, 2 * p.n, 2 * col), v.x[i]);
         } else {
-            take((const float*)p.x + at, place(r, 4 * p.n, 4 * col), v.x[i]);
+            take<FAR>((const float*)p.x + at, place(r, 4 * p.n, 4 * col), v.x[i]);
         }
     }
 }
@@ -458,7 +462,7 @@ __device__ __forceinline__ void fetch(const ColumnParams& p, uint32_t tile, int 
 // 64, FP32 16384 x 4096 63.  A workgroup a tile, three a CU, hide its barriers better than one that goes
 // on with the next tile's inputs ahead (101 to 106).  Neighbouring tiles on one XCD, as the scales of
 // four tiles lie in one line: 3% of the time.
-template <int DTYPE>
+template <int DTYPE, bool FAR>
 __global__ void __launch_bounds__(64 * kColumnWaves) quant_128x1_kernel(ColumnParams p) {
     __shared__ ColumnScales<1, kColumnWaves> lds;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(64 * kColumnWaves) quant_128x1_kernel(ColumnPa
         const int c = (int)(tile % p.col_tiles), rt = (int)(tile / p.col_tiles);
         const int64_t row0 = (int64_t)rt * kBlock;
         ColumnInputs<DTYPE> x;
-        fetch<DTYPE>(p, tile, lane_row, seg, x);
+        fetch<DTYPE, FAR>(p, tile, lane_row, seg, x);
         const uint32_t held = x.rows.held(
             lane_row, p.rows - 1 - row0 < kBlock - 1 ? (int)(p.rows - 1 - row0) : kBlock - 1);
         float v[kColumnRows][8];
@@ -502,6 +506,17 @@ __global__ void __launch_bounds__(64 * kColumnWaves) quant_128x1_kernel(ColumnPa
     }
 }
 
+template <int ACT, bool KEEP>
+const void* quant_kernel(bool far) {
+    return far ? (const void*)gated_quant_kernel<ACT, KEEP, true>
+               : (const void*)gated_quant_kernel<ACT, KEEP, false>;
+}
+template <int DTYPE>
+const void* columns_kernel(bool far) {
+    return far ? (const void*)quant_128x1_kernel<DTYPE, true>
+               : (const void*)quant_128x1_kernel<DTYPE, false>;
+}
+
 constexpr int kMostColumns = 1 << 20;
 bool activation_known(int act) { return act == FP8BS_ACT_SILU || act == FP8BS_ACT_GELU_TANH; }
 
@@ -531,12 +546,12 @@ extern "C" int fp8bs_gated_quantize(int layout, const void* g, void* hq, float* 
     GatedParams p = {(const uint16_t*)g, (uint8_t*)hq, sfh, (uint8_t*)gq, sfg, group_data, layout,
                      m, f, (int)fp8bs_get_sfa_ld(m), row_tiles,
                      far_outputs((double)slots * m * f * (gq ? 3 : 1)), (uint32_t)tiles};
-    const void* fn =
-        activation == FP8BS_ACT_SILU
-            ? gq ? (const void*)gated_quant_kernel<FP8BS_ACT_SILU, true>
-                 : (const void*)gated_quant_kernel<FP8BS_ACT_SILU, false>
-            : gq ? (const void*)gated_quant_kernel<FP8BS_ACT_GELU_TANH, true>
-                 : (const void*)gated_quant_kernel<FP8BS_ACT_GELU_TANH, false>;
+    const bool far = far_inputs((double)slots * m * f * (gq ? 7 : 5));
+    const void* fn = activation == FP8BS_ACT_SILU
+                         ? gq ? quant_kernel<FP8BS_ACT_SILU, true>(far)
+                              : quant_kernel<FP8BS_ACT_SILU, false>(far)
+                         : gq ? quant_kernel<FP8BS_ACT_GELU_TANH, true>(far)
+                              : quant_kernel<FP8BS_ACT_GELU_TANH, false>(far);
     return launch(fn, workgroups(p.tiles, 8), 256, p, stream);
 }
 
@@ -596,8 +611,10 @@ extern "C" int fp8bs_quantize_128x1(const void* x, int x_dtype, const float* sfx
     ColumnParams p = {x, sfx, (uint8_t*)q, sf, grouped_layout, rows, n, (int)fp8bs_get_sfa_ld(rows),
                       (int)fp8bs_get_sfa_ld(n), col_tiles, far_outputs((double)rows * n),
                       (uint32_t)tiles};
-    const void* fn = kept ? (const void*)quant_128x1_kernel<FP8BS_DTYPE_E4M3>
-                     : x_dtype == FP8BS_DTYPE_BF16 ? (const void*)quant_128x1_kernel<FP8BS_DTYPE_BF16>
-                                                   : (const void*)quant_128x1_kernel<FP8BS_DTYPE_F32>;
+    const bool bf16 = x_dtype == FP8BS_DTYPE_BF16;
+    const bool far = far_inputs((double)rows * n * (kept ? 2 : bf16 ? 3 : 5));
+    const void* fn = kept   ? columns_kernel<FP8BS_DTYPE_E4M3>(far)
+                     : bf16 ? columns_kernel<FP8BS_DTYPE_BF16>(far)
+                            : columns_kernel<FP8BS_DTYPE_F32>(far);
     return launch(fn, workgroups(p.tiles, 4), 64 * kColumnWaves, p, stream);
 }

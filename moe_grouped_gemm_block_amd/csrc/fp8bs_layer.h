@@ -52,6 +52,12 @@ inline int compute_units() {
 // 16384 x 7168 148 us and 141, its gradients 174 and 161, gated 33280 x 2048 92 and 87).
 inline int far_outputs(double bytes) { return bytes > 64e6; }
 
+// Whether inputs are read past the caches, from the bytes that a call reads and writes: of few the
+// kernel before has left them there, and many are gone (through the caches and past them: gated 4096 x
+// 2048, 59 MB, 11.6 us and 13.4, 8192 x 2048 24.7 and 22.8; columns of 4096 x 7168 12.4 and 15.2, 8192
+// rows 27.9 and 24.0; combine of 1024 tokens, eight choices, 2048 columns, 38 MB, 8.1 and 10.8).
+inline bool far_inputs(double bytes) { return bytes > 80e6; }
+
 template <class P>
 int launch(const void* kernel, unsigned grid, int threads, P& params, hipStream_t stream,
            size_t lds = 0) {
@@ -90,11 +96,16 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = from[i];
     }
-    // read once, past the caches
+    // past the caches
     __device__ __forceinline__ void stream(const void* x, int64_t at) {
         const u32x4* from = (const u32x4*)((const uint8_t*)x + at * (BF16 ? 2 : 4));
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = __builtin_nontemporal_load(from + i);
+    }
+    template <bool FAR>
+    __device__ __forceinline__ void take(const void* x, int64_t at) {
+        if constexpr (FAR) stream(x, at);
+        else load(x, at);
     }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (BF16) {

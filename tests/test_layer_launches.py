@@ -84,6 +84,10 @@ def test_every_kernel_is_reached():
     queries += [("gated", DENSE, 100, 256, 1, keep + 2 * act) for keep in (0, 1) for act in (0, 1)]
     queries += [("gated_back", 100, 256, kept, act) for kept in (0, 1) for act in (0, 1)]
     queries += [("columns", 100, 256, t) for t in (0, 1, 2)]
+    # (inputs read past the caches: tests/test_gpu_layer_large.py)
+    queries += [(op, 5000, 3, 4096, y) for op in ("combine", "combine_back") for y in (F32, BF16)]
+    queries += [("gated", DENSE, 15000, 1152, 1, keep + 2 * act) for keep in (0, 1) for act in (0, 1)]
+    queries += [("columns", 12345, 4096, t) for t in (0, 1, 2)]
     seen = set()
     for q, (st, launches) in zip(queries, ask(*queries)):
         assert st == 0 and launches, q
