@@ -29,6 +29,19 @@ struct NormParams {
     uint32_t units;
 };
 
+// N numbers' sum, by halves: log2 N roundings on each number's way.
+template <int N>
+__device__ __forceinline__ float sum_of(const float (&v)[N]) {
+    if constexpr (N == 1) {
+        return v[0];
+    } else {
+        float half[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) half[i] = v[2 * i] + v[2 * i + 1];
+        return sum_of<N / 2>(half);
+    }
+}
+
 // Sum over the lanes of a row: W wavefronts.  `part` alternates between two buffers, so one
 // barrier a sum is enough.
 template <int W>
@@ -38,10 +51,11 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[16], int& turn) 
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) part[turn][wave] = v;
         __syncthreads();
-        v = 0.0f;
+        float all[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) v += part[turn][i];
+        for (int i = 0; i < W; ++i) all[i] = part[turn][i];
         turn ^= 1;
+        return sum_of<W>(all);
     }
     return v;
 }
@@ -58,7 +72,6 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
     constexpr int kThreads = W == 16 ? 1024 : 256, kAtOnce = kThreads / 64 / W;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, seg = lane & 15;
     const int wr = wave % W;
-    const float over_k = 1.0f / (float)p.k;
     int turn = 0;
     int col[NV], from[NV];                     // (past the last column: the last ones again)
     Eight<WB> w[NV];                           // as they come, for all rows
@@ -94,7 +107,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (col[i] < p.k) put_values(p.out, p.out_bf16, at + col[i], s[i], p.far);
-        const float ms = row_sum<W>(sq, part, turn) * over_k;
+        const float ms = row_sum<W>(sq, part, turn) / (float)p.k;
         float rstd = 1.0f / sqrtf(ms + p.eps), told = rstd;
         if (ms > 3.0e38f) {                    // the squares overflow: those of s 2^-96 do not
             sq = 0.0f;
@@ -105,7 +118,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
                     s[i][e] *= 0x1p-96f;
                     sq += s[i][e] * s[i][e];
                 }
-            rstd = 1.0f / sqrtf(row_sum<W>(sq, part, turn) * over_k);
+            rstd = 1.0f / sqrtf(row_sum<W>(sq, part, turn) / (float)p.k);
             told = rstd * 0x1p-96f;
         }
         if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
@@ -151,7 +164,6 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
     constexpr int kThreads = W == 16 ? 1024 : 256, kAtOnce = kThreads / 64 / W;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wr = wave % W, sub = wave / W;
-    const float over_k = 1.0f / (float)p.k;
     int turn = 0;
     int col[NV];
 #pragma unroll
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
                     dot += own * w[i][e];
                     acc[i][e] += own;
                 }
-            const float mean = row_sum<W>(dot, part, turn) * over_k;
+            const float mean = row_sum<W>(dot, part, turn) / (float)p.k;
             if (in)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -229,8 +241,8 @@ struct SumParams {
     uint32_t tiles;
 };
 
-// dw = the parts' sum: a workgroup 32 columns, in 32 chains of every 32nd part each, then those in
-// order.  (Of 512 parts x 7168, with the kernel before it: 32 columns 45.7 us for 4096 rows, 16
+// dw = the parts' sum: a workgroup 32 columns, in 32 chains of every 32nd part each, then those by
+// halves.  (Of 512 parts x 7168, with the kernel before it: 32 columns 45.7 us for 4096 rows, 16
 // columns, reads of half a line, 48.3.)
 constexpr int kSumCols = 32;
 __global__ void __launch_bounds__(1024) rms_norm_sum_kernel(SumParams p) {
@@ -246,9 +258,10 @@ __global__ void __launch_bounds__(1024) rms_norm_sum_kernel(SumParams p) {
         sums[chain][c] = v;
         __syncthreads();
         if (chain == 0 && col < p.k) {
-            float all = 0.0f;
+            float each[kChains];
 #pragma unroll
-            for (int i = 0; i < kChains; ++i) all += sums[i][c];
+            for (int i = 0; i < kChains; ++i) each[i] = sums[i][c];
+            const float all = sum_of<kChains>(each);
             p.dw[col] = p.accumulate ? p.dw[col] + all : all;
         }
         __syncthreads();
