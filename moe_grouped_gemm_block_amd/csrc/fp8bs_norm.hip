@@ -92,8 +92,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
             x[i].stream(p.x, at + from[i]);
             if constexpr (RES) r[i].stream(p.res, at + from[i]);
         }
-        float s[NV][8];
-        float sq = 0.0f;
+        float s[NV][8], sq[NV] = {};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -101,24 +100,25 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
                 s[i][e] = x[i][e];
                 if constexpr (RES) s[i][e] += r[i][e];
                 if (col[i] >= p.k) s[i][e] = 0.0f;
-                sq += s[i][e] * s[i][e];
+                sq[i] += s[i][e] * s[i][e];
             }
         if (p.out && in)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (col[i] < p.k) put_values(p.out, p.out_bf16, at + col[i], s[i], p.far);
-        const float ms = row_sum<W>(sq, part, turn) / (float)p.k;
+        const float ms = row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k;
         float rstd = 1.0f / sqrtf(ms + p.eps), told = rstd;
         if (ms > 3.0e38f) {                    // the squares overflow: those of s 2^-96 do not
-            sq = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                sq[i] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     s[i][e] *= 0x1p-96f;
-                    sq += s[i][e] * s[i][e];
+                    sq[i] += s[i][e] * s[i][e];
                 }
-            rstd = 1.0f / sqrtf(row_sum<W>(sq, part, turn) / (float)p.k);
+            }
+            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k);
             told = rstd * 0x1p-96f;
         }
         if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
@@ -191,17 +191,17 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
                 g[i].stream(p.dy, at);
                 if (p.dres) d[i].stream(p.dres, at);
             }
-            float dot = 0.0f;
+            float dot[NV] = {};
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float t = g[i][e] * (s[i][e] * r);
                     const float own = in && col[i] < p.k ? +t : 0.0f;
-                    dot += own * w[i][e];
+                    dot[i] += own * w[i][e];
                     acc[i][e] += own;
                 }
-            const float mean = row_sum<W>(dot, part, turn) / (float)p.k;
+            const float mean = row_sum<W>(sum_of<NV>(dot), part, turn) / (float)p.k;
             if (in)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
