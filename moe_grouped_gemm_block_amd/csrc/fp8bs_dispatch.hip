@@ -406,7 +406,14 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardPa
         for (int col = t * 8; col < p.k; col += 2048) {
             Eight<GB> g;
             Eight<true> d[2];
-            g.template take<FAR>(p.dy, (int64_t)token * p.k + col);
+            // (past the caches only where no other pair reads it: eight choices 244 us, so 228)
+            if (FAR && pairs == 1) {
+                asm volatile("");
+                g.stream(p.dy, (int64_t)token * p.k + col);
+                asm volatile("");
+            } else {
+                g.load(p.dy, (int64_t)token * p.k + col);
+            }
             if (p.dw)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) d[j].take<FAR>(from[j], col);
