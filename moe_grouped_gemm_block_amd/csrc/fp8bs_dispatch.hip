@@ -215,8 +215,18 @@ __device__ __forceinline__ void copy_scales(const DispatchParams& p, uint32_t bl
     if (!held) return;
     const int token = p.source[(int64_t)slot * p.m + r];
     float* to = p.sfa + (int64_t)slot * p.kb * p.sfa_ld + r;
-#pragma unroll 8
-    for (int c = 0; c < p.kb; ++c) to[(int64_t)c * p.sfa_ld] = p.sfx[(int64_t)c * p.sfx_ld + token];
+    constexpr int kBatch = 8;                  // loads on their way (16 and more: the same or slower)
+    for (int c0 = 0; c0 < p.kb; c0 += kBatch) {
+        float v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {     // (past the last: that one again)
+            const int c = c0 + i < p.kb ? c0 + i : p.kb - 1;
+            v[i] = p.sfx[(int64_t)c * p.sfx_ld + token];
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (c0 + i < p.kb) to[(int64_t)(c0 + i) * p.sfa_ld] = v[i];
+    }
 }
 
 // Scales first, as their units are the longer ones (last: 13% slower).  16384 tokens of two choices,
@@ -239,51 +249,80 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchParams p, in
 
 // ---- few assignments: one launch ---------------------------------------------------
 
-constexpr int kFewAssignments = 2048;
+constexpr int kFewAssignments = 4096;
 // Up to so many assignments: the time grows with their square (every workgroup goes through them),
-// that of the three launches with the groups.  e4m3 rows of 2048 and 7168, eight choices, 8 to 16
-// groups: 1024 assignments 7.8-11.8 us against 9.6-15.1, 2048 12-16.9 against 9.9-16.2; 256 groups:
-// 2048 assignments 13.9-17 against 13.7-30.
-constexpr int few_assignments(int groups) { return groups < 64 ? 1024 : kFewAssignments; }
+// that of the three launches with the groups.  e4m3 rows, eight choices, 2048 and 7168 columns: 8 groups,
+// 2048 assignments 8.7 and 10.6 us against 9.6 and 12.8, 4096 13.0 and 16.6 against 10.3 and 15.2; 256
+// groups, 4096 assignments 13.6 and 17.0 against 18.0 and 23.0.
+constexpr int few_assignments(int groups) { return groups < 64 ? 2048 : kFewAssignments; }
 
-// Workgroup = one token at a time.  Each ranks its own choices by going through all earlier ones;
-// the token's row and scales are on their way meanwhile.  64 tokens, eight choices each, e4m3 rows
-// of 7168 into slots: 6.7 us, most of it the latency of one load after the other.
+// Workgroup = one token at a time.  Each ranks its own choices by going through all earlier ones, 512
+// at a time; the token's row and scales are on their way meanwhile.  64 tokens, eight choices each,
+// e4m3 rows of 7168 into slots: 4.8 us replayed in a graph; a load of each kind after the other took
+// 5.8.  Three sizes of the choices' registers: 8 choices take 4.4 us with two a thread, 4.6 with eight.
+template <int MOST>
 __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
-    __shared__ int16_t ids[kFewAssignments];
+    constexpr int kIds = MOST / 256;               // of a thread
+    __shared__ __attribute__((aligned(16))) int16_t ids[MOST];
     __shared__ int total[kMostGroups], start[kMostGroups + 1], wave_sums[4];
     __shared__ int32_t rows[kMostTopk];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     // (slots start at their number: the counts are outputs alone, of workgroup 0)
     const bool count = !p.masked || blockIdx.x == 0;
+    // (all loads issued before any is looked at, the choices' first; past the last: that one again)
+    uint32_t lo[kIds], hi[kIds];
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+        lo[i] = hi[i] = 0;
+        if (256 * i >= p.n) continue;
+        const int at = t + 256 * i < p.n ? t + 256 * i : p.n - 1;
+        if (p.ids64) {
+            const u32x2 w = ((const u32x2*)p.ids)[at];
+            lo[i] = w[0];
+            hi[i] = w[1];
+        } else {
+            lo[i] = ((const uint32_t*)p.ids)[at];
+        }
+    }
+    u32x4 v[4];
+    float scale = 0.0f;
+    const auto fetch = [&](int token) {
+        const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = t + 256 * i;
+            v[i] = __builtin_nontemporal_load(from + (at < p.vectors ? +at : p.vectors - 1));
+        }
+        if (t < p.kb) scale = p.sfx[(int64_t)t * p.sfx_ld + token];
+    };
+    int token = blockIdx.x;
+    if (token < p.tokens) fetch(token);
     if (count) {
         for (int e = t; e < p.groups; e += 256) total[e] = 0;
         __syncthreads();
     }
-    for (int i = t; i < p.n; i += 256) {
-        const int e = expert_of(p, i);
-        ids[i] = (int16_t)e;
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+        if (t + 256 * i >= p.n) continue;
+        const int e = hi[i] == 0 && lo[i] < (uint32_t)p.groups ? (int)lo[i] : -1;
+        ids[t + 256 * i] = (int16_t)e;
         if (count && e >= 0) atomicAdd(&total[e], 1);
     }
-    for (int token = blockIdx.x; token < p.tokens; token += gridDim.x) {
-        u32x4 v[4];
-        const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {          // (past the row's end: its last piece again)
-            const int at = t + 256 * i;
-            v[i] = __builtin_nontemporal_load(from + (at < p.vectors ? +at : p.vectors - 1));
-        }
-        const float scale = t < p.kb ? p.sfx[(int64_t)t * p.sfx_ld + token] : 0.0f;
-        __syncthreads();
-        if (token == (int)blockIdx.x && count) {
-            if (!p.masked) segment_starts(total, p.groups, start, wave_sums);
-            write_group_data(p, total, start, blockIdx.x, gridDim.x);
-        }
+    __syncthreads();
+    if (!p.masked) segment_starts(total, p.groups, start, wave_sums);
+    while (token < p.tokens) {
         for (int j = wave; j < p.topk; j += 4) {
             const int i = token * p.topk + j, e = ids[i];
             int rank = 0;
-            for (int base = 0; base < i; base += 64)
-                rank += __popcll(__ballot(base + lane < i && ids[base + lane] == e));
+            for (int base = 0; base < i; base += 512) {
+                const u32x4 w = *(const u32x4*)&ids[base + 8 * lane];
+                const int before = i - base - 8 * lane;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int other = (int16_t)(w[k / 2] >> (k % 2 * 16));
+                    rank += __popcll(__ballot(k < before && other == e));
+                }
+            }
             const int row = row_of(p, start, e, rank);
             if (lane == 0) {
                 rows[j] = row;
@@ -291,6 +330,7 @@ __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
             }
         }
         __syncthreads();
+        const u32x4* from = (const u32x4*)p.x + (int64_t)token * p.vectors;
         for (int j = 0; j < p.topk; ++j) {
             const int row = rows[j];
             if (row < 0) continue;
@@ -305,12 +345,12 @@ __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
             for (int c = t + 256; c < p.kb; c += 256)
                 sf[(int64_t)c * p.sfa_ld] = p.sfx[(int64_t)c * p.sfx_ld + token];
         }
-    }
-    if (p.tokens == 0) {                       // (group data alone)
+        token += gridDim.x;
+        if (token >= p.tokens) break;
+        fetch(token);
         __syncthreads();
-        if (!p.masked) segment_starts(total, p.groups, start, wave_sums);
-        if (count) write_group_data(p, total, start, blockIdx.x, gridDim.x);
     }
+    if (count) write_group_data(p, total, start, blockIdx.x, gridDim.x);
 }
 
 // ---- the way back ------------------------------------------------------------------
@@ -549,7 +589,10 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     if (few(n, num_groups)) {
         // (without tokens: the group data alone)
         const int64_t units = tokens > 0 ? tokens : m / 1024 + 1;
-        return launch((const void*)dispatch_few_kernel, workgroups(units, 4), 256, p, stream);
+        return launch(n <= 512    ? (const void*)dispatch_few_kernel<512>
+                      : n <= 2048 ? (const void*)dispatch_few_kernel<2048>
+                                  : (const void*)dispatch_few_kernel<kFewAssignments>,
+                      workgroups(units, 4), 256, p, stream);
     }
     p.chunk_counts = (int32_t*)workspace;
     p.source = p.chunk_counts + (int64_t)kMostChunks * num_groups;

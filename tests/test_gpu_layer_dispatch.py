@@ -90,6 +90,10 @@ CASES = [
     (5000, 8, 16, 3000, 128, "e4m3", "elsewhere"), (9000, 6, 1024, None, 128, "e4m3", "here"),
     (1100, 2, 4, None, 33024, "e4m3", "here"), (40000, 8, 3, None, 8, "f32", "here"),
     (2000, 1, 8, 0, 128, "e4m3", "here"), (20, 2, 8, 0, 128, "e4m3", "here"),
+    # around the most choices of the one-launch kernels: 512, 2048 and, of 64 groups or more, 4096
+    (171, 3, 8, None, 1152, "e4m3", "one"), (256, 8, 7, 2000, 256, "e4m3", "one"), (32, 64, 20, None, 264, "bf16", "here"),
+    (683, 3, 63, None, 128, "e4m3", "elsewhere"), (512, 8, 64, None, 256, "e4m3", "one"), (1365, 3, 300, 16, 128, "e4m3", "elsewhere"),
+    (4096, 1, 1024, None, 8, "f32", "same"), (4097, 1, 64, None, 8, "f32", "here"), (2049, 1, 3, None, 8, "bf16", "one"),
 ]
 
 
