@@ -44,10 +44,35 @@ struct DispatchParams {
     uint32_t units;
 };
 
-__device__ __forceinline__ int expert_of(const DispatchParams& p, int i) {
-    const int64_t e = p.ids64 ? ((const int64_t*)p.ids)[i] : (int64_t)((const int32_t*)p.ids)[i];
-    return e >= 0 && e < p.groups ? (int)e : -1;
-}
+// N choices of a lane, every `step`-th, as they lie: all loads issued before any is looked at.
+template <int N>
+struct Choices {
+    uint32_t lo[N], hi[N];
+    // (past the last: that one again)
+    __device__ __forceinline__ void load(const DispatchParams& p, int64_t first, int step) {
+        const u32x2* wide = (const u32x2*)p.ids;
+        const uint32_t* narrow = (const uint32_t*)p.ids;
+        if (p.ids64) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int64_t at = first + (int64_t)step * i;
+                const u32x2 w = wide[at < p.n ? at : p.n - 1];
+                lo[i] = w[0];
+                hi[i] = w[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int64_t at = first + (int64_t)step * i;
+                lo[i] = narrow[at < p.n ? at : p.n - 1];
+                hi[i] = 0;                     // (a negative number is above all experts)
+            }
+        }
+    }
+    __device__ __forceinline__ int expert(int i, int groups) const {
+        return hi[i] == 0 && lo[i] < (uint32_t)groups ? (int)lo[i] : -1;
+    }
+};
 
 // Lanes whose expert is this lane's (bits of the group number one by one).
 __device__ __forceinline__ uint64_t same_expert(int e, int groups) {
@@ -119,15 +144,24 @@ __device__ __forceinline__ int row_of(const DispatchParams& p, const int* start,
 
 // ---- many assignments: counts of chunks, ranks, rows -----------------------------
 
+constexpr int kBatch = 8;                      // loads on their way (scales: 16 and more no faster)
+
+// BATCH: choices of a lane at a time (1 where a chunk has no more).
+template <int BATCH>
 __global__ void __launch_bounds__(256) dispatch_count_kernel(DispatchParams p) {
     __shared__ int hist[kMostGroups];
     for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
         for (int e = threadIdx.x; e < p.groups; e += 256) hist[e] = 0;
         __syncthreads();
         const int64_t end = (int64_t)(c + 1) * p.chunk < p.n ? (int64_t)(c + 1) * p.chunk : p.n;
-        for (int64_t i = (int64_t)c * p.chunk + threadIdx.x; i < end; i += 256) {
-            const int e = expert_of(p, (int)i);
-            if (e >= 0) atomicAdd(&hist[e], 1);
+        for (int64_t i = (int64_t)c * p.chunk; i < end; i += 256 * BATCH) {
+            Choices<BATCH> ids;
+            ids.load(p, i + threadIdx.x, 256);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int e = ids.expert(j, p.groups);
+                if (i + 256 * j + threadIdx.x < end && e >= 0) atomicAdd(&hist[e], 1);
+            }
         }
         __syncthreads();
         for (int e = threadIdx.x; e < p.groups; e += 256)
@@ -138,7 +172,9 @@ __global__ void __launch_bounds__(256) dispatch_count_kernel(DispatchParams p) {
 
 // A chunk's four wavefronts take a quarter each, in order.  (More workgroups than chunks: the
 // others write their share of the rows' experts alone.)  16384 tokens of two choices, eight experts:
-// 6 us, with the counts' 5 before it bound by latency, a read of the choices each.
+// 6 us, with the counts' 5 before it bound by latency; of eight choices, 1024 experts, 51 together,
+// with every load waited for by itself 118.
+template <int BATCH>
 __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
     __shared__ int total[kMostGroups], start[kMostGroups + 1], wave_sums[4];
     __shared__ int next[4][kMostGroups];       // the wavefront's next rank of each expert
@@ -153,42 +189,61 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
         const int64_t end =
             c >= p.chunks ? first : first + quarter < p.n ? first + quarter : (int64_t)p.n;
         // (the first choices are on their way while the counts are added)
-        const int e0 = first + lane < end ? expert_of(p, (int)first + lane) : -1;
+        Choices<BATCH> ids;
+        ids.load(p, first + lane, 64);
         __syncthreads();
         // (assignments of earlier chunks go into next[0], those of the chunk's earlier
         // wavefronts below)
-        const int64_t all = (int64_t)p.chunks * p.groups;
-        for (int64_t i = t; i < all; i += 256) {
-            const int of = (int)(i / p.groups), e = (int)(i - (int64_t)of * p.groups);
-            const int v = p.chunk_counts[i];
-            if (v) {
-                atomicAdd(&total[e], v);
-                if (of < c) atomicAdd(&next[0][e], v);
+        const int all = p.chunks * p.groups;
+        for (int i0 = t; i0 < all; i0 += 256 * kBatch) {
+            int v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = i0 + 256 * i;   // (past the last: that one again)
+                v[i] = p.chunk_counts[at < all ? at : all - 1];
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = i0 + 256 * i, of = (int)((uint32_t)at / (uint32_t)p.groups);
+                const int e = at - of * p.groups;
+                if (at >= all || v[i] == 0) continue;
+                atomicAdd(&total[e], v[i]);
+                if (of < c) atomicAdd(&next[0][e], v[i]);
             }
         }
         if (wave < 3)
-            for (int64_t i = first + lane; i < end; i += 64) {
-                const int e = i == first + lane ? e0 : expert_of(p, (int)i);
-                if (e >= 0) atomicAdd(&next[wave + 1][e], 1);
+            for (int64_t base = first; base < end; base += 64 * BATCH) {
+                Choices<BATCH> own = ids;
+                if (base != first) own.load(p, base + lane, 64);
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    const int e = own.expert(j, p.groups);
+                    if (base + 64 * j + lane < end && e >= 0) atomicAdd(&next[wave + 1][e], 1);
+                }
             }
         __syncthreads();
         for (int e = t; e < p.groups; e += 256)
             for (int w = 1; w < 4; ++w) next[w][e] += next[w - 1][e];
         segment_starts(total, p.groups, start, wave_sums);
         write_group_data(p, total, start, c, p.rank_units);
-        for (int64_t base = first; base < end; base += 64) {
-            const int64_t i = base + lane;
-            const int e = base == first ? e0 : i < end ? expert_of(p, (int)i) : -1;
-            const uint64_t same = same_expert(e, p.groups);
-            const uint64_t below = same & ((1ull << lane) - 1ull);
-            const int rank = e < 0 ? 0 : next[wave][e] + __popcll(below);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (e >= 0 && below == 0) next[wave][e] += __popcll(same);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (i < end) {
-                const int row = row_of(p, start, e, rank);
-                p.positions[i] = row;
-                if (row >= 0 && p.kb) p.source[row] = (int)(i / p.topk);
+        for (int64_t base = first; base < end; base += 64 * BATCH) {
+            if (base != first) ids.load(p, base + lane, 64);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int64_t i = base + 64 * j + lane;
+                if (base + 64 * j >= end) break;
+                const int e = i < end ? ids.expert(j, p.groups) : -1;
+                const uint64_t same = same_expert(e, p.groups);
+                const uint64_t below = same & ((1ull << lane) - 1ull);
+                const int rank = e < 0 ? 0 : next[wave][e] + __popcll(below);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                if (e >= 0 && below == 0) next[wave][e] += __popcll(same);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                if (i < end) {
+                    const int row = row_of(p, start, e, rank);
+                    p.positions[i] = row;
+                    if (row >= 0 && p.kb) p.source[row] = (int)(i / p.topk);
+                }
             }
         }
         __syncthreads();
@@ -215,7 +270,6 @@ __device__ __forceinline__ void copy_scales(const DispatchParams& p, uint32_t bl
     if (!held) return;
     const int token = p.source[(int64_t)slot * p.m + r];
     float* to = p.sfa + (int64_t)slot * p.kb * p.sfa_ld + r;
-    constexpr int kBatch = 8;                  // loads on their way (16 and more: the same or slower)
     for (int c0 = 0; c0 < p.kb; c0 += kBatch) {
         float v[kBatch];
 #pragma unroll
@@ -251,14 +305,14 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchParams p, in
 
 constexpr int kFewAssignments = 4096;
 // Up to so many assignments: the time grows with their square (every workgroup goes through them),
-// that of the three launches with the groups.  e4m3 rows, eight choices, 2048 and 7168 columns: 8 groups,
-// 2048 assignments 8.7 and 10.6 us against 9.6 and 12.8, 4096 13.0 and 16.6 against 10.3 and 15.2; 256
-// groups, 4096 assignments 13.6 and 17.0 against 18.0 and 23.0.
+// that of the three launches with the groups.  e4m3 rows of 2048 and 7168, eight choices: 8 groups, 2048
+// assignments 8.3 and 10.2 us against 9.7 and 13.1, 4096 12.3 and 14.5 against 10.6 and 15.4; 256 groups,
+// 4096 assignments 12.9 and 14.7 against 14.9 and 20.1.
 constexpr int few_assignments(int groups) { return groups < 64 ? 2048 : kFewAssignments; }
 
 // Workgroup = one token at a time.  Each ranks its own choices by going through all earlier ones, 512
 // at a time; the token's row and scales are on their way meanwhile.  64 tokens, eight choices each,
-// e4m3 rows of 7168 into slots: 4.8 us replayed in a graph; a load of each kind after the other took
+// e4m3 rows of 7168 into slots: 4.7 us replayed in a graph; a load of each kind after the other took
 // 5.8.  Three sizes of the choices' registers: 8 choices take 4.4 us with two a thread, 4.6 with eight.
 template <int MOST>
 __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
@@ -269,21 +323,9 @@ __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     // (slots start at their number: the counts are outputs alone, of workgroup 0)
     const bool count = !p.masked || blockIdx.x == 0;
-    // (all loads issued before any is looked at, the choices' first; past the last: that one again)
-    uint32_t lo[kIds], hi[kIds];
-#pragma unroll
-    for (int i = 0; i < kIds; ++i) {
-        lo[i] = hi[i] = 0;
-        if (256 * i >= p.n) continue;
-        const int at = t + 256 * i < p.n ? t + 256 * i : p.n - 1;
-        if (p.ids64) {
-            const u32x2 w = ((const u32x2*)p.ids)[at];
-            lo[i] = w[0];
-            hi[i] = w[1];
-        } else {
-            lo[i] = ((const uint32_t*)p.ids)[at];
-        }
-    }
+    // (all loads issued before any is looked at, the choices' first)
+    Choices<kIds> choices;
+    if (p.n > 0) choices.load(p, t, 256);
     u32x4 v[4];
     float scale = 0.0f;
     const auto fetch = [&](int token) {
@@ -304,7 +346,7 @@ __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
 #pragma unroll
     for (int i = 0; i < kIds; ++i) {
         if (t + 256 * i >= p.n) continue;
-        const int e = hi[i] == 0 && lo[i] < (uint32_t)p.groups ? (int)lo[i] : -1;
+        const int e = choices.expert(i, p.groups);
         ids[t + 256 * i] = (int16_t)e;
         if (count && e >= 0) atomicAdd(&total[e], 1);
     }
@@ -510,10 +552,11 @@ int64_t capacity_of(int64_t n, int num_groups) {
     return (n + 127 * (n < num_groups ? n : (int64_t)num_groups)) / 128 * 128;
 }
 // Assignments of a chunk, a multiple of 256.  A workgroup of the ranks' launch goes through all
-// chunks' counts, so there are fewer chunks where there are many experts.
+// chunks' counts and its own chunk's choices, eight loads on their way in both: about as many steps
+// of the one as of the other (1024 experts, 8192 choices in 8 chunks 20 us, 131072 in 32 51, in 8 84).
 int chunk_of(int64_t n, int num_groups) {
-    int64_t chunks = 8192 / num_groups;
-    chunks = chunks < kMostChunks ? chunks : kMostChunks;
+    int64_t chunks = (int64_t)__builtin_sqrt(8.0 * (double)n / num_groups);
+    chunks = chunks < 1 ? 1 : chunks < kMostChunks ? chunks : kMostChunks;
     return (int)(((n + chunks - 1) / chunks + 255) / 256 * 256);
 }
 bool few(int64_t n, int groups) { return n <= few_assignments(groups); }
@@ -606,9 +649,13 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     const int64_t units = scale_units + (int64_t)tokens * pieces;
     if (units > 0x7fffffff) return FP8BS_ERR_UNSUPPORTED;
     p.units = (uint32_t)units;
-    int st = launch((const void*)dispatch_count_kernel, workgroups(p.chunks, 4), 256, p, stream);
+    const bool one = p.chunk == 256;
+    int st = launch(one ? (const void*)dispatch_count_kernel<1>
+                        : (const void*)dispatch_count_kernel<kBatch>,
+                    workgroups(p.chunks, 4), 256, p, stream);
     if (st != FP8BS_OK) return st;
-    st = launch((const void*)dispatch_rank_kernel, workgroups(p.rank_units, 4), 256, p, stream);
+    st = launch(one ? (const void*)dispatch_rank_kernel<1> : (const void*)dispatch_rank_kernel<kBatch>,
+                workgroups(p.rank_units, 4), 256, p, stream);
     if (st != FP8BS_OK || rows == 0) return st;
     uint32_t su = (uint32_t)scale_units;
     int pc = pieces;

@@ -79,7 +79,7 @@ def test_every_kernel_is_reached():
                for res in (F32, BF16, NONE) for w in (F32, BF16)]
     queries += [("norm_back", r, k, types(s, g, w), 1) for r, k in NORM for s in (F32, BF16)
                 for g in (F32, BF16) for w in (F32, BF16)]
-    queries += [("dispatch", CONTIGUOUS, t, 8, g, 128 * 4096) for t, g in ((10, 8), (200, 8), (400, 64), (5000, 8))]
+    queries += [("dispatch", CONTIGUOUS, t, 8, g, 128 * 4096) for t, g in ((10, 8), (200, 8), (400, 64), (5000, 8), (40000, 8))]
     queries += [("combine", 10, 2, 512, y) for y in (F32, BF16)] + [("combine_back", 10, 2, 512, y) for y in (F32, BF16)]
     queries += [("gated", DENSE, 100, 256, 1, keep + 2 * act) for keep in (0, 1) for act in (0, 1)]
     queries += [("gated_back", 100, 256, kept, act) for kept in (0, 1) for act in (0, 1)]
