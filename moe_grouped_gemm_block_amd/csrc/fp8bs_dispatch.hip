@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) dispatch_count_kernel(DispatchParams p) {
 
 // A chunk's four wavefronts take a quarter each, in order.  (More workgroups than chunks: the
 // others write their share of the rows' experts alone.)  16384 tokens of two choices, eight experts:
-// 6 us, with the counts' 5 before it bound by latency; of eight choices, 1024 experts, 51 together,
+// 5 us, like the counts before it bound by latency; of eight choices, 1024 experts, 51 together,
 // with every load waited for by itself 118.
 template <int BATCH>
 __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
