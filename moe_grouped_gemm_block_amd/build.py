@@ -1,4 +1,6 @@
-"""Build libfp8bs.so (HIP for gfx950) in-tree with hipcc.
+"""Build libfp8bs.so (HIP for gfx950) in-tree with hipcc, and the CPython module through which
+the layer operators' small calls reach it (host code alone, with the host compiler and torch's
+headers).
 
     python -m moe_grouped_gemm_block_amd.build
 
@@ -10,16 +12,19 @@ schedules with the AMDGPU register-pressure trackers (see DEVICE below).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libfp8bs.so")
+MODULE = os.path.join(LIBDIR, "fp8bs_layer_py.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = os.environ.get("FP8BS_OFFLOAD_ARCH", "gfx950")
 
@@ -49,11 +54,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _module() -> str:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include = os.path.join(torch, "include")
+    tmp = MODULE + ".tmp"
+    cmd = [os.environ.get("CXX", shutil.which("g++") or "c++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
+           "-I" + os.path.join(ROOT, "include"), "-isystem", include,
+           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "fp8bs_layer_py.cpp"),
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for fp8bs_layer_py.cpp:\n{r.stderr}")
+    os.replace(tmp, MODULE)
+    return MODULE
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        module = ex.submit(_module)
         objs = list(ex.map(_compile, SOURCES))
+        module.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -61,7 +84,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {MODULE}")
     return LIB
 
 

@@ -8,11 +8,17 @@ checks and marshalling only.  Operands in e4m3 are pairs of codes, uint8 (or
 ``torch.float8_e4m3fn``), and scales, float32: 1x128 as ``quantize_1x128`` gives them, 128x1 as
 ``fp8bs_k_grouped_tn_contiguous`` reads them.  Outputs are written in place; ``rms_norm_1x128``,
 ``moe_dispatch`` and ``quantize_128x1`` allocate what they return.
+
+Each call goes first to the compiled module ``fp8bs_layer_py``, which looks the operands over and
+calls the library; what it does not take -- a wrong operand, another device than the current one,
+a workspace to allocate -- comes back here, to be named or done.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 from collections import namedtuple
 
 import moe_grouped_gemm_block_amd as _pkg
@@ -32,11 +38,38 @@ __all__ = [
 DTYPE_E4M3 = 2
 
 _lib = None
+_quick = None                                       # the compiled module, once the library is loaded
+_MODULE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "fp8bs_layer_py.so")
+
+
+def _load_module(lib):
+    if not os.path.exists(_MODULE_PATH):
+        raise RuntimeError(f"{_MODULE_PATH} is missing; build it with "
+                           "`python -m moe_grouped_gemm_block_amd.build`")
+    spec = importlib.util.spec_from_file_location("fp8bs_layer_py", _MODULE_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.use(*(ctypes.cast(getattr(lib, "fp8bs_" + name), ctypes.c_void_p).value for name in (
+        "rms_norm", "rms_norm_backward", "moe_dispatch_workspace_size", "moe_dispatch", "moe_combine",
+        "moe_combine_backward", "gated_quantize", "gated_quantize_backward", "quantize_128x1")),
+        _mx._raw_stream)
+    return module
+
+
+def _done(status, name):
+    """Whether the compiled module made the call (it answers -1 if not)."""
+    if status > 0:
+        raise FP8BSError(status, name)
+    return status == 0
+
+
+def _number(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def _load():
     """The library with this module's prototypes."""
-    global _lib, _Tensor, _FP8, _BF16, _F32, _FLOAT, _INT32, _IDS, _KEPT, _ROWS, _CODE, _bf16, _u8, _f32
+    global _lib, _quick, _Tensor, _FP8, _BF16, _F32, _FLOAT, _INT32, _IDS, _KEPT, _ROWS, _CODE, _bf16, _u8, _f32
     if _lib is not None:
         return _lib
     lib = _mx._load()
@@ -67,6 +100,7 @@ def _load():
     for name in ("fp8bs_rms_norm_backward_workspace_size", "fp8bs_moe_capacity",
                  "fp8bs_moe_dispatch_workspace_size"):
         getattr(lib, name).restype = I64
+    _quick = _load_module(lib)
     _lib = lib
     return lib
 
@@ -182,6 +216,9 @@ def fp8bs_rms_norm(x, weight, residual=None, residual_out=None, y=None, q=None, 
     residual (bf16 or f32 [rows][k]) may be absent.  Outputs, as wanted: residual_out (s, in
     residual's type; may be residual), y (bf16 or f32; may be x), q e4m3 with sfa (y as 1x128; k a
     multiple of 128), rstd f32 [rows] (for the backward pass)."""
+    if _quick and _done(_quick.rms_norm(x, weight, residual, residual_out, y, q, sfa, rstd, eps, _number(stream)),
+                        "fp8bs_rms_norm"):
+        return
     index = _start(x, "x")
     xp, rows, k = _matrix(x, "x", _FLOAT, index)
     shape = x.shape
@@ -226,6 +263,9 @@ def fp8bs_rms_norm_backward(s, rstd, weight, dy, dx, dresidual=None, dweight=Non
     dweight f32 [k] (accumulate: added to what it holds), which may be None.  dresidual: the
     gradient of residual_out, in s's type; dx may be dresidual, s or dy.  workspace: uint8 tensor
     of rms_norm_backward_workspace_size() bytes, or None to allocate one."""
+    if _quick and _done(_quick.rms_norm_backward(s, rstd, weight, dy, dx, dresidual, dweight, accumulate, workspace,
+                                                 _number(stream)), "fp8bs_rms_norm_backward"):
+        return
     index = _start(s, "s")
     sp, rows, k = _matrix(s, "s", _FLOAT, index)
     shape = s.shape
@@ -270,6 +310,9 @@ def fp8bs_moe_dispatch(ids, x, a, group_data, positions, counts, sfx=None, sfa=N
     scales if e4m3.  positions int32 [tokens][topk]: each choice's row, -1 for none; counts int32
     [g]: choices of each expert.  workspace: uint8 tensor of moe_dispatch_workspace_size() bytes,
     or None to allocate one if it is needed."""
+    if _quick and _done(_quick.moe_dispatch(ids, x, a, group_data, positions, counts, sfx, sfa, workspace,
+                                            _number(stream)), "fp8bs_moe_dispatch"):
+        return
     index = _start(ids, "ids")
     ip = _ptr(ids, "ids", _IDS, 2, index)
     tokens, topk = ids.shape
@@ -345,6 +388,8 @@ def fp8bs_moe_combine(d, positions, y, weights=None, stream=None):
     """y[t] = sum over j of weights[t][j] * d[positions[t][j]]: d bf16 [m][k] or [g][m][k],
     positions as dispatch gives them, weights f32 [tokens][topk] or None (ones: the gradient of
     dispatch), y bf16 or f32 [tokens][k]."""
+    if _quick and _done(_quick.moe_combine(d, positions, y, weights, _number(stream)), "fp8bs_moe_combine"):
+        return
     index = _start(d, "d")
     dp = _ptr(d, "d", (_bf16,), 3 if d.ndim == 3 else 2, index)
     yp, tokens, k = _matrix(y, "y", _FLOAT, index)
@@ -360,6 +405,9 @@ def fp8bs_moe_combine_backward(dy, positions, d=None, weights=None, dd=None, q=N
     """Gradients of fp8bs_moe_combine: dy bf16 or f32 [tokens][k] -> the gradient of d as bf16
     (dd) or e4m3 (q, sfa), or both, at the rows that positions name, and dweights f32
     [tokens][topk] (needs d).  dd, q and d have the shape [m][k] or [g][m][k]."""
+    if _quick and _done(_quick.moe_combine_backward(dy, positions, d, weights, dd, q, sfa, dweights, _number(stream)),
+                        "fp8bs_moe_combine_backward"):
+        return
     index = _start(dy, "dy")
     gp, tokens, k = _matrix(dy, "dy", _FLOAT, index)
     pp, wp, topk = _assigned(positions, weights, tokens, index)
@@ -394,6 +442,10 @@ def fp8bs_gated_quantize(g, hq, sfh, gq=None, sfg=None, grouped_layout=None, mas
     """h = act(gate) * up as e4m3 (hq, sfh: 1x128), g bf16 [m][2f] or with masked_m [slots][m][2f]
     (gate columns, then up columns); gq, sfg: g itself as e4m3, kept for the backward pass.  Rows
     that grouped_layout (int32 [m], -1) or masked_m (int32 [slots]) leaves out are not written."""
+    if _quick and _done(_quick.gated_quantize(g, hq, sfh, gq, sfg, grouped_layout, masked_m,
+                                              _mx.ACTIVATIONS.get(activation, -1), _number(stream)),
+                        "fp8bs_gated_quantize"):
+        return
     if grouped_layout is not None and masked_m is not None:
         raise ValueError("grouped_layout and masked_m exclude each other")
     index = _start(g, "g")
@@ -424,6 +476,10 @@ def fp8bs_gated_quantize_backward(g, dh, sfg=None, d=None, dq=None, sfd=None, dq
     """Gradients of the gated activation at the checkpoint g e4m3 [m][2f] with sfg (or at g bf16),
     from dh bf16 [m][f].  Outputs, as wanted: d (bf16 [m][2f]), dq, sfd (e4m3, 1x128), dqt, sfdt
     (e4m3, 128x1: an operand of the weight gradient) and hqt, sfht (the activation h, 128x1)."""
+    if _quick and _done(_quick.gated_quantize_backward(g, dh, sfg, d, dq, sfd, dqt, sfdt, hqt, sfht, grouped_layout,
+                                                       _mx.ACTIVATIONS.get(activation, -1), _number(stream)),
+                        "fp8bs_gated_quantize_backward"):
+        return
     index = _start(g, "g")
     gp, m, two_f = _matrix(g, "g", _KEPT, index)
     f = _gated_columns(two_f)
@@ -452,6 +508,8 @@ def fp8bs_quantize_128x1(x, q, sf, sfx=None, grouped_layout=None, stream=None):
     """x [rows][n] f32, bf16 or e4m3 with sfx (1x128) -> q e4m3 [R][n], R = rows rounded up to a
     multiple of 128, and sf f32 [R/128][n]: an operand of fp8bs_k_grouped_tn_contiguous.  Rows
     that grouped_layout (int32 [rows], -1) leaves out are zeros."""
+    if _quick and _done(_quick.quantize_128x1(x, q, sf, sfx, grouped_layout, _number(stream)), "fp8bs_quantize_128x1"):
+        return
     index = _start(x, "x")
     xp, rows, n = _matrix(x, "x", _ROWS, index)
     kind = _CODE[x.dtype]

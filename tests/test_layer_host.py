@@ -251,6 +251,28 @@ def test_sizes_that_an_int_does_not_hold_are_refused():
             call()
 
 
+def test_the_compiled_module_takes_device_tensors_alone(monkeypatch):
+    m = fp8bs.layer
+    m._load()
+    t = torch.zeros(4, 128)
+    for name, count in (("rms_norm", 10), ("rms_norm_backward", 10), ("moe_dispatch", 10), ("moe_combine", 5),
+                        ("moe_combine_backward", 9), ("gated_quantize", 9), ("gated_quantize_backward", 13),
+                        ("quantize_128x1", 6)):
+        call = getattr(m._quick, name)
+        for operand in (t, None, 1, "x", torch.nn.Parameter(t), t.numpy()):
+            assert call(*[operand] * count) == -1, (name, operand)
+        assert call() == -1 and call(*[t] * (count + 1)) == -1
+    with pytest.raises(TypeError):
+        m._quick.use(1, 2)
+    with pytest.raises(TypeError):
+        m._quick.use(*["x"] * 10)
+    with pytest.raises(ValueError, match="device"):
+        fp8bs.fp8bs_rms_norm(t, t[0], y=t)
+    monkeypatch.setattr(m, "_MODULE_PATH", "/nowhere/fp8bs_layer_py.so")
+    with pytest.raises(RuntimeError, match="build it"):
+        m._load_module(m._lib)
+
+
 def test_the_reference_quantiser():
     """the tests' own quantiser against torch's cast, and its half step"""
     rng = np.random.default_rng(1)
