@@ -5,13 +5,14 @@
 // combine 6.9 and 3.3, gated activation 7.7 and 3.8, columns of 200 x 416 6.2 and 4.0.
 //
 // Each function takes its operator's operands by position and answers the library's status, or -1 if
-// anything is not as it should be -- a type, shape, device, a missing workspace -- or needs more than
-// a look: nothing has been called then, and the binding's checks in layer.py say what is wrong, or make
+// anything is not as it should be -- a type, shape, device -- or needs more than a look (a workspace on
+// another stream than the current one): nothing has been called then, and the binding's checks in layer.py say what is wrong, or make
 // the call.  It never raises.
 #include <Python.h>
 
 #include <climits>
 
+#include <ATen/ops/empty.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -37,6 +38,7 @@ int code_of(int type) { return type & kF32 ? FP8BS_DTYPE_F32 : type & kBF16 ? FP
 
 // The library's functions and torch's current stream of a device, as the binding gives them.
 decltype(&fp8bs_rms_norm) norm_fn;
+decltype(&fp8bs_rms_norm_backward_workspace_size) norm_size_fn;
 decltype(&fp8bs_rms_norm_backward) norm_backward_fn;
 decltype(&fp8bs_moe_dispatch_workspace_size) dispatch_size_fn;
 decltype(&fp8bs_moe_dispatch) dispatch_fn;
@@ -108,6 +110,15 @@ class Operands {
         return nullptr;
     }
     bool demand(bool what) { return ok_ = ok_ && what; }
+    // The caller's workspace, or for None one of `bytes` (< 0: an error) from the current stream's memory
+    // in `made`, which the caller keeps until the call has been made.
+    const at::Tensor* workspace(PyObject* o, int64_t bytes, PyObject* stream, const at::Tensor& like,
+                                at::Tensor& made) {
+        if (o != Py_None) return tensor(o, kByte, 1);
+        if (!demand(bytes == 0 || (bytes > 0 && stream == Py_None)) || bytes == 0) return nullptr;
+        made = at::empty({bytes}, like.options().dtype(at::kByte));
+        return &made;
+    }
     // A stream's number, None: the current stream
     hipStream_t stream(PyObject* o) {
         if (!ok_) return nullptr;
@@ -188,10 +199,11 @@ int norm_backward(PyObject* const* a) {
     const void* dres = in.optional(a[5], type, {rows, k});
     float* dw = (float*)in.optional(a[6], kF32, {k});
     const int accumulate = PyObject_IsTrue(a[7]);
-    const at::Tensor* space = nullptr;
-    if (a[6] != Py_None) space = in.tensor(a[8], kByte, 1);
-    in.demand(accumulate >= 0);
     if (accumulate < 0) PyErr_Clear();
+    in.demand(accumulate >= 0);
+    at::Tensor made;
+    const at::Tensor* space =
+        dw && in.ok() ? in.workspace(a[8], norm_size_fn(rows, (int)k), a[9], *s, made) : nullptr;
     hipStream_t stream = in.stream(a[9]);
     if (!in.ok()) return -1;
     const void* sp = s->data_ptr();
@@ -227,9 +239,9 @@ int dispatch(PyObject* const* a) {
     float* sfa = in.scales(a[7], codes, (masked ? g : 1) * (k / 128) * ld(m));
     if (!in.ok()) return -1;
     const int layout = masked ? FP8BS_LAYOUT_MASKED : FP8BS_LAYOUT_CONTIGUOUS;
-    const at::Tensor* space = nullptr;
-    if (a[8] != Py_None) space = in.tensor(a[8], kByte, 1);
-    else in.demand(dispatch_size_fn(layout, tokens, (int)topk, (int)g, m) == 0);
+    at::Tensor made;
+    const at::Tensor* space = in.workspace(a[8], dispatch_size_fn(layout, tokens, (int)topk, (int)g, m), a[9],
+                                           *x, made);
     hipStream_t stream = in.stream(a[9]);
     if (!in.ok()) return -1;
     const void *ip = ids->data_ptr(), *xp = x->data_ptr();
@@ -391,24 +403,26 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t count) {
 
 // Addresses of the library's functions, in the order above, and the current stream's function.
 PyObject* use(PyObject*, PyObject* args) {
-    PyObject* p[10];
-    if (!PyArg_UnpackTuple(args, "use", 10, 10, p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, p + 7, p + 8, p + 9))
+    PyObject* p[11];
+    if (!PyArg_UnpackTuple(args, "use", 11, 11, p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, p + 7, p + 8, p + 9,
+                           p + 10))
         return nullptr;
-    void* fn[9];
-    for (int i = 0; i < 9; ++i) fn[i] = PyLong_AsVoidPtr(p[i]);
+    void* fn[10];
+    for (int i = 0; i < 10; ++i) fn[i] = PyLong_AsVoidPtr(p[i]);
     if (PyErr_Occurred()) return nullptr;
     norm_fn = (decltype(norm_fn))fn[0];
-    norm_backward_fn = (decltype(norm_backward_fn))fn[1];
-    dispatch_size_fn = (decltype(dispatch_size_fn))fn[2];
-    dispatch_fn = (decltype(dispatch_fn))fn[3];
-    combine_fn = (decltype(combine_fn))fn[4];
-    combine_backward_fn = (decltype(combine_backward_fn))fn[5];
-    gated_fn = (decltype(gated_fn))fn[6];
-    gated_backward_fn = (decltype(gated_backward_fn))fn[7];
-    columns_fn = (decltype(columns_fn))fn[8];
-    Py_INCREF(p[9]);
+    norm_size_fn = (decltype(norm_size_fn))fn[1];
+    norm_backward_fn = (decltype(norm_backward_fn))fn[2];
+    dispatch_size_fn = (decltype(dispatch_size_fn))fn[3];
+    dispatch_fn = (decltype(dispatch_fn))fn[4];
+    combine_fn = (decltype(combine_fn))fn[5];
+    combine_backward_fn = (decltype(combine_backward_fn))fn[6];
+    gated_fn = (decltype(gated_fn))fn[7];
+    gated_backward_fn = (decltype(gated_backward_fn))fn[8];
+    columns_fn = (decltype(columns_fn))fn[9];
+    Py_INCREF(p[10]);
     Py_XDECREF(raw_stream);
-    raw_stream = p[9];
+    raw_stream = p[10];
     Py_RETURN_NONE;
 }
 

@@ -11,7 +11,7 @@ checks and marshalling only.  Operands in e4m3 are pairs of codes, uint8 (or
 
 Each call goes first to the compiled module ``fp8bs_layer_py``, which looks the operands over and
 calls the library; what it does not take -- a wrong operand, another device than the current one,
-a workspace to allocate -- comes back here, to be named or done.
+a workspace to allocate for another stream -- comes back here, to be named or done.
 """
 from __future__ import annotations
 
@@ -50,7 +50,7 @@ def _load_module(lib):
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.use(*(ctypes.cast(getattr(lib, "fp8bs_" + name), ctypes.c_void_p).value for name in (
-        "rms_norm", "rms_norm_backward", "moe_dispatch_workspace_size", "moe_dispatch", "moe_combine",
+        "rms_norm", "rms_norm_backward_workspace_size", "rms_norm_backward", "moe_dispatch_workspace_size", "moe_dispatch", "moe_combine",
         "moe_combine_backward", "gated_quantize", "gated_quantize_backward", "quantize_128x1")),
         _mx._raw_stream)
     return module

@@ -36,7 +36,7 @@ def operands():
         "rms_norm": ([x, w, res, zeros(rows, k, t=BF16), zeros(rows, k, t=BF16), codes(rows, k), zeros(k // 128, ld(rows)),
                       zeros(rows), 1e-6, None], (3, 4, 5, 6, 7), (2, 3, 4, 7)),
         "rms_norm_backward": ([x, torch.rand(rows, generator=gen, device="cuda"), w, dy, zeros(rows, k, t=BF16), res, zeros(k),
-                               False, ws, None], (4, 6), (5, 6)),
+                               False, ws, None], (4, 6), (5, 6, 8)),
         "moe_dispatch": ([ids, xq, codes(g, m, k), zeros(g, t=I32), zeros(rows, topk, t=I32), zeros(g, t=I32), sx,
                           zeros(g, k // 128, ld(m)), None, None], (2, 3, 4, 5, 7), (8,)),
         "moe_combine": ([d, pos, zeros(rows, k), rw, None], (2,), (3,)),
@@ -148,8 +148,16 @@ def test_parameters_views_and_a_missing_workspace():
     w = torch.nn.Parameter(x[1])
     assert layer._quick.rms_norm(x[0], w, *x[2:]) == 0
     v = a["rms_norm_backward"][0]
-    assert layer._quick.rms_norm_backward(*v[:8], None, None) == -1   # the binding allocates it
-    fp8bs.fp8bs_rms_norm_backward(*v[:8], None)
+    assert layer._quick.rms_norm_backward(*v) == 0
+    want = [v[4].clone(), v[6].clone()]
+    for stream in (None, torch.cuda.Stream()):
+        v[4].zero_(), v[6].zero_()
+        torch.cuda.synchronize()
+        if stream is not None:                                        # the binding allocates it
+            assert layer._quick.rms_norm_backward(*v[:8], None, stream.cuda_stream) == -1
+        fp8bs.fp8bs_rms_norm_backward(*v[:8], None, stream)
+        torch.cuda.synchronize()
+        assert torch.equal(v[4], want[0]) and torch.equal(v[6], want[1])
     whole = torch.zeros(100, 256, dtype=BF16, device="cuda")
     assert layer._quick.rms_norm(x[0], x[1], x[2], whole[25:75], *x[4:]) == 0
     torch.cuda.synchronize()

@@ -265,7 +265,7 @@ def test_the_compiled_module_takes_device_tensors_alone(monkeypatch):
     with pytest.raises(TypeError):
         m._quick.use(1, 2)
     with pytest.raises(TypeError):
-        m._quick.use(*["x"] * 10)
+        m._quick.use(*["x"] * 11)
     with pytest.raises(ValueError, match="device"):
         fp8bs.fp8bs_rms_norm(t, t[0], y=t)
     monkeypatch.setattr(m, "_MODULE_PATH", "/nowhere/fp8bs_layer_py.so")
