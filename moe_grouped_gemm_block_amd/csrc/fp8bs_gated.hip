@@ -110,7 +110,7 @@ constexpr int kLaneRows = 2, kTileRows = 16 * kLaneRows;
 // Workgroup: 32 rows x a group of 128 columns, of gate and up; a lane eight columns of each, of
 // two rows, all loads issued before any arithmetic.  The lane divides for one of its group's
 // blocks (block_scales): h, gate and up of each of the two rows.  33280 x 2048 with the checkpoint
-// takes 83 us (476 MB: 5.7 TB/s), without 58; 64 slots' rows of 16 x 256 x 2048 4.1 us.  HBM bounds
+// takes 83 us (476 MB: 5.7 TB/s), without 58; some 500 rows in 16 slots, without, 4.1 us.  HBM bounds
 // it, the vector units are busy for two thirds of the time.  One row a lane: 4% slower.
 template <int ACT, bool KEEP, bool FAR>
 __global__ void __launch_bounds__(256) gated_quant_kernel(GatedParams p) {

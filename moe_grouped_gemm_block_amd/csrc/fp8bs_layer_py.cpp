@@ -5,9 +5,9 @@
 // combine 6.9 and 3.3, gated activation 7.7 and 3.8, columns of 200 x 416 6.2 and 4.0.
 //
 // Each function takes its operator's operands by position and answers the library's status, or -1 if
-// anything is not as it should be -- a type, shape, device -- or needs more than a look (a workspace on
-// another stream than the current one): nothing has been called then, and the binding's checks in layer.py say what is wrong, or make
-// the call.  It never raises.
+// anything is not as it should be -- a type, shape, device -- or needs more than a look (a workspace
+// on another stream than the current one): nothing has been called then, and the binding's checks in
+// layer.py say what is wrong, or make the call.  It never raises.
 #include <Python.h>
 
 #include <climits>

@@ -62,7 +62,7 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[16], int& turn) 
 
 // Workgroup = one row on W = 4 or 16 wavefronts, or four rows (W = 1, a wavefront each).  A lane
 // holds NV runs of eight columns, 512 W apart, 16 lanes a 128-column group.  RES: type of residual
-// (0 none, 1 bf16, 2 FP32).  16384 x 7168 in bf16 takes 140 us (5.9 TB/s; a copy past the caches
+// (0 none, 1 bf16, 2 FP32).  16384 x 7168 in bf16 takes 138 us (6.0 TB/s; a copy past the caches
 // runs at 6.4): loads issued together, the weight's before the sum, a division for NV groups.  Eight rows
 // a workgroup, the next one's loads before this one's sum and scales written together, took 150.  One
 // row of 7168: 2.9 us, a launch and three latencies.
@@ -82,7 +82,10 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
         w[i].load(p.w, from[i]);
     }
     for (uint32_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-        const int64_t row = (int64_t)unit * kAtOnce + wave / W;
+        // (workgroups go round the 8 XCDs: each XCD takes eight units in a row, as far as 64 are left, so
+        // that the scales of neighbouring rows meet in one L2: 1 to 7% of the time)
+        const uint32_t place = (unit | 63) < p.units ? (unit & ~63u) | (unit & 7) << 3 | (unit >> 3 & 7) : unit;
+        const int64_t row = (int64_t)place * kAtOnce + wave / W;
         const bool in = row < p.rows;
         const int64_t at = (in ? +row : (int64_t)p.rows - 1) * p.k;
         Eight<XB> x[NV];

@@ -50,8 +50,9 @@ def _load_module(lib):
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.use(*(ctypes.cast(getattr(lib, "fp8bs_" + name), ctypes.c_void_p).value for name in (
-        "rms_norm", "rms_norm_backward_workspace_size", "rms_norm_backward", "moe_dispatch_workspace_size", "moe_dispatch", "moe_combine",
-        "moe_combine_backward", "gated_quantize", "gated_quantize_backward", "quantize_128x1")),
+        "rms_norm", "rms_norm_backward_workspace_size", "rms_norm_backward",
+        "moe_dispatch_workspace_size", "moe_dispatch", "moe_combine", "moe_combine_backward",
+        "gated_quantize", "gated_quantize_backward", "quantize_128x1")),
         _mx._raw_stream)
     return module
 
