@@ -566,7 +566,7 @@ int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void*
  *   dx        the gradient of x and of residual, in s's type; may be dresidual, s or (of its
  *             type) dy
  *   dweight   f32 [k], optional; accumulate != 0 adds to what it holds.  Written (zeros) for
- *             rows == 0 too.  Without it no workspace is needed.
+ *             rows == 0 too.  Without it no workspace is needed, nor of few rows (the size is 0).
  * Rows are added in an order that follows from the sizes alone.
  */
 int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, void* residual_out,

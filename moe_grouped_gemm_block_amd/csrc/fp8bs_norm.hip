@@ -155,16 +155,58 @@ struct BackwardParams {
     const void* dres;           // nullptr: none
     void* dx;
     float* part;                // [units][k] sums of dy h, or nullptr
-    int rows, k, far;
+    float* dw;                  // of few rows
+    int rows, k, far, accumulate;
     uint32_t units;             // unit u takes the rows u, u + units, ... (times rows at once)
+    uint32_t tiles;             // units behind those: 64 columns of dweight each, of few rows
 };
 
+// dweight of few rows, straight from the inputs: a workgroup 64 columns, eight lanes a row, in chains of
+// every (THREADS / 8)-th row, then those by halves.
+template <int THREADS, bool SB, bool GB>
+__device__ __forceinline__ void dweight_columns(const BackwardParams& p, uint32_t tile,
+                                                float (*sums)[64]) {
+    constexpr int kChains = THREADS / 8;
+    const int t = threadIdx.x, c = t % 8 * 8, chain = t / 8;
+    const int col = (int)tile * 64 + c;
+    float acc[8] = {};
+    if (col < p.k)
+#pragma unroll 4
+        for (int row = chain; row < p.rows; row += kChains) {
+            Eight<SB> s;
+            Eight<GB> g;
+            s.load(p.s, (int64_t)row * p.k + col);
+            g.load(p.dy, (int64_t)row * p.k + col);
+            const float rstd = p.rstd[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += g[e] * (s[e] * rstd);
+        }
+    store8(sums[chain], false, c, acc);
+    __syncthreads();
+    if (t < 64 && (int)tile * 64 + t < p.k) {
+        float each[kChains / 32];
+#pragma unroll
+        for (int j = 0; j < kChains / 32; ++j) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = sums[32 * j + i][t];
+            each[j] = sum_of<32>(v);
+        }
+        float* const to = p.dw + (int64_t)tile * 64 + t;
+        const float all = sum_of<kChains / 32>(each);
+        *to = p.accumulate ? *to + all : all;
+    }
+    __syncthreads();
+}
+
 // A workgroup goes through rows and keeps its part of dweight in registers; the parts are written
-// once and added by the kernel below.  16384 x 7168 in bf16 takes 156 + 5 us (940 MB: 5.9 TB/s, HBM).
+// once and added by the kernel below (few rows: workgroups of their own, above).  16384 x 7168 in bf16 takes 156 + 5 us (940 MB: 5.9 TB/s, HBM).
 template <int W, int NV, bool SB, bool GB, bool WB>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel(BackwardParams p) {
     __shared__ float part[2][16];
     constexpr int kThreads = W == 16 ? 1024 : 256, kAtOnce = kThreads / 64 / W;
+    constexpr bool kFew = W != 4 || NV != 4;   // (few rows of no length take that layout)
+    __shared__ __attribute__((aligned(16))) float columns[kFew ? kThreads / 8 : 1][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wr = wave % W, sub = wave / W;
     int turn = 0;
@@ -175,7 +217,12 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
 #pragma unroll
     for (int i = 0; i < NV; ++i) w[i].load(p.w, col[i] < p.k ? +col[i] : p.k - 8);
 
-    for (uint32_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+    for (uint32_t unit = blockIdx.x; unit < p.units + p.tiles; unit += gridDim.x) {
+        if constexpr (kFew)
+            if (unit >= p.units) {
+                dweight_columns<kThreads, SB, GB>(p, unit - p.units, columns);
+                continue;
+            }
         float acc[NV][8] = {};
         const int64_t step = (int64_t)p.units * kAtOnce;
         int64_t row = (int64_t)unit * kAtOnce + sub;
@@ -336,12 +383,20 @@ const void* backward_kernel(Shape s, bool sb, bool gb, bool wb) {
 int threads_of(Shape s) { return s.waves == 16 ? 1024 : 256; }
 int at_once(Shape s) { return s.waves == 1 ? 4 : 1; }
 
+// Few rows: dweight in the same launch, from the inputs again, which are in the caches then (so, and in
+// parts with a second launch: 7168 columns, 64 rows 3.4 us and 6.6, 256 rows 8.1 and 11.5, 384 rows 10.9
+// and 13.2, 511 rows 15.8 and 14.1; 4096 columns, 384 rows 6.0 and 9.8, 511 rows 10.1 and 10.6).
+constexpr int kDirectRows = 384;
+static_assert(kDirectRows < kFewRows, "no such row is four wavefronts' of four eights");
+bool direct(int64_t rows) { return rows > 0 && rows <= kDirectRows; }
+
 // Units of the backward pass: parts of dweight.  By sizes alone, not by the device or the cap on CUs:
 // the units' sums are added in order.  512 at most: 16384 x 7168 takes 160 us, with 256 185 (too
 // few loads in flight), with 1024 165 (twice the parts).  256 up to 1024 turns: 512 x 7168 takes
 // 13.6 us, with a unit a row 16.3.
 int64_t backward_units(int64_t rows, Shape s) {
     const int64_t turns = (rows + at_once(s) - 1) / at_once(s);
+    if (direct(rows)) return turns;
     return turns < 256 ? turns : turns < 1024 ? 256 : turns < 2048 ? turns / 4 : 512;
 }
 
@@ -378,7 +433,7 @@ extern "C" int fp8bs_rms_norm(const void* x, int x_dtype, const void* residual, 
 extern "C" int64_t fp8bs_rms_norm_backward_workspace_size(int64_t rows, int k) {
     using namespace fp8bs::layer;
     if (rows < 0 || rows > kMaxRows || k < 8 || k % 8 != 0 || k > kMostCols) return -FP8BS_ERR_SHAPE;
-    return backward_units(rows, shape_of(rows, k, true)) * k * 4;
+    return direct(rows) ? 0 : backward_units(rows, shape_of(rows, k, true)) * k * 4;
 }
 
 extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd,
@@ -396,18 +451,30 @@ extern "C" int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* 
     const Shape shape = shape_of(rows, k, true);
     if (rows > 0) {
         if (!aligned(s) || !aligned(rstd, 4) || !aligned(weight) || !aligned(dy) ||
-            !aligned_or_null(dresidual) || !aligned(dx) || (dweight && !aligned(workspace)))
+            !aligned_or_null(dresidual) || !aligned(dx) || (dweight && need > 0 && !aligned(workspace)))
             return FP8BS_ERR_POINTER;
         if (dweight && workspace_bytes < (size_t)need) return FP8BS_ERR_UNSUPPORTED;
-        BackwardParams p = {s, rstd, weight, dy, dresidual, dx, dweight ? (float*)workspace : nullptr,
-                            rows, k, far_outputs((double)rows * k * 2),
-                            (uint32_t)backward_units(rows, shape)};
-        const int st = launch(backward_kernel(shape, s_dtype == FP8BS_DTYPE_BF16,
-                                              dy_dtype == FP8BS_DTYPE_BF16,
-                                              weight_dtype == FP8BS_DTYPE_BF16),
-                              workgroups(p.units, shape.waves == 16 ? 1 : 4), threads_of(shape), p,
-                              stream);
-        if (st != FP8BS_OK) return st;
+        const bool few = direct(rows);
+        BackwardParams p = {s, rstd, weight, dy, dresidual, dx,
+                            dweight && !few ? (float*)workspace : nullptr, dweight, rows, k,
+                            far_outputs((double)rows * k * 2), accumulate != 0,
+                            (uint32_t)backward_units(rows, shape),
+                            dweight && few ? (uint32_t)((k + 63) / 64) : 0};
+        const void* fn = backward_kernel(shape, s_dtype == FP8BS_DTYPE_BF16,
+                                         dy_dtype == FP8BS_DTYPE_BF16,
+                                         weight_dtype == FP8BS_DTYPE_BF16);
+        const auto run = [&](uint32_t units, uint32_t tiles) {
+            p.units = units;
+            p.tiles = tiles;
+            return launch(fn, workgroups((int64_t)units + tiles, shape.waves == 16 ? 1 : 4),
+                          threads_of(shape), p, stream);
+        };
+        const uint32_t units = p.units, tiles = p.tiles;
+        // (in place: the columns are added before the rows are written over)
+        const bool first = tiles && (dx == s || dx == dy);
+        int st = first ? run(0, tiles) : FP8BS_OK;
+        if (st == FP8BS_OK) st = run(units, first ? 0 : tiles);
+        if (st != FP8BS_OK || few) return st;
     }
     if (!dweight) return FP8BS_OK;
     SumParams p = {(const float*)workspace, dweight,

@@ -31,12 +31,13 @@ def operands():
     gate_up, counts = rand(g, m, 2 * f), torch.tensor([0, 40, 7, 33], dtype=I32, device="cuda")
     flat, dh = rand(rows, 2 * f), rand(rows, f)
     kq, sk = fp8bs.quantize_1x128(flat)
-    ws = zeros(fp8bs.rms_norm_backward_workspace_size(rows, k), t=U8)
+    many = 400                                                        # (fewer need no workspace)
+    ws = zeros(fp8bs.rms_norm_backward_workspace_size(many, k), t=U8)
     return {
         "rms_norm": ([x, w, res, zeros(rows, k, t=BF16), zeros(rows, k, t=BF16), codes(rows, k), zeros(k // 128, ld(rows)),
                       zeros(rows), 1e-6, None], (3, 4, 5, 6, 7), (2, 3, 4, 7)),
-        "rms_norm_backward": ([x, torch.rand(rows, generator=gen, device="cuda"), w, dy, zeros(rows, k, t=BF16), res, zeros(k),
-                               False, ws, None], (4, 6), (5, 6, 8)),
+        "rms_norm_backward": ([rand(many, k), torch.rand(many, generator=gen, device="cuda"), w, rand(many, k),
+                               zeros(many, k, t=BF16), rand(many, k), zeros(k), False, ws, None], (4, 6), (5, 6, 8)),
         "moe_dispatch": ([ids, xq, codes(g, m, k), zeros(g, t=I32), zeros(rows, topk, t=I32), zeros(g, t=I32), sx,
                           zeros(g, k // 128, ld(m)), None, None], (2, 3, 4, 5, 7), (8,)),
         "moe_combine": ([d, pos, zeros(rows, k), rw, None], (2,), (3,)),

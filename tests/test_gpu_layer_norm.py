@@ -149,7 +149,7 @@ def gradients(s, rstd, w, dy, dres):
 @pytest.mark.parametrize("rows,k", [(1, 128), (1, 8), (3, 1000), (300, 512), (200, 2048), (64, 7168),
                                     (2, 9000), (1, 32768), (512, 504), (2060, 512), (700, 1024),
                                     (515, 2048), (600, 4096), (1030, 7168), (513, 16384),
-                                    (512, 20000)])
+                                    (512, 20000), (384, 16384), (385, 2048), (384, 4096)])
 @pytest.mark.parametrize("st,gt,wt", [(BF16, BF16, BF16), (F32, BF16, F32), (BF16, F32, F32),
                                       (F32, F32, BF16)])
 def test_gradients(gen, rows, k, st, gt, wt):
@@ -196,6 +196,25 @@ def test_gradients_are_the_formulas(gen):
     assert abs(numeric - (dx * d).sum()) < 1e-7 * np.abs(dx * d).sum()
 
 
+@pytest.mark.parametrize("rows,k", [(1, 128), (70, 896), (384, 264), (385, 264), (384, 1000), (200, 7168), (384, 16384),
+                                    (600, 7168)])
+def test_gradients_in_place_with_dweight(gen, rows, k):
+    """few rows' dweight is added from the inputs: the same whether dx is written over them or not"""
+    s, dy, dres = rand(gen, rows, k), rand(gen, rows, k), rand(gen, rows, k)
+    w = (1 + 0.2 * torch.randn(k, generator=gen, device="cuda"))
+    rstd = 1 / torch.sqrt(s.float().square().mean(-1) + 1e-6)
+    dx, dw = torch.empty_like(s), torch.empty(k, device="cuda")
+    fp8bs.fp8bs_rms_norm_backward(s, rstd, w, dy, dx, dres, dw)
+    _, _, want_w, size_w = gradients(s, rstd, w, dy, dres)
+    # (chains of every 32nd or 128th row at least, their sums by halves, three roundings of a product)
+    assert np.all(np.abs(host(dw) - want_w) <= (rows / 32 + 1 + 7 + 3) * E * size_w + 1e-38)
+    for i in range(3):
+        for _ in range(5):
+            args, own = [s.clone(), dy.clone(), dres.clone()], torch.empty(k, device="cuda")
+            fp8bs.fp8bs_rms_norm_backward(args[0], rstd, w, args[1], args[i], args[2], own)
+            assert torch.equal(args[i], dx) and torch.equal(own, dw)
+
+
 def test_gradients_in_place_and_of_no_rows(gen):
     s, dy, dres = rand(gen, 70, 896), rand(gen, 70, 896), rand(gen, 70, 896)
     w = (1 + 0.2 * torch.randn(896, generator=gen, device="cuda"))
@@ -217,7 +236,11 @@ def test_gradients_in_place_and_of_no_rows(gen):
 
 
 def test_the_cap_changes_no_result(gen):
-    s, dy = rand(gen, 3000, 640), rand(gen, 3000, 640)
+    for rows in (3000, 300):
+        caps_agree(rand(gen, rows, 640), rand(gen, rows, 640), gen)
+
+
+def caps_agree(s, dy, gen):
     w = (1 + 0.2 * torch.randn(640, generator=gen, device="cuda"))
     runs = []
     try:
@@ -273,6 +296,7 @@ def test_refusals_on_the_device(gen):
         fp8bs.fp8bs_rms_norm_backward(x, rstd, w, x, x.float())
     with pytest.raises(ValueError):
         fp8bs.fp8bs_rms_norm_backward(x, rstd[:3], w, x, x)
+    x, rstd = rand(gen, 400, 256), torch.ones(400, device="cuda")
     with pytest.raises(fp8bs.FP8BSError):
-        fp8bs.fp8bs_rms_norm_backward(x, rstd, w, x, x, None, w,
+        fp8bs.fp8bs_rms_norm_backward(x, rstd, w, x, x, None, w.clone(),
                                       workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -51,7 +51,7 @@ def test_norm_refusals(lib, p):
 def test_norm_backward_refusals(lib, p):
     big = 1 << 40
 
-    def back(rows=4, k=128, s=p, st=BF16, rstd=p, w=p, wt=BF16, dy=p, dt=BF16, dres=p, dx=p, dw=p,
+    def back(rows=400, k=128, s=p, st=BF16, rstd=p, w=p, wt=BF16, dy=p, dt=BF16, dres=p, dx=p, dw=p,
              ws=p, n=big):
         return lib.fp8bs_rms_norm_backward(s, st, rstd, w, wt, dy, dt, dres, dx, dw, 0, rows, k, ws,
                                            n, None)
@@ -64,11 +64,12 @@ def test_norm_backward_refusals(lib, p):
         assert back(**{name: None}) == POINTER, name
     for name in ("s", "w", "dy", "dx", "dres", "dw", "ws"):
         assert back(**{name: p + 4}) == POINTER, name
-    need = lib.fp8bs_rms_norm_backward_workspace_size(4, 128)
+    need = lib.fp8bs_rms_norm_backward_workspace_size(400, 128)
     assert need > 0 and back(n=need - 1) == UNSUPPORTED
     assert back(rows=0, s=None, rstd=None, w=None, dy=None, dx=None, dw=None, ws=None, n=0) == OK
     size = lib.fp8bs_rms_norm_backward_workspace_size
     assert size(-1, 128) == -SHAPE and size(4, 100) == -SHAPE and size(0, 128) == 0
+    assert size(384, 7168) == 0 and size(385, 7168) == 256 * 7168 * 4    # few rows need none
     # no more than 512 parts, whatever the rows
     assert size(1 << 30, 7168) == size(1 << 20, 7168) == 512 * 7168 * 4
 
