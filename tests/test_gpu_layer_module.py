@@ -1,6 +1,8 @@
 """The compiled module in front of the layer operators' binding (`-m gpu`): it makes the calls that
 it should, with the binding's own results, and leaves every call with a wrong operand to the
 binding, nothing written."""
+import threading
+
 import pytest
 import torch
 
@@ -163,3 +165,38 @@ def test_parameters_views_and_a_missing_workspace():
     assert layer._quick.rms_norm(x[0], x[1], x[2], whole[25:75], *x[4:]) == 0
     torch.cuda.synchronize()
     assert torch.equal(whole[25:75], x[3]) and not bool(whole[:25].any()) and not bool(whole[75:].any())
+
+
+def test_threads_at_once():
+    """four host threads, each with operands and a stream of its own: the module lets go of the interpreter's lock"""
+    layer._load()
+    want = []
+    for name in NAMES:
+        a, outputs, _ = operands()[name]
+        by_the_binding(name, a)
+        torch.cuda.synchronize()
+        want.append([a[i].clone() for i in outputs])
+    sets = [operands() for _ in range(4)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(own):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    for name in NAMES:
+                        by_the_binding(name, own[name][0])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(own,)) for own in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for own in sets:
+        for name, outs in zip(NAMES, want):
+            a, outputs, _ = own[name]
+            for i, t in zip(outputs, outs):
+                assert torch.equal(a[i], t), (name, i)

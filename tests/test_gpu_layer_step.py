@@ -191,6 +191,62 @@ def test_decode_step_in_a_graph(gen, tokens):
             assert float((got["y"].double() - want).norm() / want.norm()) <= 4 * 2.0 ** -4, turn
 
 
+@pytest.mark.parametrize("tokens,in_place", [(40, False), (40, True), (500, False), (500, True)])
+def test_way_back_in_a_graph(gen, tokens, in_place):
+    """the gradients' operators (few rows and many, workspaces from the graph's own memory), captured once; replays
+    with new inputs against the same calls made eagerly"""
+    topk, g, k, f = 2, 4, 384, 128
+    m = fp8bs.moe_capacity(tokens, topk, g)
+    x, res, nw, ids, rw, _, _, dy, dres = inputs(gen, tokens, topk, g, k, f, 1)
+    gate_up, d = (torch.randn(m, n, generator=gen, device="cuda").to(BF16) for n in (2 * f, k))
+    rstd = torch.rand(tokens, generator=gen, device="cuda")
+    kq, sk = fp8bs.quantize_1x128(gate_up)
+    b = dict(ddq=codes(m, k), sdd=scales(k // 128, m), drw=torch.empty_like(rw), dq=codes(m, 2 * f), sd=scales(2 * f // 128, m),
+             dqt=codes(m, 2 * f), sdt=scales(m // 128, 2 * f), hqt=codes(m, f), sht=scales(m // 128, f), ddt=codes(m, k),
+             sddt=scales(m // 128, k), dxn=torch.empty(tokens, k, dtype=BF16, device="cuda"), dx=torch.empty_like(x),
+             dnw=torch.empty(k, device="cuda"), positions=torch.empty(tokens, topk, dtype=I32, device="cuda"),
+             lay=torch.empty(m, dtype=I32, device="cuda"), counts=torch.empty(g, dtype=I32, device="cuda"),
+             a=torch.zeros(m, k, dtype=BF16, device="cuda"))
+    for t in b.values():
+        t.view(U8).zero_()
+
+    def step():
+        fp8bs.fp8bs_moe_dispatch(ids, x, b["a"], b["lay"], b["positions"], b["counts"])
+        fp8bs.fp8bs_moe_combine_backward(dy, b["positions"], d, rw, q=b["ddq"], sfa=b["sdd"], dweights=b["drw"])
+        fp8bs.fp8bs_gated_quantize_backward(kq, d[:, :f].contiguous(), sk, dq=b["dq"], sfd=b["sd"], dqt=b["dqt"], sfdt=b["sdt"],
+                                            hqt=b["hqt"], sfht=b["sht"], grouped_layout=b["lay"])
+        fp8bs.fp8bs_quantize_128x1(b["ddq"], b["ddt"], b["sddt"], b["sdd"], b["lay"])
+        fp8bs.fp8bs_moe_combine(d, b["positions"], b["dxn"])
+        dx = b["dxn"] if in_place else b["dx"]
+        fp8bs.fp8bs_rms_norm_backward(x, rstd, nw, b["dxn"], dx, dres, b["dnw"])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(4):
+        new = inputs(gen, tokens, topk, g, k, f, 1)
+        x.copy_(new[0]), ids.copy_(new[3]), rw.copy_(new[4]), dy.copy_(new[7]), dres.copy_(new[8])
+        d.normal_(generator=gen)
+        for t in b.values():                                          # (rows of no choice are not written)
+            t.view(U8).zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in b.items()}
+        for t in b.values():
+            t.view(U8).zero_()
+        step()
+        torch.cuda.synchronize()
+        for n, t in b.items():
+            assert torch.equal(got[n].view(U8), t.view(U8)), (turn, n)
+        assert bool((got["dnw"] != 0).any()) and bool((got["dqt"] != 0).any())
+
+
 def test_dispatched_rows_through_the_4_bit_layer(gen):
     """bf16 rows dispatched for the MXFP4 feed-forward layer, and brought back"""
     tokens, topk, g, k, f = 200, 2, 4, 256, 128
