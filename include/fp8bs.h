@@ -539,7 +539,8 @@ int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void*
  * fp8bs_k_grouped_tn_contiguous reads: codes [R][n], R = rows rounded up to a multiple of 128,
  * and scales f32 [R/128][ld(n)], one for each column and 128 rows.  Both quantise a block as
  * fp8bs_quantize_1x128 does, from FP32 values (a NaN's code may have either sign).
- * Sums are FP32 and each output is rounded once.  Optional buffers may be NULL.  Sizes,
+ * Sums are FP32 and each output is rounded once.  Optional buffers may be NULL; outputs overlap
+ * nothing else, but where it says that one may be an input.  Sizes,
  * streams and errors are as for the calls above (rows, of all slots for dispatch and the gradient of
  * combine, are at most 2^31 - 256); pointers are 16-byte aligned, those to rstd, positions,
  * weights, dweights, counts and group data 4-byte, ids as their type.  A workspace is device memory of at least the bytes that the

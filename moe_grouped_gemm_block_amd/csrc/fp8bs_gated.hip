@@ -294,29 +294,30 @@ __device__ __forceinline__ void fetch(const GatedBackwardParams& p, uint32_t til
     }
 }
 
-// A workgroup a CU, which goes from tile to tile: the next tile's inputs are on their way while this
-// one's scales are exchanged, which is what two barriers a tile cost most.  Gradients are FP32 until
-// their codes; each is quantised both ways from the registers, so that nothing is read twice.  33280 x
-// 2048 from the checkpoint takes 129 us (622 MB: 4.8 TB/s); the vector units are busy for two thirds of
-// that, some 50 instructions a value.  Inputs are read through the caches at every size: 129 us against
-// 127 past them, 8192 x 2048 29.7 against 35.4.  Without the inputs ahead it took 164 when it took 133 with
-// them, two workgroups of 8 wavefronts a CU 148 (there are no registers to keep inputs ahead).
-template <int ACT, bool KEPT>
-__global__ void __launch_bounds__(64 * kGradWaves)
-    gated_backward_kernel(GatedBackwardParams p) {
-    __shared__ ColumnScales<3, kGradWaves> lds;
+// What a workgroup makes of a tile: everything, or of few tiles one of two the gate's gradient, the
+// other up's and the activation.
+enum : int { kWhole, kGate, kUp };
+
+template <int ACT, bool KEPT, int PART>
+__device__ __forceinline__ void gradients(const GatedBackwardParams& p, uint32_t first, uint32_t step,
+                                          ColumnScales<3, kGradWaves>& shared) {
+    // numbers of the outputs among those that are made: dgate, dup, h
+    constexpr int kDup = PART == kWhole ? 1 : 0, kH = kDup + 1;
+    constexpr int kOuts = PART == kWhole ? 3 : PART == kGate ? 1 : 2;
+    constexpr int kRowBlocks = (PART == kWhole ? 2 : 1) * kGradRows;       // 1x128: dgate's, dup's
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int seg = lane & 15, lane_row = wave * 4 * kGradRows + (lane >> 4);
     const int fb = p.f >> 7;
+    ColumnScales<kOuts, kGradWaves>& lds = (ColumnScales<kOuts, kGradWaves>&)shared;
     GradInputs<KEPT> v;
-    fetch<KEPT>(p, blockIdx.x, lane_row, seg, v);
-    for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    fetch<KEPT>(p, first, lane_row, seg, v);
+    for (uint32_t tile = first; tile < p.tiles; tile += step) {
         const int c = (int)(tile % fb), rt = (int)(tile / fb);
         const int64_t row0 = (int64_t)rt * kBlock;
         const int last = p.m - 1 - row0 < kBlock - 1 ? (int)(p.m - 1 - row0) : kBlock - 1;
         const uint32_t held = v.rows.held(lane_row, last);
-        float dg[kGradRows][8], du[kGradRows][8], h[kGradRows][8];
-        float top[3][8] = {};
+        float out[kOuts][kGradRows][8];
+        float top[kOuts][8] = {};
         // a row that holds no token is zeros
         if (__ballot(held != (1u << kGradRows) - 1)) {
 #pragma unroll
@@ -350,34 +351,35 @@ __global__ void __launch_bounds__(64 * kGradWaves)
                 }
                 const float dh = v.dh[i][e];
                 float slope;
-                const float act = activate<ACT, true>(gate[e], slope);
-                dg[i][e] = dh * up[e] * slope;
-                du[i][e] = dh * act;
-                h[i][e] = act * up[e];
-                top[0][e] = __builtin_fmaxf(top[0][e], __builtin_fabsf(dg[i][e]));
-                top[1][e] = __builtin_fmaxf(top[1][e], __builtin_fabsf(du[i][e]));
-                top[2][e] = __builtin_fmaxf(top[2][e], __builtin_fabsf(h[i][e]));
+                const float act = activate<ACT, PART != kUp>(gate[e], slope);
+                if constexpr (PART != kUp) out[0][i][e] = dh * up[e] * slope;
+                if constexpr (PART != kGate) {
+                    out[kDup][i][e] = dh * act;
+                    out[kH][i][e] = act * up[e];
+                }
+#pragma unroll
+                for (int n = 0; n < kOuts; ++n)
+                    top[n][e] = __builtin_fmaxf(top[n][e], __builtin_fabsf(out[n][i][e]));
             }
         }
-        
+        // columns of [dgate dup] that are made here
+        const int64_t half = PART == kUp ? p.f : 0;
         if (p.dq) {
-            float most[2 * kGradRows], inv[2 * kGradRows];
+            float most[kRowBlocks], inv[kRowBlocks];
 #pragma unroll
-            for (int i = 0; i < kGradRows; ++i) {
-                most[i] = max8(dg[i]);
-                most[kGradRows + i] = max8(du[i]);
-            }
+            for (int j = 0; j < kRowBlocks; ++j) most[j] = max8(out[j / kGradRows][j % kGradRows]);
             const float scale = block_scales(most, seg, inv);
-            if (seg < 2 * kGradRows && (held >> (seg % kGradRows) & 1))
-                p.sfd[(int64_t)(seg / kGradRows * fb + c) * p.ld + row0 + lane_row +
-                      4 * (seg % kGradRows)] = scale;
-            uint8_t* const to = p.dq + row0 * 2 * p.f + kBlock * c;
+            if (seg < kRowBlocks && (held >> (seg % kGradRows) & 1))
+                p.sfd[(int64_t)((PART == kUp ? fb : 0) + seg / kGradRows * fb + c) * p.ld + row0 +
+                      lane_row + 4 * (seg % kGradRows)] = scale;
+            uint8_t* const to = p.dq + row0 * 2 * p.f + half + kBlock * c;
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i)
                 if (held >> i & 1) {
                     const uint32_t at = place(lane_row + 4 * i, 2 * p.f, 8 * seg);
-                    put_codes(to + at, codes8(dg[i], inv[i]), p.far);
-                    put_codes(to + p.f + at, codes8(du[i], inv[kGradRows + i]), p.far);
+                    put_codes(to + at, codes8(out[0][i], inv[i]), p.far);
+                    if constexpr (PART == kWhole)
+                        put_codes(to + p.f + at, codes8(out[1][i], inv[kGradRows + i]), p.far);
                 }
         }
         if (p.d)
@@ -385,32 +387,57 @@ __global__ void __launch_bounds__(64 * kGradWaves)
             for (int i = 0; i < kGradRows; ++i)
                 if (held >> i & 1) {
                     const int64_t at =
-                        (row0 + lane_row + 4 * i) * 2 * p.f + kBlock * c + 8 * seg;
-                    store8(p.d, true, at, dg[i]);
-                    store8(p.d, true, at + p.f, du[i]);
+                        (row0 + lane_row + 4 * i) * 2 * p.f + half + kBlock * c + 8 * seg;
+                    store8(p.d, true, at, out[0][i]);
+                    if constexpr (PART == kWhole) store8(p.d, true, at + p.f, out[1][i]);
                 }
-        if (tile + gridDim.x < p.tiles) fetch<KEPT>(p, tile + gridDim.x, lane_row, seg, v);
+        if (tile + step < p.tiles) fetch<KEPT>(p, tile + step, lane_row, seg, v);
         if (!p.dqt && !p.hqt) continue;
-        float* const to[3] = {
-            p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + kBlock * c : nullptr,
-            p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + p.f + kBlock * c : nullptr,
-            p.hqt ? p.sfht + (int64_t)rt * p.f + kBlock * c : nullptr};
+        float* to[kOuts];
+        to[0] = p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + half + kBlock * c : nullptr;
+        if constexpr (PART == kWhole)
+            to[1] = p.dqt ? p.sfdt + (int64_t)rt * 2 * p.f + p.f + kBlock * c : nullptr;
+        if constexpr (PART != kGate)
+            to[kH] = p.hqt ? p.sfht + (int64_t)rt * p.f + kBlock * c : nullptr;
         column_scales(lds, top, to, kBlock);
-        uint8_t* const dqt = p.dqt + row0 * 2 * p.f + kBlock * c;
+        uint8_t* const dqt = p.dqt + row0 * 2 * p.f + half + kBlock * c;
         uint8_t* const hqt = p.hqt + row0 * p.f + kBlock * c;
 #pragma unroll
         for (int i = 0; i < kGradRows; ++i) {
             const int r = lane_row + 4 * i;
             if (p.dqt) {
                 const uint32_t at = place(r, 2 * p.f, 8 * seg);
-                put_codes(dqt + at, column_codes(dg[i], &lds.inv[0][8 * seg]), p.far);
-                put_codes(dqt + p.f + at, column_codes(du[i], &lds.inv[1][8 * seg]), p.far);
+                put_codes(dqt + at, column_codes(out[0][i], &lds.inv[0][8 * seg]), p.far);
+                if constexpr (PART == kWhole)
+                    put_codes(dqt + p.f + at, column_codes(out[1][i], &lds.inv[1][8 * seg]), p.far);
             }
-            if (p.hqt)
-                put_codes(hqt + place(r, p.f, 8 * seg), column_codes(h[i], &lds.inv[2][8 * seg]),
-                          p.far);
+            if constexpr (PART != kGate)
+                if (p.hqt)
+                    put_codes(hqt + place(r, p.f, 8 * seg),
+                              column_codes(out[kH][i], &lds.inv[kH][8 * seg]), p.far);
         }
     }
+}
+
+// A workgroup a CU, which goes from tile to tile: the next tile's inputs are on their way while this
+// one's scales are exchanged, which is what two barriers a tile cost most.  Gradients are FP32 until
+// their codes; each is quantised both ways from the registers, so that nothing is read twice.  33280 x
+// 2048 from the checkpoint takes 129 us (622 MB: 4.8 TB/s); the vector units are busy for two thirds of
+// that, some 40 instructions a value.  Inputs are read through the caches at every size: 129 us against
+// 127 past them, 8192 x 2048 29.7 against 35.4.  Without the inputs ahead it took 164 when it took 133 with
+// them, two workgroups of 8 wavefronts a CU 148 (there are no registers to keep inputs ahead).  SPLIT:
+// two workgroups a tile where that leaves none waiting: a tile is 6 us of one CU's vector units (silu,
+// gelu: 128 x 2048 7.0 and 7.3 us against 8.0 and 8.8 whole, 1024 x 2048 8.9 and 9.2 against 9.8 and 10.6).
+template <int ACT, bool KEPT, bool SPLIT>
+__global__ void __launch_bounds__(64 * kGradWaves)
+    gated_backward_kernel(GatedBackwardParams p) {
+    __shared__ ColumnScales<3, kGradWaves> lds;
+    if constexpr (!SPLIT)
+        gradients<ACT, KEPT, kWhole>(p, blockIdx.x, gridDim.x, lds);
+    else if (blockIdx.x % 2 == 0)
+        gradients<ACT, KEPT, kGate>(p, blockIdx.x / 2, gridDim.x / 2, lds);
+    else
+        gradients<ACT, KEPT, kUp>(p, blockIdx.x / 2, gridDim.x / 2, lds);
 }
 
 struct ColumnParams {
@@ -511,6 +538,11 @@ const void* quant_kernel(bool far) {
     return far ? (const void*)gated_quant_kernel<ACT, KEEP, true>
                : (const void*)gated_quant_kernel<ACT, KEEP, false>;
 }
+template <int ACT, bool KEPT>
+const void* backward_kernel(bool split) {
+    return split ? (const void*)gated_backward_kernel<ACT, KEPT, true>
+                 : (const void*)gated_backward_kernel<ACT, KEPT, false>;
+}
 template <int DTYPE>
 const void* columns_kernel(bool far) {
     return far ? (const void*)quant_128x1_kernel<DTYPE, true>
@@ -583,13 +615,14 @@ extern "C" int fp8bs_gated_quantize_backward(const void* g, int g_dtype, const f
                              (uint32_t)tiles};
     const int cus = compute_units();
     if (cus <= 0) return FP8BS_ERR_HIP;
-    const void* fn =
-        activation == FP8BS_ACT_SILU
-            ? kept ? (const void*)gated_backward_kernel<FP8BS_ACT_SILU, true>
-                   : (const void*)gated_backward_kernel<FP8BS_ACT_SILU, false>
-            : kept ? (const void*)gated_backward_kernel<FP8BS_ACT_GELU_TANH, true>
-                   : (const void*)gated_backward_kernel<FP8BS_ACT_GELU_TANH, false>;
-    return launch(fn, p.tiles < (uint32_t)cus ? p.tiles : (unsigned)cus, 64 * kGradWaves, p, stream);
+    const bool split = 2 * tiles <= cus;
+    const void* fn = activation == FP8BS_ACT_SILU
+                         ? kept ? backward_kernel<FP8BS_ACT_SILU, true>(split)
+                                : backward_kernel<FP8BS_ACT_SILU, false>(split)
+                         : kept ? backward_kernel<FP8BS_ACT_GELU_TANH, true>(split)
+                                : backward_kernel<FP8BS_ACT_GELU_TANH, false>(split);
+    const uint32_t most = split ? 2 * p.tiles : p.tiles;
+    return launch(fn, most < (uint32_t)cus ? most : (unsigned)cus, 64 * kGradWaves, p, stream);
 }
 
 extern "C" int fp8bs_quantize_128x1(const void* x, int x_dtype, const float* sfx, void* q,

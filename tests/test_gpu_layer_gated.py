@@ -200,6 +200,15 @@ def test_backward(gen, kind, m, f, act, kept):
         one = {n: torch.full_like(out[n], 9.0 if n == "d" else -7.0 if n.startswith("sf") else 9) for n in names}
         fp8bs.fp8bs_gated_quantize_backward(dh=dh, **args, **one, **more, activation=act)
         assert all(torch.equal(one[n], out[n]) for n in names), names
+    # and with one workgroup a tile, as of many tiles
+    try:
+        fp8bs.set_num_cus(1)
+        for names in (tuple(out), ("d",), ("dq", "sfd"), ("dqt", "sfdt"), ("hqt", "sfht")):
+            one = {n: torch.full_like(out[n], 9.0 if n == "d" else -7.0 if n.startswith("sf") else 9) for n in names}
+            fp8bs.fp8bs_gated_quantize_backward(dh=dh, **args, **one, **more, activation=act)
+            assert all(torch.equal(one[n], out[n]) for n in names), names
+    finally:
+        fp8bs.set_num_cus(0)
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])

@@ -82,7 +82,7 @@ def test_every_kernel_is_reached():
     queries += [("dispatch", CONTIGUOUS, t, 8, g, 128 * 4096) for t, g in ((10, 8), (200, 8), (400, 64), (5000, 8), (40000, 8))]
     queries += [("combine", 10, 2, 512, y) for y in (F32, BF16)] + [("combine_back", 10, 2, 512, y) for y in (F32, BF16)]
     queries += [("gated", DENSE, 100, 256, 1, keep + 2 * act) for keep in (0, 1) for act in (0, 1)]
-    queries += [("gated_back", 100, 256, kept, act) for kept in (0, 1) for act in (0, 1)]
+    queries += [("gated_back", m, 256, kept, act) for m in (100, 20000) for kept in (0, 1) for act in (0, 1)]
     queries += [("columns", 100, 256, t) for t in (0, 1, 2)]
     # (inputs read past the caches: tests/test_gpu_layer_large.py)
     queries += [(op, 5000, 3, 4096, y) for op in ("combine", "combine_back") for y in (F32, BF16)]
