@@ -326,18 +326,19 @@ __global__ void __launch_bounds__(1024) rms_norm_sum_kernel(SumParams p) {
 //   2048 columns, 4 x 1 against 1 x 4: 64 rows 2.8 us against 3.5, 512 rows 3.2 and 3.8, 2048 rows
 //   6.2 and 5.8; the gradients 4096 rows 18.5 and 27
 //   7168 columns, 16 x 1 against 4 x 4: 64 rows 3.5 us against 3.9, 256 rows 4.1 and 4.4, 512 rows 6.3
-//   and 6.2, 1024 rows 12.2 and 11.1; the gradients 256 rows 10.1 and 10.6, 512 rows 16.5 and 16.5
+//   and 6.2, 1024 rows 12.2 and 11.1; the gradients 600 rows 15.4 and 17.4, 1024 rows 19.1 and 22.2, 2048
+//   rows 32.9 and 28.4
 struct Shape {
     int waves, eights;
 };
-constexpr int kFewRows = 512;
+constexpr int kFewRows = 512, kFewBackward = 1025;
 Shape shape_of(int64_t rows, int k, bool backward) {
     const bool few = rows < kFewRows;
     if (k <= 512) return {1, 1};
     if (k <= 2048 && !few && !backward) return {1, k <= 1024 ? 2 : 4};
     if (k <= 2048) return {4, 1};
     if (k <= 4096) return {4, 2};
-    if (k <= 8192) return few ? Shape{16, 1} : Shape{4, 4};
+    if (k <= 8192) return rows < (backward ? kFewBackward : kFewRows) ? Shape{16, 1} : Shape{4, 4};
     return {16, k <= 16384 ? 2 : 4};
 }
 
@@ -387,7 +388,7 @@ int at_once(Shape s) { return s.waves == 1 ? 4 : 1; }
 // parts with a second launch: 7168 columns, 64 rows 3.4 us and 6.6, 256 rows 8.1 and 11.5, 384 rows 10.9
 // and 13.2, 511 rows 15.8 and 14.1; 4096 columns, 384 rows 6.0 and 9.8, 511 rows 10.1 and 10.6).
 constexpr int kDirectRows = 384;
-static_assert(kDirectRows < kFewRows, "no such row is four wavefronts' of four eights");
+static_assert(kDirectRows < kFewBackward, "no such row is four wavefronts' of four eights");
 bool direct(int64_t rows) { return rows > 0 && rows <= kDirectRows; }
 
 // Units of the backward pass: parts of dweight.  By sizes alone, not by the device or the cap on CUs:

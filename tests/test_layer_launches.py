@@ -71,7 +71,7 @@ def types(x, res, weight):
 
 # the sizes of the GPU tests (tests/test_gpu_layer_*.py)
 NORM = [(1, 128), (3, 384), (1, 2048), (2, 7168), (2, 9088), (3, 16384), (2, 32768), (512, 128), (513, 1024),
-        (517, 2048), (512, 2176), (520, 7168), (512, 8320), (513, 16512), (515, 4096), (530, 264), (7, 1000)]
+        (517, 2048), (512, 2176), (520, 7168), (512, 8320), (513, 16512), (515, 4096), (530, 264), (7, 1000), (1030, 7168)]
 
 
 def test_every_kernel_is_reached():
