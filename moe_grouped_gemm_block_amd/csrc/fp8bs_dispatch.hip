@@ -602,10 +602,11 @@ extern "C" int fp8bs_moe_dispatch(int layout, const void* ids, int id_bytes, con
     const int64_t rows = masked ? (int64_t)m * num_groups : m;
     if (!aligned(counts, 4) || ((masked || m > 0) && !aligned(group_data, 4)))
         return FP8BS_ERR_POINTER;
-    if (n > 0 && (!aligned(ids, (uintptr_t)id_bytes) || !aligned(positions, 4) || !aligned(x)))
+    // (tokens' rows and scales are fetched before it is known whether their choices have a row)
+    if (n > 0 && (!aligned(ids, (uintptr_t)id_bytes) || !aligned(positions, 4) || !aligned(x) ||
+                  (e4m3 && !aligned(sfx))))
         return FP8BS_ERR_POINTER;
-    if (n > 0 && rows > 0 && (!aligned(a) || (e4m3 && (!aligned(sfx) || !aligned(sfa)))))
-        return FP8BS_ERR_POINTER;
+    if (n > 0 && rows > 0 && (!aligned(a) || (e4m3 && !aligned(sfa)))) return FP8BS_ERR_POINTER;
     if (need > 0 && !aligned(workspace)) return FP8BS_ERR_POINTER;
     if (workspace_bytes < (size_t)need) return FP8BS_ERR_UNSUPPORTED;
     DispatchParams p = {};
