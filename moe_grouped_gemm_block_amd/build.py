@@ -1,6 +1,6 @@
-"""Build libfp8bs.so (HIP for gfx950) in-tree with hipcc, and the CPython module through which
-the layer operators' small calls reach it (host code alone, with the host compiler and torch's
-headers).
+"""Build libfp8bs.so (HIP for gfx950) in-tree with hipcc, and, where torch is installed, the CPython
+module through which the layer operators' small calls reach it (host code alone, with the host
+compiler and torch's headers).
 
     python -m moe_grouped_gemm_block_amd.build
 
@@ -54,37 +54,51 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _module() -> str:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+def _module() -> str | None:
+    """The CPython module; None without torch, whose headers it takes."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     include = os.path.join(torch, "include")
     tmp = MODULE + ".tmp"
-    cmd = [os.environ.get("CXX", shutil.which("g++") or "c++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
+    # (hipcc, which the library needs anyway, where there is no other compiler)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++") or HIPCC
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
            "-I" + os.path.join(ROOT, "include"), "-isystem", include,
            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "fp8bs_layer_py.cpp"),
            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"fp8bs_layer_py.cpp: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for fp8bs_layer_py.cpp:\n{r.stderr}")
-    os.replace(tmp, MODULE)
-    return MODULE
+    return tmp
 
 
 def build(verbose: bool = False) -> str:
+    """The library, then the module.  The library needs hipcc alone, and is in place whatever becomes
+    of the module: without torch there is none, and a failure of its own is raised last."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         module = ex.submit(_module)
         objs = list(ex.map(_compile, SOURCES))
-        module.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
+    if os.path.exists(MODULE):                      # (an older one need not fit the library)
+        os.remove(MODULE)
     os.replace(tmp, LIB)
+    made = module.result()
+    if made:
+        os.replace(made, MODULE)
     if verbose:
-        print(f"built {LIB} and {MODULE}")
+        print(f"built {LIB}" + (f" and {MODULE}" if made else "; no module for the binding without torch"))
     return LIB
 
 
