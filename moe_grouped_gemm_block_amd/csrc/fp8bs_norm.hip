@@ -109,9 +109,9 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (col[i] < p.k) put_values(p.out, p.out_bf16, at + col[i], s[i], p.far);
-        const float ms = row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k;
-        float rstd = 1.0f / sqrtf(ms + p.eps), told = rstd;
-        if (ms > 3.0e38f) {                    // the squares overflow: those of s 2^-96 do not
+        const float ms = row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps;
+        float rstd = 1.0f / sqrtf(ms), told = rstd;
+        if (ms > 3.0e38f) {                    // the sums overflow: those of s 2^-96 do not
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 sq[i] = 0.0f;
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
                     sq[i] += s[i][e] * s[i][e];
                 }
             }
-            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k);
+            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps * 0x1p-96f * 0x1p-96f);
             told = rstd * 0x1p-96f;
         }
         if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
