@@ -243,14 +243,16 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_backward_kernel
             }
             float dot[NV] = {};
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float t = g[i][e] * (s[i][e] * r);
-                    const float own = in && col[i] < p.k ? +t : 0.0f;
+                    const float own = in ? +t : 0.0f;
                     dot[i] += own * w[i][e];
-                    acc[i][e] += own;
+                    acc[i][e] += own;          // (past the last column: nobody reads it)
                 }
+                if (col[i] >= p.k) dot[i] = 0.0f;      // (not by a factor: a weight may be infinite)
+            }
             const float mean = row_sum<W>(sum_of<NV>(dot), part, turn) / (float)p.k;
             if (in)
 #pragma unroll

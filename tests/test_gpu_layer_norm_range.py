@@ -37,3 +37,24 @@ def test_squares_that_overflow_with_their_eps(rows, k, eps):
     x = torch.rand(rows, k, generator=gen, device="cuda") - 0.5
     x *= torch.tensor([1e10, 1e18, 3e19, 1e25, 3e38], device="cuda").repeat(rows // 5)[:, None]
     check(x, 1 + torch.rand(k, generator=gen, device="cuda"), eps)
+
+
+# lanes past the last column read the last weights again
+@pytest.mark.parametrize("rows,k", [(3, 8), (3, 264), (1100, 264), (3, 1000), (500, 1000), (3, 3000), (400, 3000),
+                                    (3, 7000), (600, 7000), (1100, 7000), (3, 9000), (3, 20000)])
+@pytest.mark.parametrize("place", [0, -1])
+def test_gradients_of_an_infinite_weight(rows, k, place):
+    gen = torch.Generator("cuda").manual_seed(k)
+    s, dy, dres = (torch.randn(rows, k, generator=gen, device="cuda") for _ in range(3))
+    rstd, w = 1 / torch.sqrt(s.square().mean(-1)), 1 + torch.rand(k, generator=gen, device="cuda")
+    w[place] = float("inf")
+    dx, dw = torch.empty_like(s), torch.empty(k, device="cuda")
+    fp8bs.fp8bs_rms_norm_backward(s, rstd, w, dy, dx, dres, dw)
+    s, r, w, dy, dres = (host(t).astype(np.float64) for t in (s, rstd, w, dy, dres))
+    h, g = s * r[:, None], dy * w
+    with np.errstate(invalid="ignore"):
+        want = dres + r[:, None] * (g - h * (g * h).mean(-1, keepdims=True))
+    # an infinite mean makes all of a row infinite but the weight's own column, a difference of infinities
+    assert np.isinf(np.delete(want, place % k, 1)).all() and np.isnan(want[:, place]).all()
+    assert np.array_equal(host(dx), want, equal_nan=True)
+    assert np.isfinite(host(dw)).all()
