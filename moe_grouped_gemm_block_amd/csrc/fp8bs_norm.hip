@@ -111,18 +111,20 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
                 if (col[i] < p.k) put_values(p.out, p.out_bf16, at + col[i], s[i], p.far);
         const float ms = row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps;
         float rstd = 1.0f / sqrtf(ms), told = rstd;
-        if (ms > 3.0e38f) {                    // the sums overflow: those of s 2^-96 do not
+        // The sums overflow: those of s 2^-72 do not (32768 squares of at most 2^112), and values of which that
+        // is no normal number are below 2^-110 of the root.
+        if (ms > 3.0e38f) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 sq[i] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    s[i][e] *= 0x1p-96f;
+                    s[i][e] *= 0x1p-72f;
                     sq[i] += s[i][e] * s[i][e];
                 }
             }
-            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps * 0x1p-96f * 0x1p-96f);
-            told = rstd * 0x1p-96f;
+            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps * 0x1p-72f * 0x1p-72f);
+            told = rstd * 0x1p-72f;
         }
         if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
         float top[NV], inv[NV], y[NV][8];

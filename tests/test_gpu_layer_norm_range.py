@@ -58,3 +58,12 @@ def test_gradients_of_an_infinite_weight(rows, k, place):
     assert np.isinf(np.delete(want, place % k, 1)).all() and np.isnan(want[:, place]).all()
     assert np.array_equal(host(dx), want, equal_nan=True)
     assert np.isfinite(host(dw)).all()
+
+
+@pytest.mark.parametrize("rows,k", SHAPES)
+def test_small_values_beside_squares_that_overflow(rows, k):
+    gen = torch.Generator("cuda").manual_seed(k)
+    x = torch.rand(rows, k, generator=gen, device="cuda") - 0.5
+    x[:, 0] = 4e19                                 # (its square alone overflows)
+    x[:, 1:] *= torch.logspace(-17, 15, k - 1, device="cuda")
+    check(x, 1 + torch.rand(k, generator=gen, device="cuda"), 1e-6)
