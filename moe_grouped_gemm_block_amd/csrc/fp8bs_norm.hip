@@ -112,19 +112,21 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 256) rms_norm_kernel(NormPara
         const float ms = row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps;
         float rstd = 1.0f / sqrtf(ms), told = rstd;
         // The sums overflow: those of s 2^-72 do not (32768 squares of at most 2^112), and values of which that
-        // is no normal number are below 2^-110 of the root.
-        if (ms > 3.0e38f) {
+        // is no normal number are below 2^-110 of the root.  Or the squares and eps may be no normal numbers
+        // themselves, which keep fewer bits: those of s 2^72 are.
+        if (ms > 3.0e38f || ms < 0x1p-120f) {
+            const float by = ms > 1.0f ? 0x1p-72f : 0x1p72f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 sq[i] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    s[i][e] *= 0x1p-72f;
+                    s[i][e] *= by;
                     sq[i] += s[i][e] * s[i][e];
                 }
             }
-            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps * 0x1p-72f * 0x1p-72f);
-            told = rstd * 0x1p-72f;
+            rstd = 1.0f / sqrtf(row_sum<W>(sum_of<NV>(sq), part, turn) / (float)p.k + p.eps * by * by);
+            told = rstd * by;
         }
         if (p.rstd && in && wr == 0 && lane == 0) p.rstd[row] = told;
         float top[NV], inv[NV], y[NV][8];

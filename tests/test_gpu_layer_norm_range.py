@@ -67,3 +67,13 @@ def test_small_values_beside_squares_that_overflow(rows, k):
     x[:, 0] = 4e19                                 # (its square alone overflows)
     x[:, 1:] *= torch.logspace(-17, 15, k - 1, device="cuda")
     check(x, 1 + torch.rand(k, generator=gen, device="cuda"), 1e-6)
+
+
+@pytest.mark.parametrize("rows,k", SHAPES)
+@pytest.mark.parametrize("eps", [1e-6, 2.0 ** -120, 2.0 ** -126, 1e-40, 1e-43, 2.0 ** -149])
+def test_squares_and_eps_below_the_normal_range(rows, k, eps):
+    """mean and eps that are no normal numbers: statistics to FP32's precision all the same"""
+    gen = torch.Generator("cuda").manual_seed(k)
+    x = torch.rand(rows, k, generator=gen, device="cuda") - 0.5
+    x *= torch.tensor([0.0, 1e-18, 3e-20, 1e-21, 1e-23], device="cuda").repeat(rows // 5)[:, None]
+    check(x, 1 + torch.rand(k, generator=gen, device="cuda"), eps)
