@@ -557,7 +557,8 @@ int fp8bs_feed_forward_mxfp4(int layout, const void* x, int x_dtype, const void*
  *   y         f32 or bf16 (y_dtype) [rows][k], optional; may be x if of its type
  *   q, sfa    y as e4m3, 1x128 (from y's FP32 values), optional
  *   rstd      f32 [rows], optional
- * At least one of residual_out, y and q is given; eps > 0.  The norm is that of the FP32 sum.
+ * At least one of residual_out, y and q is given; eps > 0, at most 3e38.  The norm is that of the
+ * FP32 sum; squares beyond FP32's range or below its normal numbers cost rstd and y no precision.
  *
  * fp8bs_rms_norm_backward -- with g = weight * dy and h = s * rstd:
  *     dx = dresidual + rstd * (g - h * mean of g h over the row),  dweight = sum over rows of dy h
@@ -586,7 +587,7 @@ int fp8bs_rms_norm_backward(const void* s, int s_dtype, const float* rstd, const
  *              outside 0 .. num_groups-1 (experts elsewhere) take no part.  A token may choose an
  *              expert twice.
  *   x          [tokens][k] e4m3 with sfx (1x128), bf16 or f32 (x_dtype); k a multiple of 128 for
- *              e4m3, else of 8
+ *              e4m3, else of 8.  May be read where no choice of a token has a row
  *   a, sfa     [m][k] (masked [num_groups][m][k]) in x's type, sfa for e4m3.  Rows that get no
  *              token are not written.
  *   group_data contiguous: grouped_layout [m], every entry written; masked: masked_m
@@ -641,7 +642,8 @@ int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const void* d,
  *              of 128, at most 2^20
  *   hq, sfh    h as e4m3, 1x128, [m][f]
  *   gq, sfg    g as e4m3, 1x128, [m][2f], optional: all that the backward pass needs of g
- * Rows that are not valid (of the contiguous layout: a negative index) are not written.
+ * Rows that are not valid (of the contiguous layout: a negative index) are not written.  Where the
+ * logistic function in act is below 2^-126 (gates below about -87, gelu_tanh -10) it counts as 0.
  *
  * fp8bs_gated_quantize_backward -- at the values of g (e4m3 with sfg, or bf16: g_dtype):
  *     dgate = dh * up * act'(gate),  dup = dh * act(gate)
@@ -649,13 +651,13 @@ int fp8bs_moe_combine_backward(const void* dy, int dy_dtype, const void* d,
  *   d          [dgate dup] in bf16 [m][2f];  dq, sfd: as e4m3, 1x128;  dqt, sfdt: as e4m3, 128x1
  *   hqt, sfht  h as e4m3, 128x1
  * each optional, at least one of d, dq, dqt and hqt given.  grouped_layout int32 [m] or NULL
- * (all rows valid; m then any).  Rows that are not valid are not read, nor written in d and dq;
- * in dqt and hqt they, and the rows up to a multiple of 128, are zeros.
+ * (all rows valid; m then any).  Rows that are not valid do not count, whatever they hold, and are not
+ * written in d and dq; in dqt and hqt they, and the rows up to a multiple of 128, are zeros.
  *
  * fp8bs_quantize_128x1 -- x f32, bf16 or e4m3 with sfx (1x128) (x_dtype) [rows][n] -> q, sf
  * (128x1); n a multiple of 16, of 128 for e4m3, at most 2^20.  Rows with a negative grouped_layout entry
- * (int32 [rows], optional; rows then a multiple of 128) are not read and count as zeros, as do
- * the rows up to a multiple of 128.
+ * (int32 [rows], optional; rows then a multiple of 128) count as zeros, whatever they hold, as do the
+ * rows up to a multiple of 128.
  */
 int fp8bs_gated_quantize(int layout, const void* g, void* hq, float* sfh, void* gq, float* sfg,
                          const int32_t* group_data, int m, int f, int num_groups, int activation,

@@ -250,7 +250,9 @@ __global__ void __launch_bounds__(256) dispatch_rank_kernel(DispatchParams p) {
     }
 }
 
-// A wavefront copies 1 KB of a token's row to the rows of its assignments (2 KB: 4% slower, 4 KB 6%).
+// A wavefront copies 1 KB of a token's row to the rows of its assignments (2 KB: 4% slower, 4 KB 6%).  The load
+// does not wait for the positions, so tokens without a row here are read too: 16384 tokens of one choice among 64
+// experts, eight of them here, take 35 us, of eight experts 51.
 __device__ __forceinline__ void copy_row(const DispatchParams& p, int token, int at,
                                          const int32_t* rows) {
     if (at >= p.vectors) return;
@@ -313,7 +315,9 @@ constexpr int few_assignments(int groups) { return groups < 64 ? 2048 : kFewAssi
 // Workgroup = one token at a time.  Each ranks its own choices by going through all earlier ones, 512
 // at a time; the token's row and scales are on their way meanwhile.  64 tokens, eight choices each,
 // e4m3 rows of 7168 into slots: 4.7 us replayed in a graph; a load of each kind after the other took
-// 5.8.  Three sizes of the choices' registers: 8 choices take 4.4 us with two a thread, 4.6 with eight.
+// 5.8.  Three sizes of the choices' registers: 8 choices take 4.4 us with two a thread, 4.6 with eight.  The
+// workgroups share grouped_layout's rows behind their tokens: far more rows than choices cost a single token 10 us
+// of 1024, 28 of 16384, 157 of 131072 (64 tokens 12).
 template <int MOST>
 __global__ void __launch_bounds__(256) dispatch_few_kernel(DispatchParams p) {
     constexpr int kIds = MOST / 256;               // of a thread
@@ -459,7 +463,8 @@ struct CombineBackwardParams {
 // group's largest |w dy| is |w| times that of |dy| (rounding keeps the order).  Workgroups go round
 // the 8 XCDs: eight tokens' first pairs are followed by their second ones, so that a token's pairs
 // find its dy in one L2.  16384 tokens of two choices, 7168 columns: 166 us (947 MB: 5.7 TB/s; reads
-// alone run at 6.9); 512 threads take the same.
+// alone run at 6.9); 512 threads take the same.  Tokens without a row here are read too: one choice among 64 experts,
+// eight of them here, 70 us, of eight experts 110.
 template <bool GB, bool FAR>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardParams p) {
     __shared__ float dots[2][2][4];

@@ -56,7 +56,8 @@ __device__ __forceinline__ u32x2 take8(const uint8_t* base, uint32_t at) {
     const u32x2* from = (const u32x2*)(base + at);
     return FAR ? __builtin_nontemporal_load(from) : *from;
 }
-// Eight bf16 or FP32 values
+// Eight bf16 or FP32 values.  (FP32 past the caches as well, unlike Eight::stream: columns from FP32, so and through them:
+// 4096 x 4096 17.1 us and 14.5, 8192 rows 32.2 and 33.2, 16384 rows 61.5 and 61.2, 33280 x 7168 226 and 213.)
 template <bool FAR, bool BF16>
 __device__ __forceinline__ void take(const void* base, uint32_t at, Eight<BF16>& v) {
     const u32x4* from = (const u32x4*)((const uint8_t*)base + at);

@@ -96,7 +96,7 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = from[i];
     }
-    // past the caches.  FP32 is not, nor is it stored so: its two pieces are half of every 32 bytes each,
+    // past the caches.  FP32 is not here, nor is it stored so: its two pieces are half of every 32 bytes each,
     // which only a cache makes whole (norm of 8192 x 7168 in FP32 142 us, past them 156; gradients 182, 217).
     __device__ __forceinline__ void stream(const void* x, int64_t at) {
         const u32x4* from = (const u32x4*)((const uint8_t*)x + at * (BF16 ? 2 : 4));

@@ -333,7 +333,10 @@ __global__ void __launch_bounds__(1024) rms_norm_sum_kernel(SumParams p) {
 //   6.2 and 5.8; the gradients 4096 rows 18.5 and 27
 //   7168 columns, 16 x 1 against 4 x 4: 64 rows 3.5 us against 3.9, 256 rows 4.1 and 4.4, 512 rows 6.3
 //   and 6.2, 1024 rows 12.2 and 11.1; the gradients 600 rows 15.4 and 17.4, 1024 rows 19.1 and 22.2, 2048
-//   rows 32.9 and 28.4
+//   rows 32.9 and 28.4 (between those two only 4 x 4 was measured: 1025 rows 22.7, 1280 24.0, 1536 25.1)
+// Past 16384 columns, 16 x 4, the gradients' values do not fit the 128 registers that 1024 threads leave each: some
+// 100 of a lane (bf16; FP32 115) go through scratch.  4096 x 32768 takes 576 us (1.07 GB: 1.9 TB/s), FP32 819, 100 rows
+// 57; of 16384 columns 104, 219 and 6.7.
 struct Shape {
     int waves, eights;
 };
